@@ -22,6 +22,19 @@ The functions mirror the C entry points declared in ``include/gemm355.h``:
     force_fp4_path(path)              # their path for the process (diagnostic)
     gemm_mxfp4_nt(M, N, K, Aq, SA, Bq, SB, C, stream=None)
     gemm_mxfp4_nt_bias_act(M, N, K, Aq, SA, Bq, SB, bias, activation, C, stream=None)
+    gemm_bf16_nt_bias_act_res(M, N, K, A, B, bias, activation, R, Z, C, workspace=None, workspace_bytes=None,
+                              stream=None)
+    gemm_bf16_nt_bias_act_bwd(M, N, K, A, B, Z, activation, dC, dA, dB, dbias, workspace=None,
+                              workspace_bytes=None, stream=None)
+    gemm_bf16_nt_gated(M, N, K, A, B, bias, activation, Z, C, workspace=None, workspace_bytes=None, stream=None)
+    gemm_bf16_nt_gated_bwd(M, N, K, A, B, Z, activation, dC, dA, dB, dbias, workspace=None,
+                           workspace_bytes=None, stream=None)
+    newton_schulz(batch, rows, cols, G, O, steps, coefficients, eps, workspace, workspace_bytes=None, stream=None)
+    bias_act_res_workspace_size(M, N, K)               # bytes of workspace of the five calls above
+    bias_act_bwd_workspace_size(M, N, K, activation)   # on the current device
+    gated_workspace_size(M, N, K)
+    gated_bwd_workspace_size(M, N, K)
+    newton_schulz_workspace_size(batch, rows, cols)
     force_instance(instance)          # BF16 instance override (diagnostic)
     force_supergroup(width)           # band width of the tile order (diagnostic)
     supergroup(tiles_n, K, kernel)    # the default band width of a kernel's visiting order
@@ -54,6 +67,10 @@ ERR_LAUNCH = 4
 ACT_NONE = 0         # fused epilogue activations (gemm_bf16_nt_bias_act)
 ACT_RELU = 1
 ACT_GELU_TANH = 2
+ACT_SILU = 3         # the layer calls only (gemm_bf16_nt_bias_act_res and those after it)
+
+BF16 = 0             # input types of newton_schulz
+FP32 = 1
 
 INSTANCE_AUTO = 0    # gemm_bf16_nt picks the instance by shape
 INSTANCE_LARGE = 1   # 256 x 256 output tiles
@@ -122,6 +139,27 @@ def load() -> ctypes.CDLL:
     lib.gemm_mxfp4_nt.restype = i
     lib.gemm_mxfp4_nt_bias_act.argtypes = [i, i, i, p, p, p, p, p, i, p, p]
     lib.gemm_mxfp4_nt_bias_act.restype = i
+    f, psz = ctypes.c_float, ctypes.POINTER(sz)
+    lib.gemm_bf16_nt_bias_act_res.argtypes = [i, i, i, p, p, p, i, p, p, p, p, sz, p]
+    lib.gemm_bf16_nt_bias_act_res.restype = i
+    lib.gemm_bf16_nt_bias_act_res_workspace_size.argtypes = [i, i, i, psz]
+    lib.gemm_bf16_nt_bias_act_res_workspace_size.restype = i
+    lib.gemm_bf16_nt_bias_act_bwd.argtypes = [i, i, i, p, p, p, i, p, p, p, p, p, sz, p]
+    lib.gemm_bf16_nt_bias_act_bwd.restype = i
+    lib.gemm_bf16_nt_bias_act_bwd_workspace_size.argtypes = [i, i, i, i, psz]
+    lib.gemm_bf16_nt_bias_act_bwd_workspace_size.restype = i
+    lib.gemm_bf16_nt_gated.argtypes = [i, i, i, p, p, p, i, p, p, p, sz, p]
+    lib.gemm_bf16_nt_gated.restype = i
+    lib.gemm_bf16_nt_gated_workspace_size.argtypes = [i, i, i, psz]
+    lib.gemm_bf16_nt_gated_workspace_size.restype = i
+    lib.gemm_bf16_nt_gated_bwd.argtypes = [i, i, i, p, p, p, i, p, p, p, p, p, sz, p]
+    lib.gemm_bf16_nt_gated_bwd.restype = i
+    lib.gemm_bf16_nt_gated_bwd_workspace_size.argtypes = [i, i, i, psz]
+    lib.gemm_bf16_nt_gated_bwd_workspace_size.restype = i
+    lib.gemm355_newton_schulz.argtypes = [i, i, i, i, p, i, f, f, f, f, p, p, sz, p]
+    lib.gemm355_newton_schulz.restype = i
+    lib.gemm355_newton_schulz_workspace_size.argtypes = [i, i, i, psz]
+    lib.gemm355_newton_schulz_workspace_size.restype = i
     lib.gemm355_status_string.argtypes = [i]
     lib.gemm355_status_string.restype = ctypes.c_char_p
     lib.gemm355_tile_order.argtypes = [i, i, i, p, p]
@@ -397,6 +435,135 @@ def gemm_mxfp4_nt_bias_act(M: int, N: int, K: int, Aq, SA, Bq, SB, bias, activat
     c = _addr(C, M * N * 2 if nz else 0, "C")
     _check(lib.gemm_mxfp4_nt_bias_act(M, N, K, aq, sa, bq, sb, bb, int(activation), c, _stream(stream)),
            "gemm_mxfp4_nt_bias_act")
+
+
+# ---- layers ------------------------------------------------------------------
+
+def _size_of(fn, *args) -> int:
+    out = ctypes.c_size_t(0)
+    _check(getattr(load(), fn)(*args, ctypes.byref(out)), fn)
+    return out.value
+
+
+def gemm_bf16_nt_bias_act_res(M: int, N: int, K: int, A, B, bias, activation: int, R, Z, C, workspace=None,
+                              workspace_bytes=None, stream=None) -> None:
+    """C = act(A @ B^T + bias) + R, and Z = A @ B^T + bias where Z is given.
+
+    bias (N), R (M x N, may be C itself) and Z (M x N, an output) may be None;
+    activation: ACT_NONE, ACT_RELU, ACT_GELU_TANH or ACT_SILU. The workspace
+    holds bias_act_res_workspace_size(M, N, K) bytes (None when that is 0)."""
+    lib = load()
+    M, N, K = int(M), int(N), int(K)
+    nz = M > 0 and N > 0
+    a = _addr(A, M * K * 2 if nz else 0, "A")
+    b = _addr(B, N * K * 2 if nz else 0, "B")
+    bb = _addr(bias, N * 2 if nz else 0, "bias")
+    r = _addr(R, M * N * 2 if nz else 0, "R")
+    z = _addr(Z, M * N * 2 if nz else 0, "Z")
+    c = _addr(C, M * N * 2 if nz else 0, "C")
+    w, nb = _workspace(workspace, workspace_bytes)
+    _check(lib.gemm_bf16_nt_bias_act_res(M, N, K, a, b, bb, int(activation), r, z, c, w, nb, _stream(stream)),
+           "gemm_bf16_nt_bias_act_res")
+
+
+def bias_act_res_workspace_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes of gemm_bf16_nt_bias_act_res on the current device."""
+    return _size_of("gemm_bf16_nt_bias_act_res_workspace_size", int(M), int(N), int(K))
+
+
+def _backward(fn, M, N, K, rows, A, B, Z, activation, dC, dA, dB, dbias, workspace, workspace_bytes, stream):
+    M, N, K, rows = int(M), int(N), int(K), int(rows)
+    ok = M >= 0 and N >= 0 and K >= 0   # (else the call refuses the sizes)
+    a = _addr(A, M * K * 2 if ok else 0, "A")
+    b = _addr(B, rows * K * 2 if ok else 0, "B")
+    z = _addr(Z, M * rows * 2 if ok else 0, "Z")
+    dc = _addr(dC, M * N * 2 if ok else 0, "dC")
+    da = _addr(dA, M * K * 2 if ok else 0, "dA")
+    db = _addr(dB, rows * K * 2 if ok else 0, "dB")
+    dbb = _addr(dbias, rows * 2 if ok else 0, "dbias")
+    w, nb = _workspace(workspace, workspace_bytes)
+    _check(getattr(load(), fn)(M, N, K, a, b, z, int(activation), dc, da, db, dbb, w, nb, _stream(stream)), fn)
+
+
+def gemm_bf16_nt_bias_act_bwd(M: int, N: int, K: int, A, B, Z, activation: int, dC, dA, dB, dbias, workspace=None,
+                              workspace_bytes=None, stream=None) -> None:
+    """Gradients of act(A @ B^T + bias): dA (M x K), dB (N x K), dbias (N) from
+    dC (M x N) and the forward call's Z (None with ACT_NONE). Each output may
+    be None if it is not wanted (the residual's gradient is dC itself). The
+    workspace holds bias_act_bwd_workspace_size(M, N, K, activation) bytes."""
+    _backward("gemm_bf16_nt_bias_act_bwd", M, N, K, N, A, B, Z, activation, dC, dA, dB, dbias, workspace,
+              workspace_bytes, stream)
+
+
+def bias_act_bwd_workspace_size(M: int, N: int, K: int, activation: int) -> int:
+    """Workspace bytes of gemm_bf16_nt_bias_act_bwd on the current device."""
+    return _size_of("gemm_bf16_nt_bias_act_bwd_workspace_size", int(M), int(N), int(K), int(activation))
+
+
+def gemm_bf16_nt_gated(M: int, N: int, K: int, A, B, bias, activation: int, Z, C, workspace=None,
+                       workspace_bytes=None, stream=None) -> None:
+    """C = act(Z[:, :N]) * Z[:, N:] with Z = A @ B^T + bias, M x 2N: B (2N x K)
+    holds the gate rows, then the up rows. bias (2N) and Z (an output) may be
+    None; activations and workspace (gated_workspace_size(M, N, K) bytes) as
+    for gemm_bf16_nt_bias_act_res."""
+    lib = load()
+    M, N, K = int(M), int(N), int(K)
+    nz = M > 0 and N > 0
+    a = _addr(A, M * K * 2 if nz else 0, "A")
+    b = _addr(B, 2 * N * K * 2 if nz else 0, "B")
+    bb = _addr(bias, 2 * N * 2 if nz else 0, "bias")
+    z = _addr(Z, M * 2 * N * 2 if nz else 0, "Z")
+    c = _addr(C, M * N * 2 if nz else 0, "C")
+    w, nb = _workspace(workspace, workspace_bytes)
+    _check(lib.gemm_bf16_nt_gated(M, N, K, a, b, bb, int(activation), z, c, w, nb, _stream(stream)),
+           "gemm_bf16_nt_gated")
+
+
+def gated_workspace_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes of gemm_bf16_nt_gated on the current device."""
+    return _size_of("gemm_bf16_nt_gated_workspace_size", int(M), int(N), int(K))
+
+
+def gemm_bf16_nt_gated_bwd(M: int, N: int, K: int, A, B, Z, activation: int, dC, dA, dB, dbias, workspace=None,
+                           workspace_bytes=None, stream=None) -> None:
+    """Gradients of the gated layer: dA (M x K), dB (2N x K), dbias (2N) from
+    dC (M x N) and the forward call's Z (M x 2N); otherwise as for
+    gemm_bf16_nt_bias_act_bwd (gated_bwd_workspace_size(M, N, K) bytes)."""
+    _backward("gemm_bf16_nt_gated_bwd", M, N, K, 2 * int(N), A, B, Z, activation, dC, dA, dB, dbias, workspace,
+              workspace_bytes, stream)
+
+
+def gated_bwd_workspace_size(M: int, N: int, K: int) -> int:
+    """Workspace bytes of gemm_bf16_nt_gated_bwd on the current device."""
+    return _size_of("gemm_bf16_nt_gated_bwd_workspace_size", int(M), int(N), int(K))
+
+
+def newton_schulz(batch: int, rows: int, cols: int, G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
+                  eps: float = 1e-7, workspace=None, workspace_bytes=None, stream=None, g_type=None) -> None:
+    """O (BF16) = the batch's matrices G (rows x cols, BF16 or FP32) after
+    division by their Frobenius norm + eps and `steps` Newton-Schulz steps
+    X <- a X + (b X X^T + c (X X^T)^2) X with coefficients (a, b, c). G's type
+    is its tensor's (g_type, BF16 or FP32, names it for a raw address). The
+    workspace holds newton_schulz_workspace_size(batch, rows, cols) bytes."""
+    batch, rows, cols = int(batch), int(rows), int(cols)
+    if g_type is None:
+        import torch
+        types = {torch.bfloat16: BF16, torch.int16: BF16, torch.uint16: BF16, torch.float32: FP32}
+        if not isinstance(G, torch.Tensor) or G.dtype not in types:
+            raise TypeError("G: expected a BF16 or FP32 tensor, or an address with g_type")
+        g_type = types[G.dtype]
+    n = batch * rows * cols if min(batch, rows, cols) > 0 else 0
+    gg = _addr(G, n * (4 if g_type == FP32 else 2), "G")
+    o = _addr(O, n * 2, "O")
+    w, nb = _workspace(workspace, workspace_bytes)
+    a, b, c = coefficients
+    _check(load().gemm355_newton_schulz(batch, rows, cols, int(g_type), gg, int(steps), a, b, c, eps, o, w, nb,
+                                        _stream(stream)), "gemm355_newton_schulz")
+
+
+def newton_schulz_workspace_size(batch: int, rows: int, cols: int) -> int:
+    """Workspace bytes of newton_schulz on the current device."""
+    return _size_of("gemm355_newton_schulz_workspace_size", int(batch), int(rows), int(cols))
 
 
 def force_instance(instance: int) -> None:

@@ -4,15 +4,18 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libgemm355.so")
-SOURCES = [os.path.join(CSRC, "gemm355.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("gemm355.hip", "dense_ops.hip")]
 HEADERS = [os.path.join(CSRC, f) for f in ("common.hpp", "gemm_bf16.hpp", "gemm_bf16_small.hpp", "gemm_bf16_small_long.hpp", "gemm_bf16_splitk.hpp",
-                                           "gemm_fp4.hpp", "fp4_decode.hpp", "gemm_mxfp4.hpp", "schedule.hpp")] + \
+                                           "gemm_fp4.hpp", "fp4_decode.hpp", "gemm_mxfp4.hpp", "schedule.hpp", "host.hpp",
+                                           "dense_common.hpp", "dense_tile.hpp", "dense_grad.hpp", "newton_schulz.hpp")] + \
     [os.path.join(INCLUDE, "gemm355.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -21,7 +24,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # the LDS copies clobber m0 on purpose (the compiler uses m0 nowhere else)
     "-Wno-inline-asm",
@@ -30,10 +32,8 @@ FLAGS = [
 ]
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every HIP source of the library into LIB_PATH. Always recompiles."""
-    tmp = LIB_PATH + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *SOURCES]
+def _hipcc(args, verbose):
+    cmd = [HIPCC, *args]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -43,7 +43,18 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed (%d):\n%s" % (res.returncode, "\n".join(msgs)))
     if msgs and verbose:
         print("\n".join(msgs), file=sys.stderr)
-    os.replace(tmp, LIB_PATH)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every HIP source of the library into LIB_PATH. Always recompiles."""
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SOURCES]
+        with ThreadPoolExecutor(len(SOURCES)) as pool:   # one compiler process per source
+            list(pool.map(lambda so: _hipcc([*FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", "-o", so[1], so[0]], verbose),
+                          zip(SOURCES, objs)))
+        out = LIB_PATH + ".tmp%d" % os.getpid()
+        _hipcc(["--offload-arch=gfx950", "-shared", "-fPIC", "-o", out, *objs], verbose)
+    os.replace(out, LIB_PATH)
     return LIB_PATH
 
 

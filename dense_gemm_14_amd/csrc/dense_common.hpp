@@ -1,0 +1,358 @@
+// dense_common.hpp -- pieces shared by the kernels of the dense layer's fused
+// operators (linear and gated layers, their gradients, Newton-Schulz): operand
+// layouts, LDS-DMA copies, activations with their derivatives, and epilogues.
+//
+// The products are C = op(A) op(B)^T with the contraction over K:
+//   ROW_K  the operand is stored (rows x K), K contiguous: a fragment's eight
+//          K elements are 16 consecutive bytes;
+//   COL_K  it is stored (K x rows), rows contiguous, as the weights of an
+//          input gradient (dZ B) and both operands of a weight gradient
+//          (dZ^T A) are. gfx950's transposing LDS read (ds_read_b64_tr_b16)
+//          gathers a fragment's K elements, so no operand is transposed in
+//          memory first.
+#pragma once
+
+#include "common.hpp"
+
+namespace gemm355 {
+namespace dense {
+
+enum Layout { ROW_K = 0, COL_K = 1 };
+enum Epilogue {
+    EPI_STORE = 0,   // C = round(alpha acc)
+    EPI_LINEAR = 1,  // z = acc + bias, Z = round(z) if wanted, C = round(act(z) + R)
+    EPI_GATED = 2,   // gate and up sums of one column: C = round(act(zg) zu), Z = round of both if wanted
+    EPI_POLY = 3     // C = round(alpha acc + beta R + gamma [row == column])
+};
+// Activations (the values of gemm355_activation).
+enum { A_NONE = 0, A_RELU = 1, A_GELU = 2, A_SILU = 3 };
+
+struct DenseArgs {
+    const void *a, *b;
+    void *c;
+    const void *r;       // residual (EPI_LINEAR: BF16, may be NULL or c itself), second term (EPI_POLY: FP16)
+    void *z;             // EPI_LINEAR, EPI_GATED: pre-activations, or NULL
+    const void *bias;    // EPI_LINEAR: N, EPI_GATED: 2 N BF16 values, or NULL
+    float *ws;           // split K: FP32 partial tiles
+    int M, N, K;         // C is M x N (EPI_GATED: B has 2 N rows)
+    int tiles_m, tiles_n, tiles;   // tiles: per batch entry (with symmetric: on and below the diagonal)
+    int splits, steps_per_split;
+    int supergroup;
+    int act;
+    int symmetric;       // C == C^T: tiles below the diagonal are stored twice
+    int batch;
+    int grid;            // persistent kernel: its workgroups
+    float alpha, beta, gamma;
+};
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+template <class T> struct Frag;
+template <> struct Frag<__bf16> {
+    typedef bf16x8 type;
+    static __device__ inline f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+};
+template <> struct Frag<_Float16> {
+    typedef f16x8 type;
+    static __device__ inline f32x4 mma(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+};
+
+// Four elements of a transposed fragment. The 16 lanes of a group hand in the
+// addresses of four K rows (lane j: row j / 4, 8-byte piece j % 4 of its 32
+// bytes); lane j receives column j of those four rows.
+__device__ inline s16x4 read_tr(unsigned lds_addr)
+{
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(uintptr_t)lds_addr);
+}
+
+__device__ inline i32x4 rsrc_words(const void *p, unsigned bytes)
+{
+    const unsigned long long a = reinterpret_cast<unsigned long long>(p);
+    return i32x4{(int)(unsigned)a, (int)(unsigned)(a >> 32), (int)bytes, (int)RSRC_WORD3};
+}
+
+__device__ inline void wait_all_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <int N>
+__device__ inline void wait_copies_le() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+__device__ inline void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// ---- activations -----------------------------------------------------------
+//
+// Both gated-linear activations are z sigma(w(z)): w = z for SiLU and
+// w = 2 sqrt(2/pi) (z + 0.044715 z^3) for the tanh GELU, sigma the logistic
+// function, evaluated with the hardware's exponential and reciprocal (about
+// one part in 10^6, far below the 16-bit roundings that follow). Their
+// derivative is sigma + z sigma (1 - sigma) w'.
+constexpr float GELU_C0 = 1.5957691216f;   // 2 sqrt(2/pi)
+constexpr float GELU_C1 = 0.0713548163f;   // 2 sqrt(2/pi) 0.044715
+
+template <int ACT>
+__device__ inline float act_value(float z)
+{
+    if constexpr (ACT == A_RELU)
+        return z > 0.0f ? z : 0.0f;
+    if constexpr (ACT == A_GELU)
+        return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z * (GELU_C0 + GELU_C1 * z * z)));
+    if constexpr (ACT == A_SILU)
+        return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+    return z;
+}
+
+// act(z) in *value and act'(z) as the result.
+template <int ACT>
+__device__ inline float act_slope(float z, float *value)
+{
+    if constexpr (ACT == A_RELU) {
+        *value = z > 0.0f ? z : 0.0f;
+        return z > 0.0f ? 1.0f : 0.0f;
+    }
+    if constexpr (ACT == A_GELU) {
+        // past |z| = 12 sigma is 0 or 1 in FP32 and the slope with it; the
+        // clamp keeps z^3 finite there
+        const float y = fminf(fmaxf(z, -12.0f), 12.0f);
+        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-y * (GELU_C0 + GELU_C1 * y * y)));
+        *value = z * s;
+        return s + y * s * (1.0f - s) * (GELU_C0 + 3.0f * GELU_C1 * y * y);
+    }
+    if constexpr (ACT == A_SILU) {
+        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+        *value = z * s;
+        return s + z * s * (1.0f - s);
+    }
+    *value = z;
+    return 1.0f;
+}
+
+// f(Int<ACT>{}) for the activation chosen at run time (uniform).
+template <class F>
+__device__ inline void with_act(int act, F &&f)
+{
+    switch (act) {
+    case A_RELU: f(Int<A_RELU>{}); break;
+    case A_GELU: f(Int<A_GELU>{}); break;
+    case A_SILU: f(Int<A_SILU>{}); break;
+    default: f(Int<A_NONE>{}); break;
+    }
+}
+
+// ---- tile order ------------------------------------------------------------
+
+// Tile p of a symmetric result: rows of tiles, the diagonal last.
+__device__ inline void triangle_tile(int p, int &tm, int &tn)
+{
+    int t = (int)((__builtin_sqrtf(8.0f * (float)p + 1.0f) - 1.0f) * 0.5f);
+    while (t * (t + 1) / 2 > p)   // the square root is off by one at most
+        --t;
+    while ((t + 1) * (t + 2) / 2 <= p)
+        ++t;
+    tm = t;
+    tn = p - t * (t + 1) / 2;
+}
+
+__device__ inline void dense_tile(const DenseArgs &p, int pos, int &tm, int &tn)
+{
+    if (p.symmetric)
+        triangle_tile(pos, tm, tn);
+    else
+        supergroup_tile(pos, p.tiles_m, p.tiles_n, p.supergroup, tm, tn);
+}
+
+// The arguments of batch entry `b`: every array advanced by its own size.
+__device__ inline void enter_batch(DenseArgs &p, int b)
+{
+    const size_t i = (size_t)b;
+    p.a = static_cast<const uint8_t *>(p.a) + i * (size_t)p.M * (size_t)p.K * 2;
+    p.b = static_cast<const uint8_t *>(p.b) + i * (size_t)p.N * (size_t)p.K * 2;
+    p.c = static_cast<uint8_t *>(p.c) + i * (size_t)p.M * (size_t)p.N * 2;
+    if (p.r)
+        p.r = static_cast<const uint8_t *>(p.r) + i * (size_t)p.M * (size_t)p.N * 2;
+}
+
+// ---- epilogues -------------------------------------------------------------
+//
+// The matrix instruction is fed B rows as its first operand and A rows as its
+// second, so lane (l16, grp) of a 16 x 16 block holds C[m][n .. n + 3],
+// m = row + l16, n = column + 4 grp. v_permlane16_swap of two neighbouring
+// blocks x, y (columns c .. c + 15 and c + 16 .. c + 31) leaves each lane with
+// eight consecutive columns, c + 16 (grp & 1) + 8 (grp >> 1): one 16-byte
+// access. The swap is its own inverse, so 16 bytes loaded at that place turn
+// back into the two blocks' four columns each.
+
+template <class T> __device__ inline unsigned pack2(float lo, float hi);
+template <> __device__ inline unsigned pack2<__bf16>(float lo, float hi) { return pack_bf16(lo, hi); }
+template <> __device__ inline unsigned pack2<_Float16>(float lo, float hi)
+{
+    f32x2 v = {lo, hi};
+    return __builtin_bit_cast(unsigned, __builtin_convertvector(v, f16x2));   // round to nearest even
+}
+template <class T> __device__ inline f32x2 unpack2(unsigned w);
+template <> __device__ inline f32x2 unpack2<__bf16>(unsigned w) { return f32x2{bf16_lo(w), bf16_hi(w)}; }
+template <> __device__ inline f32x2 unpack2<_Float16>(unsigned w)
+{
+    return __builtin_convertvector(__builtin_bit_cast(f16x2, w), f32x2);
+}
+
+template <class T>
+__device__ inline u32x4 pack_pair(f32x4 x, f32x4 y)
+{
+    const auto s0 = __builtin_amdgcn_permlane16_swap(pack2<T>(x[0], x[1]), pack2<T>(y[0], y[1]), false, false);
+    const auto s1 = __builtin_amdgcn_permlane16_swap(pack2<T>(x[2], x[3]), pack2<T>(y[2], y[3]), false, false);
+    return u32x4{s0[0], s1[0], s0[1], s1[1]};
+}
+
+template <class T>
+__device__ inline void unpack_pair(u32x4 w, f32x4 &x, f32x4 &y)
+{
+    const auto s0 = __builtin_amdgcn_permlane16_swap(w[0], w[2], false, false);
+    const auto s1 = __builtin_amdgcn_permlane16_swap(w[1], w[3], false, false);
+    const f32x2 x0 = unpack2<T>(s0[0]), x1 = unpack2<T>(s1[0]), y0 = unpack2<T>(s0[1]), y1 = unpack2<T>(s1[1]);
+    x = f32x4{x0[0], x0[1], x1[0], x1[1]};
+    y = f32x4{y0[0], y0[1], y1[0], y1[1]};
+}
+
+__device__ inline f32x4 add_bias(f32x4 x, u32x2 w)
+{
+    return f32x4{x[0] + bf16_lo(w[0]), x[1] + bf16_hi(w[0]), x[2] + bf16_lo(w[1]), x[3] + bf16_hi(w[1])};
+}
+
+template <int ACT>
+__device__ inline f32x4 act4(f32x4 x)
+{
+    return f32x4{act_value<ACT>(x[0]), act_value<ACT>(x[1]), act_value<ACT>(x[2]), act_value<ACT>(x[3])};
+}
+
+// The epilogue's view of the arrays (each resource ends at its array's last
+// byte; a NULL array's range is empty, so its loads give zeros and its stores
+// do nothing).
+struct Views {
+    __amdgpu_buffer_rsrc_t c, r, z, bias;
+};
+
+template <int EPI>
+__device__ inline Views make_views(const DenseArgs &p)
+{
+    constexpr unsigned W = EPI == EPI_GATED ? 2 : 1;
+    const unsigned mn = (unsigned)p.M * (unsigned)p.N * 2u;
+    return Views{make_rsrc(p.c, mn), make_rsrc(p.r, p.r ? mn : 0u), make_rsrc(p.z, p.z ? W * mn : 0u),
+                 make_rsrc(p.bias, p.bias ? W * (unsigned)p.N * 2u : 0u)};
+}
+
+// Offset in bytes of this lane's eight columns of the block pair at column
+// `col` in row m of an array `width` columns wide; OOB outside C.
+__device__ inline int pair_offset(const DenseArgs &p, int m, int col, int width, int shift, int lane)
+{
+    const int grp = lane >> 4;
+    const int n = col + 16 * (grp & 1) + 8 * (grp >> 1);
+    return m < p.M && n < p.N ? (int)(((unsigned)m * (unsigned)width + (unsigned)(n + shift)) * 2u) : OOB;
+}
+
+__device__ inline u32x4 load16(const __amdgpu_buffer_rsrc_t &r, int off)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ inline u32x2 load_bias4(const __amdgpu_buffer_rsrc_t &r, int n, int limit)
+{
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, n < limit ? n * 2 : OOB, 0, 0));
+}
+
+// One row of blocks of a wave's tile: x[0 .. BJ - 1], BJ blocks side by side
+// at column `col` (EPI_GATED: BJ / 2 gate blocks at `col`, then the up blocks
+// of the same columns), this lane's row m.
+template <int EPI, class TO, int BJ>
+__device__ inline void store_row(const DenseArgs &p, const Views &v, f32x4 (&x)[BJ], int m, int col, int lane)
+{
+    const int grp = lane >> 4;
+    if constexpr (EPI == EPI_GATED) {
+        constexpr int H = BJ / 2;
+        static_assert(H % 2 == 0, "blocks are stored in pairs");
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const int n = col + 16 * j + 4 * grp;
+            x[j] = add_bias(x[j], load_bias4(v.bias, n, p.N));
+            // the up half's bias starts at N (a multiple of 8)
+            const int nu = n < p.N ? n + p.N : OOB / 2;
+            x[H + j] = add_bias(x[H + j], __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(v.bias, nu * 2, 0, 0)));
+        }
+        with_act(p.act, [&](auto act_c) {
+            constexpr int ACT = decltype(act_c)::value;
+#pragma unroll
+            for (int j = 0; j < H; j += 2) {
+                if (p.z) {
+                    __builtin_amdgcn_raw_buffer_store_b128(pack_pair<__bf16>(x[j], x[j + 1]), v.z,
+                                                           pair_offset(p, m, col + 16 * j, 2 * p.N, 0, lane), 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(pack_pair<__bf16>(x[H + j], x[H + j + 1]), v.z,
+                                                           pair_offset(p, m, col + 16 * j, 2 * p.N, p.N, lane), 0, 0);
+                }
+                const f32x4 h0 = act4<ACT>(x[j]) * x[H + j], h1 = act4<ACT>(x[j + 1]) * x[H + j + 1];
+                __builtin_amdgcn_raw_buffer_store_b128(pack_pair<__bf16>(h0, h1), v.c,
+                                                       pair_offset(p, m, col + 16 * j, p.N, 0, lane), 0, 0);
+            }
+        });
+    } else if constexpr (EPI == EPI_LINEAR) {
+        static_assert(BJ % 2 == 0, "blocks are stored in pairs");
+        u32x4 res[BJ / 2];
+#pragma unroll
+        for (int j = 0; j < BJ; j += 2)
+            res[j / 2] = p.r ? load16(v.r, pair_offset(p, m, col + 16 * j, p.N, 0, lane)) : u32x4{};
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+            x[j] = add_bias(x[j], load_bias4(v.bias, col + 16 * j + 4 * grp, p.N));
+        with_act(p.act, [&](auto act_c) {
+            constexpr int ACT = decltype(act_c)::value;
+#pragma unroll
+            for (int j = 0; j < BJ; j += 2) {
+                const int off = pair_offset(p, m, col + 16 * j, p.N, 0, lane);
+                if (p.z)
+                    __builtin_amdgcn_raw_buffer_store_b128(pack_pair<__bf16>(x[j], x[j + 1]), v.z, off, 0, 0);
+                f32x4 y0 = act4<ACT>(x[j]), y1 = act4<ACT>(x[j + 1]);
+                if (p.r) {
+                    f32x4 r0, r1;
+                    unpack_pair<__bf16>(res[j / 2], r0, r1);
+                    y0 += r0;
+                    y1 += r1;
+                }
+                __builtin_amdgcn_raw_buffer_store_b128(pack_pair<__bf16>(y0, y1), v.c, off, 0, 0);
+            }
+        });
+    } else {
+#pragma unroll
+        for (int j = 0; j < BJ; j += 2) {
+            const int off = pair_offset(p, m, col + 16 * j, p.N, 0, lane);
+            f32x4 y0 = x[j] * p.alpha, y1 = x[j + 1] * p.alpha;
+            if constexpr (EPI == EPI_POLY) {
+                f32x4 r0, r1;
+                unpack_pair<TO>(load16(v.r, off), r0, r1);
+                const int n = col + 16 * j + 4 * grp;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y0[e] += p.beta * r0[e] + (m == n + e ? p.gamma : 0.0f);
+                    y1[e] += p.beta * r1[e] + (m == n + 16 + e ? p.gamma : 0.0f);
+                }
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(pack_pair<TO>(y0, y1), v.c, off, 0, 0);
+            x[j] = y0;
+            x[j + 1] = y1;
+        }
+    }
+}
+
+// The mirror image of such a row for a symmetric result: C[n][m] = C[m][n].
+// Lanes of a group hold 16 consecutive m of one n: 32-byte runs.
+template <class TO, int BJ>
+__device__ inline void store_row_mirrored(const DenseArgs &p, const Views &v, f32x4 (&y)[BJ], int m, int col, int lane)
+{
+    const int grp = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < BJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = col + 16 * j + 4 * grp + e;
+            const int off = m < p.M && n < p.N ? (int)(((unsigned)n * (unsigned)p.N + (unsigned)m) * 2u) : OOB;
+            __builtin_amdgcn_raw_buffer_store_b16((short)(pack2<TO>(y[j][e], 0.0f) & 0xFFFFu), v.c, off, 0, 0);
+        }
+}
+
+} // namespace dense
+} // namespace gemm355

@@ -1,0 +1,516 @@
+// dense_ops.hip -- host side of the dense layer's fused operators: argument
+// checks, plans, workspace layout and launches of the kernels in
+// dense_tile.hpp, dense_grad.hpp and newton_schulz.hpp. The C ABI is declared
+// in include/gemm355.h. Nothing here allocates memory.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <math.h>
+#include <stdint.h>
+
+#include "gemm355.h"
+#include "host.hpp"
+#include "dense_tile.hpp"
+#include "dense_grad.hpp"
+#include "newton_schulz.hpp"
+
+namespace {
+
+using namespace gemm355::host;
+namespace d = gemm355::dense;
+using d::DenseArgs;
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+
+// ---- products --------------------------------------------------------------
+
+// One product C = op(A) op(B)^T of a batch, as the plans see it.
+struct Shape {
+    int M, N, K;      // of one batch entry; N: columns of C
+    int batch;
+    bool symmetric;
+    bool gated;
+};
+
+// K splits of a product on 128 x 128 tiles and the bytes of its partials. As
+// many splits as give every compute unit a tile, each at least kMinSteps K
+// steps long.
+struct TilePlan {
+    int tiles_m, tiles_n, tiles, splits, steps_per_split;
+    size_t workspace_bytes;
+};
+constexpr int kMaxSplits = 16;
+constexpr int kMinSteps = 4;
+
+TilePlan plan_tile(const Shape &s, int cus)
+{
+    TilePlan t = {};
+    t.tiles_m = (int)ceil_div(s.M, d::TILE);
+    t.tiles_n = (int)ceil_div(s.N, s.gated ? d::TILE / 2 : d::TILE);
+    t.tiles = s.symmetric ? t.tiles_m * (t.tiles_m + 1) / 2 : t.tiles_m * t.tiles_n;
+    const int nk = (int)ceil_div(s.K, d::TILE_BK);
+    int64_t n = cus / std::max<int64_t>(1, int64_t(t.tiles) * s.batch);
+    n = std::max<int64_t>(1, std::min<int64_t>({n, kMaxSplits, nk / kMinSteps}));
+    t.steps_per_split = (int)std::max<int64_t>(1, ceil_div(nk, n));
+    t.splits = std::max(1, (int)ceil_div(nk, t.steps_per_split));
+    t.workspace_bytes = t.splits > 1 ? size_t(t.tiles) * s.batch * t.splits * d::TILE_FLOATS * sizeof(float) : 0;
+    return t;
+}
+
+size_t product_workspace(const Shape &s, int cus) { return plan_tile(s, cus).workspace_bytes; }
+
+Shape shape_of(const DenseArgs &p, bool gated) { return {p.M, p.N, p.K, p.batch, p.symmetric != 0, gated}; }
+
+// Launches a product. `ws` has product_workspace() bytes.
+template <class T, int LA, int LB, int EPI, class TO = T>
+int product(DenseArgs p, int cus, void *ws, hipStream_t stream)
+{
+    if (p.M == 0 || p.N == 0 || p.batch == 0)
+        return GEMM355_OK;
+    const TilePlan t = plan_tile(shape_of(p, EPI == d::EPI_GATED), cus);
+    p.tiles_m = t.tiles_m;
+    p.tiles_n = t.tiles_n;
+    p.tiles = t.tiles;
+    p.splits = t.splits;
+    p.steps_per_split = t.steps_per_split;
+    p.supergroup = 8;
+    p.ws = static_cast<float *>(ws);
+    const int64_t items = int64_t(t.tiles) * t.splits * p.batch;
+    if (items > (int64_t(1) << 28))
+        return GEMM355_ERR_UNSUPPORTED;
+    int st = launch_kernel(d::dense_tile_kernel<T, LA, LB, EPI, TO>, (unsigned)(ceil_div(items, 8) * 8),
+                           (unsigned)d::TILE_THREADS, p, stream);
+    if (st == GEMM355_OK && t.splits > 1)
+        st = launch_kernel(d::dense_reduce_kernel<EPI, TO>,
+                           (unsigned)ceil_div(int64_t(t.tiles) * p.batch * 16, d::REDUCE_WAVES),
+                           64u * d::REDUCE_WAVES, p, stream);
+    return st;
+}
+
+DenseArgs args_of(int M, int N, int K, const void *a, const void *b, void *c)
+{
+    DenseArgs p = {};
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.a = K > 0 ? a : nullptr;
+    p.b = K > 0 ? b : nullptr;
+    p.c = c;
+    p.batch = 1;
+    p.alpha = 1.0f;
+    return p;
+}
+
+// ---- argument checks -------------------------------------------------------
+
+// An array of a call: its address, size and required alignment.
+struct Array {
+    const void *p;
+    size_t bytes;
+};
+
+// Whether any output overlaps an input, the workspace or another output.
+bool any_overlap(const Array *out, int outs, const Array *in, int ins)
+{
+    for (int i = 0; i < outs; ++i) {
+        for (int j = 0; j < ins; ++j)
+            if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+                return true;
+        for (int j = i + 1; j < outs; ++j)
+            if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                return true;
+    }
+    return false;
+}
+
+bool all_aligned(const Array *a, int n)
+{
+    for (int i = 0; i < n; ++i)
+        if (!aligned(a[i].p, 16))
+            return false;
+    return true;
+}
+
+bool act_ok(int act) { return act >= GEMM355_ACT_NONE && act <= GEMM355_ACT_SILU; }
+
+// Extents of a layer with `rows` weight rows and N outputs: every array,
+// padded to whole tiles, below 2^31 bytes.
+bool layer_extents_ok(int64_t M, int64_t N, int64_t rows, int64_t K)
+{
+    return extent_ok(M, K * 2) && extent_ok(rows, K * 2) && extent_ok(M, rows * 2) && extent_ok(M, N * 2);
+}
+
+// ---- forward layers --------------------------------------------------------
+
+template <bool GATED>
+int layer_forward(int M, int N, int K, const void *A, const void *B, const void *bias, int act, const void *R, void *Z,
+                  void *C, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (M < 0 || N < 0 || K < 0 || !act_ok(act))
+        return GEMM355_ERR_INVALID_ARG;
+    if (M == 0 || N == 0)
+        return GEMM355_OK;
+    if (!C || (K > 0 && (!A || !B)) || (workspace_bytes > 0 && !workspace))
+        return GEMM355_ERR_INVALID_ARG;
+    const size_t rows = (GATED ? 2 : 1) * size_t(N);
+    const size_t c_bytes = size_t(M) * size_t(N) * 2;
+    const Array out[] = {{C, c_bytes}, {Z, size_t(M) * rows * 2}, {workspace, workspace_bytes}};
+    // C may be R itself: every element is read before it is written, by the same lane
+    const Array in[] = {{A, size_t(M) * K * 2}, {B, rows * K * 2}, {bias, rows * 2}, {R == C ? nullptr : R, c_bytes}};
+    if (any_overlap(out, 3, in, 4) || overlaps(Z, out[1].bytes, R, c_bytes) ||
+        overlaps(workspace, workspace_bytes, R, c_bytes))
+        return GEMM355_ERR_INVALID_ARG;
+    if (!all_aligned(out, 3) || !all_aligned(in, 4) || K % 8 != 0 || N % 8 != 0 ||
+        !layer_extents_ok(M, N, GATED ? 2 * int64_t(N) : N, K))
+        return GEMM355_ERR_UNSUPPORTED;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc != GEMM355_OK)
+        return rc;
+    if (workspace_bytes < product_workspace({M, N, K, 1, false, GATED}, cus))
+        return GEMM355_ERR_UNSUPPORTED;
+    DenseArgs p = args_of(M, N, K, A, B, C);
+    p.bias = bias;
+    p.act = act;
+    p.r = R;
+    p.z = Z;
+    return product<__bf16, d::ROW_K, d::ROW_K, GATED ? d::EPI_GATED : d::EPI_LINEAR>(
+        p, cus, workspace, static_cast<hipStream_t>(stream));
+}
+
+template <bool GATED>
+int layer_forward_workspace(int M, int N, int K, size_t *bytes)
+{
+    if (M < 0 || N < 0 || K < 0 || !bytes)
+        return GEMM355_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (M == 0 || N == 0)
+        return GEMM355_OK;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc == GEMM355_OK)
+        *bytes = product_workspace({M, N, K, 1, false, GATED}, cus);
+    return rc;
+}
+
+// ---- backward layers -------------------------------------------------------
+
+// Rows of a workgroup of the elementwise pass: enough workgroups for eight per
+// compute unit (256 units) where the array has the rows, at most 64 rows.
+int grad_rows(int M, int N)
+{
+    const int64_t col_blocks = ceil_div(N, d::GRAD_COLS);
+    const int64_t rows = ceil_div(int64_t(M) * col_blocks, 2048);
+    return (int)std::min<int64_t>(64, std::max<int64_t>(d::GRAD_LANES, ceil_div(rows, d::GRAD_LANES) * d::GRAD_LANES));
+}
+
+// Workspace of a backward call: the gradient of the pre-activations (unless
+// it is dC itself), the column sums, and the partials of whichever product
+// splits more.
+struct BackwardPlan {
+    size_t sums_at, partials_at, bytes;
+};
+
+BackwardPlan plan_backward(int M, int N, int K, bool gated, int act, int cus)
+{
+    const int rows = gated ? 2 * N : N;
+    BackwardPlan w = {};
+    w.sums_at = gated || act != GEMM355_ACT_NONE ? align_up(size_t(M) * rows * 2) : 0;
+    w.partials_at = w.sums_at + align_up(size_t(ceil_div(M, grad_rows(M, N))) * rows * sizeof(float));
+    size_t part = 0;
+    if (M > 0 && K > 0)
+        part = product_workspace({M, K, rows, 1, false, false}, cus);
+    if (rows > 0 && K > 0)
+        part = std::max(part, product_workspace({rows, K, M, 1, false, false}, cus));
+    w.bytes = w.partials_at + part;
+    return w;
+}
+
+template <bool GATED>
+int layer_backward(int M, int N, int K, const void *A, const void *B, const void *Z, int act, const void *dC, void *dA,
+                   void *dB, void *dbias, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (M < 0 || N < 0 || K < 0 || !act_ok(act))
+        return GEMM355_ERR_INVALID_ARG;
+    const size_t rows = (GATED ? 2 : 1) * size_t(N);
+    const bool wants_a = dA && M > 0 && K > 0, wants_b = dB && N > 0 && K > 0, wants_bias = dbias && N > 0;
+    if (!wants_a && !wants_b && !wants_bias)
+        return GEMM355_OK;
+    const bool needs_z = GATED || act != GEMM355_ACT_NONE;
+    if (M > 0 && N > 0 && (!dC || (needs_z && !Z) || (wants_a && !B) || (wants_b && !A)))
+        return GEMM355_ERR_INVALID_ARG;
+    if (workspace_bytes > 0 && !workspace)
+        return GEMM355_ERR_INVALID_ARG;
+    const size_t a_bytes = size_t(M) * K * 2, b_bytes = rows * K * 2;
+    const Array out[] = {{dA, a_bytes}, {dB, b_bytes}, {dbias, rows * 2}, {workspace, workspace_bytes}};
+    const Array in[] = {{A, a_bytes}, {B, b_bytes}, {Z, size_t(M) * rows * 2}, {dC, size_t(M) * N * 2}};
+    if (any_overlap(out, 4, in, 4))
+        return GEMM355_ERR_INVALID_ARG;
+    if (!all_aligned(out, 4) || !all_aligned(in, 4) || K % 8 != 0 || N % 8 != 0 ||
+        !layer_extents_ok(M, N, GATED ? 2 * int64_t(N) : N, K))
+        return GEMM355_ERR_UNSUPPORTED;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc != GEMM355_OK)
+        return rc;
+    const BackwardPlan w = plan_backward(M, N, K, GATED, act, cus);
+    if (workspace_bytes < w.bytes)
+        return GEMM355_ERR_UNSUPPORTED;
+
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const void *dz = needs_z ? ws : dC;
+    float *sums = reinterpret_cast<float *>(ws + w.sums_at);
+    const int per = grad_rows(M, N), blocks = (int)ceil_div(M, per);
+    if (M > 0 && N > 0 && (needs_z || wants_bias)) {
+        d::GradArgs g = {};
+        g.z = needs_z ? static_cast<const uint16_t *>(Z) : nullptr;
+        g.dc = static_cast<const uint16_t *>(dC);
+        g.dz = needs_z ? reinterpret_cast<uint16_t *>(ws) : nullptr;
+        g.sums = wants_bias ? sums : nullptr;
+        g.M = M;
+        g.N = N;
+        g.act = act;
+        g.rows = per;
+        g.col_blocks = (int)ceil_div(N, d::GRAD_COLS);
+        const int st = launch_kernel(d::dense_grad_kernel<GATED>, (unsigned)(int64_t(g.col_blocks) * blocks),
+                                     (unsigned)d::GRAD_THREADS, g, s);
+        if (st != GEMM355_OK)
+            return st;
+    }
+    if (wants_bias) {
+        d::BiasArgs q = {sums, static_cast<uint16_t *>(dbias), (int)rows, blocks};
+        const int st = launch_kernel(d::dense_bias_kernel, (unsigned)ceil_div(rows, d::BIAS_COLS),
+                                     (unsigned)(d::BIAS_COLS * d::BIAS_LANES), q, s);
+        if (st != GEMM355_OK)
+            return st;
+    }
+    if (wants_a) {   // dA = dZ B
+        const int st = product<__bf16, d::ROW_K, d::COL_K, d::EPI_STORE>(args_of(M, K, (int)rows, dz, B, dA), cus,
+                                                                        ws + w.partials_at, s);
+        if (st != GEMM355_OK)
+            return st;
+    }
+    if (wants_b)     // dB = dZ^T A
+        return product<__bf16, d::COL_K, d::COL_K, d::EPI_STORE>(args_of((int)rows, K, M, dz, A, dB), cus,
+                                                                ws + w.partials_at, s);
+    return GEMM355_OK;
+}
+
+template <bool GATED>
+int layer_backward_workspace(int M, int N, int K, int act, size_t *bytes)
+{
+    if (M < 0 || N < 0 || K < 0 || !act_ok(act) || !bytes)
+        return GEMM355_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (N == 0 && (M == 0 || K == 0))   // no output has an element
+        return GEMM355_OK;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc == GEMM355_OK)
+        *bytes = plan_backward(M, N, K, GATED, act, cus).bytes;
+    return rc;
+}
+
+// ---- Newton-Schulz ---------------------------------------------------------
+
+// With m the smaller and n the larger side, X (rows x cols) stays as it is
+// stored: the Gram matrix is X X^T of a wide and X^T X of a tall matrix, and
+// the update P X or X P.
+constexpr float kPolyScale = 256.0f;   // S and P are held times this
+
+struct OrthoPlan {
+    size_t x1_at, s_at, p_at, norm_at, partials_at, bytes;
+    int norm_blocks;
+};
+
+void ortho_shapes(int batch, int rows, int cols, Shape *gram, Shape *square, Shape *update)
+{
+    const int m = std::min(rows, cols), n = std::max(rows, cols);
+    *gram = {m, m, n, batch, true, false};
+    *square = {m, m, m, batch, true, false};
+    *update = {rows, cols, m, batch, false, false};
+}
+
+OrthoPlan plan_ortho(int batch, int rows, int cols, int cus)
+{
+    const size_t m = (size_t)std::min(rows, cols);
+    const size_t x = align_up(size_t(batch) * rows * cols * 2), s = align_up(size_t(batch) * m * m * 2);
+    OrthoPlan o = {};
+    o.norm_blocks = (int)std::min<int64_t>(d::NS_BLOCKS, ceil_div(int64_t(rows) * cols, d::NS_THREADS * 8));
+    o.x1_at = x;
+    o.s_at = 2 * x;
+    o.p_at = o.s_at + s;
+    o.norm_at = o.p_at + s;
+    o.partials_at = o.norm_at + align_up(size_t(batch) * o.norm_blocks * sizeof(double));
+    Shape gram, square, update;
+    ortho_shapes(batch, rows, cols, &gram, &square, &update);
+    o.bytes = o.partials_at + std::max({product_workspace(gram, cus), product_workspace(square, cus),
+                                        product_workspace(update, cus)});
+    return o;
+}
+
+template <bool FP32>
+int ortho_start(const d::NormArgs &n, int batch, hipStream_t s)
+{
+    d::NormArgs a = n;
+    const unsigned blocks = (unsigned)(int64_t(n.blocks) * batch);
+    const int st = launch_kernel(d::ns_norm_kernel<FP32>, blocks, (unsigned)d::NS_THREADS, a, s);
+    return st == GEMM355_OK ? launch_kernel(d::ns_scale_kernel<FP32>, blocks, (unsigned)d::NS_THREADS, a, s) : st;
+}
+
+// One Newton-Schulz step from x to out (BF16 and unscaled after the last).
+template <bool WIDE, class TO>
+int ortho_step(const Shape &g, const Shape &q, const Shape &u, const void *x, void *S, void *P, void *out, float a,
+               float b, float c, float scale, bool last, int cus, void *ws, hipStream_t s)
+{
+    typedef _Float16 h;
+    DenseArgs p = args_of(g.M, g.N, g.K, x, x, S);
+    p.batch = g.batch;
+    p.symmetric = 1;
+    p.alpha = kPolyScale / (scale * scale);
+    int st = WIDE ? product<h, d::ROW_K, d::ROW_K, d::EPI_STORE>(p, cus, ws, s)
+                  : product<h, d::COL_K, d::COL_K, d::EPI_STORE>(p, cus, ws, s);
+    if (st != GEMM355_OK)
+        return st;
+    p = args_of(q.M, q.N, q.K, S, S, P);   // P = a I + b S + c S^2
+    p.batch = g.batch;
+    p.symmetric = 1;
+    p.r = S;
+    p.alpha = c / kPolyScale;
+    p.beta = b;
+    p.gamma = a * kPolyScale;
+    st = product<h, d::ROW_K, d::ROW_K, d::EPI_POLY>(p, cus, ws, s);
+    if (st != GEMM355_OK)
+        return st;
+    p = WIDE ? args_of(u.M, u.N, u.K, P, x, out) : args_of(u.M, u.N, u.K, x, P, out);
+    p.batch = g.batch;
+    p.alpha = (last ? 1.0f / scale : 1.0f) / kPolyScale;
+    // P = P^T: as the right-hand operand its rows are its columns
+    return WIDE ? product<h, d::ROW_K, d::COL_K, d::EPI_STORE, TO>(p, cus, ws, s)
+                : product<h, d::ROW_K, d::ROW_K, d::EPI_STORE, TO>(p, cus, ws, s);
+}
+
+bool ortho_extents_ok(int64_t rows, int64_t cols)
+{
+    const int64_t m = std::min(rows, cols);
+    return extent_ok(rows, cols * 2) && extent_ok(cols, rows * 2) && extent_ok(m, m * 2);
+}
+
+} // namespace
+
+extern "C" int gemm_bf16_nt_bias_act_res(int M, int N, int K, const void *A, const void *B, const void *bias,
+                                         int activation, const void *R, void *Z, void *C, void *workspace,
+                                         size_t workspace_bytes, void *stream)
+{
+    return layer_forward<false>(M, N, K, A, B, bias, activation, R, Z, C, workspace, workspace_bytes, stream);
+}
+
+extern "C" int gemm_bf16_nt_bias_act_res_workspace_size(int M, int N, int K, size_t *bytes)
+{
+    return layer_forward_workspace<false>(M, N, K, bytes);
+}
+
+extern "C" int gemm_bf16_nt_bias_act_bwd(int M, int N, int K, const void *A, const void *B, const void *Z,
+                                         int activation, const void *dC, void *dA, void *dB, void *dbias,
+                                         void *workspace, size_t workspace_bytes, void *stream)
+{
+    return layer_backward<false>(M, N, K, A, B, Z, activation, dC, dA, dB, dbias, workspace, workspace_bytes, stream);
+}
+
+extern "C" int gemm_bf16_nt_bias_act_bwd_workspace_size(int M, int N, int K, int activation, size_t *bytes)
+{
+    return layer_backward_workspace<false>(M, N, K, activation, bytes);
+}
+
+extern "C" int gemm_bf16_nt_gated(int M, int N, int K, const void *A, const void *B, const void *bias, int activation,
+                                  void *Z, void *C, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return layer_forward<true>(M, N, K, A, B, bias, activation, nullptr, Z, C, workspace, workspace_bytes, stream);
+}
+
+extern "C" int gemm_bf16_nt_gated_workspace_size(int M, int N, int K, size_t *bytes)
+{
+    return layer_forward_workspace<true>(M, N, K, bytes);
+}
+
+extern "C" int gemm_bf16_nt_gated_bwd(int M, int N, int K, const void *A, const void *B, const void *Z, int activation,
+                                      const void *dC, void *dA, void *dB, void *dbias, void *workspace,
+                                      size_t workspace_bytes, void *stream)
+{
+    return layer_backward<true>(M, N, K, A, B, Z, activation, dC, dA, dB, dbias, workspace, workspace_bytes, stream);
+}
+
+extern "C" int gemm_bf16_nt_gated_bwd_workspace_size(int M, int N, int K, size_t *bytes)
+{
+    return layer_backward_workspace<true>(M, N, K, GEMM355_ACT_NONE, bytes);
+}
+
+extern "C" int gemm355_newton_schulz_workspace_size(int batch, int rows, int cols, size_t *bytes)
+{
+    if (batch < 0 || rows < 0 || cols < 0 || !bytes)
+        return GEMM355_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (batch == 0 || rows == 0 || cols == 0)
+        return GEMM355_OK;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc == GEMM355_OK)
+        *bytes = plan_ortho(batch, rows, cols, cus).bytes;
+    return rc;
+}
+
+extern "C" int gemm355_newton_schulz(int batch, int rows, int cols, int g_type, const void *G, int steps, float a,
+                                     float b, float c, float eps, void *O, void *workspace, size_t workspace_bytes,
+                                     void *stream)
+{
+    if (batch < 0 || rows < 0 || cols < 0 || (g_type != GEMM355_BF16 && g_type != GEMM355_FP32) || steps < 1 ||
+        steps > 64 || !isfinite(a) || !isfinite(b) || !isfinite(c) || !isfinite(eps) || eps < 0.0f)
+        return GEMM355_ERR_INVALID_ARG;
+    if (batch == 0 || rows == 0 || cols == 0)
+        return GEMM355_OK;
+    if (!G || !O || !workspace)
+        return GEMM355_ERR_INVALID_ARG;
+    const int64_t elements = int64_t(rows) * cols;
+    const Array out[] = {{O, size_t(batch) * elements * 2}, {workspace, workspace_bytes}};
+    const Array in[] = {{G, size_t(batch) * elements * (g_type == GEMM355_FP32 ? 4 : 2)}};
+    if (any_overlap(out, 2, in, 1))
+        return GEMM355_ERR_INVALID_ARG;
+    if (!all_aligned(out, 2) || !all_aligned(in, 1) || rows % 8 != 0 || cols % 8 != 0 ||
+        !ortho_extents_ok(rows, cols) || batch > 65535)
+        return GEMM355_ERR_UNSUPPORTED;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc != GEMM355_OK)
+        return rc;
+    const OrthoPlan o = plan_ortho(batch, rows, cols, cus);
+    if (workspace_bytes < o.bytes)
+        return GEMM355_ERR_UNSUPPORTED;
+
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    // a power of two near sqrt(min(rows, cols)): exact to scale by
+    const float scale = exp2f(ceilf(0.5f * log2f((float)std::min(rows, cols))));
+    d::NormArgs n = {};
+    n.g = G;
+    n.partial = reinterpret_cast<double *>(ws + o.norm_at);
+    n.x = reinterpret_cast<uint16_t *>(ws);
+    n.elements = elements;
+    n.blocks = o.norm_blocks;
+    n.scale = scale;
+    n.eps = eps;
+    int st = g_type == GEMM355_FP32 ? ortho_start<true>(n, batch, s) : ortho_start<false>(n, batch, s);
+    Shape gram, square, update;
+    ortho_shapes(batch, rows, cols, &gram, &square, &update);
+    uint8_t *x = ws, *next = ws + o.x1_at;
+    for (int i = 0; i < steps && st == GEMM355_OK; ++i) {
+        const bool last = i == steps - 1, wide = rows <= cols;
+        auto step = wide ? (last ? ortho_step<true, __bf16> : ortho_step<true, _Float16>)
+                         : (last ? ortho_step<false, __bf16> : ortho_step<false, _Float16>);
+        st = step(gram, square, update, x, ws + o.s_at, ws + o.p_at, last ? static_cast<uint8_t *>(O) : next, a, b, c,
+                  scale, last, cus, ws + o.partials_at, s);
+        std::swap(x, next);
+    }
+    return st;
+}

@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "gemm355.h"
+#include "host.hpp"
 #include "gemm_bf16.hpp"
 #include "gemm_bf16_small.hpp"
 #include "gemm_bf16_small_long.hpp"
@@ -33,8 +34,8 @@ namespace {
 using gemm355::BM;
 using gemm355::BN;
 using gemm355::Problem;
+using namespace gemm355::host;
 
-constexpr int kMaxDevices = 64;
 // Band width of the supergroup visiting order ("NVFP4 GEMM on Blackwell",
 // "Production Kernel", "Supergroup Size"). One XCD's L2 (4 MB) serves the
 // grid / 8 = 32 tiles its workgroups compute at once; a band of w adjacent N
@@ -93,9 +94,6 @@ constexpr double kLaunchFixed = 3.0;    // prologue, epilogue, launch
 constexpr double kReduceFixed = 3.0;    // the reduction's own launch
 constexpr double kHbmBytesPerUs = 4.5e6;
 
-std::mutex g_cu_lock;
-int g_cu_count[kMaxDevices];   // 0 = not queried yet
-
 void *g_scratch_ptr[kMaxDevices];   // device address of `scratch` per device; guarded by g_cu_lock
 
 // The device address of the current device's scratch array, looked up on the
@@ -115,55 +113,6 @@ int scratch_address(void **ptr)
     *ptr = g_scratch_ptr[dev];
     return GEMM355_OK;
 }
-
-// Compute units of the current device, queried once per device.
-int compute_units(int *cus)
-{
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
-        return GEMM355_ERR_NO_DEVICE;
-    std::lock_guard<std::mutex> guard(g_cu_lock);
-    if (g_cu_count[dev] == 0) {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
-            return GEMM355_ERR_NO_DEVICE;
-        g_cu_count[dev] = n;
-    }
-    *cus = g_cu_count[dev];
-    return GEMM355_OK;
-}
-
-// One kernel launch on `stream`. The launch's own return code is the status:
-// the thread's pending HIP error is neither read nor cleared, so an error the
-// caller has not collected yet stays theirs.
-template <class Kernel, class Args>
-int launch_kernel(Kernel kernel, unsigned blocks, unsigned threads, Args &args, hipStream_t stream)
-{
-    void *argv[] = {&args};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(blocks), dim3(threads), argv,
-                                         0, stream);
-    return e == hipSuccess ? GEMM355_OK : GEMM355_ERR_LAUNCH;
-}
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool overlaps(const void *p, size_t pn, const void *q, size_t qn)
-{
-    if (!p || !q || pn == 0 || qn == 0)
-        return false;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + qn && b < a + pn;
-}
-
-// Byte extent of `rows` rows (rounded up to whole 256-row tiles) of `row_bytes`
-// each must stay below 2^31: the kernels address operands with 32-bit offsets.
-bool extent_ok(int64_t rows, int64_t row_bytes)
-{
-    const int64_t padded = (rows + 255) / 256 * 256;
-    return padded * row_bytes < (int64_t(1) << 31);
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // One launch of a persistent kernel on `stream`: tile counts for tile_m x
 // tile_n output tiles, the supergroup width, a grid of at most one workgroup

@@ -428,6 +428,143 @@ int gemm_mxfp4_nt(int M, int N, int K, const void *Aq, const void *SA, const voi
 int gemm_mxfp4_nt_bias_act(int M, int N, int K, const void *Aq, const void *SA, const void *Bq, const void *SB,
                            const void *bias, int activation, void *C, void *stream);
 
+/*
+ * ---- Layers of a network: residuals, gated blocks, gradients, updates -------
+ *
+ * The entry points below run the dense layers of a feed-forward block forward
+ * and backward, and the orthogonalised update of their weights. They share the
+ * conventions above (device pointers, dense row-major arrays, one stream, no
+ * allocation, no synchronisation; they may be captured into graphs) and, like
+ * the *_ws entry points, take a workspace:
+ *   workspace        device memory, 16-byte aligned, owned by the caller; its
+ *                    contents on entry do not matter and on return are
+ *                    unspecified. Calls that may run at the same time (other
+ *                    streams, graphs replayed side by side) need one each.
+ *   workspace_bytes  its size: at least what the matching *_workspace_size
+ *                    call says for these sizes on the current device, else
+ *                    GEMM355_ERR_UNSUPPORTED, with nothing enqueued. NULL
+ *                    with 0 bytes is accepted where that is 0; NULL with
+ *                    workspace_bytes > 0 is GEMM355_ERR_INVALID_ARG.
+ * Every output must be apart from every input, from the workspace and from the
+ * other outputs, else GEMM355_ERR_INVALID_ARG (one exception: C may be R).
+ * All arrays 16-byte aligned, sizes that are a row's length multiples of 8
+ * (N and K; M is any), and every array, padded to a multiple of 256 rows,
+ * below 2^31 bytes, else GEMM355_ERR_UNSUPPORTED. Every call is
+ * deterministic: the same call gives the same bits.
+ *
+ * Their activations are those of gemm355_activation and
+ *   GEMM355_ACT_SILU   y = z / (1 + exp(-z))
+ * which the entry points above do not take.
+ */
+enum { GEMM355_ACT_SILU = 3 };
+
+/*
+ * gemm_bf16_nt_bias_act_res -- a linear layer with its residual:
+ *
+ *   z = sum_k A[m][k] * B[n][k] + bias[n]
+ *   C[m][n] = bf16(act(z) + R[m][n]),   Z[m][n] = bf16(z)
+ *
+ * with products exact, sums, bias, activation and residual in FP32 and one
+ * rounding (to nearest, ties to even) per stored value.
+ *   A     M x K BF16 (tokens), B  N x K BF16 (weights)
+ *   bias  N BF16 values, or NULL for zeros
+ *   R     M x N BF16, or NULL for zeros; may be C itself (in-place addition)
+ *   Z     M x N BF16 output for gemm_bf16_nt_bias_act_bwd, or NULL
+ * M == 0 or N == 0 does nothing; K == 0 gives z = bias.
+ */
+int gemm_bf16_nt_bias_act_res(int M, int N, int K, const void *A, const void *B, const void *bias, int activation,
+                              const void *R, void *Z, void *C, void *workspace, size_t workspace_bytes, void *stream);
+int gemm_bf16_nt_bias_act_res_workspace_size(int M, int N, int K, size_t *bytes);
+
+/*
+ * gemm_bf16_nt_bias_act_bwd -- gradients of act(A B^T + bias) (the residual's
+ * is dC itself):
+ *
+ *   dZ[m][n] = dC[m][n] * act'(Z[m][n])
+ *   dA = dZ B  (M x K),  dB = dZ^T A  (N x K),  dbias[n] = sum_m dZ[m][n]
+ *
+ * all BF16. dZ is rounded to BF16 for the two products (the matrix cores'
+ * operand type; one half-step of relative error per product, which sums
+ * average) and enters dbias before that rounding. The derivative of ReLU at 0
+ * is 0.
+ *   Z      M x N BF16, the pre-activations that the forward call stored; may
+ *          be NULL with GEMM355_ACT_NONE
+ *   dC     M x N BF16
+ *   dA, dB, dbias  outputs; each may be NULL if it is not wanted, and A (for
+ *          dB) and B (for dA) may then be NULL too
+ * An empty sum is zero: M == 0 writes zeros to dB and dbias, N == 0 to dA.
+ */
+int gemm_bf16_nt_bias_act_bwd(int M, int N, int K, const void *A, const void *B, const void *Z, int activation,
+                              const void *dC, void *dA, void *dB, void *dbias, void *workspace,
+                              size_t workspace_bytes, void *stream);
+int gemm_bf16_nt_bias_act_bwd_workspace_size(int M, int N, int K, int activation, size_t *bytes);
+
+/*
+ * gemm_bf16_nt_gated -- a gated layer, both projections, the activation and
+ * the product of the two in one kernel:
+ *
+ *   z[m][i] = sum_k A[m][k] * B[i][k] + bias[i],   i < 2 N
+ *   C[m][n] = bf16(act(z[m][n]) * z[m][N + n]),    Z[m][i] = bf16(z[m][i])
+ *
+ *   B     2 N x K BF16: the N gate rows, then the N up rows
+ *   bias  2 N BF16 values, or NULL for zeros
+ *   Z     M x 2 N BF16 output for gemm_bf16_nt_gated_bwd, or NULL
+ * Otherwise as gemm_bf16_nt_bias_act_res.
+ */
+int gemm_bf16_nt_gated(int M, int N, int K, const void *A, const void *B, const void *bias, int activation, void *Z,
+                       void *C, void *workspace, size_t workspace_bytes, void *stream);
+int gemm_bf16_nt_gated_workspace_size(int M, int N, int K, size_t *bytes);
+
+/*
+ * gemm_bf16_nt_gated_bwd -- gradients of the gated layer:
+ *
+ *   dZ[m][n]     = dC[m][n] * Z[m][N + n] * act'(Z[m][n])
+ *   dZ[m][N + n] = dC[m][n] * act(Z[m][n])
+ *   dA = dZ B  (M x K),  dB = dZ^T A  (2 N x K),  dbias[i] = sum_m dZ[m][i]
+ *
+ * Z (M x 2 N) is always needed; otherwise as gemm_bf16_nt_bias_act_bwd.
+ */
+int gemm_bf16_nt_gated_bwd(int M, int N, int K, const void *A, const void *B, const void *Z, int activation,
+                           const void *dC, void *dA, void *dB, void *dbias, void *workspace, size_t workspace_bytes,
+                           void *stream);
+int gemm_bf16_nt_gated_bwd_workspace_size(int M, int N, int K, size_t *bytes);
+
+/* Element types of gemm355_newton_schulz's input. */
+typedef enum gemm355_type {
+    GEMM355_BF16 = 0,
+    GEMM355_FP32 = 1
+} gemm355_type;
+
+/*
+ * gemm355_newton_schulz -- orthogonalises a batch of matrices by Newton-Schulz
+ * steps, as an optimiser does with the momentum of a weight:
+ *
+ *   X = G / (||G||_F + eps), then `steps` times
+ *   S = X X^T,  X = (a I + b S + c S^2) X      (rows <= cols)
+ *   S = X^T X,  X = X (a I + b S + c S^2)      (rows >  cols)
+ *   O = bf16(X)
+ *
+ *   G      batch matrices of rows x cols, each dense and row-major, one after
+ *          the other, of type g_type (GEMM355_BF16 or GEMM355_FP32)
+ *   O      batch x rows x cols BF16
+ *   steps  1 .. 64
+ *   a, b, c  finite coefficients, for which the iteration has to stay bounded
+ *          (singular values up to 2 and |a + b s + c s^2| up to 200 over them
+ *          are safe); (3.4445, -4.7750, 2.0315) is a common choice
+ *   eps    >= 0, finite; a zero matrix gives zeros
+ * The norm is taken in FP64. X, S and a I + b S + c S^2 are rounded to FP16
+ * between the products, X held times a power of two near sqrt(min(rows, cols))
+ * and the other two times 256 so that they stay in its normal range; sums are
+ * FP32. For matrices of independent entries that is within 2e-3 of the exact
+ * result (2-norm, relative) before O's own rounding; directions whose singular
+ * value is far below the norm carry more. The symmetric S and S^2 are computed
+ * on and below the diagonal only.
+ * rows and cols multiples of 8; batch 0, rows 0 or cols 0 does nothing.
+ */
+int gemm355_newton_schulz(int batch, int rows, int cols, int g_type, const void *G, int steps, float a, float b,
+                          float c, float eps, void *O, void *workspace, size_t workspace_bytes, void *stream);
+int gemm355_newton_schulz_workspace_size(int batch, int rows, int cols, size_t *bytes);
+
 /* Human-readable text for a status code (static storage; never NULL). */
 const char *gemm355_status_string(int status);
 
