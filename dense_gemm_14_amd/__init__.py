@@ -35,6 +35,7 @@ The functions mirror the C entry points declared in ``include/gemm355.h``:
     gated_workspace_size(M, N, K)
     gated_bwd_workspace_size(M, N, K)
     newton_schulz_workspace_size(batch, rows, cols)
+    force_layer_kernel(kernel)        # kernel of these calls' products (diagnostic)
     force_instance(instance)          # BF16 instance override (diagnostic)
     force_supergroup(width)           # band width of the tile order (diagnostic)
     supergroup(tiles_n, K, kernel)    # the default band width of a kernel's visiting order
@@ -82,6 +83,10 @@ KERNEL_BF16_SMALL = 3
 FP4_PATH_AUTO = 0    # gemm_nvfp4_nt_ws: decode first by shape (gemm355_force_fp4_path)
 FP4_PATH_STAGING = 1  # always the kernel that decodes while staging
 FP4_PATH_DECODE_FIRST = 2  # always decode into the workspace, then the BF16 product
+LAYER_AUTO = 0       # the layer calls' products: by size (gemm355_force_layer_kernel)
+LAYER_LARGE = 1      # 256 x 256 output tiles
+LAYER_SHARED = 2     # the same, the last tiles' K steps shared out
+LAYER_TILE = 3       # 128 x 128 output tiles
 SCHEDULE_STATIC = 0  # the NVFP4 kernel's tile order (gemm355_force_schedule)
 SCHEDULE_DYNAMIC = 1
 INSTANCE_SPLITK = 3  # 128 x 128 output tiles; with a workspace (the *_ws calls) K split over workgroups
@@ -160,6 +165,8 @@ def load() -> ctypes.CDLL:
     lib.gemm355_newton_schulz.restype = i
     lib.gemm355_newton_schulz_workspace_size.argtypes = [i, i, i, psz]
     lib.gemm355_newton_schulz_workspace_size.restype = i
+    lib.gemm355_force_layer_kernel.argtypes = [i]
+    lib.gemm355_force_layer_kernel.restype = i
     lib.gemm355_status_string.argtypes = [i]
     lib.gemm355_status_string.restype = ctypes.c_char_p
     lib.gemm355_tile_order.argtypes = [i, i, i, p, p]
@@ -564,6 +571,12 @@ def newton_schulz(batch: int, rows: int, cols: int, G, O, steps: int = 5, coeffi
 def newton_schulz_workspace_size(batch: int, rows: int, cols: int) -> int:
     """Workspace bytes of newton_schulz on the current device."""
     return _size_of("gemm355_newton_schulz_workspace_size", int(batch), int(rows), int(cols))
+
+
+def force_layer_kernel(kernel: int) -> None:
+    """Kernel of the layer calls' products for the whole process: LAYER_AUTO
+    (default), LAYER_LARGE, LAYER_SHARED or LAYER_TILE (a diagnostic)."""
+    _check(load().gemm355_force_layer_kernel(int(kernel)), "gemm355_force_layer_kernel")
 
 
 def force_instance(instance: int) -> None:

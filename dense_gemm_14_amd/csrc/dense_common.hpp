@@ -22,7 +22,9 @@ enum Epilogue {
     EPI_STORE = 0,   // C = round(alpha acc)
     EPI_LINEAR = 1,  // z = acc + bias, Z = round(z) if wanted, C = round(act(z) + R)
     EPI_GATED = 2,   // gate and up sums of one column: C = round(act(zg) zu), Z = round of both if wanted
-    EPI_POLY = 3     // C = round(alpha acc + beta R + gamma [row == column])
+    EPI_STORE_SYM = 3,   // EPI_STORE of a symmetric product: tiles on and below the diagonal, FP16,
+                         // those below it stored a second time, mirrored
+    EPI_POLY = 4         // C = round(alpha acc + beta R + gamma [row == column]), symmetric likewise
 };
 // Activations (the values of gemm355_activation).
 enum { A_NONE = 0, A_RELU = 1, A_GELU = 2, A_SILU = 3 };
@@ -35,11 +37,10 @@ struct DenseArgs {
     const void *bias;    // EPI_LINEAR: N, EPI_GATED: 2 N BF16 values, or NULL
     float *ws;           // split K: FP32 partial tiles
     int M, N, K;         // C is M x N (EPI_GATED: B has 2 N rows)
-    int tiles_m, tiles_n, tiles;   // tiles: per batch entry (with symmetric: on and below the diagonal)
+    int tiles_m, tiles_n, tiles;   // tiles: per batch entry (symmetric: on and below the diagonal)
     int splits, steps_per_split;
     int supergroup;
     int act;
-    int symmetric;       // C == C^T: tiles below the diagonal are stored twice
     int batch;
     int grid;            // persistent kernel: its workgroups
     float alpha, beta, gamma;
@@ -151,9 +152,10 @@ __device__ inline void triangle_tile(int p, int &tm, int &tn)
     tn = p - t * (t + 1) / 2;
 }
 
+template <int EPI>
 __device__ inline void dense_tile(const DenseArgs &p, int pos, int &tm, int &tn)
 {
-    if (p.symmetric)
+    if constexpr (EPI >= EPI_STORE_SYM)
         triangle_tile(pos, tm, tn);
     else
         supergroup_tile(pos, p.tiles_m, p.tiles_n, p.supergroup, tm, tn);
@@ -248,110 +250,132 @@ __device__ inline int pair_offset(const DenseArgs &p, int m, int col, int width,
     return m < p.M && n < p.N ? (int)(((unsigned)m * (unsigned)width + (unsigned)(n + shift)) * 2u) : OOB;
 }
 
-__device__ inline u32x4 load16(const __amdgpu_buffer_rsrc_t &r, int off)
+// What a row of BJ blocks at column `col` reads besides its sums: the bias of
+// each block's columns (the same for every row) ...
+template <int EPI, int BJ>
+__device__ inline void load_bias_row(const DenseArgs &p, const Views &v, int col, int lane, u32x2 (&bias)[BJ])
 {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED) {
+        constexpr int H = EPI == EPI_GATED ? BJ / 2 : BJ;
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) {
+            // EPI_GATED: the up columns' bias starts at N
+            const int n = col + 16 * (j % H) + 4 * (lane >> 4);
+            const int off = n < p.N ? (n + (j < H ? 0 : p.N)) * 2 : OOB;
+            bias[j] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(v.bias, off, 0, 0));
+        }
+    }
 }
-__device__ inline u32x2 load_bias4(const __amdgpu_buffer_rsrc_t &r, int n, int limit)
+
+// ... and the row's residual (EPI_LINEAR) or second term (EPI_POLY).
+template <int EPI, int BJ>
+__device__ inline void load_res_row(const DenseArgs &p, const Views &v, int m, int col, int lane, u32x4 (&res)[BJ / 2])
 {
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, n < limit ? n * 2 : OOB, 0, 0));
+    if constexpr (EPI == EPI_LINEAR || EPI == EPI_POLY)
+        if (p.r)
+#pragma unroll
+            for (int j = 0; j < BJ / 2; ++j)
+                res[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                       v.r, pair_offset(p, m, col + 32 * j, p.N, 0, lane), 0, 0));
+}
+
+__device__ inline void store16(u32x4 w, const __amdgpu_buffer_rsrc_t &r, int off)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(w, r, off, 0, 0);
 }
 
 // One row of blocks of a wave's tile: x[0 .. BJ - 1], BJ blocks side by side
 // at column `col` (EPI_GATED: BJ / 2 gate blocks at `col`, then the up blocks
-// of the same columns), this lane's row m.
+// of the same columns), this lane's row m. Leaves the values before rounding
+// in x.
 template <int EPI, class TO, int BJ>
-__device__ inline void store_row(const DenseArgs &p, const Views &v, f32x4 (&x)[BJ], int m, int col, int lane)
+__device__ inline void store_row(const DenseArgs &p, const Views &v, f32x4 (&x)[BJ], int m, int col, int lane,
+                                 const u32x2 (&bias)[BJ], const u32x4 (&res)[BJ / 2])
 {
-    const int grp = lane >> 4;
+    static_assert(BJ % 4 == 0, "blocks are stored in pairs");
     if constexpr (EPI == EPI_GATED) {
         constexpr int H = BJ / 2;
-        static_assert(H % 2 == 0, "blocks are stored in pairs");
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
-            const int n = col + 16 * j + 4 * grp;
-            x[j] = add_bias(x[j], load_bias4(v.bias, n, p.N));
-            // the up half's bias starts at N (a multiple of 8)
-            const int nu = n < p.N ? n + p.N : OOB / 2;
-            x[H + j] = add_bias(x[H + j], __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(v.bias, nu * 2, 0, 0)));
-        }
+        for (int j = 0; j < BJ; ++j)
+            x[j] = add_bias(x[j], bias[j]);
         with_act(p.act, [&](auto act_c) {
             constexpr int ACT = decltype(act_c)::value;
 #pragma unroll
             for (int j = 0; j < H; j += 2) {
                 if (p.z) {
-                    __builtin_amdgcn_raw_buffer_store_b128(pack_pair<__bf16>(x[j], x[j + 1]), v.z,
-                                                           pair_offset(p, m, col + 16 * j, 2 * p.N, 0, lane), 0, 0);
-                    __builtin_amdgcn_raw_buffer_store_b128(pack_pair<__bf16>(x[H + j], x[H + j + 1]), v.z,
-                                                           pair_offset(p, m, col + 16 * j, 2 * p.N, p.N, lane), 0, 0);
+                    store16(pack_pair<TO>(x[j], x[j + 1]), v.z, pair_offset(p, m, col + 16 * j, 2 * p.N, 0, lane));
+                    store16(pack_pair<TO>(x[H + j], x[H + j + 1]), v.z,
+                            pair_offset(p, m, col + 16 * j, 2 * p.N, p.N, lane));
                 }
                 const f32x4 h0 = act4<ACT>(x[j]) * x[H + j], h1 = act4<ACT>(x[j + 1]) * x[H + j + 1];
-                __builtin_amdgcn_raw_buffer_store_b128(pack_pair<__bf16>(h0, h1), v.c,
-                                                       pair_offset(p, m, col + 16 * j, p.N, 0, lane), 0, 0);
+                store16(pack_pair<TO>(h0, h1), v.c, pair_offset(p, m, col + 16 * j, p.N, 0, lane));
             }
         });
     } else if constexpr (EPI == EPI_LINEAR) {
-        static_assert(BJ % 2 == 0, "blocks are stored in pairs");
-        u32x4 res[BJ / 2];
-#pragma unroll
-        for (int j = 0; j < BJ; j += 2)
-            res[j / 2] = p.r ? load16(v.r, pair_offset(p, m, col + 16 * j, p.N, 0, lane)) : u32x4{};
 #pragma unroll
         for (int j = 0; j < BJ; ++j)
-            x[j] = add_bias(x[j], load_bias4(v.bias, col + 16 * j + 4 * grp, p.N));
+            x[j] = add_bias(x[j], bias[j]);
         with_act(p.act, [&](auto act_c) {
             constexpr int ACT = decltype(act_c)::value;
 #pragma unroll
             for (int j = 0; j < BJ; j += 2) {
                 const int off = pair_offset(p, m, col + 16 * j, p.N, 0, lane);
                 if (p.z)
-                    __builtin_amdgcn_raw_buffer_store_b128(pack_pair<__bf16>(x[j], x[j + 1]), v.z, off, 0, 0);
+                    store16(pack_pair<TO>(x[j], x[j + 1]), v.z, off);
                 f32x4 y0 = act4<ACT>(x[j]), y1 = act4<ACT>(x[j + 1]);
                 if (p.r) {
                     f32x4 r0, r1;
-                    unpack_pair<__bf16>(res[j / 2], r0, r1);
+                    unpack_pair<TO>(res[j / 2], r0, r1);
                     y0 += r0;
                     y1 += r1;
                 }
-                __builtin_amdgcn_raw_buffer_store_b128(pack_pair<__bf16>(y0, y1), v.c, off, 0, 0);
+                store16(pack_pair<TO>(y0, y1), v.c, off);
             }
         });
     } else {
 #pragma unroll
         for (int j = 0; j < BJ; j += 2) {
             const int off = pair_offset(p, m, col + 16 * j, p.N, 0, lane);
-            f32x4 y0 = x[j] * p.alpha, y1 = x[j + 1] * p.alpha;
+            x[j] *= p.alpha;
+            x[j + 1] *= p.alpha;
             if constexpr (EPI == EPI_POLY) {
                 f32x4 r0, r1;
-                unpack_pair<TO>(load16(v.r, off), r0, r1);
-                const int n = col + 16 * j + 4 * grp;
+                unpack_pair<TO>(res[j / 2], r0, r1);
+                const int n = col + 16 * j + 4 * (lane >> 4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    y0[e] += p.beta * r0[e] + (m == n + e ? p.gamma : 0.0f);
-                    y1[e] += p.beta * r1[e] + (m == n + 16 + e ? p.gamma : 0.0f);
+                    x[j][e] += p.beta * r0[e] + (m == n + e ? p.gamma : 0.0f);
+                    x[j + 1][e] += p.beta * r1[e] + (m == n + 16 + e ? p.gamma : 0.0f);
                 }
             }
-            __builtin_amdgcn_raw_buffer_store_b128(pack_pair<TO>(y0, y1), v.c, off, 0, 0);
-            x[j] = y0;
-            x[j + 1] = y1;
+            store16(pack_pair<TO>(x[j], x[j + 1]), v.c, off);
         }
     }
 }
 
-// The mirror image of such a row for a symmetric result: C[n][m] = C[m][n].
-// Lanes of a group hold 16 consecutive m of one n: 32-byte runs.
-template <class TO, int BJ>
-__device__ inline void store_row_mirrored(const DenseArgs &p, const Views &v, f32x4 (&y)[BJ], int m, int col, int lane)
+// The mirror image of two rows of FP16 blocks (m0 and m0 + 16 their first
+// rows) of a symmetric result: C[n][m] = C[m][n]. A block in the layout above
+// is also the 16 x 16 x 16 instruction's operand layout (lane (l16, grp): row
+// l16, K 4 grp .. + 3), so a product with the identity returns it transposed,
+// every value exact, and the stores are 16 bytes wide again.
+template <int BJ>
+__device__ inline void store_mirrored(const DenseArgs &p, const Views &v, const f32x4 (&y0)[BJ], const f32x4 (&y1)[BJ],
+                                      int m0, int col, int lane)
 {
-    const int grp = lane >> 4;
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    const int l16 = lane & 15, grp = lane >> 4;
+    f16x4 eye;
 #pragma unroll
-    for (int j = 0; j < BJ; ++j)
+    for (int e = 0; e < 4; ++e)
+        eye[e] = l16 == 4 * grp + e ? (_Float16)1.0f : (_Float16)0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int n = col + 16 * j + 4 * grp + e;
-            const int off = m < p.M && n < p.N ? (int)(((unsigned)n * (unsigned)p.N + (unsigned)m) * 2u) : OOB;
-            __builtin_amdgcn_raw_buffer_store_b16((short)(pack2<TO>(y[j][e], 0.0f) & 0xFFFFu), v.c, off, 0, 0);
-        }
+    for (int j = 0; j < BJ; ++j) {
+        const f32x4 t0 = __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_convertvector(y0[j], f16x4), eye, f32x4{}, 0, 0, 0);
+        const f32x4 t1 = __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_convertvector(y1[j], f16x4), eye, f32x4{}, 0, 0, 0);
+        const int n = col + 16 * j + l16, m = m0 + 16 * (grp & 1) + 8 * (grp >> 1);
+        store16(pack_pair<_Float16>(t0, t1), v.c,
+                n < p.N && m < p.M ? (int)(((unsigned)n * (unsigned)p.N + (unsigned)m) * 2u) : OOB);
+    }
 }
 
 } // namespace dense

@@ -5,11 +5,13 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <math.h>
 #include <stdint.h>
 
 #include "gemm355.h"
 #include "host.hpp"
+#include "dense_large.hpp"
 #include "dense_tile.hpp"
 #include "dense_grad.hpp"
 #include "newton_schulz.hpp"
@@ -58,24 +60,82 @@ TilePlan plan_tile(const Shape &s, int cus)
     return t;
 }
 
-size_t product_workspace(const Shape &s, int cus) { return plan_tile(s, cus).workspace_bytes; }
+// The 256 x 256 kernel's work: `whole` rounds of whole tiles on `grid`
+// workgroups, then `shared` tiles whose K steps are cut into one run per
+// workgroup (two partial tiles of workspace each).
+struct LargePlan {
+    int tiles_m, tiles_n, tiles, grid, whole, shared;
+    size_t workspace_bytes;
+    double steps;     // of the busiest workgroup
+};
+constexpr int kMinRun = 2 * d::CUT_MIN;   // fewest K steps of a run
 
-Shape shape_of(const DenseArgs &p, bool gated) { return {p.M, p.N, p.K, p.batch, p.symmetric != 0, gated}; }
-
-// Launches a product. `ws` has product_workspace() bytes.
-template <class T, int LA, int LB, int EPI, class TO = T>
-int product(DenseArgs p, int cus, void *ws, hipStream_t stream)
+LargePlan plan_large(const Shape &s, int cus, bool share)
 {
-    if (p.M == 0 || p.N == 0 || p.batch == 0)
-        return GEMM355_OK;
-    const TilePlan t = plan_tile(shape_of(p, EPI == d::EPI_GATED), cus);
+    LargePlan t = {};
+    t.tiles_m = (int)ceil_div(s.M, d::BIG);
+    t.tiles_n = (int)ceil_div(s.N, s.gated ? d::BIG / 2 : d::BIG);
+    t.tiles = s.symmetric ? t.tiles_m * (t.tiles_m + 1) / 2 : t.tiles_m * t.tiles_n;
+    const int nk = (int)ceil_div(s.K, d::BIG_BK);
+    const int all = t.tiles * s.batch;
+    t.grid = gemm355::persistent_grid(all, cus);
+    t.whole = (int)ceil_div(all, t.grid);
+    t.steps = double(t.whole) * nk;
+    if (share && all % cus != 0) {
+        t.whole = std::max(0, all / cus - 1);
+        t.shared = all - t.whole * cus;
+        t.grid = t.whole > 0 ? cus : (int)std::min<int64_t>(cus, std::max<int64_t>(1, int64_t(t.shared) * nk / kMinRun));
+        t.workspace_bytes = size_t(t.grid) * 2 * d::BIG_FLOATS * sizeof(float);
+        t.steps = double(t.whole) * nk + double(t.shared) * nk / t.grid;
+    }
+    return t;
+}
+
+// Which kernel runs a product: 1 = 256 x 256 tiles, 2 = the same with the last
+// tiles shared, 3 = 128 x 128 tiles. Set through gemm355_force_layer_kernel
+// (0 = by size).
+std::atomic<int> g_layer_kernel{0};
+enum { KERNEL_WHOLE = 1, KERNEL_SHARED = 2, KERNEL_TILE = 3 };
+
+// Measured on MI355X: a K step of a 256 x 256 tile, of a 128 x 128 tile with a
+// workgroup on every compute unit, and what a launch of each costs besides.
+constexpr double kBigStep = 1.45, kBigFixed = 8.0;
+constexpr double kTileStep = 0.55, kTileFixed = 4.0;
+constexpr double kShareFixed = 30.0;    // writing and adding the parts
+constexpr double kReduceFixed = 4.0;
+
+int choose_kernel(const Shape &s, int cus)
+{
+    const int nk = (int)ceil_div(s.K, d::BIG_BK);
+    const bool big_ok = nk >= d::CUT_MIN;
+    const int forced = g_layer_kernel.load(std::memory_order_relaxed);
+    if (forced != 0)
+        return forced != KERNEL_TILE && !big_ok ? KERNEL_TILE : forced;
+    if (!big_ok)
+        return KERNEL_TILE;
+    const TilePlan t = plan_tile(s, cus);
+    const int64_t items = int64_t(t.tiles) * t.splits * s.batch;
+    const double tile = ceil_div(items, cus) * t.steps_per_split * kTileStep + kTileFixed + (t.splits > 1 ? kReduceFixed : 0);
+    const double whole = plan_large(s, cus, false).steps * kBigStep + kBigFixed;
+    const double shared = plan_large(s, cus, true).steps * kBigStep + kBigFixed + kShareFixed;
+    return tile <= whole && tile <= shared ? KERNEL_TILE : shared < whole ? KERNEL_SHARED : KERNEL_WHOLE;
+}
+
+size_t product_workspace(const Shape &s, int cus)
+{
+    const int k = choose_kernel(s, cus);
+    return k == KERNEL_TILE ? plan_tile(s, cus).workspace_bytes : plan_large(s, cus, k == KERNEL_SHARED).workspace_bytes;
+}
+
+template <class T, int LA, int LB, int EPI, class TO>
+int product_tile(DenseArgs p, const Shape &s, int cus, hipStream_t stream)
+{
+    const TilePlan t = plan_tile(s, cus);
     p.tiles_m = t.tiles_m;
     p.tiles_n = t.tiles_n;
     p.tiles = t.tiles;
     p.splits = t.splits;
     p.steps_per_split = t.steps_per_split;
-    p.supergroup = 8;
-    p.ws = static_cast<float *>(ws);
     const int64_t items = int64_t(t.tiles) * t.splits * p.batch;
     if (items > (int64_t(1) << 28))
         return GEMM355_ERR_UNSUPPORTED;
@@ -83,9 +143,45 @@ int product(DenseArgs p, int cus, void *ws, hipStream_t stream)
                            (unsigned)d::TILE_THREADS, p, stream);
     if (st == GEMM355_OK && t.splits > 1)
         st = launch_kernel(d::dense_reduce_kernel<EPI, TO>,
-                           (unsigned)ceil_div(int64_t(t.tiles) * p.batch * 16, d::REDUCE_WAVES),
+                           (unsigned)ceil_div(int64_t(t.tiles) * p.batch * 8, d::REDUCE_WAVES),
                            64u * d::REDUCE_WAVES, p, stream);
     return st;
+}
+
+template <class T, int LA, int LB, int EPI, class TO>
+int product_large(const DenseArgs &p, const Shape &s, int cus, bool share, hipStream_t stream)
+{
+    const LargePlan t = plan_large(s, cus, share);
+    d::LargeArgs a = {};
+    a.d = p;
+    a.d.tiles_m = t.tiles_m;
+    a.d.tiles_n = t.tiles_n;
+    a.d.tiles = t.tiles;
+    a.d.grid = t.grid;
+    a.whole = t.whole;
+    a.shared = t.shared;
+    int st = p.K % d::BIG_BK != 0
+        ? launch_kernel(d::dense_large_kernel<T, LA, LB, EPI, TO, true>, (unsigned)t.grid, (unsigned)d::BIG_THREADS, a, stream)
+        : launch_kernel(d::dense_large_kernel<T, LA, LB, EPI, TO, false>, (unsigned)t.grid, (unsigned)d::BIG_THREADS, a, stream);
+    if (st == GEMM355_OK && t.shared > 0)
+        st = launch_kernel(d::dense_large_reduce_kernel<EPI, TO>,
+                           (unsigned)ceil_div(int64_t(t.shared) * 16, d::BIG_REDUCE_WAVES),
+                           64u * d::BIG_REDUCE_WAVES, a, stream);
+    return st;
+}
+
+// Launches a product. `ws` has product_workspace() bytes.
+template <class T, int LA, int LB, int EPI, class TO = T>
+int product(DenseArgs p, int cus, void *ws, hipStream_t stream)
+{
+    if (p.M == 0 || p.N == 0 || p.batch == 0)
+        return GEMM355_OK;
+    const Shape s = {p.M, p.N, p.K, p.batch, EPI >= d::EPI_STORE_SYM, EPI == d::EPI_GATED};
+    p.supergroup = 8;
+    p.ws = static_cast<float *>(ws);
+    const int k = choose_kernel(s, cus);
+    return k == KERNEL_TILE ? product_tile<T, LA, LB, EPI, TO>(p, s, cus, stream)
+                            : product_large<T, LA, LB, EPI, TO>(p, s, cus, k == KERNEL_SHARED, stream);
 }
 
 DenseArgs args_of(int M, int N, int K, const void *a, const void *b, void *c)
@@ -368,15 +464,13 @@ int ortho_step(const Shape &g, const Shape &q, const Shape &u, const void *x, vo
     typedef _Float16 h;
     DenseArgs p = args_of(g.M, g.N, g.K, x, x, S);
     p.batch = g.batch;
-    p.symmetric = 1;
     p.alpha = kPolyScale / (scale * scale);
-    int st = WIDE ? product<h, d::ROW_K, d::ROW_K, d::EPI_STORE>(p, cus, ws, s)
-                  : product<h, d::COL_K, d::COL_K, d::EPI_STORE>(p, cus, ws, s);
+    int st = WIDE ? product<h, d::ROW_K, d::ROW_K, d::EPI_STORE_SYM>(p, cus, ws, s)
+                  : product<h, d::COL_K, d::COL_K, d::EPI_STORE_SYM>(p, cus, ws, s);
     if (st != GEMM355_OK)
         return st;
     p = args_of(q.M, q.N, q.K, S, S, P);   // P = a I + b S + c S^2
     p.batch = g.batch;
-    p.symmetric = 1;
     p.r = S;
     p.alpha = c / kPolyScale;
     p.beta = b;
@@ -399,6 +493,14 @@ bool ortho_extents_ok(int64_t rows, int64_t cols)
 }
 
 } // namespace
+
+extern "C" int gemm355_force_layer_kernel(int kernel)
+{
+    if (kernel < 0 || kernel > KERNEL_TILE)
+        return GEMM355_ERR_INVALID_ARG;
+    g_layer_kernel.store(kernel, std::memory_order_relaxed);
+    return GEMM355_OK;
+}
 
 extern "C" int gemm_bf16_nt_bias_act_res(int M, int N, int K, const void *A, const void *B, const void *bias,
                                          int activation, const void *R, void *Z, void *C, void *workspace,

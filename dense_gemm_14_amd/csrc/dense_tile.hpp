@@ -148,6 +148,7 @@ constexpr int tile_columns(int epi) { return epi == EPI_GATED ? TILE / 2 : TILE;
 // Work item -> batch entry, split and output tile. Workgroups go to the eight
 // XCDs in turn; each XCD takes a run of consecutive items, so the tiles its L2
 // serves share operand strips.
+template <int EPI>
 __device__ inline bool tile_item(const DenseArgs &p, int &b, int &split, int &tm, int &tn, int &item)
 {
     const int items = p.tiles * p.splits * p.batch;
@@ -158,21 +159,29 @@ __device__ inline bool tile_item(const DenseArgs &p, int &b, int &split, int &tm
     b = item / (p.tiles * p.splits);
     const int r = item - b * p.tiles * p.splits;
     split = r / p.tiles;
-    dense_tile(p, r - split * p.tiles, tm, tn);
+    dense_tile<EPI>(p, r - split * p.tiles, tm, tn);
     return true;
 }
 
-// Epilogue of the rows of blocks i of wave (wm, wn) of a tile.
+// Epilogue of block rows i0 and i0 + 1 of wave (wm, wn) of a tile.
 template <int EPI, class TO>
-__device__ inline void tile_store(const DenseArgs &p, f32x4 (&x)[4], int tm, int tn, int wm, int wn, int i, int lane)
+__device__ inline void tile_store(const DenseArgs &p, f32x4 (&x)[2][4], int tm, int tn, int wm, int wn, int i0, int lane)
 {
     const Views v = make_views<EPI>(p);
-    const int m = tm * TILE + 64 * wm + 16 * i + (lane & 15);
+    const int m0 = tm * TILE + 64 * wm + 16 * i0;
     const int col = tn * tile_columns(EPI) + tile_columns(EPI) / 2 * wn;
-    store_row<EPI, TO, 4>(p, v, x, m, col, lane);
-    if constexpr (EPI == EPI_STORE || EPI == EPI_POLY)
-        if (p.symmetric && tm != tn)
-            store_row_mirrored<TO, 4>(p, v, x, m, col, lane);
+    u32x2 bias[4];
+    u32x4 res[2][2];
+    load_bias_row<EPI>(p, v, col, lane, bias);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        load_res_row<EPI, 4>(p, v, m0 + 16 * i + (lane & 15), col, lane, res[i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        store_row<EPI, TO>(p, v, x[i], m0 + 16 * i + (lane & 15), col, lane, bias, res[i]);
+    if constexpr (EPI >= EPI_STORE_SYM)
+        if (tm != tn)
+            store_mirrored(p, v, x[0], x[1], m0, col, lane);
 }
 
 template <class T, int LA, int LB, int EPI, class TO>
@@ -190,7 +199,7 @@ void dense_tile_kernel(DenseArgs p)
     const int wn = (wave >> 1) & 1;  // 64-column half
 
     int b, split, tm, tn, item;
-    if (!tile_item(p, b, split, tm, tn, item))
+    if (!tile_item<EPI>(p, b, split, tm, tn, item))
         return;
     if (p.batch > 1)
         enter_batch(p, b);
@@ -292,39 +301,39 @@ void dense_tile_kernel(DenseArgs p)
             for (int j = 0; j < 4; ++j)
                 ws[((pair * 4 + 2 * kh + i) * 4 + j) * 64 + lane] = out[i][j];
     } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            tile_store<EPI, TO>(p, out[i], tm, tn, wm, wn, 2 * kh + i, lane);
+        tile_store<EPI, TO>(p, out, tm, tn, wm, wn, 2 * kh, lane);
     }
 }
 
-// Adds the splits' partials in order and runs the epilogue: one wave per row
-// of blocks (16 rows x 64 columns) of a tile.
+// Adds the splits' partials in order and runs the epilogue: one wave per two
+// rows of blocks (32 rows x 64 columns) of a tile.
 constexpr int REDUCE_WAVES = 4;
 template <int EPI, class TO>
 __global__ __launch_bounds__(64 * REDUCE_WAVES) void dense_reduce_kernel(DenseArgs p)
 {
     const int lane = threadIdx.x & 63;
     const int unit = (int)blockIdx.x * REDUCE_WAVES + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int entry = unit >> 4;            // tile of a batch entry
+    const int entry = unit >> 3;            // tile of a batch entry
     if (entry >= p.tiles * p.batch)
         return;
     const int b = entry / p.tiles, tile = entry - b * p.tiles;
-    const int pair = (unit >> 2) & 3, i = unit & 3;
+    const int pair = (unit >> 1) & 3, i0 = 2 * (unit & 1);
     int tm, tn;
-    dense_tile(p, tile, tm, tn);
+    dense_tile<EPI>(p, tile, tm, tn);
     const f32x4 *ws = reinterpret_cast<const f32x4 *>(p.ws) +
-                      ((size_t)b * p.splits * p.tiles + tile) * (TILE_FLOATS / 4) + ((pair * 4 + i) * 4) * 64 + lane;
-    f32x4 x[4] = {};
+                      ((size_t)b * p.splits * p.tiles + tile) * (TILE_FLOATS / 4) + ((pair * 4 + i0) * 4) * 64 + lane;
+    f32x4 x[2][4] = {};
     for (int z = 0; z < p.splits; ++z) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            x[j] += ws[j * 64];
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[i][j] += ws[(i * 4 + j) * 64];
         ws += (size_t)p.tiles * (TILE_FLOATS / 4);
     }
     if (p.batch > 1)
         enter_batch(p, b);
-    tile_store<EPI, TO>(p, x, tm, tn, pair & 1, pair >> 1, i, lane);
+    tile_store<EPI, TO>(p, x, tm, tn, pair & 1, pair >> 1, i0, lane);
 }
 
 } // namespace dense

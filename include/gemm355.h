@@ -565,6 +565,18 @@ int gemm355_newton_schulz(int batch, int rows, int cols, int g_type, const void 
                           float c, float eps, void *O, void *workspace, size_t workspace_bytes, void *stream);
 int gemm355_newton_schulz_workspace_size(int batch, int rows, int cols, size_t *bytes);
 
+/*
+ * gemm355_force_layer_kernel -- override the choice of kernel for the products
+ * of the layer calls (gemm_bf16_nt_bias_act_res and those after it), a
+ * process-wide diagnostic for tests and measurements: 0 (the default) by size,
+ * 1 = 256 x 256 tiles, 2 = the same with the K steps of the last tiles shared
+ * out over the workgroups, 3 = 128 x 128 tiles. Products with K <= 192 always
+ * take 128 x 128 tiles. The workspace sizes follow the setting. Returns
+ * GEMM355_OK, or GEMM355_ERR_INVALID_ARG for another value (setting
+ * unchanged). No HIP call is made.
+ */
+int gemm355_force_layer_kernel(int kernel);
+
 /* Human-readable text for a status code (static storage; never NULL). */
 const char *gemm355_status_string(int status);
 

@@ -1,0 +1,93 @@
+"""Every kernel of the layer calls' products, forced in turn: whole and shared
+256 x 256 tiles and 128 x 128 tiles give the right values at sizes that cross
+their borders, in every layout, with one tile and with several rounds of them."""
+import pytest
+import torch
+
+import dense_gemm_14_amd as g
+from tests.dense_util import Out, backward, close, forward, randn, workspace
+from tests.gpu_util import need_gpu
+from tests.test_gpu_dense import dev, gen_of, ortho_exact, run_backward, run_forward, run_ortho
+
+pytestmark = pytest.mark.gpu
+KERNELS = [g.LAYER_LARGE, g.LAYER_SHARED, g.LAYER_TILE]
+
+
+@pytest.fixture(params=KERNELS, ids=["large", "shared", "tile"])
+def kernel(request):
+    need_gpu()
+    g.force_layer_kernel(request.param)
+    yield request.param
+    g.force_layer_kernel(g.LAYER_AUTO)
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 8, 256), (300, 264, 520), (257, 520, 1032), (513, 1032, 200)])
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+def test_layers(kernel, gated, M, N, K):
+    rows = 2 * N if gated else N
+    gen = gen_of(M, N, K, 31)
+    A, B, bias = randn(gen, M, K), randn(gen, rows, K, std=K ** -0.5), randn(gen, rows)
+    R = None if gated else randn(gen, M, N)
+    print("kernel", kernel, gated, M, N, K, flush=True)
+    C, Z = run_forward(gated, M, N, K, A, B, bias, g.ACT_GELU_TANH, R, True)
+    y, ey, z, ez = forward(A, B, bias, g.ACT_GELU_TANH, R, gated)
+    close(C, y, ey, "C")
+    close(Z, z, ez, "Z")
+    dC, Zin = randn(gen, M, N), randn(gen, M, rows)
+    got = run_backward(gated, M, N, K, A, B, Zin, g.ACT_SILU, dC)
+    for k, (v, e) in backward(A, B, Zin, g.ACT_SILU, dC, gated).items():
+        close(got[k], v, e, k)
+
+
+@pytest.mark.parametrize("shape", [(1, 520, 264), (2, 264, 776), (1, 1032, 1032), (3, 776, 520)])
+def test_newton_schulz(kernel, shape):
+    gen = gen_of(*shape, 37)
+    G = (torch.randn(*shape, generator=gen) * 1e-3)
+    print("kernel", kernel, shape, flush=True)
+    got, want = run_ortho(G), ortho_exact(G, 5, (3.4445, -4.7750, 2.0315), 1e-7)
+    rel = ((got - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)).max().item()
+    assert rel <= 15 ** 0.5 * 2.0 ** -11 * 2 + 2.0 ** -8 / 3 ** 0.5, rel
+
+
+def whole(gen, *shape, top=2):
+    return torch.randint(-top, top + 1, shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("M,N,K", [(4608, 4600, 328), (6200, 6152, 256), (1032, 2056, 4104)])
+def test_many_tiles_are_exact(kernel, M, N, K):
+    # whole numbers whose sums are exact in FP32: one right value each; more
+    # tiles than workgroups, so items follow each other in one workgroup
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(M)
+    A, B, R, dC = whole(gen, M, K), whole(gen, N, K), whole(gen, M, N), whole(gen, M, N, top=1)
+    print("kernel", kernel, M, N, K, flush=True)
+    C, dA, dB, dbias = Out(M, N), Out(M, K), Out(N, K), Out(N)
+    ws, nb, check = workspace(max(g.bias_act_res_workspace_size(M, N, K),
+                                  g.bias_act_bwd_workspace_size(M, N, K, g.ACT_NONE)))
+    for _ in range(2):     # twice: nothing is left behind in the workspace
+        g.gemm_bf16_nt_bias_act_res(M, N, K, A, B, None, g.ACT_RELU, R, None, C.t, ws, nb)
+        g.gemm_bf16_nt_bias_act_bwd(M, N, K, A, B, None, g.ACT_NONE, dC, dA.t, dB.t, dbias.t, ws, nb)
+        torch.cuda.synchronize()
+        check()
+        a, b, d = A.float(), B.float(), dC.float()
+        for got, want in ((C, ((a @ b.t()).clamp(min=0) + R.float())), (dA, d @ b), (dB, d.t().contiguous() @ a),
+                          (dbias, d.sum(0))):
+            assert torch.equal(got.get(), want.bfloat16().double().cpu())
+
+
+def test_kernels_agree_with_the_workspace_each_asks_for():
+    need_gpu()
+    M, N, K = 700, 1032, 520
+    gen = gen_of(41)
+    A, B = randn(gen, M, K), randn(gen, N, K)
+    try:
+        for k in KERNELS + [g.LAYER_AUTO]:
+            g.force_layer_kernel(k)
+            nb = g.bias_act_res_workspace_size(M, N, K)
+            if nb:
+                ws, _, _ = workspace(nb)
+                with pytest.raises(g.Gemm355Error) as e:
+                    g.gemm_bf16_nt_bias_act_res(M, N, K, dev(A), dev(B), None, 0, None, None, Out(M, N).t, ws, nb - 1)
+                assert e.value.status == g.ERR_UNSUPPORTED
+    finally:
+        g.force_layer_kernel(g.LAYER_AUTO)
