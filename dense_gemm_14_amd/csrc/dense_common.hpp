@@ -79,6 +79,36 @@ template <int N>
 __device__ inline void wait_copies_le() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 __device__ inline void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
+// ---- global -> LDS copies ----------------------------------------------------
+
+// Buffer offset past every range (extents are below 2^31), after any
+// instruction offset too.
+constexpr unsigned OFF_NONE = 0xFFFF0000u;
+constexpr int NEVER = 1 << 30;   // K offset past every K
+// The resources start COPY_SHIFT bytes early, so that a lane's offset less the
+// second copy's instruction offset (1024) is never negative.
+constexpr int COPY_SHIFT = 1024;
+
+// Two 1 KiB global -> LDS copies: lane i's 16 bytes at buffer offset v0 (v1 +
+// 1024) land at lds_addr (+ 1024) + 16 i. Inline assembly, so that the compiler
+// does not order every later LDS read after the LDS writes in flight; the
+// kernel orders them with vmcnt waits and barriers. The s_nop: an LDS-DMA
+// instruction must not directly follow a scalar write of m0.
+__device__ inline void copy_two(const i32x4 &rsrc, unsigned lds_addr, unsigned v0, unsigned v1)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+                 "buffer_load_dwordx4 %1, %3, 0 offen offset:0 lds\n\t"
+                 "buffer_load_dwordx4 %2, %3, 0 offen offset:1024 lds"
+                 :
+                 : "s"(lds_addr), "v"(v0), "v"(v1), "s"(rsrc)
+                 : "memory", "m0");
+}
+
+// LDS places of the 16-byte chunks of a 128-byte ROW_K row, and of the 32-byte
+// segments of a COL_K K row of 256 bytes or more.
+__device__ inline int swizzle_row(int r, int c) { return c ^ ((r >> 1) & 7); }
+__device__ inline int key_col(int k) { return (k & 3) | ((k >> 1) & 4); }
+
 // ---- activations -----------------------------------------------------------
 //
 // Both gated-linear activations are z sigma(w(z)): w = z for SiLU and

@@ -22,9 +22,9 @@ constexpr int GRAD_COLS = 256;    // columns per workgroup
 constexpr int GRAD_LANES = 8;     // rows side by side
 
 struct GradArgs {
-    const uint16_t *z;    // M x N (gated: M x 2 N) BF16; NULL with the identity
+    const uint16_t *z;    // M x N (gated: M x 2 N) BF16
     const uint16_t *dc;   // M x N
-    uint16_t *dz;         // M x N (gated: M x 2 N); NULL: sums only
+    uint16_t *dz;         // M x N (gated: M x 2 N)
     float *sums;          // [row blocks][N or 2 N], or NULL
     int M, N;
     int act;
@@ -79,8 +79,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void dense_grad_kernel(GradArgs p)
             for (int m = rb * p.rows + ty; m < m_end; m += GRAD_LANES) {
                 float d[8], g[8], u[8];
                 unpack8(*reinterpret_cast<const u32x4 *>(p.dc + (size_t)m * p.N + n), d);
-                if (GATED || ACT != A_NONE)
-                    unpack8(*reinterpret_cast<const u32x4 *>(p.z + (size_t)m * width + n), g);
+                unpack8(*reinterpret_cast<const u32x4 *>(p.z + (size_t)m * width + n), g);
                 if constexpr (GATED) {
                     unpack8(*reinterpret_cast<const u32x4 *>(p.z + (size_t)m * width + p.N + n), u);
 #pragma unroll
@@ -97,14 +96,11 @@ __global__ __launch_bounds__(GRAD_THREADS) void dense_grad_kernel(GradArgs p)
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        if constexpr (ACT != A_NONE) {
-                            float value;
-                            d[e] *= act_slope<ACT>(g[e], &value);
-                        }
+                        float value;
+                        d[e] *= act_slope<ACT>(g[e], &value);
                         sg[e] += d[e];
                     }
-                    if (p.dz)
-                        *reinterpret_cast<u32x4 *>(p.dz + (size_t)m * width + n) = pack8(d);
+                    *reinterpret_cast<u32x4 *>(p.dz + (size_t)m * width + n) = pack8(d);
                 }
             }
         });
@@ -116,26 +112,60 @@ __global__ __launch_bounds__(GRAD_THREADS) void dense_grad_kernel(GradArgs p)
     }
 }
 
-// dbias[c] = bf16(sum of the `blocks` rows of column sums).
+// The bias gradient of 64 columns by 512 threads: from the workgroups' column
+// sums, or, where nothing else has to pass over dC (the identity), from dC
+// itself. `part`: 64 x 65 floats of LDS.
 struct BiasArgs {
-    const float *sums;
+    const float *sums;     // [blocks][cols], or NULL
+    const uint16_t *dc;    // else: blocks x cols BF16
     uint16_t *dbias;
     int cols, blocks;
 };
-constexpr int BIAS_COLS = 64, BIAS_LANES = 4;
-__global__ __launch_bounds__(BIAS_COLS * BIAS_LANES) void dense_bias_kernel(BiasArgs p)
+constexpr int BIAS_COLS = 64, BIAS_THREADS = 512, BIAS_PITCH = 65;
+__device__ inline void bias_block(const BiasArgs &p, int block, float *part)
 {
-    __shared__ float part[BIAS_LANES][BIAS_COLS];
-    const int tx = threadIdx.x % BIAS_COLS, ty = threadIdx.x / BIAS_COLS;
-    const int c = (int)blockIdx.x * BIAS_COLS + tx;
-    float t = 0.0f;
-    if (c < p.cols)
-        for (int r = ty; r < p.blocks; r += BIAS_LANES)
-            t += p.sums[(size_t)r * p.cols + c];
-    part[ty][tx] = t;
+    const int c0 = block * BIAS_COLS;
+    int lanes;
+    if (p.sums) {
+        const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6, c = c0 + tx;
+        float t = 0.0f;
+        if (c < p.cols)
+#pragma unroll 4
+            for (int r = ty; r < p.blocks; r += 8)
+                t += p.sums[(size_t)r * p.cols + c];
+        part[ty * BIAS_PITCH + tx] = t;
+        lanes = 8;
+    } else {
+        const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, c = c0 + 8 * tx;
+        float s[8] = {};
+        if (c < p.cols)
+#pragma unroll 4
+            for (int r = ty; r < p.blocks; r += 64) {
+                float x[8];
+                unpack8(*reinterpret_cast<const u32x4 *>(p.dc + (size_t)r * p.cols + c), x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    s[e] += x[e];
+            }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            part[ty * BIAS_PITCH + 8 * tx + e] = s[e];
+        lanes = 64;
+    }
     __syncthreads();
-    if (ty == 0 && c < p.cols)
-        p.dbias[c] = (uint16_t)pack_bf16(part[0][tx] + part[1][tx] + part[2][tx] + part[3][tx], 0.0f);
+    const int tx = threadIdx.x;
+    if (tx < BIAS_COLS && c0 + tx < p.cols) {
+        float t = 0.0f;
+        for (int r = 0; r < lanes; ++r)
+            t += part[r * BIAS_PITCH + tx];
+        p.dbias[c0 + tx] = (uint16_t)pack_bf16(t, 0.0f);
+    }
+}
+
+__global__ __launch_bounds__(BIAS_THREADS) void dense_bias_kernel(BiasArgs p)
+{
+    __shared__ float part[64 * BIAS_PITCH];
+    bias_block(p, (int)blockIdx.x, part);
 }
 
 } // namespace dense

@@ -38,7 +38,6 @@ constexpr int CUT_MIN = 4;                    // fewest steps of a work item
 // carries the instruction offset 1024 (j % 4), which moves the LDS destination
 // and the global address alike, and the lane's offset stays non-negative.
 constexpr int BIG_SHIFT = 3 * 1024;
-constexpr unsigned BIG_NONE = 0xFFFF0000u;    // beyond every range
 
 static_assert(BIG_SLOTS * BIG_UNIT <= 163840, "LDS ring exceeds the 160 KiB of a gfx950 workgroup");
 
@@ -117,9 +116,6 @@ __device__ inline int fresh_lane()
     return l;
 }
 
-__device__ inline int big_swizzle(int r, int c) { return c ^ ((r >> 1) & 7); }
-__device__ inline int big_key(int k) { return (k & 3) | ((k >> 1) & 4); }
-
 // Keeps a row of accumulators in its accumulation registers up to this point:
 // without it the compiler moves all 64 blocks out before the epilogue starts,
 // which spills.
@@ -190,7 +186,7 @@ void dense_large_kernel(LargeArgs args)
             const int block = BIG_COPIES * wave + j;   // 1 KiB block of the unit
             if constexpr (L == ROW_K) {
                 const int r = 8 * block + (ln >> 3);
-                const int c = big_swizzle(r, ln & 7);
+                const int c = swizzle_row(r, ln & 7);
                 // gated: a wave's first four block columns are gate columns,
                 // its last four the up columns of the same outputs
                 const int row = gated ? ((r & 64) ? rows : 0) + min(row0 + 64 * (r >> 7) + (r & 63), rows - 1)
@@ -198,7 +194,7 @@ void dense_large_kernel(LargeArgs args)
                 o[j] = ((unsigned)row * (unsigned)p.K + 8u * (unsigned)c) * 2u + BIG_SHIFT - 1024u * (j & 3);
             } else {
                 const int k = 2 * block + (ln >> 5), pos = ln & 31;
-                const int c = (((pos >> 1) ^ big_key(k)) << 1) | (pos & 1);
+                const int c = (((pos >> 1) ^ key_col(k)) << 1) | (pos & 1);
                 const int col = min(row0 + 8 * c, rows - 8);
                 o[j] = ((unsigned)k * (unsigned)rows + (unsigned)col) * 2u + BIG_SHIFT - 1024u * (j & 3);
             }
@@ -218,7 +214,7 @@ void dense_large_kernel(LargeArgs args)
     bool tail_ok[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-        tail_ok[j] = (nk - 1) * BIG_BK + 8 * big_swizzle(8 * (BIG_COPIES * wave + j) + (lane >> 3), lane & 7) < p.K;
+        tail_ok[j] = (nk - 1) * BIG_BK + 8 * swizzle_row(8 * (BIG_COPIES * wave + j) + (lane >> 3), lane & 7) < p.K;
 
     // Per-step bases, hidden from the optimiser at every step so that addresses
     // are formed where they are used instead of living in registers.
@@ -230,8 +226,8 @@ void dense_large_kernel(LargeArgs args)
     unsigned ra[2], rb[2];
     auto read_base = [&](auto layout_c, unsigned (&o)[2], int half) {
         if constexpr (decltype(layout_c)::value == ROW_K) {
-            o[0] = lds_base + (unsigned)((half * 128 + l16) * 128 + (big_swizzle(l16, grp) << 4));
-            o[1] = lds_base + (unsigned)((half * 128 + l16) * 128 + (big_swizzle(l16, 4 + grp) << 4));
+            o[0] = lds_base + (unsigned)((half * 128 + l16) * 128 + (swizzle_row(l16, grp) << 4));
+            o[1] = lds_base + (unsigned)((half * 128 + l16) * 128 + (swizzle_row(l16, 4 + grp) << 4));
         } else {
             o[0] = lds_base + (unsigned)((8 * grp + (l16 >> 2)) * 512 + half * 256 + (l16 & 3) * 8);
             o[1] = (unsigned)(((l16 >> 2) | ((grp & 1) << 2)) << 5);
@@ -286,7 +282,7 @@ void dense_large_kernel(LargeArgs args)
         const bool row_k = op ? LB == ROW_K : LA == ROW_K;
         unsigned v = voff[op][j];
         if constexpr (TAIL) {
-            v = row_k && tail && !tail_ok[j & 1] ? BIG_NONE : v + ks_off;
+            v = row_k && tail && !tail_ok[j & 1] ? OFF_NONE : v + ks_off;
             const unsigned long long base = op ? gb : ga;
             const i32x4 rsrc = {(int)(unsigned)base, (int)(unsigned)(base >> 32), (int)((op ? b_bytes : a_bytes) + BIG_SHIFT),
                                 (int)RSRC_WORD3};

@@ -12,6 +12,7 @@
 #include "gemm355.h"
 #include "host.hpp"
 #include "dense_large.hpp"
+#include "dense_small.hpp"
 #include "dense_tile.hpp"
 #include "dense_grad.hpp"
 #include "newton_schulz.hpp"
@@ -91,11 +92,31 @@ LargePlan plan_large(const Shape &s, int cus, bool share)
     return t;
 }
 
+// The small-tile kernel's tile, in blocks of 16 rows of A and of B.
+struct SmallPlan {
+    int mb, nb, tiles_m, tiles_n, tiles;
+};
+
+// Few tokens (forward layers only): 16 or 32 rows against narrow tiles, so
+// that every compute unit streams weights; otherwise 64 x 64.
+SmallPlan plan_small(const Shape &s, bool layer)
+{
+    SmallPlan t = {4, 4, 0, 0, 0};
+    if (layer && s.M <= 32) {
+        t.mb = s.M <= 16 ? 1 : 2;
+        t.nb = s.gated ? 2 : 1;
+    }
+    t.tiles_m = (int)ceil_div(s.M, 16 * t.mb);
+    t.tiles_n = (int)ceil_div(s.N, s.gated ? 8 * t.nb : 16 * t.nb);
+    t.tiles = s.symmetric ? t.tiles_m * (t.tiles_m + 1) / 2 : t.tiles_m * t.tiles_n;
+    return t;
+}
+
 // Which kernel runs a product: 1 = 256 x 256 tiles, 2 = the same with the last
-// tiles shared, 3 = 128 x 128 tiles. Set through gemm355_force_layer_kernel
-// (0 = by size).
+// tiles shared, 3 = 128 x 128 tiles, 4 = small tiles. Set through
+// gemm355_force_layer_kernel (0 = by size).
 std::atomic<int> g_layer_kernel{0};
-enum { KERNEL_WHOLE = 1, KERNEL_SHARED = 2, KERNEL_TILE = 3 };
+enum { KERNEL_WHOLE = 1, KERNEL_SHARED = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4 };
 
 // Measured on MI355X: a K step of a 256 x 256 tile, of a 128 x 128 tile with a
 // workgroup on every compute unit, and what a launch of each costs besides.
@@ -103,28 +124,57 @@ constexpr double kBigStep = 1.45, kBigFixed = 8.0;
 constexpr double kTileStep = 0.55, kTileFixed = 4.0;
 constexpr double kShareFixed = 30.0;    // writing and adding the parts
 constexpr double kReduceFixed = 4.0;
+constexpr double kSmallSlice = 0.8, kSmallFixed = 3.0;
 
-int choose_kernel(const Shape &s, int cus)
+int choose_kernel(const Shape &s, bool layer, int cus)
 {
     const int nk = (int)ceil_div(s.K, d::BIG_BK);
     const bool big_ok = nk >= d::CUT_MIN;
     const int forced = g_layer_kernel.load(std::memory_order_relaxed);
     if (forced != 0)
-        return forced != KERNEL_TILE && !big_ok ? KERNEL_TILE : forced;
-    if (!big_ok)
-        return KERNEL_TILE;
+        return forced <= KERNEL_SHARED && !big_ok ? KERNEL_TILE : forced;
+    const SmallPlan q = plan_small(s, layer);
+    const double small = double(ceil_div(int64_t(q.tiles) * s.batch, cus)) *
+                         (ceil_div(nk, d::SMALL_WAVES) * kSmallSlice + kSmallFixed);
     const TilePlan t = plan_tile(s, cus);
     const int64_t items = int64_t(t.tiles) * t.splits * s.batch;
     const double tile = ceil_div(items, cus) * t.steps_per_split * kTileStep + kTileFixed + (t.splits > 1 ? kReduceFixed : 0);
-    const double whole = plan_large(s, cus, false).steps * kBigStep + kBigFixed;
-    const double shared = plan_large(s, cus, true).steps * kBigStep + kBigFixed + kShareFixed;
-    return tile <= whole && tile <= shared ? KERNEL_TILE : shared < whole ? KERNEL_SHARED : KERNEL_WHOLE;
+    const double whole = big_ok ? plan_large(s, cus, false).steps * kBigStep + kBigFixed : 1e30;
+    const double shared = big_ok ? plan_large(s, cus, true).steps * kBigStep + kBigFixed + kShareFixed : 1e30;
+    const double best = std::min({small, tile, whole, shared});
+    return best == small ? KERNEL_SMALL : best == tile ? KERNEL_TILE : best == whole ? KERNEL_WHOLE : KERNEL_SHARED;
 }
 
-size_t product_workspace(const Shape &s, int cus)
+size_t product_workspace(const Shape &s, bool layer, int cus)
 {
-    const int k = choose_kernel(s, cus);
-    return k == KERNEL_TILE ? plan_tile(s, cus).workspace_bytes : plan_large(s, cus, k == KERNEL_SHARED).workspace_bytes;
+    switch (choose_kernel(s, layer, cus)) {
+    case KERNEL_SMALL: return 0;
+    case KERNEL_TILE: return plan_tile(s, cus).workspace_bytes;
+    case KERNEL_WHOLE: return 0;
+    default: return plan_large(s, cus, true).workspace_bytes;
+    }
+}
+
+// The small-tile instances: every tile shape for the forward layers, 64 x 64
+// for the other products.
+template <class T, int LA, int LB, int EPI, class TO>
+int product_small(DenseArgs p, const SmallPlan &t, hipStream_t stream)
+{
+    p.tiles_m = t.tiles_m;
+    p.tiles_n = t.tiles_n;
+    p.tiles = t.tiles;
+    const int64_t items = int64_t(t.tiles) * p.batch;
+    if (items > (int64_t(1) << 28))
+        return GEMM355_ERR_UNSUPPORTED;
+    const unsigned blocks = (unsigned)(ceil_div(items, 8) * 8), threads = d::SMALL_THREADS;
+    if constexpr (EPI == d::EPI_LINEAR || EPI == d::EPI_GATED) {
+        constexpr int NARROW = EPI == d::EPI_GATED ? 2 : 1;
+        if (t.mb == 1)
+            return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, NARROW>, blocks, threads, p, stream);
+        if (t.mb == 2)
+            return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, NARROW>, blocks, threads, p, stream);
+    }
+    return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4>, blocks, threads, p, stream);
 }
 
 template <class T, int LA, int LB, int EPI, class TO>
@@ -179,7 +229,10 @@ int product(DenseArgs p, int cus, void *ws, hipStream_t stream)
     const Shape s = {p.M, p.N, p.K, p.batch, EPI >= d::EPI_STORE_SYM, EPI == d::EPI_GATED};
     p.supergroup = 8;
     p.ws = static_cast<float *>(ws);
-    const int k = choose_kernel(s, cus);
+    constexpr bool LAYER = EPI == d::EPI_LINEAR || EPI == d::EPI_GATED;
+    const int k = choose_kernel(s, LAYER, cus);
+    if (k == KERNEL_SMALL)
+        return product_small<T, LA, LB, EPI, TO>(p, plan_small(s, LAYER), stream);
     return k == KERNEL_TILE ? product_tile<T, LA, LB, EPI, TO>(p, s, cus, stream)
                             : product_large<T, LA, LB, EPI, TO>(p, s, cus, k == KERNEL_SHARED, stream);
 }
@@ -264,7 +317,7 @@ int layer_forward(int M, int N, int K, const void *A, const void *B, const void 
     const int rc = compute_units(&cus);
     if (rc != GEMM355_OK)
         return rc;
-    if (workspace_bytes < product_workspace({M, N, K, 1, false, GATED}, cus))
+    if (workspace_bytes < product_workspace({M, N, K, 1, false, GATED}, true, cus))
         return GEMM355_ERR_UNSUPPORTED;
     DenseArgs p = args_of(M, N, K, A, B, C);
     p.bias = bias;
@@ -286,7 +339,7 @@ int layer_forward_workspace(int M, int N, int K, size_t *bytes)
     int cus = 0;
     const int rc = compute_units(&cus);
     if (rc == GEMM355_OK)
-        *bytes = product_workspace({M, N, K, 1, false, GATED}, cus);
+        *bytes = product_workspace({M, N, K, 1, false, GATED}, true, cus);
     return rc;
 }
 
@@ -316,11 +369,35 @@ BackwardPlan plan_backward(int M, int N, int K, bool gated, int act, int cus)
     w.partials_at = w.sums_at + align_up(size_t(ceil_div(M, grad_rows(M, N))) * rows * sizeof(float));
     size_t part = 0;
     if (M > 0 && K > 0)
-        part = product_workspace({M, K, rows, 1, false, false}, cus);
+        part = product_workspace({M, K, rows, 1, false, false}, false, cus);
     if (rows > 0 && K > 0)
-        part = std::max(part, product_workspace({rows, K, M, 1, false, false}, cus));
+        part = std::max(part, product_workspace({rows, K, M, 1, false, false}, false, cus));
     w.bytes = w.partials_at + part;
     return w;
+}
+
+// What is wanted of a small backward pass, in one launch.
+int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const d::BiasArgs &bias, int bias_blocks,
+                   hipStream_t s)
+{
+    d::SmallBwdArgs g = {};
+    auto place = [](DenseArgs &p, bool wanted) {
+        const SmallPlan t = plan_small({p.M, p.N, p.K, 1, false, false}, false);
+        p.tiles_m = t.tiles_m;
+        p.tiles_n = t.tiles_n;
+        p.tiles = wanted ? t.tiles : 0;
+        p.supergroup = 8;
+    };
+    place(pa, wants_a);
+    place(pb, wants_b);
+    g.a = pa;
+    g.b = pb;
+    g.bias = bias;
+    g.bias_blocks = bias_blocks;
+    const int64_t items = int64_t(pa.tiles) + pb.tiles + bias_blocks;
+    if (items > (int64_t(1) << 28))
+        return GEMM355_ERR_UNSUPPORTED;
+    return launch_kernel(d::dense_small_bwd_kernel, (unsigned)(ceil_div(items, 8) * 8), (unsigned)d::SMALL_THREADS, g, s);
 }
 
 template <bool GATED>
@@ -359,11 +436,11 @@ int layer_backward(int M, int N, int K, const void *A, const void *B, const void
     const void *dz = needs_z ? ws : dC;
     float *sums = reinterpret_cast<float *>(ws + w.sums_at);
     const int per = grad_rows(M, N), blocks = (int)ceil_div(M, per);
-    if (M > 0 && N > 0 && (needs_z || wants_bias)) {
+    if (needs_z && M > 0 && N > 0) {
         d::GradArgs g = {};
-        g.z = needs_z ? static_cast<const uint16_t *>(Z) : nullptr;
+        g.z = static_cast<const uint16_t *>(Z);
         g.dc = static_cast<const uint16_t *>(dC);
-        g.dz = needs_z ? reinterpret_cast<uint16_t *>(ws) : nullptr;
+        g.dz = reinterpret_cast<uint16_t *>(ws);
         g.sums = wants_bias ? sums : nullptr;
         g.M = M;
         g.N = N;
@@ -375,23 +452,25 @@ int layer_backward(int M, int N, int K, const void *A, const void *B, const void
         if (st != GEMM355_OK)
             return st;
     }
+    d::BiasArgs q = {needs_z ? sums : nullptr, static_cast<const uint16_t *>(dC), static_cast<uint16_t *>(dbias), (int)rows,
+                     needs_z ? blocks : M};
+    const int bias_blocks = wants_bias ? (int)ceil_div(rows, d::BIAS_COLS) : 0;
+    const DenseArgs pa = args_of(M, K, (int)rows, dz, B, dA);          // dA = dZ B
+    const DenseArgs pb = args_of((int)rows, K, M, dz, A, dB);          // dB = dZ^T A
+    const Shape sa = {M, K, (int)rows, 1, false, false}, sb = {(int)rows, K, M, 1, false, false};
+    if ((!wants_a || choose_kernel(sa, false, cus) == KERNEL_SMALL) && (!wants_b || choose_kernel(sb, false, cus) == KERNEL_SMALL))
+        return backward_small(pa, wants_a, pb, wants_b, q, bias_blocks, s);
     if (wants_bias) {
-        d::BiasArgs q = {sums, static_cast<uint16_t *>(dbias), (int)rows, blocks};
-        const int st = launch_kernel(d::dense_bias_kernel, (unsigned)ceil_div(rows, d::BIAS_COLS),
-                                     (unsigned)(d::BIAS_COLS * d::BIAS_LANES), q, s);
+        const int st = launch_kernel(d::dense_bias_kernel, (unsigned)bias_blocks, (unsigned)d::BIAS_THREADS, q, s);
         if (st != GEMM355_OK)
             return st;
     }
-    if (wants_a) {   // dA = dZ B
-        const int st = product<__bf16, d::ROW_K, d::COL_K, d::EPI_STORE>(args_of(M, K, (int)rows, dz, B, dA), cus,
-                                                                        ws + w.partials_at, s);
+    if (wants_a) {
+        const int st = product<__bf16, d::ROW_K, d::COL_K, d::EPI_STORE>(pa, cus, ws + w.partials_at, s);
         if (st != GEMM355_OK)
             return st;
     }
-    if (wants_b)     // dB = dZ^T A
-        return product<__bf16, d::COL_K, d::COL_K, d::EPI_STORE>(args_of((int)rows, K, M, dz, A, dB), cus,
-                                                                ws + w.partials_at, s);
-    return GEMM355_OK;
+    return wants_b ? product<__bf16, d::COL_K, d::COL_K, d::EPI_STORE>(pb, cus, ws + w.partials_at, s) : GEMM355_OK;
 }
 
 template <bool GATED>
@@ -442,8 +521,8 @@ OrthoPlan plan_ortho(int batch, int rows, int cols, int cus)
     o.partials_at = o.norm_at + align_up(size_t(batch) * o.norm_blocks * sizeof(double));
     Shape gram, square, update;
     ortho_shapes(batch, rows, cols, &gram, &square, &update);
-    o.bytes = o.partials_at + std::max({product_workspace(gram, cus), product_workspace(square, cus),
-                                        product_workspace(update, cus)});
+    o.bytes = o.partials_at + std::max({product_workspace(gram, false, cus), product_workspace(square, false, cus),
+                                        product_workspace(update, false, cus)});
     return o;
 }
 
@@ -496,7 +575,7 @@ bool ortho_extents_ok(int64_t rows, int64_t cols)
 
 extern "C" int gemm355_force_layer_kernel(int kernel)
 {
-    if (kernel < 0 || kernel > KERNEL_TILE)
+    if (kernel < 0 || kernel > KERNEL_SMALL)
         return GEMM355_ERR_INVALID_ARG;
     g_layer_kernel.store(kernel, std::memory_order_relaxed);
     return GEMM355_OK;

@@ -42,32 +42,6 @@ constexpr int TILE_COPIES = 4;                           // per wave and step: t
 static_assert(TILE_LDS <= 163840, "LDS ring exceeds the 160 KiB of a gfx950 workgroup");
 static_assert(TILE_COPIES * (TILE_STAGES - 1) <= 63, "vmcnt counts at most 63 outstanding operations");
 
-// Buffer offset past every range (extents are below 2^31), after any
-// instruction offset too.
-constexpr unsigned OFF_NONE = 0xFFFF0000u;
-constexpr int NEVER = 1 << 30;   // K offset past every K
-// The resources start TILE_SHIFT bytes early, so that a lane's offset less the
-// second copy's instruction offset (1024) is never negative.
-constexpr int TILE_SHIFT = 1024;
-
-// Two 1 KiB global -> LDS copies: lane i's 16 bytes at buffer offset v0 (v1 +
-// 1024) land at lds_addr (+ 1024) + 16 i. Inline assembly, so that the compiler
-// does not order every later LDS read after the LDS writes in flight; the
-// kernel orders them with vmcnt waits and barriers. The s_nop: an LDS-DMA
-// instruction must not directly follow a scalar write of m0.
-__device__ inline void copy_two(const i32x4 &rsrc, unsigned lds_addr, unsigned v0, unsigned v1)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
-                 "buffer_load_dwordx4 %1, %3, 0 offen offset:0 lds\n\t"
-                 "buffer_load_dwordx4 %2, %3, 0 offen offset:1024 lds"
-                 :
-                 : "s"(lds_addr), "v"(v0), "v"(v1), "s"(rsrc)
-                 : "memory", "m0");
-}
-
-__device__ inline int swizzle_row(int r, int c) { return c ^ ((r >> 1) & 7); }
-__device__ inline int key_col(int k) { return (k & 3) | ((k >> 1) & 4); }
-
 // One operand of a 128-row tile: where this lane copies from, and where it
 // reads its fragments.
 // GATED: LDS row r of the unit holds weight row (r & 32 ? gate_rows : 0) +
@@ -89,7 +63,7 @@ struct TileOperand {
     {
         const int l16 = lane & 15, grp = lane >> 4;
         const unsigned extent = (unsigned)(GATED ? 2 * gate_rows : rows) * (unsigned)K * 2u;
-        rsrc = rsrc_words(static_cast<const uint8_t *>(base) - TILE_SHIFT, base ? extent + TILE_SHIFT : 0u);
+        rsrc = rsrc_words(static_cast<const uint8_t *>(base) - COPY_SHIFT, base ? extent + COPY_SHIFT : 0u);
         copy_lds = lds + (unsigned)(2048 * wave);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -98,12 +72,12 @@ struct TileOperand {
                 const int r = 8 * block + (lane >> 3);
                 const int c = swizzle_row(r, lane & 7);
                 const int row = GATED ? ((r & 32) ? gate_rows : 0) + row0 + 32 * (r >> 6) + (r & 31) : row0 + r;
-                off[t] = ((unsigned)row * (unsigned)K + 8u * (unsigned)c) * 2u + TILE_SHIFT - 1024u * t;
+                off[t] = ((unsigned)row * (unsigned)K + 8u * (unsigned)c) * 2u + COPY_SHIFT - 1024u * t;
                 chunk_k[t] = 8 * c;   // rows past the operand lie past its range
             } else {
                 const int k = 4 * block + (lane >> 4), pos = lane & 15;
                 const int col = row0 + 8 * ((((pos >> 1) ^ key_col(k)) << 1) | (pos & 1));
-                off[t] = ((unsigned)k * (unsigned)rows + (unsigned)col) * 2u + TILE_SHIFT - 1024u * t;
+                off[t] = ((unsigned)k * (unsigned)rows + (unsigned)col) * 2u + COPY_SHIFT - 1024u * t;
                 chunk_k[t] = col < rows ? 0 : NEVER;   // K rows past the operand lie past its range
             }
         }
