@@ -201,32 +201,56 @@ def status_string(status: int) -> str:
 
 # ---- marshalling -----------------------------------------------------------
 
-def _addr(x, need_bytes: int, what: str):
-    """Device address of a tensor (checked) or a raw int address (unchecked)."""
+_torch = None   # imported with the first tensor or stream
+_raw_stream = None
+
+
+def _import_torch():
+    global _torch, _raw_stream
+    import torch
+    # the address of a device's current stream without building a Stream object
+    # (3 us a call, as long as the rest of a small product's call)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
+    return torch
+
+
+def _addr(x, need_bytes: int, what: str, device=None):
+    """Device address of a tensor (checked) or a raw int address (unchecked).
+    With `device`, the tensor has to be on that one."""
     if x is None:
         return None
     if isinstance(x, int):
         return x
-    import torch
+    torch = _torch or _import_torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError("%s: expected a torch tensor or an int address, got %r" % (what, type(x)))
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("%s must be on the GPU, got device %s" % (what, x.device))
+    if device is not None and x.get_device() != device:
+        raise ValueError("%s is on device %d, the current device is %d" % (what, x.get_device(), device))
     if not x.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
-    have = x.numel() * x.element_size()
-    if have < need_bytes:
-        raise ValueError("%s holds %d bytes, the sizes need %d" % (what, have, need_bytes))
+    if x.nbytes < need_bytes:
+        raise ValueError("%s holds %d bytes, the sizes need %d" % (what, x.nbytes, need_bytes))
     return x.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        torch = _torch or _import_torch()
+        return _raw_stream(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
+    if device is not None and stream.device_index != device:
+        raise ValueError("the stream is on device %d, the current device is %d" % (stream.device_index, device))
     return stream.cuda_stream
+
+
+def _device() -> int:
+    """The current device, which runs the layer calls."""
+    return (_torch or _import_torch()).cuda.current_device()
 
 
 def _check(status: int, what: str):
@@ -261,7 +285,7 @@ def gemm_bf16_nt_bias_act(M: int, N: int, K: int, A, B, bias, activation: int, C
            "gemm_bf16_nt_bias_act")
 
 
-def _workspace(ws, nbytes):
+def _workspace(ws, nbytes, device=None):
     """(address, bytes) of a workspace tensor, int address or None."""
     if ws is None:
         return None, 0 if nbytes is None else int(nbytes)
@@ -269,11 +293,11 @@ def _workspace(ws, nbytes):
         if nbytes is None:
             raise ValueError("workspace_bytes is needed with a raw workspace address")
         return ws, int(nbytes)
-    have = ws.numel() * ws.element_size()
+    have = ws.nbytes
     nb = have if nbytes is None else int(nbytes)
     if nb > have:
         raise ValueError("workspace holds %d bytes, workspace_bytes says %d" % (have, nb))
-    return _addr(ws, nb, "workspace"), nb
+    return _addr(ws, nb, "workspace", device), nb
 
 
 def gemm_bf16_nt_ws(M: int, N: int, K: int, A, B, C, workspace, workspace_bytes=None, stream=None) -> None:
@@ -460,17 +484,17 @@ def gemm_bf16_nt_bias_act_res(M: int, N: int, K: int, A, B, bias, activation: in
     bias (N), R (M x N, may be C itself) and Z (M x N, an output) may be None;
     activation: ACT_NONE, ACT_RELU, ACT_GELU_TANH or ACT_SILU. The workspace
     holds bias_act_res_workspace_size(M, N, K) bytes (None when that is 0)."""
-    lib = load()
+    lib, dev = load(), _device()
     M, N, K = int(M), int(N), int(K)
     nz = M > 0 and N > 0
-    a = _addr(A, M * K * 2 if nz else 0, "A")
-    b = _addr(B, N * K * 2 if nz else 0, "B")
-    bb = _addr(bias, N * 2 if nz else 0, "bias")
-    r = _addr(R, M * N * 2 if nz else 0, "R")
-    z = _addr(Z, M * N * 2 if nz else 0, "Z")
-    c = _addr(C, M * N * 2 if nz else 0, "C")
-    w, nb = _workspace(workspace, workspace_bytes)
-    _check(lib.gemm_bf16_nt_bias_act_res(M, N, K, a, b, bb, int(activation), r, z, c, w, nb, _stream(stream)),
+    a = _addr(A, M * K * 2 if nz else 0, "A", dev)
+    b = _addr(B, N * K * 2 if nz else 0, "B", dev)
+    bb = _addr(bias, N * 2 if nz else 0, "bias", dev)
+    r = _addr(R, M * N * 2 if nz else 0, "R", dev)
+    z = _addr(Z, M * N * 2 if nz else 0, "Z", dev)
+    c = _addr(C, M * N * 2 if nz else 0, "C", dev)
+    w, nb = _workspace(workspace, workspace_bytes, dev)
+    _check(lib.gemm_bf16_nt_bias_act_res(M, N, K, a, b, bb, int(activation), r, z, c, w, nb, _stream(stream, dev)),
            "gemm_bf16_nt_bias_act_res")
 
 
@@ -480,17 +504,18 @@ def bias_act_res_workspace_size(M: int, N: int, K: int) -> int:
 
 
 def _backward(fn, M, N, K, rows, A, B, Z, activation, dC, dA, dB, dbias, workspace, workspace_bytes, stream):
+    dev = _device()
     M, N, K, rows = int(M), int(N), int(K), int(rows)
     ok = M >= 0 and N >= 0 and K >= 0   # (else the call refuses the sizes)
-    a = _addr(A, M * K * 2 if ok else 0, "A")
-    b = _addr(B, rows * K * 2 if ok else 0, "B")
-    z = _addr(Z, M * rows * 2 if ok else 0, "Z")
-    dc = _addr(dC, M * N * 2 if ok else 0, "dC")
-    da = _addr(dA, M * K * 2 if ok else 0, "dA")
-    db = _addr(dB, rows * K * 2 if ok else 0, "dB")
-    dbb = _addr(dbias, rows * 2 if ok else 0, "dbias")
-    w, nb = _workspace(workspace, workspace_bytes)
-    _check(getattr(load(), fn)(M, N, K, a, b, z, int(activation), dc, da, db, dbb, w, nb, _stream(stream)), fn)
+    a = _addr(A, M * K * 2 if ok else 0, "A", dev)
+    b = _addr(B, rows * K * 2 if ok else 0, "B", dev)
+    z = _addr(Z, M * rows * 2 if ok else 0, "Z", dev)
+    dc = _addr(dC, M * N * 2 if ok else 0, "dC", dev)
+    da = _addr(dA, M * K * 2 if ok else 0, "dA", dev)
+    db = _addr(dB, rows * K * 2 if ok else 0, "dB", dev)
+    dbb = _addr(dbias, rows * 2 if ok else 0, "dbias", dev)
+    w, nb = _workspace(workspace, workspace_bytes, dev)
+    _check(getattr(load(), fn)(M, N, K, a, b, z, int(activation), dc, da, db, dbb, w, nb, _stream(stream, dev)), fn)
 
 
 def gemm_bf16_nt_bias_act_bwd(M: int, N: int, K: int, A, B, Z, activation: int, dC, dA, dB, dbias, workspace=None,
@@ -514,16 +539,16 @@ def gemm_bf16_nt_gated(M: int, N: int, K: int, A, B, bias, activation: int, Z, C
     holds the gate rows, then the up rows. bias (2N) and Z (an output) may be
     None; activations and workspace (gated_workspace_size(M, N, K) bytes) as
     for gemm_bf16_nt_bias_act_res."""
-    lib = load()
+    lib, dev = load(), _device()
     M, N, K = int(M), int(N), int(K)
     nz = M > 0 and N > 0
-    a = _addr(A, M * K * 2 if nz else 0, "A")
-    b = _addr(B, 2 * N * K * 2 if nz else 0, "B")
-    bb = _addr(bias, 2 * N * 2 if nz else 0, "bias")
-    z = _addr(Z, M * 2 * N * 2 if nz else 0, "Z")
-    c = _addr(C, M * N * 2 if nz else 0, "C")
-    w, nb = _workspace(workspace, workspace_bytes)
-    _check(lib.gemm_bf16_nt_gated(M, N, K, a, b, bb, int(activation), z, c, w, nb, _stream(stream)),
+    a = _addr(A, M * K * 2 if nz else 0, "A", dev)
+    b = _addr(B, 2 * N * K * 2 if nz else 0, "B", dev)
+    bb = _addr(bias, 2 * N * 2 if nz else 0, "bias", dev)
+    z = _addr(Z, M * 2 * N * 2 if nz else 0, "Z", dev)
+    c = _addr(C, M * N * 2 if nz else 0, "C", dev)
+    w, nb = _workspace(workspace, workspace_bytes, dev)
+    _check(lib.gemm_bf16_nt_gated(M, N, K, a, b, bb, int(activation), z, c, w, nb, _stream(stream, dev)),
            "gemm_bf16_nt_gated")
 
 
@@ -560,13 +585,14 @@ def newton_schulz(batch: int, rows: int, cols: int, G, O, steps: int = 5, coeffi
         if not isinstance(G, torch.Tensor) or G.dtype not in types:
             raise TypeError("G: expected a BF16 or FP32 tensor, or an address with g_type")
         g_type = types[G.dtype]
+    dev = _device()
     n = batch * rows * cols if min(batch, rows, cols) > 0 else 0
-    gg = _addr(G, n * (4 if g_type == FP32 else 2), "G")
-    o = _addr(O, n * 2, "O")
-    w, nb = _workspace(workspace, workspace_bytes)
+    gg = _addr(G, n * (4 if g_type == FP32 else 2), "G", dev)
+    o = _addr(O, n * 2, "O", dev)
+    w, nb = _workspace(workspace, workspace_bytes, dev)
     a, b, c = coefficients
     _check(load().gemm355_newton_schulz(batch, rows, cols, int(g_type), gg, int(steps), a, b, c, eps, o, w, nb,
-                                        _stream(stream)), "gemm355_newton_schulz")
+                                        _stream(stream, dev)), "gemm355_newton_schulz")
 
 
 def newton_schulz_workspace_size(batch: int, rows: int, cols: int) -> int:
