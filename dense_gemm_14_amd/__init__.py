@@ -85,7 +85,7 @@ FP4_PATH_STAGING = 1  # always the kernel that decodes while staging
 FP4_PATH_DECODE_FIRST = 2  # always decode into the workspace, then the BF16 product
 LAYER_AUTO = 0       # the layer calls' products: by size (gemm355_force_layer_kernel)
 LAYER_LARGE = 1      # 256 x 256 output tiles
-LAYER_SHARED = 2     # the same, the last tiles' K steps shared out
+LAYER_SPLIT = 2      # the same, K of the last round's tiles split
 LAYER_TILE = 3       # 128 x 128 output tiles
 LAYER_SMALL = 4      # 64 x 64 and narrower
 SCHEDULE_STATIC = 0  # the NVFP4 kernel's tile order (gemm355_force_schedule)
@@ -602,7 +602,7 @@ def newton_schulz_workspace_size(batch: int, rows: int, cols: int) -> int:
 
 def force_layer_kernel(kernel: int) -> None:
     """Kernel of the layer calls' products for the whole process: LAYER_AUTO
-    (default), LAYER_LARGE, LAYER_SHARED, LAYER_TILE or LAYER_SMALL (a
+    (default), LAYER_LARGE, LAYER_SPLIT, LAYER_TILE or LAYER_SMALL (a
     diagnostic)."""
     _check(load().gemm355_force_layer_kernel(int(kernel)), "gemm355_force_layer_kernel")
 

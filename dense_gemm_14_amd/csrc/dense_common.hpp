@@ -38,11 +38,12 @@ struct DenseArgs {
     float *ws;           // split K: FP32 partial tiles
     int M, N, K;         // C is M x N (EPI_GATED: B has 2 N rows)
     int tiles_m, tiles_n, tiles;   // tiles: per batch entry (symmetric: on and below the diagonal)
-    int splits, steps_per_split;
+    int whole;           // tiles (over the batch) that one workgroup each runs whole; the K steps of
+    int splits, steps_per_split;   // the tiles after them are split
     int supergroup;
     int act;
     int batch;
-    int grid;            // persistent kernel: its workgroups
+    int grid;            // workgroups of a round
     float alpha, beta, gamma;
 };
 
@@ -189,6 +190,25 @@ __device__ inline void dense_tile(const DenseArgs &p, int pos, int &tm, int &tn)
         triangle_tile(pos, tm, tn);
     else
         supergroup_tile(pos, p.tiles_m, p.tiles_n, p.supergroup, tm, tn);
+}
+
+// A work item: a tile of a batch entry and, for the tiles whose K is split
+// (those from `whole` on), its part. Items come in rounds of p.grid; the tail's
+// are ordered split by split, so that the workgroups of one round that share
+// operand strips also read the same K range of them at the same time.
+struct WorkItem {
+    int tile, split;
+};
+__device__ inline int work_items(const DenseArgs &p)
+{
+    return p.whole + (p.tiles * p.batch - p.whole) * p.splits;
+}
+__device__ inline WorkItem work_item(const DenseArgs &p, int item)
+{
+    if (item < p.whole)
+        return WorkItem{item, 0};
+    const int tail = p.tiles * p.batch - p.whole, q = item - p.whole;
+    return WorkItem{p.whole + q % tail, q / tail};
 }
 
 // The arguments of batch entry `b`: every array advanced by its own size.

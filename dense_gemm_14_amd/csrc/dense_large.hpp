@@ -1,6 +1,6 @@
 // dense_large.hpp -- 256 x 256 output tiles for the dense layer's operators
 // on large problems: any pair of operand layouts, BF16 or FP16, every epilogue,
-// batches, and tiles whose K range is shared by two workgroups.
+// batches, and a last round whose tiles are split along K.
 //
 // The main loop is the chained one of gemm_bf16.hpp: four waves of 128 x 128
 // (8 x 8 blocks, 256 accumulation registers), one ring of five 32 KiB LDS units
@@ -11,13 +11,13 @@
 //     row k sits at s ^ key_col(k), so that the eight K rows half a transposing
 //     read touches fall into eight different bank groups. A fragment is two
 //     such reads per K half (8 bytes each) instead of one of 16 bytes.
-//   * Work items. Whole tiles are dealt out while every workgroup gets one;
-//     the K steps of the rest are cut into equal runs, one per workgroup, so
-//     the last round is as full as the others. A run covers the end of one
-//     tile and the start of another; both parts leave FP32 partials in the
+//   * Work items. Tiles that do not fill the last round of workgroups may have
+//     their K steps split over all of them. The parts leave FP32 partials in the
 //     workspace, in the order of the registers, and a second kernel adds a
 //     tile's parts in K order and runs its epilogue: results do not depend on
-//     timing. Cuts within CUT_MIN steps of a tile's border move to the border.
+//     timing. (Cutting the tail's steps into equal runs that cross tile borders
+//     balances better, but its workgroups read a strip's K range at different
+//     times: a step then took 2.2 us instead of 1.45, the L2s' hits lost.)
 //   * Epilogues: those of dense_common.hpp.
 #pragma once
 
@@ -33,7 +33,7 @@ constexpr int BIG_UNIT = BIG * BIG_BK * 2;    // 32 KiB
 constexpr int BIG_SLOTS = 5;
 constexpr int BIG_COPIES = 8;                 // 1 KiB copies per wave and unit
 constexpr int BIG_FLOATS = BIG * BIG;
-constexpr int CUT_MIN = 4;                    // fewest steps of a work item
+constexpr int BIG_MIN_STEPS = 4;              // fewest steps of a work item
 // Buffer resources and bases start BIG_SHIFT bytes early: copy j of a unit
 // carries the instruction offset 1024 (j % 4), which moves the LDS destination
 // and the global address alike, and the lane's offset stays non-negative.
@@ -43,57 +43,6 @@ static_assert(BIG_SLOTS * BIG_UNIT <= 163840, "LDS ring exceeds the 160 KiB of a
 
 // Columns of C per tile.
 constexpr int big_columns(int epi) { return epi == EPI_GATED ? BIG / 2 : BIG; }
-
-// Cut g of the shared K steps: tile border or K step of a tile, in steps from
-// the first shared tile. cuts: number of runs; g = 0 and g = cuts are the ends.
-__host__ __device__ inline int shared_cut(int steps, int nk, int cuts, int g)
-{
-    const int x = (int)((int64_t)steps * g / cuts);
-    const int r = x % nk;
-    return r < CUT_MIN ? x - r : nk - r < CUT_MIN ? x + nk - r : x;
-}
-
-// Arguments beside DenseArgs: p.grid workgroups; the first `whole` rounds take
-// whole tiles; the tiles after them are shared.
-struct LargeArgs {
-    DenseArgs d;
-    int whole;
-    int shared;      // tiles
-};
-
-struct WorkItem {
-    int tile;        // over all batch entries; -1: none
-    int first, steps;
-};
-
-// The successive work items of one workgroup; all uniform.
-struct WorkList {
-    int place, round, at, end;
-    __device__ inline void start(const LargeArgs &p, int nk)
-    {
-        place = schedule_position(blockIdx.x, 0, p.d.grid);
-        round = 0;
-        at = end = 0;
-        if (p.shared > 0) {
-            at = shared_cut(p.shared * nk, nk, p.d.grid, place);
-            end = shared_cut(p.shared * nk, nk, p.d.grid, place + 1);
-        }
-    }
-    __device__ inline WorkItem next(const LargeArgs &p, int nk)
-    {
-        if (round < p.whole) {
-            const int t = round * p.d.grid + place;
-            ++round;
-            return t < p.d.tiles * p.d.batch ? WorkItem{t, 0, nk} : WorkItem{-1, 0, 0};
-        }
-        if (at >= end)
-            return WorkItem{-1, 0, 0};
-        const int t = at / nk, k = at - t * nk;
-        const int n = min(nk - k, end - at);
-        at += n;
-        return WorkItem{p.whole * p.d.grid + t, k, n};
-    }
-};
 
 __device__ inline void big_set_m0(unsigned lds_addr) { asm volatile("s_mov_b32 m0, %0" ::"s"(lds_addr) : "m0"); }
 template <int O>
@@ -143,11 +92,10 @@ constexpr int big_b_copy_at(int q, bool last) { return 32 + (last ? 2 : 8) * q; 
 // the range for the chunks past K; COL_K: those K rows lie past the operand).
 template <class T, int LA, int LB, int EPI, class TO, bool TAIL>
 __global__ __attribute__((amdgpu_flat_work_group_size(BIG_THREADS, BIG_THREADS), amdgpu_waves_per_eu(1, 1)))
-void dense_large_kernel(LargeArgs args)
+void dense_large_kernel(DenseArgs p)
 {
     typedef typename Frag<T>::type frag_t;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[BIG_SLOTS * BIG_UNIT];
-    const DenseArgs &p = args.d;
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -163,12 +111,23 @@ void dense_large_kernel(LargeArgs args)
     const unsigned a_bytes = (unsigned)p.M * (unsigned)p.K * 2u;
     const unsigned b_bytes = (unsigned)p.N * (unsigned)p.K * 2u * (EPI == EPI_GATED ? 2u : 1u);
 
-    WorkList list;
-    list.start(args, nk);
-    WorkItem item = list.next(args, nk);
-    if (item.tile < 0)
+    // The workgroup's items: one per round.
+    struct Item {
+        int at;              // its number; -1: none
+        int tile, first, steps;
+    };
+    const int place = schedule_position(blockIdx.x, 0, p.grid), items = work_items(p);
+    auto item_at = [&](int at) {
+        if (at >= items)
+            return Item{-1, 0, 0, 0};
+        const WorkItem w = work_item(p, at);
+        const int first = w.split * p.steps_per_split;
+        return w.tile < p.whole ? Item{at, w.tile, 0, nk} : Item{at, w.tile, first, min(p.steps_per_split, nk - first)};
+    };
+    Item item = item_at(place);
+    if (item.at < 0)
         return;
-    WorkItem next = list.next(args, nk);
+    Item next = item_at(place + p.grid);
 
     // Where the copies read: the operands' addresses (of the batch entry) and
     // this lane's offsets. Two steps before an item ends they move to the next
@@ -403,11 +362,11 @@ void dense_large_kernel(LargeArgs args)
                 asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
                 acc[i][j] = f32x4{zero, zero, zero, zero};
             }
-        // every item has at least CUT_MIN steps
+        // every item has at least BIG_MIN_STEPS steps
         step(item.first + 2, Int<1>{}, Int<0>{});
         for (int s = 1; s < item.steps - 2; ++s)
             step(item.first + s + 2, Int<0>{}, Int<0>{});
-        const bool more = next.tile >= 0;
+        const bool more = next.at >= 0;
         const int after = more ? next.first : item.first;
         place_copies(more ? next.tile : item.tile);
 #pragma clang loop unroll(disable)
@@ -419,10 +378,7 @@ void dense_large_kernel(LargeArgs args)
 
         const int ln = fresh_lane();
         if (item.steps < nk) {
-            // a part of a tile: its place is the workgroup's first (it starts
-            // inside a tile) or second part
-            f32x4 *ws = reinterpret_cast<f32x4 *>(p.ws) +
-                        (size_t)(2 * list.place + (item.first > 0 ? 0 : 1)) * (BIG_FLOATS / 4) + wave * 64 * 64 + ln;
+            f32x4 *ws = reinterpret_cast<f32x4 *>(p.ws) + (size_t)(item.at - p.whole) * (BIG_FLOATS / 4) + wave * 64 * 64 + ln;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 hold_row(acc[i]);
@@ -462,51 +418,36 @@ void dense_large_kernel(LargeArgs args)
         if (!more)
             break;
         item = next;
-        next = list.next(args, nk);
+        next = item_at(item.at + p.grid);
     }
 
     wait_reads();
     wait_all_copies();   // no copy may still be writing LDS when the workgroup ends
 }
 
-// Adds the parts of every shared tile that no workgroup ran whole, in K order,
-// and runs the epilogue: one wave per two rows of blocks (32 rows x 128
-// columns of B rows) of a tile.
+// Adds the parts of the split tiles in K order and runs the epilogue: one wave
+// per two rows of blocks (32 rows x 128 columns of B rows) of a tile.
 constexpr int BIG_REDUCE_WAVES = 4;
 template <int EPI, class TO>
-__global__ __launch_bounds__(64 * BIG_REDUCE_WAVES) void dense_large_reduce_kernel(LargeArgs args)
+__global__ __launch_bounds__(64 * BIG_REDUCE_WAVES) void dense_large_reduce_kernel(DenseArgs p)
 {
-    const DenseArgs &p = args.d;
     const int lane = threadIdx.x & 63;
     const int unit = (int)blockIdx.x * BIG_REDUCE_WAVES + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int t = unit >> 4;
-    if (t >= args.shared)
+    const int tail = p.tiles * p.batch - p.whole, t = unit >> 4;
+    if (t >= tail)
         return;
     const int wave = (unit >> 2) & 3, i0 = 2 * (unit & 3);
-    const int nk = (p.K + BIG_BK - 1) / BIG_BK;
-    const int steps = args.shared * nk, lo = t * nk, hi = lo + nk;
-    // the first run that ends behind the tile's start
-    int g = (int)((int64_t)lo * p.grid / steps);
-    while (g > 0 && shared_cut(steps, nk, p.grid, g) > lo)
-        --g;
-    while (shared_cut(steps, nk, p.grid, g + 1) <= lo)
-        ++g;
-    int from = shared_cut(steps, nk, p.grid, g), to = shared_cut(steps, nk, p.grid, g + 1);
-    if (from <= lo && to >= hi)
-        return;   // one workgroup ran it whole
     f32x4 x[2][8] = {};
-    for (; from < hi; ++g, from = to, to = g < p.grid ? shared_cut(steps, nk, p.grid, g + 1) : steps) {
-        if (to <= from)
-            continue;
-        const f32x4 *ws = reinterpret_cast<const f32x4 *>(p.ws) + (size_t)(2 * g + (from > lo ? 0 : 1)) * (BIG_FLOATS / 4) +
-                          (wave * 64 + i0 * 8) * 64 + lane;
+    const f32x4 *ws = reinterpret_cast<const f32x4 *>(p.ws) + (size_t)t * (BIG_FLOATS / 4) + (wave * 64 + i0 * 8) * 64 + lane;
+    for (int z = 0; z < p.splits; ++z) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 x[i][j] += ws[(i * 8 + j) * 64];
+        ws += (size_t)tail * (BIG_FLOATS / 4);
     }
-    const int tile = args.whole * p.grid + t;
+    const int tile = p.whole + t;
     const int b = tile / p.tiles;
     int tm, tn;
     dense_tile<EPI>(p, tile - b * p.tiles, tm, tn);

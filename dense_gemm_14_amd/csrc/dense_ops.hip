@@ -36,61 +36,46 @@ struct Shape {
     bool gated;
 };
 
-// K splits of a product on 128 x 128 tiles and the bytes of its partials. As
-// many splits as give every compute unit a tile, each at least kMinSteps K
-// steps long.
+// How a product runs on tiles of one size, in rounds of `grid` workgroups: the
+// first `whole` tiles one workgroup each, the K steps of the rest (fewer than a
+// round) split over as many workgroups as a round has.
 struct TilePlan {
-    int tiles_m, tiles_n, tiles, splits, steps_per_split;
-    size_t workspace_bytes;
-};
-constexpr int kMaxSplits = 16;
-constexpr int kMinSteps = 4;
-
-TilePlan plan_tile(const Shape &s, int cus)
-{
-    TilePlan t = {};
-    t.tiles_m = (int)ceil_div(s.M, d::TILE);
-    t.tiles_n = (int)ceil_div(s.N, s.gated ? d::TILE / 2 : d::TILE);
-    t.tiles = s.symmetric ? t.tiles_m * (t.tiles_m + 1) / 2 : t.tiles_m * t.tiles_n;
-    const int nk = (int)ceil_div(s.K, d::TILE_BK);
-    int64_t n = cus / std::max<int64_t>(1, int64_t(t.tiles) * s.batch);
-    n = std::max<int64_t>(1, std::min<int64_t>({n, kMaxSplits, nk / kMinSteps}));
-    t.steps_per_split = (int)std::max<int64_t>(1, ceil_div(nk, n));
-    t.splits = std::max(1, (int)ceil_div(nk, t.steps_per_split));
-    t.workspace_bytes = t.splits > 1 ? size_t(t.tiles) * s.batch * t.splits * d::TILE_FLOATS * sizeof(float) : 0;
-    return t;
-}
-
-// The 256 x 256 kernel's work: `whole` rounds of whole tiles on `grid`
-// workgroups, then `shared` tiles whose K steps are cut into one run per
-// workgroup (two partial tiles of workspace each).
-struct LargePlan {
-    int tiles_m, tiles_n, tiles, grid, whole, shared;
+    int tiles_m, tiles_n, tiles, grid, whole, splits, steps_per_split;
     size_t workspace_bytes;
     double steps;     // of the busiest workgroup
 };
-constexpr int kMinRun = 2 * d::CUT_MIN;   // fewest K steps of a run
+constexpr int kMaxSplits = 16;
 
-LargePlan plan_large(const Shape &s, int cus, bool share)
+TilePlan plan_tiles(const Shape &s, int side, int cus, int min_steps, bool split)
 {
-    LargePlan t = {};
-    t.tiles_m = (int)ceil_div(s.M, d::BIG);
-    t.tiles_n = (int)ceil_div(s.N, s.gated ? d::BIG / 2 : d::BIG);
+    TilePlan t = {};
+    t.tiles_m = (int)ceil_div(s.M, side);
+    t.tiles_n = (int)ceil_div(s.N, s.gated ? side / 2 : side);
     t.tiles = s.symmetric ? t.tiles_m * (t.tiles_m + 1) / 2 : t.tiles_m * t.tiles_n;
-    const int nk = (int)ceil_div(s.K, d::BIG_BK);
-    const int all = t.tiles * s.batch;
-    t.grid = gemm355::persistent_grid(all, cus);
-    t.whole = (int)ceil_div(all, t.grid);
-    t.steps = double(t.whole) * nk;
-    if (share && all % cus != 0) {
-        t.whole = std::max(0, all / cus - 1);
-        t.shared = all - t.whole * cus;
-        t.grid = t.whole > 0 ? cus : (int)std::min<int64_t>(cus, std::max<int64_t>(1, int64_t(t.shared) * nk / kMinRun));
-        t.workspace_bytes = size_t(t.grid) * 2 * d::BIG_FLOATS * sizeof(float);
-        t.steps = double(t.whole) * nk + double(t.shared) * nk / t.grid;
+    t.grid = std::max(8, cus & ~7);
+    const int nk = (int)ceil_div(s.K, d::TILE_BK);
+    const int all = t.tiles * s.batch, tail = all % t.grid;
+    t.whole = all;
+    t.splits = 1;
+    t.steps_per_split = nk;
+    if (split && tail > 0) {
+        int n = std::min({t.grid / tail, kMaxSplits, nk / min_steps});
+        // no part shorter than min_steps, the last one included
+        while (n > 1 && nk - ceil_div(nk, n) * (n - 1) < min_steps)
+            --n;
+        if (n > 1) {
+            t.splits = n;
+            t.steps_per_split = (int)ceil_div(nk, n);
+            t.whole = all - tail;
+            t.workspace_bytes = size_t(tail) * n * side * side * sizeof(float);
+        }
     }
+    t.steps = double(t.whole / t.grid) * nk + (all % t.grid != 0 ? t.steps_per_split : 0);
     return t;
 }
+
+TilePlan plan_tile(const Shape &s, int cus) { return plan_tiles(s, d::TILE, cus, 4, true); }
+TilePlan plan_large(const Shape &s, int cus, bool split) { return plan_tiles(s, d::BIG, cus, d::BIG_MIN_STEPS, split); }
 
 // The small-tile kernel's tile, in blocks of 16 rows of A and of B.
 struct SmallPlan {
@@ -113,36 +98,40 @@ SmallPlan plan_small(const Shape &s, bool layer)
 }
 
 // Which kernel runs a product: 1 = 256 x 256 tiles, 2 = the same with the last
-// tiles shared, 3 = 128 x 128 tiles, 4 = small tiles. Set through
+// round's tiles split, 3 = 128 x 128 tiles, 4 = small tiles. Set through
 // gemm355_force_layer_kernel (0 = by size).
 std::atomic<int> g_layer_kernel{0};
-enum { KERNEL_WHOLE = 1, KERNEL_SHARED = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4 };
+enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4 };
 
 // Measured on MI355X: a K step of a 256 x 256 tile, of a 128 x 128 tile with a
 // workgroup on every compute unit, and what a launch of each costs besides.
-constexpr double kBigStep = 1.45, kBigFixed = 8.0;
-constexpr double kTileStep = 0.55, kTileFixed = 4.0;
-constexpr double kShareFixed = 30.0;    // writing and adding the parts
+constexpr double kBigStep = 1.42, kBigFixed = 10.0;
+constexpr double kTileStep = 0.52, kTileFixed = 5.0;
+constexpr double kSplitFixed = 8.0, kSplitBytesPerUs = 2.5e6;    // a 256 x 256 split: the second launch, its parts
 constexpr double kReduceFixed = 4.0;
 constexpr double kSmallSlice = 0.8, kSmallFixed = 3.0;
 
 int choose_kernel(const Shape &s, bool layer, int cus)
 {
     const int nk = (int)ceil_div(s.K, d::BIG_BK);
-    const bool big_ok = nk >= d::CUT_MIN;
+    const bool big_ok = nk >= d::BIG_MIN_STEPS;
     const int forced = g_layer_kernel.load(std::memory_order_relaxed);
     if (forced != 0)
-        return forced <= KERNEL_SHARED && !big_ok ? KERNEL_TILE : forced;
+        return forced <= KERNEL_SPLIT && !big_ok ? KERNEL_TILE : forced;
     const SmallPlan q = plan_small(s, layer);
     const double small = double(ceil_div(int64_t(q.tiles) * s.batch, cus)) *
                          (ceil_div(nk, d::SMALL_WAVES) * kSmallSlice + kSmallFixed);
     const TilePlan t = plan_tile(s, cus);
-    const int64_t items = int64_t(t.tiles) * t.splits * s.batch;
-    const double tile = ceil_div(items, cus) * t.steps_per_split * kTileStep + kTileFixed + (t.splits > 1 ? kReduceFixed : 0);
-    const double whole = big_ok ? plan_large(s, cus, false).steps * kBigStep + kBigFixed : 1e30;
-    const double shared = big_ok ? plan_large(s, cus, true).steps * kBigStep + kBigFixed + kShareFixed : 1e30;
-    const double best = std::min({small, tile, whole, shared});
-    return best == small ? KERNEL_SMALL : best == tile ? KERNEL_TILE : best == whole ? KERNEL_WHOLE : KERNEL_SHARED;
+    const double tile = t.steps * kTileStep + kTileFixed + (t.splits > 1 ? kReduceFixed : 0);
+    double whole = 1e30, split = 1e30;
+    if (big_ok) {
+        whole = plan_large(s, cus, false).steps * kBigStep + kBigFixed;
+        const TilePlan b = plan_large(s, cus, true);
+        if (b.splits > 1)
+            split = b.steps * kBigStep + kBigFixed + kSplitFixed + double(b.workspace_bytes) / kSplitBytesPerUs;
+    }
+    const double best = std::min({small, tile, whole, split});
+    return best == small ? KERNEL_SMALL : best == tile ? KERNEL_TILE : best == whole ? KERNEL_WHOLE : KERNEL_SPLIT;
 }
 
 size_t product_workspace(const Shape &s, bool layer, int cus)
@@ -177,46 +166,44 @@ int product_small(DenseArgs p, const SmallPlan &t, hipStream_t stream)
     return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4>, blocks, threads, p, stream);
 }
 
-template <class T, int LA, int LB, int EPI, class TO>
-int product_tile(DenseArgs p, const Shape &s, int cus, hipStream_t stream)
+void set_plan(DenseArgs &p, const TilePlan &t)
 {
-    const TilePlan t = plan_tile(s, cus);
     p.tiles_m = t.tiles_m;
     p.tiles_n = t.tiles_n;
     p.tiles = t.tiles;
+    p.grid = t.grid;
+    p.whole = t.whole;
     p.splits = t.splits;
     p.steps_per_split = t.steps_per_split;
-    const int64_t items = int64_t(t.tiles) * t.splits * p.batch;
-    if (items > (int64_t(1) << 28))
-        return GEMM355_ERR_UNSUPPORTED;
-    int st = launch_kernel(d::dense_tile_kernel<T, LA, LB, EPI, TO>, (unsigned)(ceil_div(items, 8) * 8),
-                           (unsigned)d::TILE_THREADS, p, stream);
-    if (st == GEMM355_OK && t.splits > 1)
-        st = launch_kernel(d::dense_reduce_kernel<EPI, TO>,
-                           (unsigned)ceil_div(int64_t(t.tiles) * p.batch * 8, d::REDUCE_WAVES),
+}
+
+template <class T, int LA, int LB, int EPI, class TO>
+int product_tile(DenseArgs p, const TilePlan &t, hipStream_t stream)
+{
+    set_plan(p, t);
+    const int64_t tail = int64_t(t.tiles) * p.batch - t.whole, items = t.whole + tail * t.splits;
+    // whole rounds, then the last one's runs for each of the eight XCDs
+    const int64_t blocks = items / t.grid * t.grid + ceil_div(items % t.grid, 8) * 8;
+    int st = launch_kernel(d::dense_tile_kernel<T, LA, LB, EPI, TO>, (unsigned)blocks, (unsigned)d::TILE_THREADS, p, stream);
+    if (st == GEMM355_OK && tail > 0)
+        st = launch_kernel(d::dense_reduce_kernel<EPI, TO>, (unsigned)ceil_div(tail * 8, d::REDUCE_WAVES),
                            64u * d::REDUCE_WAVES, p, stream);
     return st;
 }
 
 template <class T, int LA, int LB, int EPI, class TO>
-int product_large(const DenseArgs &p, const Shape &s, int cus, bool share, hipStream_t stream)
+int product_large(DenseArgs p, const TilePlan &t, hipStream_t stream)
 {
-    const LargePlan t = plan_large(s, cus, share);
-    d::LargeArgs a = {};
-    a.d = p;
-    a.d.tiles_m = t.tiles_m;
-    a.d.tiles_n = t.tiles_n;
-    a.d.tiles = t.tiles;
-    a.d.grid = t.grid;
-    a.whole = t.whole;
-    a.shared = t.shared;
+    set_plan(p, t);
+    const int64_t tail = int64_t(t.tiles) * p.batch - t.whole;
+    // persistent: a workgroup per compute unit at most, each an item per round
+    p.grid = (int)std::min<int64_t>(t.grid, ceil_div(t.whole + tail * t.splits, 8) * 8);
     int st = p.K % d::BIG_BK != 0
-        ? launch_kernel(d::dense_large_kernel<T, LA, LB, EPI, TO, true>, (unsigned)t.grid, (unsigned)d::BIG_THREADS, a, stream)
-        : launch_kernel(d::dense_large_kernel<T, LA, LB, EPI, TO, false>, (unsigned)t.grid, (unsigned)d::BIG_THREADS, a, stream);
-    if (st == GEMM355_OK && t.shared > 0)
-        st = launch_kernel(d::dense_large_reduce_kernel<EPI, TO>,
-                           (unsigned)ceil_div(int64_t(t.shared) * 16, d::BIG_REDUCE_WAVES),
-                           64u * d::BIG_REDUCE_WAVES, a, stream);
+        ? launch_kernel(d::dense_large_kernel<T, LA, LB, EPI, TO, true>, (unsigned)p.grid, (unsigned)d::BIG_THREADS, p, stream)
+        : launch_kernel(d::dense_large_kernel<T, LA, LB, EPI, TO, false>, (unsigned)p.grid, (unsigned)d::BIG_THREADS, p, stream);
+    if (st == GEMM355_OK && tail > 0)
+        st = launch_kernel(d::dense_large_reduce_kernel<EPI, TO>, (unsigned)ceil_div(tail * 16, d::BIG_REDUCE_WAVES),
+                           64u * d::BIG_REDUCE_WAVES, p, stream);
     return st;
 }
 
@@ -233,8 +220,8 @@ int product(DenseArgs p, int cus, void *ws, hipStream_t stream)
     const int k = choose_kernel(s, LAYER, cus);
     if (k == KERNEL_SMALL)
         return product_small<T, LA, LB, EPI, TO>(p, plan_small(s, LAYER), stream);
-    return k == KERNEL_TILE ? product_tile<T, LA, LB, EPI, TO>(p, s, cus, stream)
-                            : product_large<T, LA, LB, EPI, TO>(p, s, cus, k == KERNEL_SHARED, stream);
+    return k == KERNEL_TILE ? product_tile<T, LA, LB, EPI, TO>(p, plan_tile(s, cus), stream)
+                            : product_large<T, LA, LB, EPI, TO>(p, plan_large(s, cus, k == KERNEL_SPLIT), stream);
 }
 
 DenseArgs args_of(int M, int N, int K, const void *a, const void *b, void *c)
@@ -659,7 +646,8 @@ extern "C" int gemm355_newton_schulz(int batch, int rows, int cols, int g_type, 
     if (any_overlap(out, 2, in, 1))
         return GEMM355_ERR_INVALID_ARG;
     if (!all_aligned(out, 2) || !all_aligned(in, 1) || rows % 8 != 0 || cols % 8 != 0 ||
-        !ortho_extents_ok(rows, cols) || batch > 65535)
+        !ortho_extents_ok(rows, cols) || batch > 65535 ||
+        int64_t(batch) * ceil_div(rows, 64) * ceil_div(cols, 64) > (int64_t(1) << 28))
         return GEMM355_ERR_UNSUPPORTED;
     int cus = 0;
     const int rc = compute_units(&cus);

@@ -20,9 +20,10 @@
 //     left before the last barrier, wait for this wave's copies of step s + 1,
 //     one barrier, then the 16 matrix instructions of step s with the reads of
 //     step s + 1 between them.
-//   * Split K: partials go to the workspace in the order of the registers (16
-//     bytes per lane and block), and a second kernel adds them in split order
-//     and runs the same epilogue: results do not depend on timing.
+//   * Split K: tiles that do not fill a round of workgroups are split over all
+//     of them. Their partials go to the workspace in the order of the registers
+//     (16 bytes per lane and block), and a second kernel adds them in split
+//     order and runs the same epilogue: results do not depend on timing.
 #pragma once
 
 #include "dense_common.hpp"
@@ -119,22 +120,15 @@ struct TileOperand {
 // Columns of C per tile.
 constexpr int tile_columns(int epi) { return epi == EPI_GATED ? TILE / 2 : TILE; }
 
-// Work item -> batch entry, split and output tile. Workgroups go to the eight
-// XCDs in turn; each XCD takes a run of consecutive items, so the tiles its L2
-// serves share operand strips.
-template <int EPI>
-__device__ inline bool tile_item(const DenseArgs &p, int &b, int &split, int &tm, int &tn, int &item)
+// Workgroup -> work item, or -1. Workgroups go to the eight XCDs in turn; in
+// every round each XCD takes a run of consecutive items, so the tiles its L2
+// serves at one time share operand strips.
+__device__ inline int tile_item(const DenseArgs &p)
 {
-    const int items = p.tiles * p.splits * p.batch;
-    const int run = (items + 7) / 8;
-    item = ((int)blockIdx.x & 7) * run + ((int)blockIdx.x >> 3);
-    if ((int)blockIdx.x >> 3 >= run || item >= items)
-        return false;
-    b = item / (p.tiles * p.splits);
-    const int r = item - b * p.tiles * p.splits;
-    split = r / p.tiles;
-    dense_tile<EPI>(p, r - split * p.tiles, tm, tn);
-    return true;
+    const int round = (int)blockIdx.x / p.grid, i = (int)blockIdx.x - round * p.grid;
+    const int count = min(p.grid, work_items(p) - round * p.grid), run = (count + 7) / 8;
+    const int at = (i & 7) * run + (i >> 3);
+    return (i >> 3) < run && at < count ? round * p.grid + at : -1;
 }
 
 // Epilogue of block rows i0 and i0 + 1 of wave (wm, wn) of a tile.
@@ -172,9 +166,14 @@ void dense_tile_kernel(DenseArgs p)
     const int wm = wave & 1;         // 64-row half of the tile
     const int wn = (wave >> 1) & 1;  // 64-column half
 
-    int b, split, tm, tn, item;
-    if (!tile_item<EPI>(p, b, split, tm, tn, item))
+    const int item = tile_item(p);
+    if (item < 0)
         return;
+    const WorkItem w = work_item(p, item);
+    const bool parts = w.tile >= p.whole && p.splits > 1;
+    const int b = w.tile / p.tiles;
+    int tm, tn;
+    dense_tile<EPI>(p, w.tile - b * p.tiles, tm, tn);
     if (p.batch > 1)
         enter_batch(p, b);
 
@@ -185,8 +184,8 @@ void dense_tile_kernel(DenseArgs p)
     ob.init(p.b, p.N, tn * tile_columns(EPI), p.K, p.N, lds_base + TILE_STAGES * TILE_UNIT, wave, lane, wn, kh);
 
     const int nk = (p.K + TILE_BK - 1) / TILE_BK;
-    const int first = split * p.steps_per_split;
-    const int steps = max(0, min(p.steps_per_split, nk - first));
+    const int first = parts ? w.split * p.steps_per_split : 0;
+    const int steps = parts ? max(0, min(p.steps_per_split, nk - first)) : nk;
 
     auto copies = [&](int s) {
         const unsigned slot = (unsigned)(s % TILE_STAGES) * TILE_UNIT;
@@ -265,10 +264,10 @@ void dense_tile_kernel(DenseArgs p)
         for (int j = 0; j < 4; ++j)
             out[i][j] += xch[slot_of(kh, i, j)];
 
-    if (p.splits > 1) {
+    if (parts) {
         // partial tile, in register order: block row u = 2 kh + i of wave
         // (wm, wn) is the run [pair][u][j][lane]
-        f32x4 *ws = reinterpret_cast<f32x4 *>(p.ws) + (size_t)item * (TILE_FLOATS / 4);
+        f32x4 *ws = reinterpret_cast<f32x4 *>(p.ws) + (size_t)(item - p.whole) * (TILE_FLOATS / 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -287,15 +286,14 @@ __global__ __launch_bounds__(64 * REDUCE_WAVES) void dense_reduce_kernel(DenseAr
 {
     const int lane = threadIdx.x & 63;
     const int unit = (int)blockIdx.x * REDUCE_WAVES + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int entry = unit >> 3;            // tile of a batch entry
-    if (entry >= p.tiles * p.batch)
+    const int tail = p.tiles * p.batch - p.whole, q = unit >> 3;
+    if (q >= tail)
         return;
-    const int b = entry / p.tiles, tile = entry - b * p.tiles;
+    const int b = (p.whole + q) / p.tiles;
     const int pair = (unit >> 1) & 3, i0 = 2 * (unit & 1);
     int tm, tn;
-    dense_tile<EPI>(p, tile, tm, tn);
-    const f32x4 *ws = reinterpret_cast<const f32x4 *>(p.ws) +
-                      ((size_t)b * p.splits * p.tiles + tile) * (TILE_FLOATS / 4) + ((pair * 4 + i0) * 4) * 64 + lane;
+    dense_tile<EPI>(p, p.whole + q - b * p.tiles, tm, tn);
+    const f32x4 *ws = reinterpret_cast<const f32x4 *>(p.ws) + (size_t)q * (TILE_FLOATS / 4) + ((pair * 4 + i0) * 4) * 64 + lane;
     f32x4 x[2][4] = {};
     for (int z = 0; z < p.splits; ++z) {
 #pragma unroll
@@ -303,7 +301,7 @@ __global__ __launch_bounds__(64 * REDUCE_WAVES) void dense_reduce_kernel(DenseAr
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 x[i][j] += ws[(i * 4 + j) * 64];
-        ws += (size_t)p.tiles * (TILE_FLOATS / 4);
+        ws += (size_t)tail * (TILE_FLOATS / 4);
     }
     if (p.batch > 1)
         enter_batch(p, b);

@@ -1,4 +1,4 @@
-"""Every kernel of the layer calls' products, forced in turn: whole and shared
+"""Every kernel of the layer calls' products, forced in turn: whole and split
 256 x 256 tiles and 128 x 128 tiles give the right values at sizes that cross
 their borders, in every layout, with one tile and with several rounds of them."""
 import pytest
@@ -10,10 +10,10 @@ from tests.gpu_util import need_gpu
 from tests.test_gpu_dense import dev, gen_of, ortho_exact, run_backward, run_forward, run_ortho
 
 pytestmark = pytest.mark.gpu
-KERNELS = [g.LAYER_LARGE, g.LAYER_SHARED, g.LAYER_TILE, g.LAYER_SMALL]
+KERNELS = [g.LAYER_LARGE, g.LAYER_SPLIT, g.LAYER_TILE, g.LAYER_SMALL]
 
 
-@pytest.fixture(params=KERNELS, ids=["large", "shared", "tile", "small"])
+@pytest.fixture(params=KERNELS, ids=["large", "split", "tile", "small"])
 def kernel(request):
     need_gpu()
     g.force_layer_kernel(request.param)
