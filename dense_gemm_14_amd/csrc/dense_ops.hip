@@ -103,13 +103,33 @@ SmallPlan plan_small(const Shape &s, bool layer)
 std::atomic<int> g_layer_kernel{0};
 enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4 };
 
-// Measured on MI355X: a K step of a 256 x 256 tile, of a 128 x 128 tile with a
-// workgroup on every compute unit, and what a launch of each costs besides.
-constexpr double kBigStep = 1.42, kBigFixed = 10.0;
-constexpr double kTileStep = 0.52, kTileFixed = 5.0;
-constexpr double kSplitFixed = 8.0, kSplitBytesPerUs = 2.5e6;    // a 256 x 256 split: the second launch, its parts
-constexpr double kReduceFixed = 4.0;
-constexpr double kSmallSlice = 0.8, kSmallFixed = 3.0;
+// Estimated microseconds of each kernel, fitted to 1000 products measured on
+// MI355X (M from 1, N and K from 64 to 8192, forward layers and both gradient
+// products; a typical estimate is 10 % off, and the choice by them costs 2 %
+// over the best kernel of every product).
+//   small tiles: per K slice of a wave, a wait that the ring's stages share and
+//     the traffic, by the tile's width and how many units are busy;
+//   128 and 256: per K step, part of it only when every unit is busy; per round
+//     the tiles' beginning and end; for a split the second launch and its
+//     partials (MB).
+double time_small(const SmallPlan &t, int nk, int batch, int cus)
+{
+    const double tiles = double(t.tiles) * batch, fill = std::min(1.0, tiles / cus);
+    const double width = (t.mb + t.nb) / 8.0, stages = d::small_stages(t.mb, t.nb);
+    return 3.2 + ceil(tiles / cus) * (1.5 + double(ceil_div(nk, d::SMALL_WAVES)) * (1.1 / stages + width * fill));
+}
+struct TileTimes {
+    double fixed, step, step_full, round, split, split_mb;
+};
+constexpr TileTimes kTile = {2.3, 0.35, 0.19, 4.6, 4.0, 0.42}, kBig = {1.1, 1.19, 0.41, 10.9, 0.0, 0.0},
+                    kBigSplit = {0.9, 1.30, 0.0, 15.0, 0.9, 0.33};
+double time_tiles(const TilePlan &t, int batch, const TileTimes &c)
+{
+    const int64_t items = t.whole + (int64_t(t.tiles) * batch - t.whole) * t.splits;
+    const double fill = std::min(1.0, double(items) / t.grid);
+    return c.fixed + t.steps * (c.step + c.step_full * fill) + double(ceil_div(items, t.grid)) * c.round +
+           (t.splits > 1 ? c.split + c.split_mb * 1e-6 * double(t.workspace_bytes) : 0.0);
+}
 
 int choose_kernel(const Shape &s, bool layer, int cus)
 {
@@ -118,17 +138,14 @@ int choose_kernel(const Shape &s, bool layer, int cus)
     const int forced = g_layer_kernel.load(std::memory_order_relaxed);
     if (forced != 0)
         return forced <= KERNEL_SPLIT && !big_ok ? KERNEL_TILE : forced;
-    const SmallPlan q = plan_small(s, layer);
-    const double small = double(ceil_div(int64_t(q.tiles) * s.batch, cus)) *
-                         (ceil_div(nk, d::SMALL_WAVES) * kSmallSlice + kSmallFixed);
-    const TilePlan t = plan_tile(s, cus);
-    const double tile = t.steps * kTileStep + kTileFixed + (t.splits > 1 ? kReduceFixed : 0);
+    const double small = time_small(plan_small(s, layer), nk, s.batch, cus);
+    const double tile = time_tiles(plan_tile(s, cus), s.batch, kTile);
     double whole = 1e30, split = 1e30;
     if (big_ok) {
-        whole = plan_large(s, cus, false).steps * kBigStep + kBigFixed;
+        whole = time_tiles(plan_large(s, cus, false), s.batch, kBig);
         const TilePlan b = plan_large(s, cus, true);
         if (b.splits > 1)
-            split = b.steps * kBigStep + kBigFixed + kSplitFixed + double(b.workspace_bytes) / kSplitBytesPerUs;
+            split = time_tiles(b, s.batch, kBigSplit);
     }
     const double best = std::min({small, tile, whole, split});
     return best == small ? KERNEL_SMALL : best == tile ? KERNEL_TILE : best == whole ? KERNEL_WHOLE : KERNEL_SPLIT;
