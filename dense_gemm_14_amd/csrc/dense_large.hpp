@@ -439,6 +439,7 @@ __global__ __launch_bounds__(64 * BIG_REDUCE_WAVES) void dense_large_reduce_kern
     const int wave = (unit >> 2) & 3, i0 = 2 * (unit & 3);
     f32x4 x[2][8] = {};
     const f32x4 *ws = reinterpret_cast<const f32x4 *>(p.ws) + (size_t)t * (BIG_FLOATS / 4) + (wave * 64 + i0 * 8) * 64 + lane;
+#pragma unroll 2
     for (int z = 0; z < p.splits; ++z) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)

@@ -82,14 +82,15 @@ struct SmallPlan {
     int mb, nb, tiles_m, tiles_n, tiles;
 };
 
-// Few tokens (forward layers only): 16 or 32 rows against narrow tiles, so
-// that every compute unit streams weights; otherwise 64 x 64.
-SmallPlan plan_small(const Shape &s, bool layer)
+// 64 x 64 tiles, or narrow ones: 32 x 32, and for the few tokens of a forward
+// layer 16 or 32 rows against 16 columns (16 gate and 16 up rows of a gated
+// layer), so that every compute unit streams weights.
+SmallPlan plan_small(const Shape &s, bool layer, bool narrow)
 {
     SmallPlan t = {4, 4, 0, 0, 0};
-    if (layer && s.M <= 32) {
-        t.mb = s.M <= 16 ? 1 : 2;
-        t.nb = s.gated ? 2 : 1;
+    if (narrow) {
+        t.mb = layer && s.M <= 16 ? 1 : 2;
+        t.nb = layer && s.M <= 32 && !s.gated ? 1 : 2;
     }
     t.tiles_m = (int)ceil_div(s.M, 16 * t.mb);
     t.tiles_n = (int)ceil_div(s.N, s.gated ? 8 * t.nb : 16 * t.nb);
@@ -98,10 +99,10 @@ SmallPlan plan_small(const Shape &s, bool layer)
 }
 
 // Which kernel runs a product: 1 = 256 x 256 tiles, 2 = the same with the last
-// round's tiles split, 3 = 128 x 128 tiles, 4 = small tiles. Set through
-// gemm355_force_layer_kernel (0 = by size).
+// round's tiles split, 3 = 128 x 128 tiles, 4 = 64 x 64 tiles, 5 = narrow
+// tiles. Set through gemm355_force_layer_kernel (0 = by size).
 std::atomic<int> g_layer_kernel{0};
-enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4 };
+enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4, KERNEL_NARROW = 5 };
 
 // Estimated microseconds of each kernel, fitted to 1000 products measured on
 // MI355X (M from 1, N and K from 64 to 8192, forward layers and both gradient
@@ -131,38 +132,39 @@ double time_tiles(const TilePlan &t, int batch, const TileTimes &c)
            (t.splits > 1 ? c.split + c.split_mb * 1e-6 * double(t.workspace_bytes) : 0.0);
 }
 
-int choose_kernel(const Shape &s, bool layer, int cus)
+struct Choice {
+    int kernel;
+    double us;
+};
+Choice choose_kernel(const Shape &s, bool layer, int cus)
 {
     const int nk = (int)ceil_div(s.K, d::BIG_BK);
     const bool big_ok = nk >= d::BIG_MIN_STEPS;
     const int forced = g_layer_kernel.load(std::memory_order_relaxed);
     if (forced != 0)
-        return forced <= KERNEL_SPLIT && !big_ok ? KERNEL_TILE : forced;
-    const double small = time_small(plan_small(s, layer), nk, s.batch, cus);
-    const double tile = time_tiles(plan_tile(s, cus), s.batch, kTile);
-    double whole = 1e30, split = 1e30;
+        return {forced <= KERNEL_SPLIT && !big_ok ? KERNEL_TILE : forced, 0.0};
+    Choice best = {KERNEL_TILE, time_tiles(plan_tile(s, cus), s.batch, kTile)};
+    auto offer = [&](int kernel, double us) {
+        if (us < best.us)
+            best = {kernel, us};
+    };
+    offer(KERNEL_SMALL, time_small(plan_small(s, layer, false), nk, s.batch, cus));
+    offer(KERNEL_NARROW, time_small(plan_small(s, layer, true), nk, s.batch, cus));
     if (big_ok) {
-        whole = time_tiles(plan_large(s, cus, false), s.batch, kBig);
+        offer(KERNEL_WHOLE, time_tiles(plan_large(s, cus, false), s.batch, kBig));
         const TilePlan b = plan_large(s, cus, true);
         if (b.splits > 1)
-            split = time_tiles(b, s.batch, kBigSplit);
+            offer(KERNEL_SPLIT, time_tiles(b, s.batch, kBigSplit));
     }
-    const double best = std::min({small, tile, whole, split});
-    return best == small ? KERNEL_SMALL : best == tile ? KERNEL_TILE : best == whole ? KERNEL_WHOLE : KERNEL_SPLIT;
+    return best;
 }
 
 size_t product_workspace(const Shape &s, bool layer, int cus)
 {
-    switch (choose_kernel(s, layer, cus)) {
-    case KERNEL_SMALL: return 0;
-    case KERNEL_TILE: return plan_tile(s, cus).workspace_bytes;
-    case KERNEL_WHOLE: return 0;
-    default: return plan_large(s, cus, true).workspace_bytes;
-    }
+    const int k = choose_kernel(s, layer, cus).kernel;
+    return k == KERNEL_TILE ? plan_tile(s, cus).workspace_bytes : k == KERNEL_SPLIT ? plan_large(s, cus, true).workspace_bytes : 0;
 }
 
-// The small-tile instances: every tile shape for the forward layers, 64 x 64
-// for the other products.
 template <class T, int LA, int LB, int EPI, class TO>
 int product_small(DenseArgs p, const SmallPlan &t, hipStream_t stream)
 {
@@ -173,14 +175,17 @@ int product_small(DenseArgs p, const SmallPlan &t, hipStream_t stream)
     if (items > (int64_t(1) << 28))
         return GEMM355_ERR_UNSUPPORTED;
     const unsigned blocks = (unsigned)(ceil_div(items, 8) * 8), threads = d::SMALL_THREADS;
-    if constexpr (EPI == d::EPI_LINEAR || EPI == d::EPI_GATED) {
-        constexpr int NARROW = EPI == d::EPI_GATED ? 2 : 1;
-        if (t.mb == 1)
-            return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, NARROW>, blocks, threads, p, stream);
-        if (t.mb == 2)
-            return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, NARROW>, blocks, threads, p, stream);
+    if constexpr (EPI == d::EPI_LINEAR) {
+        if (t.nb == 1)
+            return t.mb == 1 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 1>, blocks, threads, p, stream)
+                             : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 1>, blocks, threads, p, stream);
     }
-    return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4>, blocks, threads, p, stream);
+    if constexpr (EPI == d::EPI_GATED) {
+        if (t.mb == 1)
+            return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 2>, blocks, threads, p, stream);
+    }
+    return t.mb == 2 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 2>, blocks, threads, p, stream)
+                     : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4>, blocks, threads, p, stream);
 }
 
 void set_plan(DenseArgs &p, const TilePlan &t)
@@ -234,9 +239,9 @@ int product(DenseArgs p, int cus, void *ws, hipStream_t stream)
     p.supergroup = 8;
     p.ws = static_cast<float *>(ws);
     constexpr bool LAYER = EPI == d::EPI_LINEAR || EPI == d::EPI_GATED;
-    const int k = choose_kernel(s, LAYER, cus);
-    if (k == KERNEL_SMALL)
-        return product_small<T, LA, LB, EPI, TO>(p, plan_small(s, LAYER), stream);
+    const int k = choose_kernel(s, LAYER, cus).kernel;
+    if (k == KERNEL_SMALL || k == KERNEL_NARROW)
+        return product_small<T, LA, LB, EPI, TO>(p, plan_small(s, LAYER, k == KERNEL_NARROW), stream);
     return k == KERNEL_TILE ? product_tile<T, LA, LB, EPI, TO>(p, plan_tile(s, cus), stream)
                             : product_large<T, LA, LB, EPI, TO>(p, plan_large(s, cus, k == KERNEL_SPLIT), stream);
 }
@@ -380,13 +385,14 @@ BackwardPlan plan_backward(int M, int N, int K, bool gated, int act, int cus)
     return w;
 }
 
-// What is wanted of a small backward pass, in one launch.
+// A backward pass whose products are small, in one launch. `narrow`: 32 x 32
+// tiles.
 int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const d::BiasArgs &bias, int bias_blocks,
-                   hipStream_t s)
+                   bool narrow, hipStream_t s)
 {
     d::SmallBwdArgs g = {};
-    auto place = [](DenseArgs &p, bool wanted) {
-        const SmallPlan t = plan_small({p.M, p.N, p.K, 1, false, false}, false);
+    auto place = [&](DenseArgs &p, bool wanted) {
+        const SmallPlan t = plan_small({p.M, p.N, p.K, 1, false, false}, false, narrow);
         p.tiles_m = t.tiles_m;
         p.tiles_n = t.tiles_n;
         p.tiles = wanted ? t.tiles : 0;
@@ -401,7 +407,39 @@ int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const
     const int64_t items = int64_t(pa.tiles) + pb.tiles + bias_blocks;
     if (items > (int64_t(1) << 28))
         return GEMM355_ERR_UNSUPPORTED;
-    return launch_kernel(d::dense_small_bwd_kernel, (unsigned)(ceil_div(items, 8) * 8), (unsigned)d::SMALL_THREADS, g, s);
+    const unsigned blocks = (unsigned)(ceil_div(items, 8) * 8), threads = d::SMALL_THREADS;
+    return narrow ? launch_kernel(d::dense_small_bwd_kernel<2>, blocks, threads, g, s)
+                  : launch_kernel(d::dense_small_bwd_kernel<4>, blocks, threads, g, s);
+}
+
+// Whether a backward pass runs as one launch of small tiles (KERNEL_SMALL or
+// KERNEL_NARROW; 0: its products one by one). Together its tiles fill the
+// compute units better and two launches of about 3 us fall away; what they
+// take together is estimated as the sum of both without the second's start.
+constexpr double kLaunches = 6.0, kStart = 3.2;
+int backward_together(const Shape &a, bool wants_a, const Shape &b, bool wants_b, int cus)
+{
+    const int forced = g_layer_kernel.load(std::memory_order_relaxed);
+    if (forced != 0)
+        return forced >= KERNEL_SMALL ? forced : 0;
+    double apart = wants_a && wants_b ? kLaunches : 0.5 * kLaunches;
+    if (wants_a)
+        apart += choose_kernel(a, false, cus).us;
+    if (wants_b)
+        apart += choose_kernel(b, false, cus).us;
+    int best = 0;
+    for (const int k : {KERNEL_SMALL, KERNEL_NARROW}) {
+        double us = kStart;
+        if (wants_a)
+            us += time_small(plan_small(a, false, k == KERNEL_NARROW), (int)ceil_div(a.K, d::BIG_BK), 1, cus) - kStart;
+        if (wants_b)
+            us += time_small(plan_small(b, false, k == KERNEL_NARROW), (int)ceil_div(b.K, d::BIG_BK), 1, cus) - kStart;
+        if (us < apart) {
+            apart = us;
+            best = k;
+        }
+    }
+    return best;
 }
 
 template <bool GATED>
@@ -462,8 +500,9 @@ int layer_backward(int M, int N, int K, const void *A, const void *B, const void
     const DenseArgs pa = args_of(M, K, (int)rows, dz, B, dA);          // dA = dZ B
     const DenseArgs pb = args_of((int)rows, K, M, dz, A, dB);          // dB = dZ^T A
     const Shape sa = {M, K, (int)rows, 1, false, false}, sb = {(int)rows, K, M, 1, false, false};
-    if ((!wants_a || choose_kernel(sa, false, cus) == KERNEL_SMALL) && (!wants_b || choose_kernel(sb, false, cus) == KERNEL_SMALL))
-        return backward_small(pa, wants_a, pb, wants_b, q, bias_blocks, s);
+    const int together = backward_together(sa, wants_a, sb, wants_b, cus);
+    if (together != 0)
+        return backward_small(pa, wants_a, pb, wants_b, q, bias_blocks, together == KERNEL_NARROW, s);
     if (wants_bias) {
         const int st = launch_kernel(d::dense_bias_kernel, (unsigned)bias_blocks, (unsigned)d::BIAS_THREADS, q, s);
         if (st != GEMM355_OK)
@@ -579,7 +618,7 @@ bool ortho_extents_ok(int64_t rows, int64_t cols)
 
 extern "C" int gemm355_force_layer_kernel(int kernel)
 {
-    if (kernel < 0 || kernel > KERNEL_SMALL)
+    if (kernel < 0 || kernel > KERNEL_NARROW)
         return GEMM355_ERR_INVALID_ARG;
     g_layer_kernel.store(kernel, std::memory_order_relaxed);
     return GEMM355_OK;

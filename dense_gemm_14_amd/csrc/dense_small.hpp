@@ -14,9 +14,9 @@
 //   * The eight partial tiles meet in LDS (rows padded by 16 bytes: sixteen rows'
 //     16-byte writes fall into 64 different banks), are added in wave order, and
 //     each thread finishes eight consecutive columns of a row.
-//   * Tiles: 64 x 64 for small layers; 16 or 32 rows for few tokens, where a
-//     narrow tile (16 columns of weights, 32 with both halves of a gated layer)
-//     gives every compute unit weights to stream.
+//   * Tiles: 64 x 64; 32 x 32 where those leave compute units idle; for few tokens
+//     16 or 32 rows against 16 columns of weights (16 + 16 of a gated layer), so
+//     that every compute unit has weights to stream.
 #pragma once
 
 #include "dense_common.hpp"
@@ -348,26 +348,27 @@ struct SmallBwdArgs {
     int bias_blocks;
 };
 
+template <int BLOCKS>
 __global__ __launch_bounds__(SMALL_THREADS, 1) void dense_small_bwd_kernel(SmallBwdArgs p)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[small_lds(4, 4)];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[small_lds(BLOCKS, BLOCKS)];
     const int item = small_item(p.a.tiles + p.b.tiles + p.bias_blocks);
     if (item < 0)
         return;
     int tm, tn;
     if (item < p.a.tiles) {
         dense_tile<EPI_STORE>(p.a, item, tm, tn);
-        small_tile<__bf16, ROW_K, COL_K, EPI_STORE, __bf16, 4, 4>(p.a, 0, tm, tn, lds);
+        small_tile<__bf16, ROW_K, COL_K, EPI_STORE, __bf16, BLOCKS, BLOCKS>(p.a, 0, tm, tn, lds);
     } else if (item < p.a.tiles + p.b.tiles) {
         dense_tile<EPI_STORE>(p.b, item - p.a.tiles, tm, tn);
-        small_tile<__bf16, COL_K, COL_K, EPI_STORE, __bf16, 4, 4>(p.b, 0, tm, tn, lds);
+        small_tile<__bf16, COL_K, COL_K, EPI_STORE, __bf16, BLOCKS, BLOCKS>(p.b, 0, tm, tn, lds);
     } else {
         bias_block(p.bias, item - p.a.tiles - p.b.tiles, reinterpret_cast<float *>(lds));
     }
 }
 
 static_assert(SMALL_THREADS == BIAS_THREADS, "the bias blocks share the launch");
-static_assert(64 * BIAS_PITCH * 4 <= small_lds(4, 4), "and its LDS");
+static_assert(64 * BIAS_PITCH * 4 <= small_lds(2, 2), "and its LDS");
 
 } // namespace dense
 } // namespace gemm355

@@ -295,6 +295,7 @@ __global__ __launch_bounds__(64 * REDUCE_WAVES) void dense_reduce_kernel(DenseAr
     dense_tile<EPI>(p, p.whole + q - b * p.tiles, tm, tn);
     const f32x4 *ws = reinterpret_cast<const f32x4 *>(p.ws) + (size_t)q * (TILE_FLOATS / 4) + ((pair * 4 + i0) * 4) * 64 + lane;
     f32x4 x[2][4] = {};
+#pragma unroll 4
     for (int z = 0; z < p.splits; ++z) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)

@@ -18,7 +18,7 @@ namespace gemm355 {
 namespace dense {
 
 constexpr int NS_THREADS = 256;
-constexpr int NS_BLOCKS = 256;   // workgroups (partial sums) per matrix at most
+constexpr int NS_BLOCKS = 1024;  // workgroups (partial sums) per matrix at most
 
 struct NormArgs {
     const void *g;       // batch matrices of `elements` each
@@ -84,7 +84,10 @@ template <bool FP32>
 __global__ __launch_bounds__(NS_THREADS) void ns_scale_kernel(NormArgs p)
 {
     const int b = (int)blockIdx.x / p.blocks, k = (int)blockIdx.x % p.blocks;
-    const double norm2 = block_sum((int)threadIdx.x < p.blocks ? p.partial[(size_t)b * p.blocks + threadIdx.x] : 0.0);
+    double mine = 0.0;
+    for (int i = threadIdx.x; i < p.blocks; i += NS_THREADS)
+        mine += p.partial[(size_t)b * p.blocks + i];
+    const double norm2 = block_sum(mine);
     const double below = sqrt(norm2) + p.eps;
     const double f = below > 0.0 ? p.scale / below : 0.0;   // a zero matrix stays zero
     for (int64_t at = ((int64_t)k * NS_THREADS + threadIdx.x) * 8; at < p.elements; at += (int64_t)p.blocks * NS_THREADS * 8) {
@@ -98,8 +101,6 @@ __global__ __launch_bounds__(NS_THREADS) void ns_scale_kernel(NormArgs p)
                   pack2<_Float16>(x[6], x[7])};
     }
 }
-
-static_assert(NS_BLOCKS <= NS_THREADS, "one thread reads one partial sum");
 
 } // namespace dense
 } // namespace gemm355
