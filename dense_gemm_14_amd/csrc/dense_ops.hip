@@ -104,7 +104,7 @@ SmallPlan plan_small(const Shape &s, bool layer, bool narrow)
 std::atomic<int> g_layer_kernel{0};
 enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4, KERNEL_NARROW = 5 };
 
-// Estimated microseconds of each kernel, fitted to 1000 products measured on
+// Estimated microseconds of each kernel, fitted to 1800 products measured on
 // MI355X (M from 1, N and K from 64 to 8192, forward layers and both gradient
 // products; a typical estimate is 10 % off, and the choice by them costs 2 %
 // over the best kernel of every product).
@@ -113,17 +113,22 @@ enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4, KE
 //   128 and 256: per K step, part of it only when every unit is busy; per round
 //     the tiles' beginning and end; for a split the second launch and its
 //     partials (MB).
+constexpr double kStart = 3.5;
+double time_small_tile(const SmallPlan &t, int nk, double fill)
+{
+    const double width = (t.mb + t.nb) / 8.0, stages = d::small_stages(t.mb, t.nb);
+    return 1.1 + double(ceil_div(nk, d::SMALL_WAVES)) * (1.05 / stages + 1.13 * width * fill);
+}
 double time_small(const SmallPlan &t, int nk, int batch, int cus)
 {
-    const double tiles = double(t.tiles) * batch, fill = std::min(1.0, tiles / cus);
-    const double width = (t.mb + t.nb) / 8.0, stages = d::small_stages(t.mb, t.nb);
-    return 3.2 + ceil(tiles / cus) * (1.5 + double(ceil_div(nk, d::SMALL_WAVES)) * (1.1 / stages + width * fill));
+    const double tiles = double(t.tiles) * batch;
+    return kStart + ceil(tiles / cus) * time_small_tile(t, nk, std::min(1.0, tiles / cus));
 }
 struct TileTimes {
     double fixed, step, step_full, round, split, split_mb;
 };
-constexpr TileTimes kTile = {2.3, 0.35, 0.19, 4.6, 4.0, 0.42}, kBig = {1.1, 1.19, 0.41, 10.9, 0.0, 0.0},
-                    kBigSplit = {0.9, 1.30, 0.0, 15.0, 0.9, 0.33};
+constexpr TileTimes kTile = {1.9, 0.43, 0.11, 4.6, 4.3, 0.51}, kBig = {4.8, 1.19, 0.41, 7.1, 0.0, 0.0},
+                    kBigSplit = {1.9, 1.30, 0.0, 13.1, 1.4, 0.33};
 double time_tiles(const TilePlan &t, int batch, const TileTimes &c)
 {
     const int64_t items = t.whole + (int64_t(t.tiles) * batch - t.whole) * t.splits;
@@ -143,7 +148,11 @@ Choice choose_kernel(const Shape &s, bool layer, int cus)
     const int forced = g_layer_kernel.load(std::memory_order_relaxed);
     if (forced != 0)
         return {forced <= KERNEL_SPLIT && !big_ok ? KERNEL_TILE : forced, 0.0};
-    Choice best = {KERNEL_TILE, time_tiles(plan_tile(s, cus), s.batch, kTile)};
+    // The symmetric products are FP16, whose 128 x 128 steps take 15 % longer
+    // than the BF16 ones of the fit (the 256 x 256 ones do not): 4096 x 4096
+    // orthogonalised in 1410 us on 256 x 256 tiles, in 1620 with 128 x 128 ones
+    // for the symmetric products.
+    Choice best = {KERNEL_TILE, time_tiles(plan_tile(s, cus), s.batch, kTile) * (s.symmetric ? 1.15 : 1.0)};
     auto offer = [&](int kernel, double us) {
         if (us < best.us)
             best = {kernel, us};
@@ -404,19 +413,20 @@ int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const
     g.b = pb;
     g.bias = bias;
     g.bias_blocks = bias_blocks;
+    g.first_b = pb.K > pa.K;
     const int64_t items = int64_t(pa.tiles) + pb.tiles + bias_blocks;
     if (items > (int64_t(1) << 28))
         return GEMM355_ERR_UNSUPPORTED;
-    const unsigned blocks = (unsigned)(ceil_div(items, 8) * 8), threads = d::SMALL_THREADS;
+    const unsigned blocks = (unsigned)items, threads = d::SMALL_THREADS;
     return narrow ? launch_kernel(d::dense_small_bwd_kernel<2>, blocks, threads, g, s)
                   : launch_kernel(d::dense_small_bwd_kernel<4>, blocks, threads, g, s);
 }
 
 // Whether a backward pass runs as one launch of small tiles (KERNEL_SMALL or
 // KERNEL_NARROW; 0: its products one by one). Together its tiles fill the
-// compute units better and two launches of about 3 us fall away; what they
-// take together is estimated as the sum of both without the second's start.
-constexpr double kLaunches = 6.0, kStart = 3.2;
+// compute units better and two launches of about 3 us fall away. Estimate: the
+// tiles' time shared out over the units, and no less than the longest tile.
+constexpr double kLaunches = 6.0;
 int backward_together(const Shape &a, bool wants_a, const Shape &b, bool wants_b, int cus)
 {
     const int forced = g_layer_kernel.load(std::memory_order_relaxed);
@@ -429,11 +439,13 @@ int backward_together(const Shape &a, bool wants_a, const Shape &b, bool wants_b
         apart += choose_kernel(b, false, cus).us;
     int best = 0;
     for (const int k : {KERNEL_SMALL, KERNEL_NARROW}) {
-        double us = kStart;
-        if (wants_a)
-            us += time_small(plan_small(a, false, k == KERNEL_NARROW), (int)ceil_div(a.K, d::BIG_BK), 1, cus) - kStart;
-        if (wants_b)
-            us += time_small(plan_small(b, false, k == KERNEL_NARROW), (int)ceil_div(b.K, d::BIG_BK), 1, cus) - kStart;
+        const SmallPlan ta = plan_small(a, false, k == KERNEL_NARROW), tb = plan_small(b, false, k == KERNEL_NARROW);
+        const double na = wants_a ? ta.tiles : 0, nb = wants_b ? tb.tiles : 0, fill = std::min(1.0, (na + nb) / cus);
+        const double one_a = time_small_tile(ta, (int)ceil_div(a.K, d::BIG_BK), fill);
+        const double one_b = time_small_tile(tb, (int)ceil_div(b.K, d::BIG_BK), fill);
+        const double longest = std::max(na > 0 ? one_a : 0.0, nb > 0 ? one_b : 0.0);
+        // (the last tiles end up to one short tile apart)
+        const double us = kStart + std::max(longest, (na * one_a + nb * one_b) / cus + 0.5 * std::min(one_a, one_b));
         if (us < apart) {
             apart = us;
             best = k;
