@@ -307,6 +307,8 @@ __device__ inline void load_bias_row(const DenseArgs &p, const Views &v, int col
 {
     if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED) {
         constexpr int H = EPI == EPI_GATED ? BJ / 2 : BJ;
+        if (!p.bias)
+            return;
 #pragma unroll
         for (int j = 0; j < BJ; ++j) {
             // EPI_GATED: the up columns' bias starts at N
@@ -345,9 +347,10 @@ __device__ inline void store_row(const DenseArgs &p, const Views &v, f32x4 (&x)[
     static_assert(BJ % 4 == 0, "blocks are stored in pairs");
     if constexpr (EPI == EPI_GATED) {
         constexpr int H = BJ / 2;
+        if (p.bias)
 #pragma unroll
-        for (int j = 0; j < BJ; ++j)
-            x[j] = add_bias(x[j], bias[j]);
+            for (int j = 0; j < BJ; ++j)
+                x[j] = add_bias(x[j], bias[j]);
         with_act(p.act, [&](auto act_c) {
             constexpr int ACT = decltype(act_c)::value;
 #pragma unroll
@@ -362,9 +365,10 @@ __device__ inline void store_row(const DenseArgs &p, const Views &v, f32x4 (&x)[
             }
         });
     } else if constexpr (EPI == EPI_LINEAR) {
+        if (p.bias)
 #pragma unroll
-        for (int j = 0; j < BJ; ++j)
-            x[j] = add_bias(x[j], bias[j]);
+            for (int j = 0; j < BJ; ++j)
+                x[j] = add_bias(x[j], bias[j]);
         with_act(p.act, [&](auto act_c) {
             constexpr int ACT = decltype(act_c)::value;
 #pragma unroll

@@ -84,13 +84,16 @@ struct SmallPlan {
 
 // 64 x 64 tiles, or narrow ones: 32 x 32, and for the few tokens of a forward
 // layer 16 or 32 rows against 16 columns (16 gate and 16 up rows of a gated
-// layer), so that every compute unit streams weights.
-SmallPlan plan_small(const Shape &s, bool layer, bool narrow)
+// layer), so that every compute unit streams weights; with 16 rows, as many
+// columns up to 64 as still leave a tile for every unit.
+SmallPlan plan_small(const Shape &s, bool layer, bool narrow, int cus)
 {
     SmallPlan t = {4, 4, 0, 0, 0};
     if (narrow) {
         t.mb = layer && s.M <= 16 ? 1 : 2;
         t.nb = layer && s.M <= 32 && !s.gated ? 1 : 2;
+        while (t.mb == 1 && t.nb < 4 && ceil_div(s.N, s.gated ? 16 * t.nb : 32 * t.nb) * s.batch >= cus)
+            t.nb *= 2;
     }
     t.tiles_m = (int)ceil_div(s.M, 16 * t.mb);
     t.tiles_n = (int)ceil_div(s.N, s.gated ? 8 * t.nb : 16 * t.nb);
@@ -157,8 +160,8 @@ Choice choose_kernel(const Shape &s, bool layer, int cus)
         if (us < best.us)
             best = {kernel, us};
     };
-    offer(KERNEL_SMALL, time_small(plan_small(s, layer, false), nk, s.batch, cus));
-    offer(KERNEL_NARROW, time_small(plan_small(s, layer, true), nk, s.batch, cus));
+    offer(KERNEL_SMALL, time_small(plan_small(s, layer, false, cus), nk, s.batch, cus));
+    offer(KERNEL_NARROW, time_small(plan_small(s, layer, true, cus), nk, s.batch, cus));
     if (big_ok) {
         offer(KERNEL_WHOLE, time_tiles(plan_large(s, cus, false), s.batch, kBig));
         const TilePlan b = plan_large(s, cus, true);
@@ -189,9 +192,10 @@ int product_small(DenseArgs p, const SmallPlan &t, hipStream_t stream)
             return t.mb == 1 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 1>, blocks, threads, p, stream)
                              : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 1>, blocks, threads, p, stream);
     }
-    if constexpr (EPI == d::EPI_GATED) {
+    if constexpr (EPI == d::EPI_LINEAR || EPI == d::EPI_GATED) {
         if (t.mb == 1)
-            return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 2>, blocks, threads, p, stream);
+            return t.nb == 2 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 2>, blocks, threads, p, stream)
+                             : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 4>, blocks, threads, p, stream);
     }
     return t.mb == 2 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 2>, blocks, threads, p, stream)
                      : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4>, blocks, threads, p, stream);
@@ -250,7 +254,7 @@ int product(DenseArgs p, int cus, void *ws, hipStream_t stream)
     constexpr bool LAYER = EPI == d::EPI_LINEAR || EPI == d::EPI_GATED;
     const int k = choose_kernel(s, LAYER, cus).kernel;
     if (k == KERNEL_SMALL || k == KERNEL_NARROW)
-        return product_small<T, LA, LB, EPI, TO>(p, plan_small(s, LAYER, k == KERNEL_NARROW), stream);
+        return product_small<T, LA, LB, EPI, TO>(p, plan_small(s, LAYER, k == KERNEL_NARROW, cus), stream);
     return k == KERNEL_TILE ? product_tile<T, LA, LB, EPI, TO>(p, plan_tile(s, cus), stream)
                             : product_large<T, LA, LB, EPI, TO>(p, plan_large(s, cus, k == KERNEL_SPLIT), stream);
 }
@@ -397,11 +401,11 @@ BackwardPlan plan_backward(int M, int N, int K, bool gated, int act, int cus)
 // A backward pass whose products are small, in one launch. `narrow`: 32 x 32
 // tiles.
 int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const d::BiasArgs &bias, int bias_blocks,
-                   bool narrow, hipStream_t s)
+                   bool narrow, int cus, hipStream_t s)
 {
     d::SmallBwdArgs g = {};
     auto place = [&](DenseArgs &p, bool wanted) {
-        const SmallPlan t = plan_small({p.M, p.N, p.K, 1, false, false}, false, narrow);
+        const SmallPlan t = plan_small({p.M, p.N, p.K, 1, false, false}, false, narrow, cus);
         p.tiles_m = t.tiles_m;
         p.tiles_n = t.tiles_n;
         p.tiles = wanted ? t.tiles : 0;
@@ -439,7 +443,7 @@ int backward_together(const Shape &a, bool wants_a, const Shape &b, bool wants_b
         apart += choose_kernel(b, false, cus).us;
     int best = 0;
     for (const int k : {KERNEL_SMALL, KERNEL_NARROW}) {
-        const SmallPlan ta = plan_small(a, false, k == KERNEL_NARROW), tb = plan_small(b, false, k == KERNEL_NARROW);
+        const SmallPlan ta = plan_small(a, false, k == KERNEL_NARROW, cus), tb = plan_small(b, false, k == KERNEL_NARROW, cus);
         const double na = wants_a ? ta.tiles : 0, nb = wants_b ? tb.tiles : 0, fill = std::min(1.0, (na + nb) / cus);
         const double one_a = time_small_tile(ta, (int)ceil_div(a.K, d::BIG_BK), fill);
         const double one_b = time_small_tile(tb, (int)ceil_div(b.K, d::BIG_BK), fill);
@@ -514,7 +518,7 @@ int layer_backward(int M, int N, int K, const void *A, const void *B, const void
     const Shape sa = {M, K, (int)rows, 1, false, false}, sb = {(int)rows, K, M, 1, false, false};
     const int together = backward_together(sa, wants_a, sb, wants_b, cus);
     if (together != 0)
-        return backward_small(pa, wants_a, pb, wants_b, q, bias_blocks, together == KERNEL_NARROW, s);
+        return backward_small(pa, wants_a, pb, wants_b, q, bias_blocks, together == KERNEL_NARROW, cus, s);
     if (wants_bias) {
         const int st = launch_kernel(d::dense_bias_kernel, (unsigned)bias_blocks, (unsigned)d::BIAS_THREADS, q, s);
         if (st != GEMM355_OK)
