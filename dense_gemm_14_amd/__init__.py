@@ -89,7 +89,6 @@ LAYER_SPLIT = 2      # the same, K of the last round's tiles split
 LAYER_TILE = 3       # 128 x 128 output tiles
 LAYER_SMALL = 4      # 64 x 64 output tiles
 LAYER_NARROW = 5     # 32 x 32 and, for few tokens, narrower ones
-LAYER_WIDE = 6       # 256 x 128 output tiles
 SCHEDULE_STATIC = 0  # the NVFP4 kernel's tile order (gemm355_force_schedule)
 SCHEDULE_DYNAMIC = 1
 INSTANCE_SPLITK = 3  # 128 x 128 output tiles; with a workspace (the *_ws calls) K split over workgroups
@@ -604,8 +603,8 @@ def newton_schulz_workspace_size(batch: int, rows: int, cols: int) -> int:
 
 def force_layer_kernel(kernel: int) -> None:
     """Kernel of the layer calls' products for the whole process: LAYER_AUTO
-    (default), LAYER_LARGE, LAYER_SPLIT, LAYER_TILE, LAYER_SMALL,
-    LAYER_NARROW or LAYER_WIDE (a diagnostic)."""
+    (default), LAYER_LARGE, LAYER_SPLIT, LAYER_TILE, LAYER_SMALL or
+    LAYER_NARROW (a diagnostic)."""
     _check(load().gemm355_force_layer_kernel(int(kernel)), "gemm355_force_layer_kernel")
 
 

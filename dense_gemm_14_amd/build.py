@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(HERE, "libgemm355.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("gemm355.hip", "dense_ops.hip")]
 HEADERS = [os.path.join(CSRC, f) for f in ("common.hpp", "gemm_bf16.hpp", "gemm_bf16_small.hpp", "gemm_bf16_small_long.hpp", "gemm_bf16_splitk.hpp",
                                            "gemm_fp4.hpp", "fp4_decode.hpp", "gemm_mxfp4.hpp", "schedule.hpp", "host.hpp",
-                                           "dense_common.hpp", "dense_large.hpp", "dense_small.hpp", "dense_tile.hpp", "dense_wide.hpp", "dense_grad.hpp", "newton_schulz.hpp")] + \
+                                           "dense_common.hpp", "dense_large.hpp", "dense_small.hpp", "dense_tile.hpp", "dense_grad.hpp", "newton_schulz.hpp")] + \
     [os.path.join(INCLUDE, "gemm355.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -105,16 +105,6 @@ __device__ inline void copy_two(const i32x4 &rsrc, unsigned lds_addr, unsigned v
                  : "memory", "m0");
 }
 
-// One such copy.
-__device__ inline void copy_one(const i32x4 &rsrc, unsigned lds_addr, unsigned v)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
-                 "buffer_load_dwordx4 %1, %2, 0 offen offset:0 lds"
-                 :
-                 : "s"(lds_addr), "v"(v), "s"(rsrc)
-                 : "memory", "m0");
-}
-
 // LDS places of the 16-byte chunks of a 128-byte ROW_K row, and of the 32-byte
 // segments of a COL_K K row of 256 bytes or more.
 __device__ inline int swizzle_row(int r, int c) { return c ^ ((r >> 1) & 7); }

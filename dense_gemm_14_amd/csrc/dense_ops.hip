@@ -14,7 +14,6 @@
 #include "dense_large.hpp"
 #include "dense_small.hpp"
 #include "dense_tile.hpp"
-#include "dense_wide.hpp"
 #include "dense_grad.hpp"
 #include "newton_schulz.hpp"
 
@@ -47,16 +46,14 @@ struct TilePlan {
 };
 constexpr int kMaxSplits = 16;
 
-TilePlan plan_tiles(const Shape &s, int rows, int cols, int bk, int cus, int min_steps, bool split)
+TilePlan plan_tiles(const Shape &s, int side, int cus, int min_steps, bool split)
 {
     TilePlan t = {};
-    t.tiles_m = (int)ceil_div(s.M, rows);
-    t.tiles_n = (int)ceil_div(s.N, s.gated ? cols / 2 : cols);
-    t.tiles = t.tiles_m * t.tiles_n;
-    if (s.symmetric)   // square tiles, or twice as high as wide (the last row may lack its last tile)
-        t.tiles = rows == cols ? t.tiles_m * (t.tiles_m + 1) / 2 : t.tiles_m * (t.tiles_m + 1) - (2 * t.tiles_m - t.tiles_n);
+    t.tiles_m = (int)ceil_div(s.M, side);
+    t.tiles_n = (int)ceil_div(s.N, s.gated ? side / 2 : side);
+    t.tiles = s.symmetric ? t.tiles_m * (t.tiles_m + 1) / 2 : t.tiles_m * t.tiles_n;
     t.grid = std::max(8, cus & ~7);
-    const int nk = (int)ceil_div(s.K, bk);
+    const int nk = (int)ceil_div(s.K, d::TILE_BK);
     const int all = t.tiles * s.batch, tail = all % t.grid;
     t.whole = all;
     t.splits = 1;
@@ -70,19 +67,15 @@ TilePlan plan_tiles(const Shape &s, int rows, int cols, int bk, int cus, int min
             t.splits = n;
             t.steps_per_split = (int)ceil_div(nk, n);
             t.whole = all - tail;
-            t.workspace_bytes = size_t(tail) * n * rows * cols * sizeof(float);
+            t.workspace_bytes = size_t(tail) * n * side * side * sizeof(float);
         }
     }
     t.steps = double(t.whole / t.grid) * nk + (all % t.grid != 0 ? t.steps_per_split : 0);
     return t;
 }
 
-TilePlan plan_tile(const Shape &s, int cus) { return plan_tiles(s, d::TILE, d::TILE, d::TILE_BK, cus, 4, true); }
-TilePlan plan_wide(const Shape &s, int cus) { return plan_tiles(s, d::WIDE_M, d::WIDE_N, d::WIDE_BK, cus, 8, true); }
-TilePlan plan_large(const Shape &s, int cus, bool split)
-{
-    return plan_tiles(s, d::BIG, d::BIG, d::BIG_BK, cus, d::BIG_MIN_STEPS, split);
-}
+TilePlan plan_tile(const Shape &s, int cus) { return plan_tiles(s, d::TILE, cus, 4, true); }
+TilePlan plan_large(const Shape &s, int cus, bool split) { return plan_tiles(s, d::BIG, cus, d::BIG_MIN_STEPS, split); }
 
 // The small-tile kernel's tile, in blocks of 16 rows of A and of B.
 struct SmallPlan {
@@ -110,9 +103,9 @@ SmallPlan plan_small(const Shape &s, bool layer, bool narrow, int cus)
 
 // Which kernel runs a product: 1 = 256 x 256 tiles, 2 = the same with the last
 // round's tiles split, 3 = 128 x 128 tiles, 4 = 64 x 64 tiles, 5 = narrow
-// tiles, 6 = 256 x 128 tiles. Set through gemm355_force_layer_kernel (0 = by size).
+// tiles. Set through gemm355_force_layer_kernel (0 = by size).
 std::atomic<int> g_layer_kernel{0};
-enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4, KERNEL_NARROW = 5, KERNEL_WIDE = 6 };
+enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4, KERNEL_NARROW = 5 };
 
 // Estimated microseconds of each kernel, fitted to 1800 products measured on
 // MI355X (M from 1, N and K from 64 to 8192, forward layers and both gradient
@@ -181,10 +174,7 @@ Choice choose_kernel(const Shape &s, bool layer, int cus)
 size_t product_workspace(const Shape &s, bool layer, int cus)
 {
     const int k = choose_kernel(s, layer, cus).kernel;
-    return k == KERNEL_TILE    ? plan_tile(s, cus).workspace_bytes
-           : k == KERNEL_WIDE  ? plan_wide(s, cus).workspace_bytes
-           : k == KERNEL_SPLIT ? plan_large(s, cus, true).workspace_bytes
-                               : 0;
+    return k == KERNEL_TILE ? plan_tile(s, cus).workspace_bytes : k == KERNEL_SPLIT ? plan_large(s, cus, true).workspace_bytes : 0;
 }
 
 template <class T, int LA, int LB, int EPI, class TO>
@@ -222,20 +212,17 @@ void set_plan(DenseArgs &p, const TilePlan &t)
     p.steps_per_split = t.steps_per_split;
 }
 
-// A product on 128 x 128 (WIDE: 256 x 128) tiles.
-template <bool WIDE, class T, int LA, int LB, int EPI, class TO>
+template <class T, int LA, int LB, int EPI, class TO>
 int product_tile(DenseArgs p, const TilePlan &t, hipStream_t stream)
 {
     set_plan(p, t);
     const int64_t tail = int64_t(t.tiles) * p.batch - t.whole, items = t.whole + tail * t.splits;
     // whole rounds, then the last one's runs for each of the eight XCDs
     const int64_t blocks = items / t.grid * t.grid + ceil_div(items % t.grid, 8) * 8;
-    auto kernel = WIDE ? d::dense_wide_kernel<T, LA, LB, EPI, TO> : d::dense_tile_kernel<T, LA, LB, EPI, TO>;
-    int st = launch_kernel(kernel, (unsigned)blocks, (unsigned)(WIDE ? d::WIDE_THREADS : d::TILE_THREADS), p, stream);
-    if (st == GEMM355_OK && tail > 0) {
-        auto reduce = WIDE ? d::dense_wide_reduce_kernel<EPI, TO> : d::dense_reduce_kernel<EPI, TO>;
-        st = launch_kernel(reduce, (unsigned)ceil_div(tail * (WIDE ? 16 : 8), d::REDUCE_WAVES), 64u * d::REDUCE_WAVES, p, stream);
-    }
+    int st = launch_kernel(d::dense_tile_kernel<T, LA, LB, EPI, TO>, (unsigned)blocks, (unsigned)d::TILE_THREADS, p, stream);
+    if (st == GEMM355_OK && tail > 0)
+        st = launch_kernel(d::dense_reduce_kernel<EPI, TO>, (unsigned)ceil_div(tail * 8, d::REDUCE_WAVES),
+                           64u * d::REDUCE_WAVES, p, stream);
     return st;
 }
 
@@ -268,9 +255,8 @@ int product(DenseArgs p, int cus, void *ws, hipStream_t stream)
     const int k = choose_kernel(s, LAYER, cus).kernel;
     if (k == KERNEL_SMALL || k == KERNEL_NARROW)
         return product_small<T, LA, LB, EPI, TO>(p, plan_small(s, LAYER, k == KERNEL_NARROW, cus), stream);
-    return k == KERNEL_TILE   ? product_tile<false, T, LA, LB, EPI, TO>(p, plan_tile(s, cus), stream)
-           : k == KERNEL_WIDE ? product_tile<true, T, LA, LB, EPI, TO>(p, plan_wide(s, cus), stream)
-                              : product_large<T, LA, LB, EPI, TO>(p, plan_large(s, cus, k == KERNEL_SPLIT), stream);
+    return k == KERNEL_TILE ? product_tile<T, LA, LB, EPI, TO>(p, plan_tile(s, cus), stream)
+                            : product_large<T, LA, LB, EPI, TO>(p, plan_large(s, cus, k == KERNEL_SPLIT), stream);
 }
 
 DenseArgs args_of(int M, int N, int K, const void *a, const void *b, void *c)
@@ -449,7 +435,7 @@ int backward_together(const Shape &a, bool wants_a, const Shape &b, bool wants_b
 {
     const int forced = g_layer_kernel.load(std::memory_order_relaxed);
     if (forced != 0)
-        return forced == KERNEL_SMALL || forced == KERNEL_NARROW ? forced : 0;
+        return forced >= KERNEL_SMALL ? forced : 0;
     double apart = wants_a && wants_b ? kLaunches : 0.5 * kLaunches;
     if (wants_a)
         apart += choose_kernel(a, false, cus).us;
@@ -648,7 +634,7 @@ bool ortho_extents_ok(int64_t rows, int64_t cols)
 
 extern "C" int gemm355_force_layer_kernel(int kernel)
 {
-    if (kernel < 0 || kernel > KERNEL_WIDE)
+    if (kernel < 0 || kernel > KERNEL_NARROW)
         return GEMM355_ERR_INVALID_ARG;
     g_layer_kernel.store(kernel, std::memory_order_relaxed);
     return GEMM355_OK;

@@ -16,12 +16,10 @@
 //     K row k at s ^ key(k), key = k % 4 + 4 ((k >> 3) & 1): the eight K rows
 //     that half of a transposing read touches (0..3 and 8..11 of a group of
 //     sixteen) fall into eight different bank groups.
-//   * Step s: wait for this wave's copies of step s + 1, one barrier, then the 16
-//     matrix instructions of step s; between them the reads of step s + 1 and the
-//     copies of step s + 3, into the slot that every wave left before the last
-//     barrier. The copies are spread out because a compute unit takes one in 16
-//     cycles: issued together before the barrier, those of all waves kept the
-//     matrix cores waiting for as long as they worked.
+//   * Step s: issue the copies of step s + 3 into the slot that every wave
+//     left before the last barrier, wait for this wave's copies of step s + 1,
+//     one barrier, then the 16 matrix instructions of step s with the reads of
+//     step s + 1 between them.
 //   * Split K: tiles that do not fill a round of workgroups are split over all
 //     of them. Their partials go to the workspace in the order of the registers
 //     (16 bytes per lane and block), and a second kernel adds them in split
@@ -66,7 +64,7 @@ struct TileOperand {
     {
         const int l16 = lane & 15, grp = lane >> 4;
         const unsigned extent = (unsigned)(GATED ? 2 * gate_rows : rows) * (unsigned)K * 2u;
-        rsrc = rsrc_words(base, base ? extent : 0u);
+        rsrc = rsrc_words(static_cast<const uint8_t *>(base) - COPY_SHIFT, base ? extent + COPY_SHIFT : 0u);
         copy_lds = lds + (unsigned)(2048 * wave);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -75,12 +73,12 @@ struct TileOperand {
                 const int r = 8 * block + (lane >> 3);
                 const int c = swizzle_row(r, lane & 7);
                 const int row = GATED ? ((r & 32) ? gate_rows : 0) + row0 + 32 * (r >> 6) + (r & 31) : row0 + r;
-                off[t] = ((unsigned)row * (unsigned)K + 8u * (unsigned)c) * 2u;
+                off[t] = ((unsigned)row * (unsigned)K + 8u * (unsigned)c) * 2u + COPY_SHIFT - 1024u * t;
                 chunk_k[t] = 8 * c;   // rows past the operand lie past its range
             } else {
                 const int k = 4 * block + (lane >> 4), pos = lane & 15;
                 const int col = row0 + 8 * ((((pos >> 1) ^ key_col(k)) << 1) | (pos & 1));
-                off[t] = ((unsigned)k * (unsigned)rows + (unsigned)col) * 2u;
+                off[t] = ((unsigned)k * (unsigned)rows + (unsigned)col) * 2u + COPY_SHIFT - 1024u * t;
                 chunk_k[t] = col < rows ? 0 : NEVER;   // K rows past the operand lie past its range
             }
         }
@@ -95,12 +93,15 @@ struct TileOperand {
         }
     }
 
-    // This wave's copy t of K step `ks` into the unit at byte `slot` of the
-    // ring; zeros when !in.
-    __device__ inline void copy(int t, int ks, bool in, unsigned slot, int K) const
+    // This wave's copies of K step `ks` into the unit at byte `slot` of the
+    // ring; nothing but zeros when !in.
+    __device__ inline void copy(int ks, bool in, unsigned slot, int K) const
     {
-        const unsigned v = in && ks * TILE_BK + chunk_k[t] < K ? off[t] + (unsigned)ks * step : OFF_NONE;
-        copy_one(rsrc, __builtin_amdgcn_readfirstlane(copy_lds + slot + 1024u * t), v);
+        unsigned v[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            v[t] = in && ks * TILE_BK + chunk_k[t] < K ? off[t] + (unsigned)ks * step : OFF_NONE;
+        copy_two(rsrc, __builtin_amdgcn_readfirstlane(copy_lds + slot), v[0], v[1]);
     }
 
     // Fragment of block `blk` (16 rows) of this wave's half of the K step.
@@ -186,13 +187,10 @@ void dense_tile_kernel(DenseArgs p)
     const int first = parts ? w.split * p.steps_per_split : 0;
     const int steps = parts ? max(0, min(p.steps_per_split, nk - first)) : nk;
 
-    // Copy c of this wave's four (two of A, two of B) for step s.
-    auto copy = [&](int c, int s) {
+    auto copies = [&](int s) {
         const unsigned slot = (unsigned)(s % TILE_STAGES) * TILE_UNIT;
-        if (c < 2)
-            oa.copy(c, first + s, s < steps, slot, p.K);
-        else
-            ob.copy(c - 2, first + s, s < steps, slot, p.K);
+        oa.copy(first + s, s < steps, slot, p.K);
+        ob.copy(first + s, s < steps, slot, p.K);
     };
     f32x4 acc[4][4];
 #pragma unroll
@@ -204,8 +202,7 @@ void dense_tile_kernel(DenseArgs p)
 
     if (steps > 0) {
         for (int s = 0; s < TILE_STAGES - 1; ++s)
-            for (int c = 0; c < TILE_COPIES; ++c)
-                copy(c, s);
+            copies(s);
         wait_copies_le<TILE_COPIES * (TILE_STAGES - 2)>();
         lds_barrier();
 #pragma unroll
@@ -215,8 +212,9 @@ void dense_tile_kernel(DenseArgs p)
         }
         auto step = [&](int s, auto buf_c) {
             constexpr int buf = decltype(buf_c)::value;
+            copies(s + TILE_STAGES - 1);
             wait_reads();
-            wait_copies_le<TILE_COPIES * (TILE_STAGES - 3)>();
+            wait_copies_le<TILE_COPIES * (TILE_STAGES - 2)>();
             lds_barrier();
             SCHED_FENCE();
             const unsigned next = (unsigned)((s + 1) % TILE_STAGES) * TILE_UNIT;
@@ -231,8 +229,6 @@ void dense_tile_kernel(DenseArgs p)
                     else
                         fa[buf ^ 1][t >> 1] = oa.read(next, t >> 1);
                 }
-                if constexpr (t % 4 == 3)
-                    copy(t / 4, s + TILE_STAGES - 1);
                 SCHED_VALU_ONLY();
             });
         };

@@ -571,7 +571,7 @@ int gemm355_newton_schulz_workspace_size(int batch, int rows, int cols, size_t *
  * process-wide diagnostic for tests and measurements: 0 (the default) by size,
  * 1 = 256 x 256 tiles, 2 = the same with the K steps of the last round's tiles
  * split over the workgroups, 3 = 128 x 128 tiles, 4 = 64 x 64 tiles, 5 = 32 x 32
- * tiles and, for few tokens, narrower ones, 6 = 256 x 128 tiles. Products with K <= 192 take 128 x 128 tiles for 1 and 2. The workspace sizes follow the setting. Returns
+ * tiles and, for few tokens, narrower ones. Products with K <= 192 take 128 x 128 tiles for 1 and 2. The workspace sizes follow the setting. Returns
  * GEMM355_OK, or GEMM355_ERR_INVALID_ARG for another value (setting
  * unchanged). No HIP call is made.
  */

@@ -10,10 +10,10 @@ from tests.gpu_util import need_gpu
 from tests.test_gpu_dense import dev, gen_of, ortho_exact, run_backward, run_forward, run_ortho
 
 pytestmark = pytest.mark.gpu
-KERNELS = [g.LAYER_LARGE, g.LAYER_SPLIT, g.LAYER_TILE, g.LAYER_SMALL, g.LAYER_NARROW, g.LAYER_WIDE]
+KERNELS = [g.LAYER_LARGE, g.LAYER_SPLIT, g.LAYER_TILE, g.LAYER_SMALL, g.LAYER_NARROW]
 
 
-@pytest.fixture(params=KERNELS, ids=["large", "split", "tile", "small", "narrow", "wide"])
+@pytest.fixture(params=KERNELS, ids=["large", "split", "tile", "small", "narrow"])
 def kernel(request):
     need_gpu()
     g.force_layer_kernel(request.param)

@@ -77,7 +77,7 @@ def test_captured_and_replayed(M, N, K):
     del graph
 
 
-@pytest.mark.parametrize("kernel", [g.LAYER_AUTO, g.LAYER_LARGE, g.LAYER_SPLIT, g.LAYER_TILE, g.LAYER_SMALL, g.LAYER_NARROW, g.LAYER_WIDE])
+@pytest.mark.parametrize("kernel", [g.LAYER_AUTO, g.LAYER_LARGE, g.LAYER_SPLIT, g.LAYER_TILE, g.LAYER_SMALL, g.LAYER_NARROW])
 def test_streams_side_by_side_and_repeated(kernel):
     # two layers on two streams of default priority, interleaved call by call;
     # every result equals the one computed alone, bit by bit
@@ -106,7 +106,7 @@ def test_streams_side_by_side_and_repeated(kernel):
         g.force_layer_kernel(g.LAYER_AUTO)
 
 
-@pytest.mark.parametrize("kernel", [g.LAYER_LARGE, g.LAYER_SPLIT, g.LAYER_TILE, g.LAYER_SMALL, g.LAYER_NARROW, g.LAYER_WIDE])
+@pytest.mark.parametrize("kernel", [g.LAYER_LARGE, g.LAYER_SPLIT, g.LAYER_TILE, g.LAYER_SMALL, g.LAYER_NARROW])
 @pytest.mark.parametrize("M,N,K", [(77, 136, 264), (301, 520, 328)])
 def test_memory_around_the_inputs_does_not_matter(kernel, M, N, K):
     # every input between bands of NaN: the results are those of inputs alone
