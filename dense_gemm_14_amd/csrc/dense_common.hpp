@@ -300,15 +300,32 @@ __device__ inline int pair_offset(const DenseArgs &p, int m, int col, int width,
     return m < p.M && n < p.N ? (int)(((unsigned)m * (unsigned)width + (unsigned)(n + shift)) * 2u) : OOB;
 }
 
-// What a row of BJ blocks at column `col` reads besides its sums: the bias of
-// each block's columns (the same for every row) ...
-template <int EPI, int BJ>
-__device__ inline void load_bias_row(const DenseArgs &p, const Views &v, int col, int lane, u32x2 (&bias)[BJ])
+// The epilogue's variant: f(Int<activation>{}, Int<EXTRA>{}), EXTRA: there is a
+// bias, a residual or Z. Chosen once per tile, so that the rows' code has no
+// branches (with them, 256 x 256 tiles spilled, and the reloads waited for the
+// stores before them: 12 us a tile, of 90).
+template <int EPI, class F>
+__device__ inline void with_epilogue(const DenseArgs &p, F &&f)
 {
     if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED) {
+        with_act(p.act, [&](auto act_c) {
+            if (p.bias || p.z || p.r)
+                f(act_c, Int<1>{});
+            else
+                f(act_c, Int<0>{});
+        });
+    } else {
+        f(Int<A_NONE>{}, Int<EPI == EPI_POLY>{});
+    }
+}
+
+// What a row of BJ blocks at column `col` reads besides its sums: the bias of
+// each block's columns (the same for every row; zeros without one) ...
+template <int EPI, int EXTRA, int BJ>
+__device__ inline void load_bias_row(const DenseArgs &p, const Views &v, int col, int lane, u32x2 (&bias)[BJ])
+{
+    if constexpr (EXTRA && (EPI == EPI_LINEAR || EPI == EPI_GATED)) {
         constexpr int H = EPI == EPI_GATED ? BJ / 2 : BJ;
-        if (!p.bias)
-            return;
 #pragma unroll
         for (int j = 0; j < BJ; ++j) {
             // EPI_GATED: the up columns' bias starts at N
@@ -319,16 +336,16 @@ __device__ inline void load_bias_row(const DenseArgs &p, const Views &v, int col
     }
 }
 
-// ... and the row's residual (EPI_LINEAR) or second term (EPI_POLY).
-template <int EPI, int BJ>
+// ... and the row's residual (EPI_LINEAR) or second term (EPI_POLY); zeros
+// without one.
+template <int EPI, int EXTRA, int BJ>
 __device__ inline void load_res_row(const DenseArgs &p, const Views &v, int m, int col, int lane, u32x4 (&res)[BJ / 2])
 {
-    if constexpr (EPI == EPI_LINEAR || EPI == EPI_POLY)
-        if (p.r)
+    if constexpr (EXTRA && (EPI == EPI_LINEAR || EPI == EPI_POLY))
 #pragma unroll
-            for (int j = 0; j < BJ / 2; ++j)
-                res[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                       v.r, pair_offset(p, m, col + 32 * j, p.N, 0, lane), 0, 0));
+        for (int j = 0; j < BJ / 2; ++j)
+            res[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   v.r, pair_offset(p, m, col + 32 * j, p.N, 0, lane), 0, 0));
 }
 
 __device__ inline void store16(u32x4 w, const __amdgpu_buffer_rsrc_t &r, int off)
@@ -336,60 +353,49 @@ __device__ inline void store16(u32x4 w, const __amdgpu_buffer_rsrc_t &r, int off
     __builtin_amdgcn_raw_buffer_store_b128(w, r, off, 0, 0);
 }
 
-// One row of blocks of a wave's tile: x[0 .. BJ - 1], BJ blocks side by side
-// at column `col` (EPI_GATED: BJ / 2 gate blocks at `col`, then the up blocks
-// of the same columns), this lane's row m. Leaves the values before rounding
-// in x.
-template <int EPI, class TO, int BJ>
-__device__ inline void store_row(const DenseArgs &p, const Views &v, f32x4 (&x)[BJ], int m, int col, int lane,
-                                 const u32x2 (&bias)[BJ], const u32x4 (&res)[BJ / 2])
+// A finished row of blocks, packed as it is stored: pairs of blocks of C, and
+// of Z (EPI_GATED: the gate's pairs, then the up's).
+template <int EPI, int BJ>
+struct PackedRow {
+    static constexpr int C = EPI == EPI_GATED ? BJ / 4 : BJ / 2;
+    u32x4 c[C], z[BJ / 2];
+};
+
+// The epilogue's arithmetic for one row of blocks of a wave's tile: x[0 .. BJ
+// - 1], BJ blocks side by side at column `col` (EPI_GATED: BJ / 2 gate blocks
+// at `col`, then the up blocks of the same columns), this lane's row m. Leaves
+// the values before rounding in x. Apart from the stores, so that a caller can
+// ask for a later row's residual in between: memory operations complete in
+// order, and a load asked for after a store is not there before it.
+template <int EPI, class TO, int ACT, int EXTRA, int BJ>
+__device__ inline void finish_row(const DenseArgs &p, f32x4 (&x)[BJ], int m, int col, int lane, const u32x2 (&bias)[BJ],
+                                  const u32x4 (&res)[BJ / 2], PackedRow<EPI, BJ> &out)
 {
     static_assert(BJ % 4 == 0, "blocks are stored in pairs");
-    if constexpr (EPI == EPI_GATED) {
-        constexpr int H = BJ / 2;
-        if (p.bias)
+    if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED) {
+        if constexpr (EXTRA) {
 #pragma unroll
             for (int j = 0; j < BJ; ++j)
                 x[j] = add_bias(x[j], bias[j]);
-        with_act(p.act, [&](auto act_c) {
-            constexpr int ACT = decltype(act_c)::value;
 #pragma unroll
-            for (int j = 0; j < H; j += 2) {
-                if (p.z) {
-                    store16(pack_pair<TO>(x[j], x[j + 1]), v.z, pair_offset(p, m, col + 16 * j, 2 * p.N, 0, lane));
-                    store16(pack_pair<TO>(x[H + j], x[H + j + 1]), v.z,
-                            pair_offset(p, m, col + 16 * j, 2 * p.N, p.N, lane));
-                }
-                const f32x4 h0 = act4<ACT>(x[j]) * x[H + j], h1 = act4<ACT>(x[j + 1]) * x[H + j + 1];
-                store16(pack_pair<TO>(h0, h1), v.c, pair_offset(p, m, col + 16 * j, p.N, 0, lane));
-            }
-        });
-    } else if constexpr (EPI == EPI_LINEAR) {
-        if (p.bias)
+            for (int j = 0; j < BJ; j += 2)
+                out.z[j / 2] = pack_pair<TO>(x[j], x[j + 1]);
+        }
+        constexpr int H = EPI == EPI_GATED ? BJ / 2 : BJ;
 #pragma unroll
-            for (int j = 0; j < BJ; ++j)
-                x[j] = add_bias(x[j], bias[j]);
-        with_act(p.act, [&](auto act_c) {
-            constexpr int ACT = decltype(act_c)::value;
+        for (int j = 0; j < H; ++j)
+            x[j] = EPI == EPI_GATED ? act4<ACT>(x[j]) * x[(H + j) % BJ] : act4<ACT>(x[j]);
+        if constexpr (EXTRA && EPI == EPI_LINEAR)
 #pragma unroll
             for (int j = 0; j < BJ; j += 2) {
-                const int off = pair_offset(p, m, col + 16 * j, p.N, 0, lane);
-                if (p.z)
-                    store16(pack_pair<TO>(x[j], x[j + 1]), v.z, off);
-                f32x4 y0 = act4<ACT>(x[j]), y1 = act4<ACT>(x[j + 1]);
-                if (p.r) {
-                    f32x4 r0, r1;
-                    unpack_pair<TO>(res[j / 2], r0, r1);
-                    y0 += r0;
-                    y1 += r1;
-                }
-                store16(pack_pair<TO>(y0, y1), v.c, off);
+                f32x4 r0, r1;
+                unpack_pair<TO>(res[j / 2], r0, r1);
+                x[j] += r0;
+                x[j + 1] += r1;
             }
-        });
     } else {
 #pragma unroll
         for (int j = 0; j < BJ; j += 2) {
-            const int off = pair_offset(p, m, col + 16 * j, p.N, 0, lane);
             x[j] *= p.alpha;
             x[j + 1] *= p.alpha;
             if constexpr (EPI == EPI_POLY) {
@@ -402,9 +408,27 @@ __device__ inline void store_row(const DenseArgs &p, const Views &v, f32x4 (&x)[
                     x[j + 1][e] += p.beta * r1[e] + (m == n + 16 + e ? p.gamma : 0.0f);
                 }
             }
-            store16(pack_pair<TO>(x[j], x[j + 1]), v.c, off);
         }
     }
+#pragma unroll
+    for (int j = 0; j < PackedRow<EPI, BJ>::C; ++j)
+        out.c[j] = pack_pair<TO>(x[2 * j], x[2 * j + 1]);
+}
+
+template <int EXTRA, int EPI, int BJ>
+__device__ inline void store_row(const DenseArgs &p, const Views &v, const PackedRow<EPI, BJ> &row, int m, int col, int lane)
+{
+    if constexpr (EXTRA && (EPI == EPI_LINEAR || EPI == EPI_GATED))
+        if (p.z)
+#pragma unroll
+            for (int j = 0; j < BJ / 2; ++j) {
+                constexpr int H = EPI == EPI_GATED ? BJ / 4 : BJ / 2;   // pairs of one half
+                store16(row.z[j], v.z,
+                        pair_offset(p, m, col + 32 * (j % H), EPI == EPI_GATED ? 2 * p.N : p.N, j < H ? 0 : p.N, lane));
+            }
+#pragma unroll
+    for (int j = 0; j < PackedRow<EPI, BJ>::C; ++j)
+        store16(row.c[j], v.c, pair_offset(p, m, col + 32 * j, p.N, 0, lane));
 }
 
 // The mirror image of two rows of FP16 blocks (m0 and m0 + 16 their first

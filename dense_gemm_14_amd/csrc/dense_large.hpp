@@ -291,17 +291,24 @@ void dense_large_kernel(DenseArgs p)
             copy(u & 1, Int<2 * c + 1>{}, off, ks == nk - 1);
         });
     }
-    wait_all_copies();
-    lds_barrier();
+    // The fragments of an item's first step that are not read within it. The
+    // last step of the item before reads them too; where the epilogue needs the
+    // registers (REREAD) they are read again behind it.
+    constexpr bool REREAD = EPI == EPI_LINEAR || EPI == EPI_POLY;
+    auto read_first = [&]() {
 #pragma unroll
-    for (int j = 0; j < 7; ++j) {
-        if (j < 4) {
-            read_a(ring[0], j);
+        for (int j = 0; j < 7; ++j) {
+            if (j < 4) {
+                read_a(ring[0], j);
+                SCHED_FENCE();
+            }
+            read_b(ring[1], j);
             SCHED_FENCE();
         }
-        read_b(ring[1], j);
-        SCHED_FENCE();
-    }
+    };
+    wait_all_copies();
+    lds_barrier();
+    read_first();
 
     // K step that step s of the current item copies for: two steps ahead, the
     // next item's first two in the last two.
@@ -396,25 +403,33 @@ void dense_large_kernel(DenseArgs p)
             const Views v = make_views<EPI>(q);
             const int m0 = tm * BIG + 128 * wm;
             const int col = tn * big_columns(EPI) + big_columns(EPI) / 2 * wn;
-            u32x2 bias[8];
-            load_bias_row<EPI>(q, v, col, ln, bias);
-            // residual rows are requested AHEAD block rows before their use
-            constexpr int AHEAD = 2;
-            u32x4 res[AHEAD][4];
+            with_epilogue<EPI>(q, [&](auto act_c, auto extra_c) {
+                constexpr int ACT = decltype(act_c)::value, EXTRA = decltype(extra_c)::value;
+                u32x2 bias[8];
+                load_bias_row<EPI, EXTRA>(q, v, col, ln, bias);
+                // residual rows are asked for AHEAD rows before their use, and
+                // before the stores of the row at hand
+                constexpr int AHEAD = 3;
+                u32x4 res[AHEAD][4];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-                load_res_row<EPI, 8>(q, v, m0 + 16 * i + (ln & 15), col, ln, res[i]);
+                for (int i = 0; i < AHEAD; ++i)
+                    load_res_row<EPI, EXTRA, 8>(q, v, m0 + 16 * i + (ln & 15), col, ln, res[i]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                hold_row(acc[i]);
-                store_row<EPI, TO>(q, v, acc[i], m0 + 16 * i + (ln & 15), col, ln, bias, res[i % AHEAD]);
-                if (i + AHEAD < 8)
-                    load_res_row<EPI, 8>(q, v, m0 + 16 * (i + AHEAD) + (ln & 15), col, ln, res[i % AHEAD]);
-                if constexpr (EPI >= EPI_STORE_SYM)
-                    if ((i & 1) && tm != tn)
-                        store_mirrored(q, v, acc[i - 1], acc[i], m0 + 16 * (i - 1), col, ln);
-            }
+                for (int i = 0; i < 8; ++i) {
+                    hold_row(acc[i]);
+                    PackedRow<EPI, 8> row;
+                    finish_row<EPI, TO, ACT, EXTRA>(q, acc[i], m0 + 16 * i + (ln & 15), col, ln, bias, res[i % AHEAD], row);
+                    if (i + AHEAD < 8)
+                        load_res_row<EPI, EXTRA, 8>(q, v, m0 + 16 * (i + AHEAD) + (ln & 15), col, ln, res[i % AHEAD]);
+                    store_row<EXTRA>(q, v, row, m0 + 16 * i + (ln & 15), col, ln);
+                    if constexpr (EPI >= EPI_STORE_SYM)
+                        if ((i & 1) && tm != tn)
+                            store_mirrored(q, v, acc[i - 1], acc[i], m0 + 16 * (i - 1), col, ln);
+                }
+            });
         }
+        if constexpr (REREAD)
+            read_first();
         if (!more)
             break;
         item = next;
@@ -458,15 +473,21 @@ __global__ __launch_bounds__(64 * BIG_REDUCE_WAVES) void dense_large_reduce_kern
     const Views v = make_views<EPI>(q);
     const int m0 = tm * BIG + 128 * (wave & 1) + 16 * i0;
     const int col = tn * big_columns(EPI) + big_columns(EPI) / 2 * (wave >> 1);
-    u32x2 bias[8];
-    u32x4 res[2][4];
-    load_bias_row<EPI>(q, v, col, lane, bias);
+    with_epilogue<EPI>(q, [&](auto act_c, auto extra_c) {
+        constexpr int ACT = decltype(act_c)::value, EXTRA = decltype(extra_c)::value;
+        u32x2 bias[8];
+        u32x4 res[2][4];
+        load_bias_row<EPI, EXTRA>(q, v, col, lane, bias);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        load_res_row<EPI, 8>(q, v, m0 + 16 * i + (lane & 15), col, lane, res[i]);
+        for (int i = 0; i < 2; ++i)
+            load_res_row<EPI, EXTRA, 8>(q, v, m0 + 16 * i + (lane & 15), col, lane, res[i]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        store_row<EPI, TO>(q, v, x[i], m0 + 16 * i + (lane & 15), col, lane, bias, res[i]);
+        for (int i = 0; i < 2; ++i) {
+            PackedRow<EPI, 8> row;
+            finish_row<EPI, TO, ACT, EXTRA>(q, x[i], m0 + 16 * i + (lane & 15), col, lane, bias, res[i], row);
+            store_row<EXTRA>(q, v, row, m0 + 16 * i + (lane & 15), col, lane);
+        }
+    });
     if constexpr (EPI >= EPI_STORE_SYM)
         if (tm != tn)
             store_mirrored(q, v, x[0], x[1], m0, col, lane);

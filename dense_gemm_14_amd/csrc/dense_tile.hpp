@@ -138,15 +138,21 @@ __device__ inline void tile_store(const DenseArgs &p, f32x4 (&x)[2][4], int tm, 
     const Views v = make_views<EPI>(p);
     const int m0 = tm * TILE + 64 * wm + 16 * i0;
     const int col = tn * tile_columns(EPI) + tile_columns(EPI) / 2 * wn;
-    u32x2 bias[4];
-    u32x4 res[2][2];
-    load_bias_row<EPI>(p, v, col, lane, bias);
+    with_epilogue<EPI>(p, [&](auto act_c, auto extra_c) {
+        constexpr int ACT = decltype(act_c)::value, EXTRA = decltype(extra_c)::value;
+        u32x2 bias[4];
+        u32x4 res[2][2];
+        load_bias_row<EPI, EXTRA>(p, v, col, lane, bias);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        load_res_row<EPI, 4>(p, v, m0 + 16 * i + (lane & 15), col, lane, res[i]);
+        for (int i = 0; i < 2; ++i)
+            load_res_row<EPI, EXTRA, 4>(p, v, m0 + 16 * i + (lane & 15), col, lane, res[i]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        store_row<EPI, TO>(p, v, x[i], m0 + 16 * i + (lane & 15), col, lane, bias, res[i]);
+        for (int i = 0; i < 2; ++i) {
+            PackedRow<EPI, 4> row;
+            finish_row<EPI, TO, ACT, EXTRA>(p, x[i], m0 + 16 * i + (lane & 15), col, lane, bias, res[i], row);
+            store_row<EXTRA>(p, v, row, m0 + 16 * i + (lane & 15), col, lane);
+        }
+    });
     if constexpr (EPI >= EPI_STORE_SYM)
         if (tm != tn)
             store_mirrored(p, v, x[0], x[1], m0, col, lane);
