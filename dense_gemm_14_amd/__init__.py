@@ -203,17 +203,18 @@ def status_string(status: int) -> str:
 # ---- marshalling -----------------------------------------------------------
 
 _torch = None   # imported with the first tensor or stream
-_raw_stream = None
+_tensor = _raw_stream = _current_device = None
 
 
 def _import_torch():
-    global _torch, _raw_stream
+    global _torch, _tensor, _raw_stream, _current_device
     import torch
     # the address of a device's current stream without building a Stream object
     # (3 us a call, as long as the rest of a small product's call)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
-    _torch = torch
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _torch, _tensor = torch, torch.Tensor
     return torch
 
 
@@ -238,6 +239,16 @@ def _addr(x, need_bytes: int, what: str, device=None):
     return x.data_ptr()
 
 
+def _ptr(x, need_bytes: int, what: str, device: int):
+    """_addr of the layer calls: what is right is found right at once, the
+    rest (other kinds of arguments, and the refusals) goes there."""
+    if x is None:
+        return None
+    if type(x) is _tensor and x.get_device() == device and x.nbytes >= need_bytes and x.is_contiguous():
+        return x.data_ptr()
+    return _addr(x, need_bytes, what, device)
+
+
 def _stream(stream, device=None):
     if stream is None:
         torch = _torch or _import_torch()
@@ -251,7 +262,9 @@ def _stream(stream, device=None):
 
 def _device() -> int:
     """The current device, which runs the layer calls."""
-    return (_torch or _import_torch()).cuda.current_device()
+    if _torch is None:
+        _import_torch()
+    return _current_device()
 
 
 def _check(status: int, what: str):
@@ -298,7 +311,7 @@ def _workspace(ws, nbytes, device=None):
     nb = have if nbytes is None else int(nbytes)
     if nb > have:
         raise ValueError("workspace holds %d bytes, workspace_bytes says %d" % (have, nb))
-    return _addr(ws, nb, "workspace", device), nb
+    return (_addr(ws, nb, "workspace") if device is None else _ptr(ws, nb, "workspace", device)), nb
 
 
 def gemm_bf16_nt_ws(M: int, N: int, K: int, A, B, C, workspace, workspace_bytes=None, stream=None) -> None:
@@ -488,12 +501,12 @@ def gemm_bf16_nt_bias_act_res(M: int, N: int, K: int, A, B, bias, activation: in
     lib, dev = load(), _device()
     M, N, K = int(M), int(N), int(K)
     nz = M > 0 and N > 0
-    a = _addr(A, M * K * 2 if nz else 0, "A", dev)
-    b = _addr(B, N * K * 2 if nz else 0, "B", dev)
-    bb = _addr(bias, N * 2 if nz else 0, "bias", dev)
-    r = _addr(R, M * N * 2 if nz else 0, "R", dev)
-    z = _addr(Z, M * N * 2 if nz else 0, "Z", dev)
-    c = _addr(C, M * N * 2 if nz else 0, "C", dev)
+    a = _ptr(A, M * K * 2 if nz else 0, "A", dev)
+    b = _ptr(B, N * K * 2 if nz else 0, "B", dev)
+    bb = _ptr(bias, N * 2 if nz else 0, "bias", dev)
+    r = _ptr(R, M * N * 2 if nz else 0, "R", dev)
+    z = _ptr(Z, M * N * 2 if nz else 0, "Z", dev)
+    c = _ptr(C, M * N * 2 if nz else 0, "C", dev)
     w, nb = _workspace(workspace, workspace_bytes, dev)
     _check(lib.gemm_bf16_nt_bias_act_res(M, N, K, a, b, bb, int(activation), r, z, c, w, nb, _stream(stream, dev)),
            "gemm_bf16_nt_bias_act_res")
@@ -508,13 +521,13 @@ def _backward(fn, M, N, K, rows, A, B, Z, activation, dC, dA, dB, dbias, workspa
     dev = _device()
     M, N, K, rows = int(M), int(N), int(K), int(rows)
     ok = M >= 0 and N >= 0 and K >= 0   # (else the call refuses the sizes)
-    a = _addr(A, M * K * 2 if ok else 0, "A", dev)
-    b = _addr(B, rows * K * 2 if ok else 0, "B", dev)
-    z = _addr(Z, M * rows * 2 if ok else 0, "Z", dev)
-    dc = _addr(dC, M * N * 2 if ok else 0, "dC", dev)
-    da = _addr(dA, M * K * 2 if ok else 0, "dA", dev)
-    db = _addr(dB, rows * K * 2 if ok else 0, "dB", dev)
-    dbb = _addr(dbias, rows * 2 if ok else 0, "dbias", dev)
+    a = _ptr(A, M * K * 2 if ok else 0, "A", dev)
+    b = _ptr(B, rows * K * 2 if ok else 0, "B", dev)
+    z = _ptr(Z, M * rows * 2 if ok else 0, "Z", dev)
+    dc = _ptr(dC, M * N * 2 if ok else 0, "dC", dev)
+    da = _ptr(dA, M * K * 2 if ok else 0, "dA", dev)
+    db = _ptr(dB, rows * K * 2 if ok else 0, "dB", dev)
+    dbb = _ptr(dbias, rows * 2 if ok else 0, "dbias", dev)
     w, nb = _workspace(workspace, workspace_bytes, dev)
     _check(getattr(load(), fn)(M, N, K, a, b, z, int(activation), dc, da, db, dbb, w, nb, _stream(stream, dev)), fn)
 
@@ -543,11 +556,11 @@ def gemm_bf16_nt_gated(M: int, N: int, K: int, A, B, bias, activation: int, Z, C
     lib, dev = load(), _device()
     M, N, K = int(M), int(N), int(K)
     nz = M > 0 and N > 0
-    a = _addr(A, M * K * 2 if nz else 0, "A", dev)
-    b = _addr(B, 2 * N * K * 2 if nz else 0, "B", dev)
-    bb = _addr(bias, 2 * N * 2 if nz else 0, "bias", dev)
-    z = _addr(Z, M * 2 * N * 2 if nz else 0, "Z", dev)
-    c = _addr(C, M * N * 2 if nz else 0, "C", dev)
+    a = _ptr(A, M * K * 2 if nz else 0, "A", dev)
+    b = _ptr(B, 2 * N * K * 2 if nz else 0, "B", dev)
+    bb = _ptr(bias, 2 * N * 2 if nz else 0, "bias", dev)
+    z = _ptr(Z, M * 2 * N * 2 if nz else 0, "Z", dev)
+    c = _ptr(C, M * N * 2 if nz else 0, "C", dev)
     w, nb = _workspace(workspace, workspace_bytes, dev)
     _check(lib.gemm_bf16_nt_gated(M, N, K, a, b, bb, int(activation), z, c, w, nb, _stream(stream, dev)),
            "gemm_bf16_nt_gated")
@@ -588,8 +601,8 @@ def newton_schulz(batch: int, rows: int, cols: int, G, O, steps: int = 5, coeffi
         g_type = types[G.dtype]
     dev = _device()
     n = batch * rows * cols if min(batch, rows, cols) > 0 else 0
-    gg = _addr(G, n * (4 if g_type == FP32 else 2), "G", dev)
-    o = _addr(O, n * 2, "O", dev)
+    gg = _ptr(G, n * (4 if g_type == FP32 else 2), "G", dev)
+    o = _ptr(O, n * 2, "O", dev)
     w, nb = _workspace(workspace, workspace_bytes, dev)
     a, b, c = coefficients
     _check(load().gemm355_newton_schulz(batch, rows, cols, int(g_type), gg, int(steps), a, b, c, eps, o, w, nb,

@@ -47,6 +47,16 @@ struct DenseArgs {
     float alpha, beta, gamma;
 };
 
+// Asks for all arguments at the kernel's start, at once: left to the compiler
+// they are fetched in three dependent steps, which a product of a few
+// microseconds notices.
+__device__ inline void fetch_args(const DenseArgs &p)
+{
+    asm volatile("" ::"s"(p.a), "s"(p.b), "s"(p.c), "s"(p.r), "s"(p.z), "s"(p.bias), "s"(p.M), "s"(p.N), "s"(p.K),
+                 "s"(p.tiles_m), "s"(p.tiles_n), "s"(p.tiles), "s"(p.whole), "s"(p.splits), "s"(p.supergroup), "s"(p.act),
+                 "s"(p.batch), "s"(p.grid));
+}
+
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));

@@ -329,12 +329,14 @@ template <class T, int LA, int LB, int EPI, class TO, int MB, int NB>
 __global__ __launch_bounds__(SMALL_THREADS, 1) void dense_small_kernel(DenseArgs p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[small_lds(MB, NB)];
+    fetch_args(p);
     const int item = small_item(p.tiles * p.batch);
     if (item < 0)
         return;
-    const int b = item / p.tiles;
-    int tm, tn;
-    dense_tile<EPI>(p, item - b * p.tiles, tm, tn);
+    const int b = p.batch > 1 ? item / p.tiles : 0;
+    int tm = 0, tn = item - b * p.tiles;
+    if (p.tiles_m > 1)   // (few tokens: no divisions)
+        dense_tile<EPI>(p, item - b * p.tiles, tm, tn);
     small_tile<T, LA, LB, EPI, TO, MB, NB>(p, b, tm, tn, lds);
 }
 

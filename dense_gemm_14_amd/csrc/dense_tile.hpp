@@ -172,12 +172,13 @@ void dense_tile_kernel(DenseArgs p)
     const int wm = wave & 1;         // 64-row half of the tile
     const int wn = (wave >> 1) & 1;  // 64-column half
 
+    fetch_args(p);
     const int item = tile_item(p);
     if (item < 0)
         return;
     const WorkItem w = work_item(p, item);
     const bool parts = w.tile >= p.whole && p.splits > 1;
-    const int b = w.tile / p.tiles;
+    const int b = p.batch > 1 ? w.tile / p.tiles : 0;
     int tm, tn;
     dense_tile<EPI>(p, w.tile - b * p.tiles, tm, tn);
     if (p.batch > 1)
