@@ -107,7 +107,7 @@ SmallPlan plan_small(const Shape &s, bool layer, bool narrow, int cus)
 std::atomic<int> g_layer_kernel{0};
 enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4, KERNEL_NARROW = 5 };
 
-// Estimated microseconds of each kernel, fitted to 1800 products measured on
+// Estimated microseconds of each kernel, fitted to 1200 products measured on
 // MI355X (M from 1, N and K from 64 to 8192, forward layers and both gradient
 // products; a typical estimate is 10 % off, and the choice by them costs 2 %
 // over the best kernel of every product).
@@ -116,11 +116,11 @@ enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4, KE
 //   128 and 256: per K step, part of it only when every unit is busy; per round
 //     the tiles' beginning and end; for a split the second launch and its
 //     partials (MB).
-constexpr double kStart = 3.5;
+constexpr double kStart = 3.4;
 double time_small_tile(const SmallPlan &t, int nk, double fill)
 {
     const double width = (t.mb + t.nb) / 8.0, stages = d::small_stages(t.mb, t.nb);
-    return 1.1 + double(ceil_div(nk, d::SMALL_WAVES)) * (1.05 / stages + 1.13 * width * fill);
+    return 0.8 + double(ceil_div(nk, d::SMALL_WAVES)) * (1.08 / stages + 1.27 * width * fill);
 }
 double time_small(const SmallPlan &t, int nk, int batch, int cus)
 {
@@ -130,8 +130,8 @@ double time_small(const SmallPlan &t, int nk, int batch, int cus)
 struct TileTimes {
     double fixed, step, step_full, round, split, split_mb;
 };
-constexpr TileTimes kTile = {1.9, 0.43, 0.11, 4.6, 4.3, 0.51}, kBig = {4.8, 1.19, 0.41, 7.1, 0.0, 0.0},
-                    kBigSplit = {1.9, 1.30, 0.0, 13.1, 1.4, 0.33};
+constexpr TileTimes kTile = {2.2, 0.31, 0.22, 4.3, 5.1, 0.46}, kBig = {4.0, 1.19, 0.42, 6.0, 0.0, 0.0},
+                    kBigSplit = {1.6, 1.25, 0.0, 13.4, 1.6, 0.30};
 double time_tiles(const TilePlan &t, int batch, const TileTimes &c)
 {
     const int64_t items = t.whole + (int64_t(t.tiles) * batch - t.whole) * t.splits;
@@ -436,18 +436,20 @@ int backward_together(const Shape &a, bool wants_a, const Shape &b, bool wants_b
     const int forced = g_layer_kernel.load(std::memory_order_relaxed);
     if (forced != 0)
         return forced >= KERNEL_SMALL ? forced : 0;
-    double apart = wants_a && wants_b ? kLaunches : 0.5 * kLaunches;
-    if (wants_a)
-        apart += choose_kernel(a, false, cus).us;
-    if (wants_b)
-        apart += choose_kernel(b, false, cus).us;
+    if (!wants_a || !wants_b) {   // alone, a product runs as it would anywhere
+        const int k = wants_a || wants_b ? choose_kernel(wants_a ? a : b, false, cus).kernel : KERNEL_SMALL;
+        return k == KERNEL_SMALL || k == KERNEL_NARROW ? k : 0;
+    }
+    double apart = kLaunches + choose_kernel(a, false, cus).us + choose_kernel(b, false, cus).us;
     int best = 0;
     for (const int k : {KERNEL_SMALL, KERNEL_NARROW}) {
         const SmallPlan ta = plan_small(a, false, k == KERNEL_NARROW, cus), tb = plan_small(b, false, k == KERNEL_NARROW, cus);
-        const double na = wants_a ? ta.tiles : 0, nb = wants_b ? tb.tiles : 0, fill = std::min(1.0, (na + nb) / cus);
-        const double one_a = time_small_tile(ta, (int)ceil_div(a.K, d::BIG_BK), fill);
-        const double one_b = time_small_tile(tb, (int)ceil_div(b.K, d::BIG_BK), fill);
-        const double longest = std::max(na > 0 ? one_a : 0.0, nb > 0 ? one_b : 0.0);
+        const double na = ta.tiles, nb = tb.tiles, fill = std::min(1.0, (na + nb) / cus);
+        const int ka = (int)ceil_div(a.K, d::BIG_BK), kb = (int)ceil_div(b.K, d::BIG_BK);
+        const double one_a = time_small_tile(ta, ka, fill), one_b = time_small_tile(tb, kb, fill);
+        // a long tile goes on when the others are done
+        const double longest = std::max(time_small_tile(ta, ka, std::min(1.0, na / cus)),
+                                        time_small_tile(tb, kb, std::min(1.0, nb / cus)));
         // (the last tiles end up to one short tile apart)
         const double us = kStart + std::max(longest, (na * one_a + nb * one_b) / cus + 0.5 * std::min(one_a, one_b));
         if (us < apart) {
