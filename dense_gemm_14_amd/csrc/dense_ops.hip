@@ -171,10 +171,25 @@ Choice choose_kernel(const Shape &s, bool layer, int cus)
     return best;
 }
 
-size_t product_workspace(const Shape &s, bool layer, int cus)
+// What a product runs, decided once per call (the kernel's override may change
+// at any time): the workspace it was given and what it launches agree.
+struct ProductPlan {
+    int kernel;
+    double us;                // estimated
+    TilePlan tiles;           // KERNEL_WHOLE, _SPLIT, _TILE
+    SmallPlan small;          // KERNEL_SMALL, _NARROW
+    size_t workspace_bytes;
+};
+ProductPlan plan_product(const Shape &s, bool layer, int cus)
 {
-    const int k = choose_kernel(s, layer, cus).kernel;
-    return k == KERNEL_TILE ? plan_tile(s, cus).workspace_bytes : k == KERNEL_SPLIT ? plan_large(s, cus, true).workspace_bytes : 0;
+    const Choice c = choose_kernel(s, layer, cus);
+    ProductPlan p = {c.kernel, c.us, {}, {}, 0};
+    if (c.kernel >= KERNEL_SMALL)
+        p.small = plan_small(s, layer, c.kernel == KERNEL_NARROW, cus);
+    else
+        p.tiles = c.kernel == KERNEL_TILE ? plan_tile(s, cus) : plan_large(s, cus, c.kernel == KERNEL_SPLIT);
+    p.workspace_bytes = p.tiles.workspace_bytes;
+    return p;
 }
 
 template <class T, int LA, int LB, int EPI, class TO>
@@ -183,10 +198,7 @@ int product_small(DenseArgs p, const SmallPlan &t, hipStream_t stream)
     p.tiles_m = t.tiles_m;
     p.tiles_n = t.tiles_n;
     p.tiles = t.tiles;
-    const int64_t items = int64_t(t.tiles) * p.batch;
-    if (items > (int64_t(1) << 28))
-        return GEMM355_ERR_UNSUPPORTED;
-    const unsigned blocks = (unsigned)(ceil_div(items, 8) * 8), threads = d::SMALL_THREADS;
+    const unsigned blocks = (unsigned)(ceil_div(int64_t(t.tiles) * p.batch, 8) * 8), threads = d::SMALL_THREADS;
     if constexpr (EPI == d::EPI_LINEAR) {
         if (t.nb == 1)
             return t.mb == 1 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 1>, blocks, threads, p, stream)
@@ -242,21 +254,16 @@ int product_large(DenseArgs p, const TilePlan &t, hipStream_t stream)
     return st;
 }
 
-// Launches a product. `ws` has product_workspace() bytes.
+// Launches a product as planned; `ws` has the plan's workspace_bytes.
 template <class T, int LA, int LB, int EPI, class TO = T>
-int product(DenseArgs p, int cus, void *ws, hipStream_t stream)
+int product(DenseArgs p, const ProductPlan &plan, void *ws, hipStream_t stream)
 {
-    if (p.M == 0 || p.N == 0 || p.batch == 0)
-        return GEMM355_OK;
-    const Shape s = {p.M, p.N, p.K, p.batch, EPI >= d::EPI_STORE_SYM, EPI == d::EPI_GATED};
     p.supergroup = 8;
     p.ws = static_cast<float *>(ws);
-    constexpr bool LAYER = EPI == d::EPI_LINEAR || EPI == d::EPI_GATED;
-    const int k = choose_kernel(s, LAYER, cus).kernel;
-    if (k == KERNEL_SMALL || k == KERNEL_NARROW)
-        return product_small<T, LA, LB, EPI, TO>(p, plan_small(s, LAYER, k == KERNEL_NARROW, cus), stream);
-    return k == KERNEL_TILE ? product_tile<T, LA, LB, EPI, TO>(p, plan_tile(s, cus), stream)
-                            : product_large<T, LA, LB, EPI, TO>(p, plan_large(s, cus, k == KERNEL_SPLIT), stream);
+    if (plan.kernel >= KERNEL_SMALL)
+        return product_small<T, LA, LB, EPI, TO>(p, plan.small, stream);
+    return plan.kernel == KERNEL_TILE ? product_tile<T, LA, LB, EPI, TO>(p, plan.tiles, stream)
+                                      : product_large<T, LA, LB, EPI, TO>(p, plan.tiles, stream);
 }
 
 DenseArgs args_of(int M, int N, int K, const void *a, const void *b, void *c)
@@ -306,9 +313,10 @@ bool all_aligned(const Array *a, int n)
 bool act_ok(int act) { return act >= GEMM355_ACT_NONE && act <= GEMM355_ACT_SILU; }
 
 // Extents of a layer with `rows` weight rows and N outputs: every array,
-// padded to whole tiles, below 2^31 bytes.
+// padded to whole tiles (at least one), below 2^31 bytes.
 bool layer_extents_ok(int64_t M, int64_t N, int64_t rows, int64_t K)
 {
+    M = std::max<int64_t>(M, 1);
     return extent_ok(M, K * 2) && extent_ok(rows, K * 2) && extent_ok(M, rows * 2) && extent_ok(M, N * 2);
 }
 
@@ -339,7 +347,8 @@ int layer_forward(int M, int N, int K, const void *A, const void *B, const void 
     const int rc = compute_units(&cus);
     if (rc != GEMM355_OK)
         return rc;
-    if (workspace_bytes < product_workspace({M, N, K, 1, false, GATED}, true, cus))
+    const ProductPlan plan = plan_product({M, N, K, 1, false, GATED}, true, cus);
+    if (workspace_bytes < plan.workspace_bytes)
         return GEMM355_ERR_UNSUPPORTED;
     DenseArgs p = args_of(M, N, K, A, B, C);
     p.bias = bias;
@@ -347,7 +356,7 @@ int layer_forward(int M, int N, int K, const void *A, const void *B, const void 
     p.r = R;
     p.z = Z;
     return product<__bf16, d::ROW_K, d::ROW_K, GATED ? d::EPI_GATED : d::EPI_LINEAR>(
-        p, cus, workspace, static_cast<hipStream_t>(stream));
+        p, plan, workspace, static_cast<hipStream_t>(stream));
 }
 
 template <bool GATED>
@@ -355,13 +364,15 @@ int layer_forward_workspace(int M, int N, int K, size_t *bytes)
 {
     if (M < 0 || N < 0 || K < 0 || !bytes)
         return GEMM355_ERR_INVALID_ARG;
+    if (!layer_extents_ok(M, N, GATED ? 2 * int64_t(N) : N, K))
+        return GEMM355_ERR_UNSUPPORTED;
     *bytes = 0;
     if (M == 0 || N == 0)
         return GEMM355_OK;
     int cus = 0;
     const int rc = compute_units(&cus);
     if (rc == GEMM355_OK)
-        *bytes = product_workspace({M, N, K, 1, false, GATED}, true, cus);
+        *bytes = plan_product({M, N, K, 1, false, GATED}, true, cus).workspace_bytes;
     return rc;
 }
 
@@ -374,28 +385,6 @@ int grad_rows(int M, int N)
     const int64_t col_blocks = ceil_div(N, d::GRAD_COLS);
     const int64_t rows = ceil_div(int64_t(M) * col_blocks, 2048);
     return (int)std::min<int64_t>(64, std::max<int64_t>(d::GRAD_LANES, ceil_div(rows, d::GRAD_LANES) * d::GRAD_LANES));
-}
-
-// Workspace of a backward call: the gradient of the pre-activations (unless
-// it is dC itself), the column sums, and the partials of whichever product
-// splits more.
-struct BackwardPlan {
-    size_t sums_at, partials_at, bytes;
-};
-
-BackwardPlan plan_backward(int M, int N, int K, bool gated, int act, int cus)
-{
-    const int rows = gated ? 2 * N : N;
-    BackwardPlan w = {};
-    w.sums_at = gated || act != GEMM355_ACT_NONE ? align_up(size_t(M) * rows * 2) : 0;
-    w.partials_at = w.sums_at + align_up(size_t(ceil_div(M, grad_rows(M, N))) * rows * sizeof(float));
-    size_t part = 0;
-    if (M > 0 && K > 0)
-        part = product_workspace({M, K, rows, 1, false, false}, false, cus);
-    if (rows > 0 && K > 0)
-        part = std::max(part, product_workspace({rows, K, M, 1, false, false}, false, cus));
-    w.bytes = w.partials_at + part;
-    return w;
 }
 
 // A backward pass whose products are small, in one launch. `narrow`: 32 x 32
@@ -418,29 +407,23 @@ int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const
     g.bias = bias;
     g.bias_blocks = bias_blocks;
     g.first_b = pb.K > pa.K;
-    const int64_t items = int64_t(pa.tiles) + pb.tiles + bias_blocks;
-    if (items > (int64_t(1) << 28))
-        return GEMM355_ERR_UNSUPPORTED;
-    const unsigned blocks = (unsigned)items, threads = d::SMALL_THREADS;
+    const unsigned blocks = (unsigned)(pa.tiles + pb.tiles + bias_blocks), threads = d::SMALL_THREADS;
     return narrow ? launch_kernel(d::dense_small_bwd_kernel<2>, blocks, threads, g, s)
                   : launch_kernel(d::dense_small_bwd_kernel<4>, blocks, threads, g, s);
 }
 
 // Whether a backward pass runs as one launch of small tiles (KERNEL_SMALL or
-// KERNEL_NARROW; 0: its products one by one). Together its tiles fill the
-// compute units better and two launches of about 3 us fall away. Estimate: the
-// tiles' time shared out over the units, and no less than the longest tile.
+// KERNEL_NARROW; 0: its products one by one); pa, pb: the plans of the products
+// that are wanted. Together the tiles fill the compute units better and two
+// launches of about 3 us fall away. Estimate: the tiles' time shared out over
+// the units, and no less than the longest tile.
 constexpr double kLaunches = 6.0;
-int backward_together(const Shape &a, bool wants_a, const Shape &b, bool wants_b, int cus)
+int backward_together(const Shape &a, const ProductPlan *pa, const Shape &b, const ProductPlan *pb, int cus)
 {
-    const int forced = g_layer_kernel.load(std::memory_order_relaxed);
-    if (forced != 0)
-        return forced >= KERNEL_SMALL ? forced : 0;
-    if (!wants_a || !wants_b) {   // alone, a product runs as it would anywhere
-        const int k = wants_a || wants_b ? choose_kernel(wants_a ? a : b, false, cus).kernel : KERNEL_SMALL;
-        return k == KERNEL_SMALL || k == KERNEL_NARROW ? k : 0;
-    }
-    double apart = kLaunches + choose_kernel(a, false, cus).us + choose_kernel(b, false, cus).us;
+    const bool small = (!pa || pa->kernel >= KERNEL_SMALL) && (!pb || pb->kernel >= KERNEL_SMALL);
+    if (!pa || !pb || pa->us == 0.0)   // alone, a product runs as it would anywhere; so do forced kernels
+        return !small ? 0 : pa ? pa->kernel : pb ? pb->kernel : KERNEL_SMALL;
+    double apart = kLaunches + pa->us + pb->us;
     int best = 0;
     for (const int k : {KERNEL_SMALL, KERNEL_NARROW}) {
         const SmallPlan ta = plan_small(a, false, k == KERNEL_NARROW, cus), tb = plan_small(b, false, k == KERNEL_NARROW, cus);
@@ -458,6 +441,32 @@ int backward_together(const Shape &a, bool wants_a, const Shape &b, bool wants_b
         }
     }
     return best;
+}
+
+// A backward call: its two products (dA = dZ B and dB = dZ^T A), whether they
+// run as one launch of small tiles, and its workspace: the gradient of the
+// pre-activations (unless it is dC itself), the column sums, and the partials
+// of whichever product splits more.
+struct BackwardPlan {
+    ProductPlan a, b;
+    int together;     // KERNEL_SMALL or KERNEL_NARROW; 0: one by one
+    size_t sums_at, partials_at, bytes;
+};
+
+BackwardPlan plan_backward(int M, int N, int K, bool gated, int act, bool wants_a, bool wants_b, int cus)
+{
+    const int rows = gated ? 2 * N : N;
+    const Shape a = {M, K, rows, 1, false, false}, b = {rows, K, M, 1, false, false};
+    BackwardPlan w = {};
+    w.sums_at = gated || act != GEMM355_ACT_NONE ? align_up(size_t(M) * rows * 2) : 0;
+    w.partials_at = w.sums_at + align_up(size_t(ceil_div(M, grad_rows(M, N))) * rows * sizeof(float));
+    if (M > 0 && K > 0)
+        w.a = plan_product(a, false, cus);
+    if (rows > 0 && K > 0)
+        w.b = plan_product(b, false, cus);
+    w.together = backward_together(a, wants_a ? &w.a : nullptr, b, wants_b ? &w.b : nullptr, cus);
+    w.bytes = w.partials_at + std::max(w.a.workspace_bytes, w.b.workspace_bytes);
+    return w;
 }
 
 template <bool GATED>
@@ -487,7 +496,7 @@ int layer_backward(int M, int N, int K, const void *A, const void *B, const void
     const int rc = compute_units(&cus);
     if (rc != GEMM355_OK)
         return rc;
-    const BackwardPlan w = plan_backward(M, N, K, GATED, act, cus);
+    const BackwardPlan w = plan_backward(M, N, K, GATED, act, wants_a, wants_b, cus);
     if (workspace_bytes < w.bytes)
         return GEMM355_ERR_UNSUPPORTED;
 
@@ -517,21 +526,19 @@ int layer_backward(int M, int N, int K, const void *A, const void *B, const void
     const int bias_blocks = wants_bias ? (int)ceil_div(rows, d::BIAS_COLS) : 0;
     const DenseArgs pa = args_of(M, K, (int)rows, dz, B, dA);          // dA = dZ B
     const DenseArgs pb = args_of((int)rows, K, M, dz, A, dB);          // dB = dZ^T A
-    const Shape sa = {M, K, (int)rows, 1, false, false}, sb = {(int)rows, K, M, 1, false, false};
-    const int together = backward_together(sa, wants_a, sb, wants_b, cus);
-    if (together != 0)
-        return backward_small(pa, wants_a, pb, wants_b, q, bias_blocks, together == KERNEL_NARROW, cus, s);
+    if (w.together != 0)
+        return backward_small(pa, wants_a, pb, wants_b, q, bias_blocks, w.together == KERNEL_NARROW, cus, s);
     if (wants_bias) {
         const int st = launch_kernel(d::dense_bias_kernel, (unsigned)bias_blocks, (unsigned)d::BIAS_THREADS, q, s);
         if (st != GEMM355_OK)
             return st;
     }
     if (wants_a) {
-        const int st = product<__bf16, d::ROW_K, d::COL_K, d::EPI_STORE>(pa, cus, ws + w.partials_at, s);
+        const int st = product<__bf16, d::ROW_K, d::COL_K, d::EPI_STORE>(pa, w.a, ws + w.partials_at, s);
         if (st != GEMM355_OK)
             return st;
     }
-    return wants_b ? product<__bf16, d::COL_K, d::COL_K, d::EPI_STORE>(pb, cus, ws + w.partials_at, s) : GEMM355_OK;
+    return wants_b ? product<__bf16, d::COL_K, d::COL_K, d::EPI_STORE>(pb, w.b, ws + w.partials_at, s) : GEMM355_OK;
 }
 
 template <bool GATED>
@@ -539,13 +546,15 @@ int layer_backward_workspace(int M, int N, int K, int act, size_t *bytes)
 {
     if (M < 0 || N < 0 || K < 0 || !act_ok(act) || !bytes)
         return GEMM355_ERR_INVALID_ARG;
+    if (!layer_extents_ok(M, N, GATED ? 2 * int64_t(N) : N, K))
+        return GEMM355_ERR_UNSUPPORTED;
     *bytes = 0;
     if (N == 0 && (M == 0 || K == 0))   // no output has an element
         return GEMM355_OK;
     int cus = 0;
     const int rc = compute_units(&cus);
-    if (rc == GEMM355_OK)
-        *bytes = plan_backward(M, N, K, GATED, act, cus).bytes;
+    if (rc == GEMM355_OK)   // (the same whichever outputs are wanted)
+        *bytes = plan_backward(M, N, K, GATED, act, true, true, cus).bytes;
     return rc;
 }
 
@@ -557,33 +566,26 @@ int layer_backward_workspace(int M, int N, int K, int act, size_t *bytes)
 constexpr float kPolyScale = 256.0f;   // S and P are held times this
 
 struct OrthoPlan {
+    ProductPlan gram, square, update;
     size_t x1_at, s_at, p_at, norm_at, partials_at, bytes;
     int norm_blocks;
 };
 
-void ortho_shapes(int batch, int rows, int cols, Shape *gram, Shape *square, Shape *update)
-{
-    const int m = std::min(rows, cols), n = std::max(rows, cols);
-    *gram = {m, m, n, batch, true, false};
-    *square = {m, m, m, batch, true, false};
-    *update = {rows, cols, m, batch, false, false};
-}
-
 OrthoPlan plan_ortho(int batch, int rows, int cols, int cus)
 {
-    const size_t m = (size_t)std::min(rows, cols);
+    const int m = std::min(rows, cols), n = std::max(rows, cols);
     const size_t x = align_up(size_t(batch) * rows * cols * 2), s = align_up(size_t(batch) * m * m * 2);
     OrthoPlan o = {};
+    o.gram = plan_product({m, m, n, batch, true, false}, false, cus);
+    o.square = plan_product({m, m, m, batch, true, false}, false, cus);
+    o.update = plan_product({rows, cols, m, batch, false, false}, false, cus);
     o.norm_blocks = (int)std::min<int64_t>(d::NS_BLOCKS, ceil_div(int64_t(rows) * cols, d::NS_THREADS * 8));
     o.x1_at = x;
     o.s_at = 2 * x;
     o.p_at = o.s_at + s;
     o.norm_at = o.p_at + s;
     o.partials_at = o.norm_at + align_up(size_t(batch) * o.norm_blocks * sizeof(double));
-    Shape gram, square, update;
-    ortho_shapes(batch, rows, cols, &gram, &square, &update);
-    o.bytes = o.partials_at + std::max({product_workspace(gram, false, cus), product_workspace(square, false, cus),
-                                        product_workspace(update, false, cus)});
+    o.bytes = o.partials_at + std::max({o.gram.workspace_bytes, o.square.workspace_bytes, o.update.workspace_bytes});
     return o;
 }
 
@@ -598,38 +600,43 @@ int ortho_start(const d::NormArgs &n, int batch, hipStream_t s)
 
 // One Newton-Schulz step from x to out (BF16 and unscaled after the last).
 template <bool WIDE, class TO>
-int ortho_step(const Shape &g, const Shape &q, const Shape &u, const void *x, void *S, void *P, void *out, float a,
-               float b, float c, float scale, bool last, int cus, void *ws, hipStream_t s)
+int ortho_step(const OrthoPlan &o, int batch, int rows, int cols, const void *x, uint8_t *ws, void *out, float a, float b,
+               float c, float scale, bool last, hipStream_t s)
 {
     typedef _Float16 h;
-    DenseArgs p = args_of(g.M, g.N, g.K, x, x, S);
-    p.batch = g.batch;
+    const int m = WIDE ? rows : cols, n = WIDE ? cols : rows;
+    void *S = ws + o.s_at, *P = ws + o.p_at, *partials = ws + o.partials_at;
+    DenseArgs p = args_of(m, m, n, x, x, S);
+    p.batch = batch;
     p.alpha = kPolyScale / (scale * scale);
-    int st = WIDE ? product<h, d::ROW_K, d::ROW_K, d::EPI_STORE_SYM>(p, cus, ws, s)
-                  : product<h, d::COL_K, d::COL_K, d::EPI_STORE_SYM>(p, cus, ws, s);
+    int st = WIDE ? product<h, d::ROW_K, d::ROW_K, d::EPI_STORE_SYM>(p, o.gram, partials, s)
+                  : product<h, d::COL_K, d::COL_K, d::EPI_STORE_SYM>(p, o.gram, partials, s);
     if (st != GEMM355_OK)
         return st;
-    p = args_of(q.M, q.N, q.K, S, S, P);   // P = a I + b S + c S^2
-    p.batch = g.batch;
+    p = args_of(m, m, m, S, S, P);   // P = a I + b S + c S^2
+    p.batch = batch;
     p.r = S;
     p.alpha = c / kPolyScale;
     p.beta = b;
     p.gamma = a * kPolyScale;
-    st = product<h, d::ROW_K, d::ROW_K, d::EPI_POLY>(p, cus, ws, s);
+    st = product<h, d::ROW_K, d::ROW_K, d::EPI_POLY>(p, o.square, partials, s);
     if (st != GEMM355_OK)
         return st;
-    p = WIDE ? args_of(u.M, u.N, u.K, P, x, out) : args_of(u.M, u.N, u.K, x, P, out);
-    p.batch = g.batch;
+    p = WIDE ? args_of(rows, cols, m, P, x, out) : args_of(rows, cols, m, x, P, out);
+    p.batch = batch;
     p.alpha = (last ? 1.0f / scale : 1.0f) / kPolyScale;
     // P = P^T: as the right-hand operand its rows are its columns
-    return WIDE ? product<h, d::ROW_K, d::COL_K, d::EPI_STORE, TO>(p, cus, ws, s)
-                : product<h, d::ROW_K, d::ROW_K, d::EPI_STORE, TO>(p, cus, ws, s);
+    return WIDE ? product<h, d::ROW_K, d::COL_K, d::EPI_STORE, TO>(p, o.update, partials, s)
+                : product<h, d::ROW_K, d::ROW_K, d::EPI_STORE, TO>(p, o.update, partials, s);
 }
 
-bool ortho_extents_ok(int64_t rows, int64_t cols)
+// Each matrix as any other operand; the batch's blocks of 16 x 16 (of which no
+// tile has fewer) below 2^28, so that counts of tiles stay within 32 bits.
+bool ortho_extents_ok(int64_t batch, int64_t rows, int64_t cols)
 {
     const int64_t m = std::min(rows, cols);
-    return extent_ok(rows, cols * 2) && extent_ok(cols, rows * 2) && extent_ok(m, m * 2);
+    return extent_ok(rows, cols * 2) && extent_ok(cols, rows * 2) && extent_ok(m, m * 2) && batch <= 65535 &&
+           batch * ceil_div(rows, 16) * ceil_div(cols, 16) <= (int64_t(1) << 28);
 }
 
 } // namespace
@@ -693,6 +700,8 @@ extern "C" int gemm355_newton_schulz_workspace_size(int batch, int rows, int col
 {
     if (batch < 0 || rows < 0 || cols < 0 || !bytes)
         return GEMM355_ERR_INVALID_ARG;
+    if (!ortho_extents_ok(batch, rows, cols))
+        return GEMM355_ERR_UNSUPPORTED;
     *bytes = 0;
     if (batch == 0 || rows == 0 || cols == 0)
         return GEMM355_OK;
@@ -720,8 +729,7 @@ extern "C" int gemm355_newton_schulz(int batch, int rows, int cols, int g_type, 
     if (any_overlap(out, 2, in, 1))
         return GEMM355_ERR_INVALID_ARG;
     if (!all_aligned(out, 2) || !all_aligned(in, 1) || rows % 8 != 0 || cols % 8 != 0 ||
-        !ortho_extents_ok(rows, cols) || batch > 65535 ||
-        int64_t(batch) * ceil_div(rows, 64) * ceil_div(cols, 64) > (int64_t(1) << 28))
+        !ortho_extents_ok(batch, rows, cols))
         return GEMM355_ERR_UNSUPPORTED;
     int cus = 0;
     const int rc = compute_units(&cus);
@@ -744,15 +752,12 @@ extern "C" int gemm355_newton_schulz(int batch, int rows, int cols, int g_type, 
     n.scale = scale;
     n.eps = eps;
     int st = g_type == GEMM355_FP32 ? ortho_start<true>(n, batch, s) : ortho_start<false>(n, batch, s);
-    Shape gram, square, update;
-    ortho_shapes(batch, rows, cols, &gram, &square, &update);
     uint8_t *x = ws, *next = ws + o.x1_at;
     for (int i = 0; i < steps && st == GEMM355_OK; ++i) {
         const bool last = i == steps - 1, wide = rows <= cols;
         auto step = wide ? (last ? ortho_step<true, __bf16> : ortho_step<true, _Float16>)
                          : (last ? ortho_step<false, __bf16> : ortho_step<false, _Float16>);
-        st = step(gram, square, update, x, ws + o.s_at, ws + o.p_at, last ? static_cast<uint8_t *>(O) : next, a, b, c,
-                  scale, last, cus, ws + o.partials_at, s);
+        st = step(o, batch, rows, cols, x, ws, last ? O : next, a, b, c, scale, last, s);
         std::swap(x, next);
     }
     return st;

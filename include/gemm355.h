@@ -442,8 +442,10 @@ int gemm_mxfp4_nt_bias_act(int M, int N, int K, const void *Aq, const void *SA, 
  *                    streams, graphs replayed side by side) need one each.
  *   workspace_bytes  its size: at least what the matching *_workspace_size
  *                    call says for these sizes on the current device, else
- *                    GEMM355_ERR_UNSUPPORTED, with nothing enqueued. NULL
- *                    with 0 bytes is accepted where that is 0; NULL with
+ *                    GEMM355_ERR_UNSUPPORTED, with nothing enqueued (that
+ *                    call gives UNSUPPORTED for arrays that are too large
+ *                    and otherwise the errors of
+ *                    gemm_bf16_nt_workspace_size). NULL with 0 bytes is accepted where that is 0; NULL with
  *                    workspace_bytes > 0 is GEMM355_ERR_INVALID_ARG.
  * Every output must be apart from every input, from the workspace and from the
  * other outputs, else GEMM355_ERR_INVALID_ARG (one exception: C may be R).

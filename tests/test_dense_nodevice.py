@@ -116,5 +116,21 @@ def test_workspace_size_refusals():
     assert lib.gemm_bf16_nt_bias_act_bwd_workspace_size(8, 8, 8, 4, ctypes.byref(n)) == g.ERR_INVALID_ARG
 
 
+def test_sizes_beyond_the_limit():
+    # the largest ints: refused as too large, with no arithmetic running over
+    lib, n, top = g.load(), ctypes.c_size_t(7), (1 << 31) - 8
+    for name, args in (("gemm_bf16_nt_bias_act_res", ()), ("gemm_bf16_nt_gated", ()), ("gemm_bf16_nt_gated_bwd", ()),
+                       ("gemm_bf16_nt_bias_act_bwd", (0,))):
+        fn = getattr(lib, name + "_workspace_size")
+        for sizes in ((top, top, top), (8, top, 8), (0, top, 0), (top, 8, 8), (8, 8, top)):
+            assert fn(*sizes, *args, ctypes.byref(n)) == g.ERR_UNSUPPORTED, (name, sizes)
+    for sizes in ((top, 8, 8), (1, top, top), (65535, 1 << 14, 1 << 14)):
+        assert lib.gemm355_newton_schulz_workspace_size(*sizes, ctypes.byref(n)) == g.ERR_UNSUPPORTED, sizes
+    assert n.value == 7
+    assert linear(M=8, N=top, K=0, a=None, b=None, bias=None, r=None, z=None, c=1 << 45) == g.ERR_UNSUPPORTED
+    assert gated_bwd(M=0, N=top, K=0, a=None, b=None, z=None, dc=None, da=None, db=None, dbias=1 << 45) == g.ERR_UNSUPPORTED
+    assert ortho(batch=65535, rows=1 << 14, cols=1 << 14, G=1 << 50, o=1 << 52, ws=1 << 54) == g.ERR_UNSUPPORTED
+
+
 def test_the_older_calls_still_refuse_silu():
     assert g.load().gemm_bf16_nt_bias_act(8, 8, 64, A, B, BIAS, g.ACT_SILU, C, None) == g.ERR_INVALID_ARG

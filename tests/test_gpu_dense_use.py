@@ -1,6 +1,8 @@
 """The layer calls as programs use them: captured into graphs and replayed, on
 several streams at once, repeated, next to memory that holds NaN, at the largest
 arrays they take, and with arguments the binding refuses."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -104,6 +106,45 @@ def test_streams_side_by_side_and_repeated(kernel):
                     assert torch.equal(o, w), (kernel, r, k, i)
     finally:
         g.force_layer_kernel(g.LAYER_AUTO)
+
+
+def test_threads_with_a_stream_each():
+    # calls from several threads at once, while another thread changes the
+    # kernels' override: a call runs as planned or is refused for its workspace
+    need_gpu()
+    layers = [Layer(130 + 40 * i, 264, 520, 80 + i) for i in range(4)]
+    want = []
+    for layer in layers:
+        layer.run()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in layer.outs])
+    refused = [0] * len(layers)
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                try:
+                    layers[i].run()
+                except g.Gemm355Error as e:
+                    assert e.status == g.ERR_UNSUPPORTED
+                    refused[i] += 1
+            torch.cuda.current_stream().synchronize()
+
+    def toggle():
+        for k in [g.LAYER_SPLIT, g.LAYER_TILE, g.LAYER_SMALL, g.LAYER_AUTO] * 25:
+            g.force_layer_kernel(k)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(layers))] + [threading.Thread(target=toggle)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    g.force_layer_kernel(g.LAYER_AUTO)
+    torch.cuda.synchronize()
+    for layer, w in zip(layers, want):
+        layer.wipe()
+        layer.run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, v) for o, v in zip(layer.outs, w))
 
 
 @pytest.mark.parametrize("kernel", [g.LAYER_LARGE, g.LAYER_SPLIT, g.LAYER_TILE, g.LAYER_SMALL, g.LAYER_NARROW])
