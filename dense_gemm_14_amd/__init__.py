@@ -1,7 +1,8 @@
 """Python binding of libgemm355 (gfx950 HIP kernels behind a C ABI).
 
-Argument marshalling only: every step of the product runs in the HIP kernels
-of ``libgemm355.so``. There is no CPU path and no fallback -- if the library
+Argument marshalling only (through ctypes, the layer calls through
+csrc/marshal.c): every step of the product runs in the HIP kernels of
+``libgemm355.so``. There is no CPU path and no fallback -- if the library
 cannot be loaded, every call raises.
 
 The functions mirror the C entry points declared in ``include/gemm355.h``:
@@ -239,16 +240,6 @@ def _addr(x, need_bytes: int, what: str, device=None):
     return x.data_ptr()
 
 
-def _ptr(x, need_bytes: int, what: str, device: int):
-    """_addr of the layer calls: what is right is found right at once, the
-    rest (other kinds of arguments, and the refusals) goes there."""
-    if x is None:
-        return None
-    if type(x) is _tensor and x.get_device() == device and x.nbytes >= need_bytes and x.is_contiguous():
-        return x.data_ptr()
-    return _addr(x, need_bytes, what, device)
-
-
 def _stream(stream, device=None):
     if stream is None:
         torch = _torch or _import_torch()
@@ -311,7 +302,7 @@ def _workspace(ws, nbytes, device=None):
     nb = have if nbytes is None else int(nbytes)
     if nb > have:
         raise ValueError("workspace holds %d bytes, workspace_bytes says %d" % (have, nb))
-    return (_addr(ws, nb, "workspace") if device is None else _ptr(ws, nb, "workspace", device)), nb
+    return _addr(ws, nb, "workspace", device), nb
 
 
 def gemm_bf16_nt_ws(M: int, N: int, K: int, A, B, C, workspace, workspace_bytes=None, stream=None) -> None:
@@ -485,6 +476,28 @@ def gemm_mxfp4_nt_bias_act(M: int, N: int, K: int, Aq, SA, Bq, SB, bias, activat
 
 # ---- layers ------------------------------------------------------------------
 
+_bound = None   # csrc/marshal.c: checks the arguments and makes the call
+
+
+def _layers():
+    """The compiled marshalling of the layer calls, bound to the library."""
+    global _bound
+    if _bound is None:
+        lib = load()
+        if _torch is None:
+            _import_torch()
+        from . import build as _build
+        if not os.path.exists(_build.MARSHAL_PATH):
+            _build.build_marshal()
+        from . import _marshal as m
+        m.bind(_tensor, _current_device, _raw_stream, _addr, _workspace, _stream,
+               *[ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in (
+                   "gemm_bf16_nt_bias_act_res", "gemm_bf16_nt_gated", "gemm_bf16_nt_bias_act_bwd",
+                   "gemm_bf16_nt_gated_bwd")])
+        _bound = m
+    return _bound
+
+
 def _size_of(fn, *args) -> int:
     out = ctypes.c_size_t(0)
     _check(getattr(load(), fn)(*args, ctypes.byref(out)), fn)
@@ -498,38 +511,15 @@ def gemm_bf16_nt_bias_act_res(M: int, N: int, K: int, A, B, bias, activation: in
     bias (N), R (M x N, may be C itself) and Z (M x N, an output) may be None;
     activation: ACT_NONE, ACT_RELU, ACT_GELU_TANH or ACT_SILU. The workspace
     holds bias_act_res_workspace_size(M, N, K) bytes (None when that is 0)."""
-    lib, dev = load(), _device()
-    M, N, K = int(M), int(N), int(K)
-    nz = M > 0 and N > 0
-    a = _ptr(A, M * K * 2 if nz else 0, "A", dev)
-    b = _ptr(B, N * K * 2 if nz else 0, "B", dev)
-    bb = _ptr(bias, N * 2 if nz else 0, "bias", dev)
-    r = _ptr(R, M * N * 2 if nz else 0, "R", dev)
-    z = _ptr(Z, M * N * 2 if nz else 0, "Z", dev)
-    c = _ptr(C, M * N * 2 if nz else 0, "C", dev)
-    w, nb = _workspace(workspace, workspace_bytes, dev)
-    _check(lib.gemm_bf16_nt_bias_act_res(M, N, K, a, b, bb, int(activation), r, z, c, w, nb, _stream(stream, dev)),
-           "gemm_bf16_nt_bias_act_res")
+    status = (_bound or _layers()).forward(0, M, N, K, A, B, bias, activation, R, Z, C, workspace, workspace_bytes,
+                                             stream)
+    if status:
+        raise Gemm355Error(status, "gemm_bf16_nt_bias_act_res")
 
 
 def bias_act_res_workspace_size(M: int, N: int, K: int) -> int:
     """Workspace bytes of gemm_bf16_nt_bias_act_res on the current device."""
     return _size_of("gemm_bf16_nt_bias_act_res_workspace_size", int(M), int(N), int(K))
-
-
-def _backward(fn, M, N, K, rows, A, B, Z, activation, dC, dA, dB, dbias, workspace, workspace_bytes, stream):
-    dev = _device()
-    M, N, K, rows = int(M), int(N), int(K), int(rows)
-    ok = M >= 0 and N >= 0 and K >= 0   # (else the call refuses the sizes)
-    a = _ptr(A, M * K * 2 if ok else 0, "A", dev)
-    b = _ptr(B, rows * K * 2 if ok else 0, "B", dev)
-    z = _ptr(Z, M * rows * 2 if ok else 0, "Z", dev)
-    dc = _ptr(dC, M * N * 2 if ok else 0, "dC", dev)
-    da = _ptr(dA, M * K * 2 if ok else 0, "dA", dev)
-    db = _ptr(dB, rows * K * 2 if ok else 0, "dB", dev)
-    dbb = _ptr(dbias, rows * 2 if ok else 0, "dbias", dev)
-    w, nb = _workspace(workspace, workspace_bytes, dev)
-    _check(getattr(load(), fn)(M, N, K, a, b, z, int(activation), dc, da, db, dbb, w, nb, _stream(stream, dev)), fn)
 
 
 def gemm_bf16_nt_bias_act_bwd(M: int, N: int, K: int, A, B, Z, activation: int, dC, dA, dB, dbias, workspace=None,
@@ -538,8 +528,10 @@ def gemm_bf16_nt_bias_act_bwd(M: int, N: int, K: int, A, B, Z, activation: int, 
     dC (M x N) and the forward call's Z (None with ACT_NONE). Each output may
     be None if it is not wanted (the residual's gradient is dC itself). The
     workspace holds bias_act_bwd_workspace_size(M, N, K, activation) bytes."""
-    _backward("gemm_bf16_nt_bias_act_bwd", M, N, K, N, A, B, Z, activation, dC, dA, dB, dbias, workspace,
-              workspace_bytes, stream)
+    status = (_bound or _layers()).backward(0, M, N, K, A, B, Z, activation, dC, dA, dB, dbias, workspace,
+                                              workspace_bytes, stream)
+    if status:
+        raise Gemm355Error(status, "gemm_bf16_nt_bias_act_bwd")
 
 
 def bias_act_bwd_workspace_size(M: int, N: int, K: int, activation: int) -> int:
@@ -553,17 +545,10 @@ def gemm_bf16_nt_gated(M: int, N: int, K: int, A, B, bias, activation: int, Z, C
     holds the gate rows, then the up rows. bias (2N) and Z (an output) may be
     None; activations and workspace (gated_workspace_size(M, N, K) bytes) as
     for gemm_bf16_nt_bias_act_res."""
-    lib, dev = load(), _device()
-    M, N, K = int(M), int(N), int(K)
-    nz = M > 0 and N > 0
-    a = _ptr(A, M * K * 2 if nz else 0, "A", dev)
-    b = _ptr(B, 2 * N * K * 2 if nz else 0, "B", dev)
-    bb = _ptr(bias, 2 * N * 2 if nz else 0, "bias", dev)
-    z = _ptr(Z, M * 2 * N * 2 if nz else 0, "Z", dev)
-    c = _ptr(C, M * N * 2 if nz else 0, "C", dev)
-    w, nb = _workspace(workspace, workspace_bytes, dev)
-    _check(lib.gemm_bf16_nt_gated(M, N, K, a, b, bb, int(activation), z, c, w, nb, _stream(stream, dev)),
-           "gemm_bf16_nt_gated")
+    status = (_bound or _layers()).forward(1, M, N, K, A, B, bias, activation, None, Z, C, workspace,
+                                             workspace_bytes, stream)
+    if status:
+        raise Gemm355Error(status, "gemm_bf16_nt_gated")
 
 
 def gated_workspace_size(M: int, N: int, K: int) -> int:
@@ -576,8 +561,10 @@ def gemm_bf16_nt_gated_bwd(M: int, N: int, K: int, A, B, Z, activation: int, dC,
     """Gradients of the gated layer: dA (M x K), dB (2N x K), dbias (2N) from
     dC (M x N) and the forward call's Z (M x 2N); otherwise as for
     gemm_bf16_nt_bias_act_bwd (gated_bwd_workspace_size(M, N, K) bytes)."""
-    _backward("gemm_bf16_nt_gated_bwd", M, N, K, 2 * int(N), A, B, Z, activation, dC, dA, dB, dbias, workspace,
-              workspace_bytes, stream)
+    status = (_bound or _layers()).backward(1, M, N, K, A, B, Z, activation, dC, dA, dB, dbias, workspace,
+                                              workspace_bytes, stream)
+    if status:
+        raise Gemm355Error(status, "gemm_bf16_nt_gated_bwd")
 
 
 def gated_bwd_workspace_size(M: int, N: int, K: int) -> int:
@@ -601,8 +588,8 @@ def newton_schulz(batch: int, rows: int, cols: int, G, O, steps: int = 5, coeffi
         g_type = types[G.dtype]
     dev = _device()
     n = batch * rows * cols if min(batch, rows, cols) > 0 else 0
-    gg = _ptr(G, n * (4 if g_type == FP32 else 2), "G", dev)
-    o = _ptr(O, n * 2, "O", dev)
+    gg = _addr(G, n * (4 if g_type == FP32 else 2), "G", dev)
+    o = _addr(O, n * 2, "O", dev)
     w, nb = _workspace(workspace, workspace_bytes, dev)
     a, b, c = coefficients
     _check(load().gemm355_newton_schulz(batch, rows, cols, int(g_type), gg, int(steps), a, b, c, eps, o, w, nb,

@@ -1,9 +1,11 @@
-"""Build libgemm355.so in-tree with hipcc for gfx950 (no GPU needed to compile)."""
+"""Build libgemm355.so in-tree with hipcc for gfx950 (no GPU needed to compile),
+and the binding's _marshal.so with gcc."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -17,6 +19,9 @@ HEADERS = [os.path.join(CSRC, f) for f in ("common.hpp", "gemm_bf16.hpp", "gemm_
                                            "gemm_fp4.hpp", "fp4_decode.hpp", "gemm_mxfp4.hpp", "schedule.hpp", "host.hpp",
                                            "dense_common.hpp", "dense_large.hpp", "dense_small.hpp", "dense_tile.hpp", "dense_grad.hpp", "newton_schulz.hpp")] + \
     [os.path.join(INCLUDE, "gemm355.h")]
+
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.c")
+MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -45,8 +50,20 @@ def _hipcc(args, verbose):
         print("\n".join(msgs), file=sys.stderr)
 
 
+def build_marshal() -> str:
+    out = MARSHAL_PATH + ".tmp%d" % os.getpid()
+    res = subprocess.run(["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-o", out,
+                          MARSHAL_SOURCE], capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("gcc failed (%d):\n%s" % (res.returncode, res.stdout + res.stderr))
+    os.replace(out, MARSHAL_PATH)
+    return MARSHAL_PATH
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source of the library into LIB_PATH. Always recompiles."""
+    """Compile every HIP source of the library into LIB_PATH, and the binding's
+    marshalling. Always recompiles."""
+    build_marshal()
     with tempfile.TemporaryDirectory() as tmp:
         objs = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SOURCES]
         with ThreadPoolExecutor(len(SOURCES)) as pool:   # one compiler process per source
@@ -59,7 +76,7 @@ def build(verbose: bool = False) -> str:
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(MARSHAL_PATH):
         return True
     t = os.path.getmtime(LIB_PATH)
     return any(os.path.getmtime(s) > t for s in SOURCES + HEADERS)

@@ -274,3 +274,46 @@ def test_binding_refuses():
     with pytest.raises(g.Gemm355Error) as e:
         g.newton_schulz(1, 64, 64, B, t(64, 64), workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert e.value.status == g.ERR_UNSUPPORTED
+
+
+def test_binding_takes_every_kind_of_argument():
+    # tensors, parameters, raw addresses, numpy sizes, streams as objects and as
+    # addresses, a workspace with its size: the same results
+    need_gpu()
+    M, N, K = 40, 136, 4104
+    gen = gen_of(91)
+    A, B, R = bf(gen, M, K), bf(gen, N, K, std=K ** -0.5), bf(gen, M, N)
+    nb = max(g.bias_act_res_workspace_size(M, N, K), g.bias_act_bwd_workspace_size(M, N, K, g.ACT_SILU))
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    new = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    results = []
+    param = torch.nn.Parameter(B)
+    for sizes, arg, w, stream in (((M, N, K), lambda t: t, (ws,), None),
+                                  (np.array([M, N, K]), lambda t: t.data_ptr(), (ws.data_ptr(), nb), s.cuda_stream),
+                                  ((M, N, K), lambda t: param if t is B else t, (ws, nb), s)):
+        C, Z, dA, dB, db = new(M, N), new(M, N), new(M, K), new(N, K), new(N)
+        g.gemm_bf16_nt_bias_act_res(*sizes, arg(A), arg(B), None, g.ACT_SILU, arg(R), arg(Z), arg(C), *w, stream=stream)
+        g.gemm_bf16_nt_bias_act_bwd(*sizes, arg(A), arg(B), arg(Z), g.ACT_SILU, arg(R), arg(dA), arg(dB), arg(db), *w,
+                                    stream=stream)
+        torch.cuda.synchronize()
+        results.append((C, Z, dA, dB, db))
+    for r in results[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(r, results[0]))
+    C = new(M, N)
+    with pytest.raises(ValueError, match="workspace_bytes"):
+        g.gemm_bf16_nt_bias_act_res(M, N, K, A, B, None, 0, None, None, C, ws.data_ptr())
+    with pytest.raises(ValueError, match="workspace"):
+        g.gemm_bf16_nt_bias_act_res(M, N, K, A, B, None, 0, None, None, C, ws, nb + 1)
+    with pytest.raises(ValueError, match="GPU"):
+        g.gemm_bf16_nt_bias_act_res(M, N, K, A, B, None, 0, None, None, C, ws.cpu())
+    with pytest.raises(OverflowError):
+        g.gemm_bf16_nt_bias_act_res(1 << 40, N, K, A, B, None, 0, None, None, C, ws)
+    with pytest.raises(g.Gemm355Error) as e:
+        g.gemm_bf16_nt_bias_act_res(-M, N, K, A, B, None, 0, None, None, C, ws)
+    assert e.value.status == g.ERR_INVALID_ARG
+    # what was refused left nothing behind: the next call is right
+    g.gemm_bf16_nt_bias_act_res(M, N, K, A, B, None, g.ACT_SILU, R, None, C, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(C, results[0][0])
