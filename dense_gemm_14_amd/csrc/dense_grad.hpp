@@ -112,9 +112,9 @@ __global__ __launch_bounds__(GRAD_THREADS) void dense_grad_kernel(GradArgs p)
     }
 }
 
-// The bias gradient of 64 columns by 512 threads: from the workgroups' column
-// sums, or, where nothing else has to pass over dC (the identity), from dC
-// itself. `part`: 64 x 65 floats of LDS.
+// The bias gradient of 64 columns by THREADS threads: from the workgroups'
+// column sums, or, where nothing else has to pass over dC (the identity), from dC
+// itself. `part`: THREADS / 8 x 65 floats of LDS.
 struct BiasArgs {
     const float *sums;     // [blocks][cols], or NULL
     const uint16_t *dc;    // else: blocks x cols BF16
@@ -122,6 +122,7 @@ struct BiasArgs {
     int cols, blocks;
 };
 constexpr int BIAS_COLS = 64, BIAS_THREADS = 512, BIAS_PITCH = 65;
+template <int THREADS>
 __device__ inline void bias_block(const BiasArgs &p, int block, float *part)
 {
     const int c0 = block * BIAS_COLS;
@@ -131,16 +132,16 @@ __device__ inline void bias_block(const BiasArgs &p, int block, float *part)
         float t = 0.0f;
         if (c < p.cols)
 #pragma unroll 4
-            for (int r = ty; r < p.blocks; r += 8)
+            for (int r = ty; r < p.blocks; r += THREADS / 64)
                 t += p.sums[(size_t)r * p.cols + c];
         part[ty * BIAS_PITCH + tx] = t;
-        lanes = 8;
+        lanes = THREADS / 64;
     } else {
         const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, c = c0 + 8 * tx;
         float s[8] = {};
         if (c < p.cols)
 #pragma unroll 4
-            for (int r = ty; r < p.blocks; r += 64) {
+            for (int r = ty; r < p.blocks; r += THREADS / 8) {
                 float x[8];
                 unpack8(*reinterpret_cast<const u32x4 *>(p.dc + (size_t)r * p.cols + c), x);
 #pragma unroll
@@ -150,7 +151,7 @@ __device__ inline void bias_block(const BiasArgs &p, int block, float *part)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             part[ty * BIAS_PITCH + 8 * tx + e] = s[e];
-        lanes = 64;
+        lanes = THREADS / 8;
     }
     __syncthreads();
     const int tx = threadIdx.x;
@@ -164,8 +165,8 @@ __device__ inline void bias_block(const BiasArgs &p, int block, float *part)
 
 __global__ __launch_bounds__(BIAS_THREADS) void dense_bias_kernel(BiasArgs p)
 {
-    __shared__ float part[64 * BIAS_PITCH];
-    bias_block(p, (int)blockIdx.x, part);
+    __shared__ float part[BIAS_THREADS / 8 * BIAS_PITCH];
+    bias_block<BIAS_THREADS>(p, (int)blockIdx.x, part);
 }
 
 } // namespace dense

@@ -77,9 +77,10 @@ TilePlan plan_tiles(const Shape &s, int side, int cus, int min_steps, bool split
 TilePlan plan_tile(const Shape &s, int cus) { return plan_tiles(s, d::TILE, cus, 4, true); }
 TilePlan plan_large(const Shape &s, int cus, bool split) { return plan_tiles(s, d::BIG, cus, d::BIG_MIN_STEPS, split); }
 
-// The small-tile kernel's tile, in blocks of 16 rows of A and of B.
+// The small-tile kernel's tile, in blocks of 16 rows of A and of B, and its
+// waves (8, or 4 with two workgroups per compute unit).
 struct SmallPlan {
-    int mb, nb, tiles_m, tiles_n, tiles;
+    int mb, nb, waves, tiles_m, tiles_n, tiles;
 };
 
 // 64 x 64 tiles, or narrow ones: 32 x 32, and for the few tokens of a forward
@@ -88,7 +89,7 @@ struct SmallPlan {
 // columns up to 64 as still leave a tile for every unit.
 SmallPlan plan_small(const Shape &s, bool layer, bool narrow, int cus)
 {
-    SmallPlan t = {4, 4, 0, 0, 0};
+    SmallPlan t = {4, 4, 8, 0, 0, 0};
     if (narrow) {
         t.mb = layer && s.M <= 16 ? 1 : 2;
         t.nb = layer && s.M <= 32 && !s.gated ? 1 : 2;
@@ -117,15 +118,29 @@ enum { KERNEL_WHOLE = 1, KERNEL_SPLIT = 2, KERNEL_TILE = 3, KERNEL_SMALL = 4, KE
 //     the tiles' beginning and end; for a split the second launch and its
 //     partials (MB).
 constexpr double kStart = 3.4;
+int small_slots(const SmallPlan &t, int cus) { return cus * (8 / t.waves); }
 double time_small_tile(const SmallPlan &t, int nk, double fill)
 {
     const double width = (t.mb + t.nb) / 8.0, stages = d::small_stages(t.mb, t.nb);
-    return 0.8 + double(ceil_div(nk, d::SMALL_WAVES)) * (1.08 / stages + 1.27 * width * fill);
+    return 0.8 + double(ceil_div(nk, t.waves)) * (1.08 / stages + 1.27 * width * fill);
 }
 double time_small(const SmallPlan &t, int nk, int batch, int cus)
 {
-    const double tiles = double(t.tiles) * batch;
-    return kStart + ceil(tiles / cus) * time_small_tile(t, nk, std::min(1.0, tiles / cus));
+    const double tiles = double(t.tiles) * batch, slots = small_slots(t, cus);
+    return kStart + ceil(tiles / slots) * time_small_tile(t, nk, std::min(1.0, tiles / slots));
+}
+// 64 x 64 tiles with four waves where that is estimated faster: two workgroups
+// then share a compute unit, so a second round begins at twice as many tiles.
+// Measured, eight waves against four (us): 1024 x 1152 x 1024, 288 tiles, 11.8
+// against 8.7; 64 x 18000 x 512 9.7 against 6.6; a backward pass of 170 x 1528 x
+// 1608 15.1 against 9.8. Eight waves keep long contractions of few tiles, where
+// a wave's share of K is what takes the time (1024 x 1024 x 1024: 6.9).
+SmallPlan plan_small_waves(const Shape &s, bool layer, bool narrow, int cus)
+{
+    SmallPlan t = plan_small(s, layer, narrow, cus), u = t;
+    u.waves = 4;
+    const int nk = (int)ceil_div(s.K, d::SMALL_BK);
+    return !narrow && time_small(u, nk, s.batch, cus) < time_small(t, nk, s.batch, cus) ? u : t;
 }
 struct TileTimes {
     double fixed, step, step_full, round, split, split_mb;
@@ -160,7 +175,7 @@ Choice choose_kernel(const Shape &s, bool layer, int cus)
         if (us < best.us)
             best = {kernel, us};
     };
-    offer(KERNEL_SMALL, time_small(plan_small(s, layer, false, cus), nk, s.batch, cus));
+    offer(KERNEL_SMALL, time_small(plan_small_waves(s, layer, false, cus), nk, s.batch, cus));
     offer(KERNEL_NARROW, time_small(plan_small(s, layer, true, cus), nk, s.batch, cus));
     if (big_ok) {
         offer(KERNEL_WHOLE, time_tiles(plan_large(s, cus, false), s.batch, kBig));
@@ -185,7 +200,7 @@ ProductPlan plan_product(const Shape &s, bool layer, int cus)
     const Choice c = choose_kernel(s, layer, cus);
     ProductPlan p = {c.kernel, c.us, {}, {}, 0};
     if (c.kernel >= KERNEL_SMALL)
-        p.small = plan_small(s, layer, c.kernel == KERNEL_NARROW, cus);
+        p.small = plan_small_waves(s, layer, c.kernel == KERNEL_NARROW, cus);
     else
         p.tiles = c.kernel == KERNEL_TILE ? plan_tile(s, cus) : plan_large(s, cus, c.kernel == KERNEL_SPLIT);
     p.workspace_bytes = p.tiles.workspace_bytes;
@@ -198,19 +213,21 @@ int product_small(DenseArgs p, const SmallPlan &t, hipStream_t stream)
     p.tiles_m = t.tiles_m;
     p.tiles_n = t.tiles_n;
     p.tiles = t.tiles;
-    const unsigned blocks = (unsigned)(ceil_div(int64_t(t.tiles) * p.batch, 8) * 8), threads = d::SMALL_THREADS;
+    const unsigned blocks = (unsigned)(ceil_div(int64_t(t.tiles) * p.batch, 8) * 8), threads = 64u * t.waves;
     if constexpr (EPI == d::EPI_LINEAR) {
         if (t.nb == 1)
-            return t.mb == 1 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 1>, blocks, threads, p, stream)
-                             : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 1>, blocks, threads, p, stream);
+            return t.mb == 1 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 1, 8>, blocks, threads, p, stream)
+                             : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 1, 8>, blocks, threads, p, stream);
     }
     if constexpr (EPI == d::EPI_LINEAR || EPI == d::EPI_GATED) {
         if (t.mb == 1)
-            return t.nb == 2 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 2>, blocks, threads, p, stream)
-                             : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 4>, blocks, threads, p, stream);
+            return t.nb == 2 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 2, 8>, blocks, threads, p, stream)
+                             : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 4, 8>, blocks, threads, p, stream);
     }
-    return t.mb == 2 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 2>, blocks, threads, p, stream)
-                     : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4>, blocks, threads, p, stream);
+    if (t.mb == 2)
+        return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 2, 8>, blocks, threads, p, stream);
+    return t.waves == 8 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 8>, blocks, threads, p, stream)
+                        : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 4>, blocks, threads, p, stream);
 }
 
 void set_plan(DenseArgs &p, const TilePlan &t)
@@ -387,14 +404,19 @@ int grad_rows(int M, int N)
     return (int)std::min<int64_t>(64, std::max<int64_t>(d::GRAD_LANES, ceil_div(rows, d::GRAD_LANES) * d::GRAD_LANES));
 }
 
-// A backward pass whose products are small, in one launch. `narrow`: 32 x 32
-// tiles.
+// How a backward pass runs as one launch (kernel 0: not).
+struct Together {
+    int kernel, waves;
+};
+
+// A backward pass whose products are small, in one launch: 32 x 32 tiles, or
+// 64 x 64 with eight or four waves.
 int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const d::BiasArgs &bias, int bias_blocks,
-                   bool narrow, int cus, hipStream_t s)
+                   const Together &how, int cus, hipStream_t s)
 {
     d::SmallBwdArgs g = {};
     auto place = [&](DenseArgs &p, bool wanted) {
-        const SmallPlan t = plan_small({p.M, p.N, p.K, 1, false, false}, false, narrow, cus);
+        const SmallPlan t = plan_small({p.M, p.N, p.K, 1, false, false}, false, how.kernel == KERNEL_NARROW, cus);
         p.tiles_m = t.tiles_m;
         p.tiles_n = t.tiles_n;
         p.tiles = wanted ? t.tiles : 0;
@@ -407,9 +429,10 @@ int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const
     g.bias = bias;
     g.bias_blocks = bias_blocks;
     g.first_b = pb.K > pa.K;
-    const unsigned blocks = (unsigned)(pa.tiles + pb.tiles + bias_blocks), threads = d::SMALL_THREADS;
-    return narrow ? launch_kernel(d::dense_small_bwd_kernel<2>, blocks, threads, g, s)
-                  : launch_kernel(d::dense_small_bwd_kernel<4>, blocks, threads, g, s);
+    const unsigned blocks = (unsigned)(pa.tiles + pb.tiles + bias_blocks), threads = 64u * how.waves;
+    return how.kernel == KERNEL_NARROW ? launch_kernel(d::dense_small_bwd_kernel<2, 8>, blocks, threads, g, s)
+           : how.waves == 8            ? launch_kernel(d::dense_small_bwd_kernel<4, 8>, blocks, threads, g, s)
+                                       : launch_kernel(d::dense_small_bwd_kernel<4, 4>, blocks, threads, g, s);
 }
 
 // Whether a backward pass runs as one launch of small tiles (KERNEL_SMALL or
@@ -418,26 +441,33 @@ int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const
 // launches of about 3 us fall away. Estimate: the tiles' time shared out over
 // the units, and no less than the longest tile.
 constexpr double kLaunches = 6.0;
-int backward_together(const Shape &a, const ProductPlan *pa, const Shape &b, const ProductPlan *pb, int cus)
+Together backward_together(const Shape &a, const ProductPlan *pa, const Shape &b, const ProductPlan *pb, int cus)
 {
     const bool small = (!pa || pa->kernel >= KERNEL_SMALL) && (!pb || pb->kernel >= KERNEL_SMALL);
-    if (!pa || !pb || pa->us == 0.0)   // alone, a product runs as it would anywhere; so do forced kernels
-        return !small ? 0 : pa ? pa->kernel : pb ? pb->kernel : KERNEL_SMALL;
-    double apart = kLaunches + pa->us + pb->us;
-    int best = 0;
-    for (const int k : {KERNEL_SMALL, KERNEL_NARROW}) {
-        const SmallPlan ta = plan_small(a, false, k == KERNEL_NARROW, cus), tb = plan_small(b, false, k == KERNEL_NARROW, cus);
-        const double na = ta.tiles, nb = tb.tiles, fill = std::min(1.0, (na + nb) / cus);
-        const int ka = (int)ceil_div(a.K, d::BIG_BK), kb = (int)ceil_div(b.K, d::BIG_BK);
+    if (!pa || !pb)   // alone, a product runs as it would anywhere
+        return !small ? Together{0, 0} : pa ? Together{pa->kernel, pa->small.waves} : pb ? Together{pb->kernel, pb->small.waves}
+                                                                                         : Together{KERNEL_SMALL, 8};
+    const bool forced = pa->us == 0.0;
+    if (forced && !small)
+        return {0, 0};
+    double best_us = forced ? 1e30 : kLaunches + pa->us + pb->us;
+    Together best = {0, 0};
+    for (const Together &how : {Together{KERNEL_SMALL, 8}, Together{KERNEL_SMALL, 4}, Together{KERNEL_NARROW, 8}}) {
+        if (forced && how.kernel != pa->kernel)
+            continue;
+        SmallPlan ta = plan_small(a, false, how.kernel == KERNEL_NARROW, cus), tb = plan_small(b, false, how.kernel == KERNEL_NARROW, cus);
+        ta.waves = tb.waves = how.waves;
+        const double na = ta.tiles, nb = tb.tiles, slots = small_slots(ta, cus), fill = std::min(1.0, (na + nb) / slots);
+        const int ka = (int)ceil_div(a.K, d::SMALL_BK), kb = (int)ceil_div(b.K, d::SMALL_BK);
         const double one_a = time_small_tile(ta, ka, fill), one_b = time_small_tile(tb, kb, fill);
         // a long tile goes on when the others are done
-        const double longest = std::max(time_small_tile(ta, ka, std::min(1.0, na / cus)),
-                                        time_small_tile(tb, kb, std::min(1.0, nb / cus)));
+        const double longest = std::max(time_small_tile(ta, ka, std::min(1.0, na / slots)),
+                                        time_small_tile(tb, kb, std::min(1.0, nb / slots)));
         // (the last tiles end up to one short tile apart)
-        const double us = kStart + std::max(longest, (na * one_a + nb * one_b) / cus + 0.5 * std::min(one_a, one_b));
-        if (us < apart) {
-            apart = us;
-            best = k;
+        const double us = kStart + std::max(longest, (na * one_a + nb * one_b) / slots + 0.5 * std::min(one_a, one_b));
+        if (us < best_us) {
+            best_us = us;
+            best = how;
         }
     }
     return best;
@@ -449,7 +479,7 @@ int backward_together(const Shape &a, const ProductPlan *pa, const Shape &b, con
 // of whichever product splits more.
 struct BackwardPlan {
     ProductPlan a, b;
-    int together;     // KERNEL_SMALL or KERNEL_NARROW; 0: one by one
+    Together together;
     size_t sums_at, partials_at, bytes;
 };
 
@@ -526,8 +556,8 @@ int layer_backward(int M, int N, int K, const void *A, const void *B, const void
     const int bias_blocks = wants_bias ? (int)ceil_div(rows, d::BIAS_COLS) : 0;
     const DenseArgs pa = args_of(M, K, (int)rows, dz, B, dA);          // dA = dZ B
     const DenseArgs pb = args_of((int)rows, K, M, dz, A, dB);          // dB = dZ^T A
-    if (w.together != 0)
-        return backward_small(pa, wants_a, pb, wants_b, q, bias_blocks, w.together == KERNEL_NARROW, cus, s);
+    if (w.together.kernel != 0)
+        return backward_small(pa, wants_a, pb, wants_b, q, bias_blocks, w.together, cus, s);
     if (wants_bias) {
         const int st = launch_kernel(d::dense_bias_kernel, (unsigned)bias_blocks, (unsigned)d::BIAS_THREADS, q, s);
         if (st != GEMM355_OK)

@@ -2,16 +2,19 @@
 // latency counts: few tokens, small layers. One launch, nothing in a workspace.
 //
 //   * A workgroup owns 16 MB rows x 16 NB columns (of B rows) of the output; its
-//     eight waves share out K: wave w takes the K slices (64 elements) w, w + 8,
-//     ... and computes the whole tile for them, so no LDS byte is read twice and
-//     the waves never wait for each other until they add their sums.
+//     WAVES waves share out K: wave w takes the K slices (64 elements) w, w +
+//     WAVES, ... and computes the whole tile for them, so no LDS byte is read twice
+//     and the waves never wait for each other until they add their sums. Eight
+//     waves fill a compute unit; where there are more tiles than units, 64 x 64
+//     tiles also run with four, two workgroups to a unit, so that the last tiles
+//     do not wait for a unit of their own.
 //   * A wave copies its slices through the memory pipeline into its own LDS
 //     ring (SMALL_STAGES stages of 2 KiB per block and slice): it waits for a
 //     stage, reads the whole slice into registers, refills the stage at once and
 //     then multiplies, so close to 128 KiB per compute unit are in flight all the
 //     time -- several times HBM's latency times a compute unit's share of its
 //     rate, which is what bounds these sizes.
-//   * The eight partial tiles meet in LDS (rows padded by 16 bytes: sixteen rows'
+//   * The waves' partial tiles meet in LDS (rows padded by 16 bytes: sixteen rows'
 //     16-byte writes fall into 64 different banks), are added in wave order, and
 //     each thread finishes eight consecutive columns of a row.
 //   * Tiles: 64 x 64; 32 x 32 where those leave compute units idle; for few tokens
@@ -25,16 +28,14 @@
 namespace gemm355 {
 namespace dense {
 
-constexpr int SMALL_WAVES = 8;
-constexpr int SMALL_THREADS = 64 * SMALL_WAVES;
 constexpr int SMALL_BK = 64;
 constexpr int small_stage(int mb, int nb) { return (mb + nb) * 2048; }
 constexpr int small_stages(int mb, int nb) { return 20480 / small_stage(mb, nb); }
 // floats per row of a partial tile
 constexpr int small_pitch(int nb) { return 16 * nb + 4; }
-constexpr int small_lds(int mb, int nb)
+constexpr int small_lds(int mb, int nb, int waves)
 {
-    return SMALL_WAVES * (small_stages(mb, nb) * small_stage(mb, nb) > 16 * mb * small_pitch(nb) * 4
+    return waves * (small_stages(mb, nb) * small_stage(mb, nb) > 16 * mb * small_pitch(nb) * 4
                               ? small_stages(mb, nb) * small_stage(mb, nb) : 16 * mb * small_pitch(nb) * 4);
 }
 
@@ -202,7 +203,7 @@ __device__ inline void finish8(const DenseArgs &p, float (&x)[8], float (&u)[8],
 
 constexpr int small_columns(int epi, int nb) { return epi == EPI_GATED ? 8 * nb : 16 * nb; }
 
-template <class T, int LA, int LB, int EPI, class TO, int MB, int NB>
+template <class T, int LA, int LB, int EPI, class TO, int MB, int NB, int WAVES>
 __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *lds)
 {
     typedef typename Frag<T>::type frag_t;
@@ -222,7 +223,7 @@ __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *
 
     const int nk = (p.K + SMALL_BK - 1) / SMALL_BK;
     auto copies = [&](int s, unsigned slot) {
-        const int ks = wave + SMALL_WAVES * s;
+        const int ks = wave + WAVES * s;
         oa.copy(ks, ks < nk, slot, p.K);
         ob.copy(ks, ks < nk, slot, p.K);
     };
@@ -232,7 +233,7 @@ __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             acc[i][j] = f32x4{};
-    const int slices = wave < nk ? (nk - wave + SMALL_WAVES - 1) / SMALL_WAVES : 0;
+    const int slices = wave < nk ? (nk - wave + WAVES - 1) / WAVES : 0;
     if (slices > 0) {
         for (int s = 0; s < STAGES; ++s)
             copies(s, (unsigned)(s * STAGE));
@@ -288,7 +289,7 @@ __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *
         for (int e = 0; e < 8; ++e)
             x[e] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < SMALL_WAVES; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             const f32x4 lo = *reinterpret_cast<const f32x4 *>(at + w * PART), hi = *reinterpret_cast<const f32x4 *>(at + w * PART + 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -297,7 +298,7 @@ __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *
             }
         }
     };
-    for (int q = threadIdx.x; q < 16 * MB * RUNS; q += SMALL_THREADS) {
+    for (int q = threadIdx.x; q < 16 * MB * RUNS; q += 64 * WAVES) {
         const int r = q / RUNS, c = 8 * (q % RUNS);
         const int m = tm * 16 * MB + r, n = tn * COLS + c;
         if (m < p.M && n < p.N) {
@@ -325,10 +326,11 @@ __device__ inline int small_item(int items)
     return ((int)blockIdx.x >> 3) < run && item < items ? item : -1;
 }
 
-template <class T, int LA, int LB, int EPI, class TO, int MB, int NB>
-__global__ __launch_bounds__(SMALL_THREADS, 1) void dense_small_kernel(DenseArgs p)
+template <class T, int LA, int LB, int EPI, class TO, int MB, int NB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void dense_small_kernel(DenseArgs p)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[small_lds(MB, NB)];
+    static_assert(small_lds(MB, NB, WAVES) * (8 / WAVES) <= 163840, "8 / WAVES workgroups share a compute unit's LDS");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[small_lds(MB, NB, WAVES)];
     fetch_args(p);
     const int item = small_item(p.tiles * p.batch);
     if (item < 0)
@@ -337,7 +339,7 @@ __global__ __launch_bounds__(SMALL_THREADS, 1) void dense_small_kernel(DenseArgs
     int tm = 0, tn = item - b * p.tiles;
     if (p.tiles_m > 1)   // (few tokens: no divisions)
         dense_tile<EPI>(p, item - b * p.tiles, tm, tn);
-    small_tile<T, LA, LB, EPI, TO, MB, NB>(p, b, tm, tn, lds);
+    small_tile<T, LA, LB, EPI, TO, MB, NB, WAVES>(p, b, tm, tn, lds);
 }
 
 // Both products of a small backward pass and its bias gradient in one launch:
@@ -354,26 +356,25 @@ struct SmallBwdArgs {
     int first_b;
 };
 
-template <int BLOCKS>
-__global__ __launch_bounds__(SMALL_THREADS, 1) void dense_small_bwd_kernel(SmallBwdArgs p)
+template <int BLOCKS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void dense_small_bwd_kernel(SmallBwdArgs p)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[small_lds(BLOCKS, BLOCKS)];
+    constexpr int LDS = small_lds(BLOCKS, BLOCKS, WAVES);
+    static_assert(8 * WAVES * BIAS_PITCH * 4 <= LDS, "the bias blocks share the launch and its LDS");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
     const int ahead = p.first_b ? p.b.tiles : 0;
     const int item = (int)blockIdx.x - ahead;
     int tm, tn;
     if (item >= 0 && item < p.a.tiles) {
         dense_tile<EPI_STORE>(p.a, item, tm, tn);
-        small_tile<__bf16, ROW_K, COL_K, EPI_STORE, __bf16, BLOCKS, BLOCKS>(p.a, 0, tm, tn, lds);
+        small_tile<__bf16, ROW_K, COL_K, EPI_STORE, __bf16, BLOCKS, BLOCKS, WAVES>(p.a, 0, tm, tn, lds);
     } else if (item < p.a.tiles + p.b.tiles - ahead) {
         dense_tile<EPI_STORE>(p.b, item < 0 ? item + ahead : item - p.a.tiles, tm, tn);
-        small_tile<__bf16, COL_K, COL_K, EPI_STORE, __bf16, BLOCKS, BLOCKS>(p.b, 0, tm, tn, lds);
+        small_tile<__bf16, COL_K, COL_K, EPI_STORE, __bf16, BLOCKS, BLOCKS, WAVES>(p.b, 0, tm, tn, lds);
     } else {
-        bias_block(p.bias, item - (p.a.tiles + p.b.tiles - ahead), reinterpret_cast<float *>(lds));
+        bias_block<64 * WAVES>(p.bias, item - (p.a.tiles + p.b.tiles - ahead), reinterpret_cast<float *>(lds));
     }
 }
-
-static_assert(SMALL_THREADS == BIAS_THREADS, "the bias blocks share the launch");
-static_assert(64 * BIAS_PITCH * 4 <= small_lds(2, 2), "and its LDS");
 
 } // namespace dense
 } // namespace gemm355

@@ -75,6 +75,32 @@ def test_many_tiles_are_exact(kernel, M, N, K):
             assert torch.equal(got.get(), want.bfloat16().double().cpu())
 
 
+@pytest.mark.parametrize("choice", [g.LAYER_AUTO, g.LAYER_SMALL], ids=["auto", "small"])
+@pytest.mark.parametrize("M,N,K", [(1100, 1104, 1104), (64, 18000, 520), (2001, 664, 104), (170, 1528, 1608)])
+def test_small_tiles_around_one_per_unit_are_exact(choice, M, N, K):
+    # between one and two 64 x 64 tiles per compute unit, in one product or in
+    # both of a backward pass: workgroups of four waves, two to a unit
+    need_gpu()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(M)
+    A, B, dC = whole(gen, M, K), whole(gen, N, K), whole(gen, M, N, top=1)
+    print("choice", choice, M, N, K, flush=True)
+    C, dA, dB, dbias = Out(M, N), Out(M, K), Out(N, K), Out(N)
+    g.force_layer_kernel(choice)
+    try:
+        ws, nb, check = workspace(max(g.bias_act_res_workspace_size(M, N, K),
+                                      g.bias_act_bwd_workspace_size(M, N, K, g.ACT_NONE)))
+        g.gemm_bf16_nt_bias_act_res(M, N, K, A, B, None, g.ACT_NONE, None, None, C.t, ws, nb)
+        g.gemm_bf16_nt_bias_act_bwd(M, N, K, A, B, None, g.ACT_NONE, dC, dA.t, dB.t, dbias.t, ws, nb)
+        torch.cuda.synchronize()
+    finally:
+        g.force_layer_kernel(g.LAYER_AUTO)
+    check()
+    a, b, d = A.float(), B.float(), dC.float()
+    for got, want in ((C, a @ b.t()), (dA, d @ b), (dB, d.t().contiguous() @ a), (dbias, d.sum(0))):
+        assert torch.equal(got.get(), want.bfloat16().double().cpu())
+
+
 def test_kernels_agree_with_the_workspace_each_asks_for():
     need_gpu()
     M, N, K = 700, 1032, 520
