@@ -381,7 +381,7 @@ template <int EPI, class TO, int ACT, int EXTRA, int BJ>
 __device__ inline void finish_row(const DenseArgs &p, f32x4 (&x)[BJ], int m, int col, int lane, const u32x2 (&bias)[BJ],
                                   const u32x4 (&res)[BJ / 2], PackedRow<EPI, BJ> &out)
 {
-    static_assert(BJ % 4 == 0, "blocks are stored in pairs");
+    static_assert(BJ % (EPI == EPI_GATED ? 4 : 2) == 0, "blocks are stored in pairs");
     if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED) {
         if constexpr (EXTRA) {
 #pragma unroll

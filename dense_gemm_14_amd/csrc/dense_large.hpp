@@ -18,6 +18,8 @@
 //     timing. (Cutting the tail's steps into equal runs that cross tile borders
 //     balances better, but its workgroups read a strip's K range at different
 //     times: a step then took 2.2 us instead of 1.45, the L2s' hits lost.)
+//   * Tiles of 192 x 192 (six blocks to a wave's side) for symmetric products,
+//     where those leave fewer units idle.
 //   * Epilogues: those of dense_common.hpp.
 #pragma once
 
@@ -29,20 +31,22 @@ namespace dense {
 constexpr int BIG = 256;                      // output tile rows, and columns of B rows
 constexpr int BIG_BK = 64;
 constexpr int BIG_THREADS = 256;
-constexpr int BIG_UNIT = BIG * BIG_BK * 2;    // 32 KiB
 constexpr int BIG_SLOTS = 5;
-constexpr int BIG_COPIES = 8;                 // 1 KiB copies per wave and unit
 constexpr int BIG_FLOATS = BIG * BIG;
 constexpr int BIG_MIN_STEPS = 4;              // fewest steps of a work item
+// A wave's blocks per side, 8 or 6, give tiles of 256 or 192 rows; its 1 KiB
+// copies per unit are as many.
+constexpr int MID = 192;
+constexpr int big_unit(int blocks) { return 32 * blocks * BIG_BK * 2; }
 // Buffer resources and bases start BIG_SHIFT bytes early: copy j of a unit
 // carries the instruction offset 1024 (j % 4), which moves the LDS destination
 // and the global address alike, and the lane's offset stays non-negative.
 constexpr int BIG_SHIFT = 3 * 1024;
 
-static_assert(BIG_SLOTS * BIG_UNIT <= 163840, "LDS ring exceeds the 160 KiB of a gfx950 workgroup");
+static_assert(BIG_SLOTS * big_unit(8) <= 163840, "LDS ring exceeds the 160 KiB of a gfx950 workgroup");
 
 // Columns of C per tile.
-constexpr int big_columns(int epi) { return epi == EPI_GATED ? BIG / 2 : BIG; }
+constexpr int big_columns(int epi, int side = BIG) { return epi == EPI_GATED ? side / 2 : side; }
 
 __device__ inline void big_set_m0(unsigned lds_addr) { asm volatile("s_mov_b32 m0, %0" ::"s"(lds_addr) : "m0"); }
 template <int O>
@@ -68,39 +72,50 @@ __device__ inline int fresh_lane()
 // Keeps a row of accumulators in its accumulation registers up to this point:
 // without it the compiler moves all 64 blocks out before the epilogue starts,
 // which spills.
-__device__ inline void hold_row(f32x4 (&x)[8])
+template <int BJ>
+__device__ inline void hold_row(f32x4 (&x)[BJ])
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < BJ; ++j)
         asm volatile("" : "+a"(x[j]));
 }
 
-// Block pairs of a step, as in gemm_bf16.hpp: the first 32 walk block rows
-// 0..3 column by column, the last 32 rows 4..7; a fragment is read after the
-// last pair that uses its registers and at least eight pairs before its first
-// use.
-constexpr int big_pair_row(int q) { return (q < 32 ? 0 : 4) + (q & 3); }
-constexpr int big_pair_col(int q) { return (q & 31) >> 2; }
-constexpr int big_a_read_at(int i) { return i < 4 ? 34 + 4 * i : 8 + 6 * (i - 4); }
-constexpr int big_b_read_at(int j) { return 36 + 4 * j; }
-constexpr int BIG_B7_READ = 2;
-constexpr int big_a_copy_at(int q) { return 8 * q + 2; }
-constexpr int big_b_copy_at(int q, bool last) { return 32 + (last ? 2 : 8) * q; }
+// Block pairs of a step, as in gemm_bf16.hpp: the first half walks the upper
+// half of the block rows column by column, the second half the lower one; a
+// fragment is read after the last pair that uses its registers and at least
+// eight pairs before its first use.
+template <int BLOCKS>
+struct BigOrder {
+    static constexpr int HALF = BLOCKS * BLOCKS / 2, ROWS = BLOCKS / 2;
+    static constexpr int row(int q) { return (q < HALF ? 0 : ROWS) + q % ROWS; }
+    static constexpr int col(int q) { return q % HALF / ROWS; }
+    static constexpr int a_read_at(int i)
+    {
+        return BLOCKS == 8 ? (i < 4 ? 34 + 4 * i : 8 + 6 * (i - 4)) : i < 3 ? 19 + 3 * i : 5 + 3 * (i - 3);
+    }
+    static constexpr int b_read_at(int j) { return BLOCKS == 8 ? 36 + 4 * j : 21 + 3 * j; }   // but for the last j
+    static constexpr int LAST_B_READ = 2;
+    static constexpr int a_copy_at(int c) { return BLOCKS * c + 2; }
+    static constexpr int b_copy_at(int c, bool last) { return HALF + (last ? 2 : BLOCKS) * c; }
+};
 
 // TAIL: K is not a multiple of 64. The copies then go through the buffer form,
 // whose range check fills what lies past K with zeros (ROW_K: by an offset past
 // the range for the chunks past K; COL_K: those K rows lie past the operand).
-template <class T, int LA, int LB, int EPI, class TO, bool TAIL>
+template <class T, int LA, int LB, int EPI, class TO, bool TAIL, int BLOCKS = 8>
 __global__ __attribute__((amdgpu_flat_work_group_size(BIG_THREADS, BIG_THREADS), amdgpu_waves_per_eu(1, 1)))
 void dense_large_kernel(DenseArgs p)
 {
     typedef typename Frag<T>::type frag_t;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[BIG_SLOTS * BIG_UNIT];
+    static_assert(BLOCKS == 8 || (BLOCKS == 6 && LA == ROW_K && LB == ROW_K && EPI != EPI_GATED));
+    typedef BigOrder<BLOCKS> order;
+    constexpr int SIDE = 32 * BLOCKS, UNIT = big_unit(BLOCKS), COPIES = BLOCKS, COLS = big_columns(EPI, SIDE);
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[BIG_SLOTS * UNIT];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave & 1;   // 128-row half of the tile (A rows)
+    const int wm = wave & 1;   // half of the tile's rows (A rows)
     const int wn = wave >> 1;  // half of its B rows
     const int l16 = lane & 15, grp = lane >> 4;
     const int nk = (p.K + BIG_BK - 1) / BIG_BK;
@@ -136,13 +151,13 @@ void dense_large_kernel(DenseArgs p)
     // past M or N (ROW_K) are clamped to the last one, columns past them
     // (COL_K) to the last eight: they only feed outputs that are not stored.
     unsigned long long ga, gb;
-    unsigned voff[2][BIG_COPIES];
-    auto place_rows = [&](auto layout_c, unsigned (&o)[BIG_COPIES], int row0, int rows, bool gated) {
+    unsigned voff[2][COPIES];
+    auto place_rows = [&](auto layout_c, unsigned (&o)[COPIES], int row0, int rows, bool gated) {
         constexpr int L = decltype(layout_c)::value;
         const int ln = fresh_lane();
 #pragma unroll
-        for (int j = 0; j < BIG_COPIES; ++j) {
-            const int block = BIG_COPIES * wave + j;   // 1 KiB block of the unit
+        for (int j = 0; j < COPIES; ++j) {
+            const int block = COPIES * wave + j;   // 1 KiB block of the unit
             if constexpr (L == ROW_K) {
                 const int r = 8 * block + (ln >> 3);
                 const int c = swizzle_row(r, ln & 7);
@@ -165,28 +180,28 @@ void dense_large_kernel(DenseArgs p)
         dense_tile<EPI>(p, tile - b * p.tiles, tm, tn);
         ga = reinterpret_cast<unsigned long long>(p.a) + (unsigned long long)b * a_bytes - BIG_SHIFT;
         gb = reinterpret_cast<unsigned long long>(p.b) + (unsigned long long)b * b_bytes - BIG_SHIFT;
-        place_rows(Int<LA>{}, voff[0], tm * BIG, p.M, false);
-        place_rows(Int<LB>{}, voff[1], tn * big_columns(EPI), p.N, EPI == EPI_GATED);
+        place_rows(Int<LA>{}, voff[0], tm * SIDE, p.M, false);
+        place_rows(Int<LB>{}, voff[1], tn * COLS, p.N, EPI == EPI_GATED);
     };
     place_copies(item.tile);
     // ROW_K, per block parity: this lane's chunk of the last K step lies below K
     bool tail_ok[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-        tail_ok[j] = (nk - 1) * BIG_BK + 8 * swizzle_row(8 * (BIG_COPIES * wave + j) + (lane >> 3), lane & 7) < p.K;
+        tail_ok[j] = (nk - 1) * BIG_BK + 8 * swizzle_row(8 * (COPIES * wave + j) + (lane >> 3), lane & 7) < p.K;
 
     // Per-step bases, hidden from the optimiser at every step so that addresses
     // are formed where they are used instead of living in registers.
-    unsigned copy_base[2] = {lds_base + (unsigned)(BIG_COPIES * wave * 1024),
-                             lds_base + (unsigned)(BIG_COPIES * wave * 1024 + 4096)};
+    unsigned copy_base[2] = {lds_base + (unsigned)(COPIES * wave * 1024),
+                             lds_base + (unsigned)(COPIES * wave * 1024 + 4096)};
     // ROW_K: lane (l16, grp) reads row l16 of a block, chunk grp (first K half)
     // or 4 + grp. COL_K: rd[0] is the lane's place in segment 0 of the wave's
     // half, rd[1] the flip of the segment number (shifted to bytes).
     unsigned ra[2], rb[2];
     auto read_base = [&](auto layout_c, unsigned (&o)[2], int half) {
         if constexpr (decltype(layout_c)::value == ROW_K) {
-            o[0] = lds_base + (unsigned)((half * 128 + l16) * 128 + (swizzle_row(l16, grp) << 4));
-            o[1] = lds_base + (unsigned)((half * 128 + l16) * 128 + (swizzle_row(l16, 4 + grp) << 4));
+            o[0] = lds_base + (unsigned)((half * 16 * BLOCKS + l16) * 128 + (swizzle_row(l16, grp) << 4));
+            o[1] = lds_base + (unsigned)((half * 16 * BLOCKS + l16) * 128 + (swizzle_row(l16, 4 + grp) << 4));
         } else {
             o[0] = lds_base + (unsigned)((8 * grp + (l16 >> 2)) * 512 + half * 256 + (l16 & 3) * 8);
             o[1] = (unsigned)(((l16 >> 2) | ((grp & 1) << 2)) << 5);
@@ -200,7 +215,7 @@ void dense_large_kernel(DenseArgs p)
     unsigned ring[BIG_SLOTS];
 #pragma unroll
     for (int x = 0; x < BIG_SLOTS; ++x)
-        ring[x] = (unsigned)(x * BIG_UNIT);
+        ring[x] = (unsigned)(x * UNIT);
     auto rotate = [&]() {
         const unsigned r0 = ring[0], r1 = ring[1];
         ring[0] = ring[2];
@@ -210,8 +225,8 @@ void dense_large_kernel(DenseArgs p)
         ring[4] = r1;
     };
 
-    f32x4 acc[8][8];
-    frag_t fa[2][8], fb[2][8];
+    f32x4 acc[BLOCKS][BLOCKS];
+    frag_t fa[2][BLOCKS], fb[2][BLOCKS];
     typedef __attribute__((address_space(3))) const frag_t *lds_frag;
     auto read_half = [&](auto layout_c, const unsigned (&rd)[2], unsigned slot, int blk, int h) {
         if constexpr (decltype(layout_c)::value == ROW_K) {
@@ -251,7 +266,7 @@ void dense_large_kernel(DenseArgs p)
         }
     };
     auto mma2 = [&](int q) {
-        const int i = big_pair_row(q), j = big_pair_col(q);
+        const int i = order::row(q), j = order::col(q);
         asm volatile("" ::"v"(fb[1][j]), "v"(fa[1][i]));
         SCHED_FENCE();
         acc[i][j] = Frag<T>::mma(fb[0][j], fa[0][i], acc[i][j]);
@@ -263,7 +278,7 @@ void dense_large_kernel(DenseArgs p)
     // each of its two instructions.
     auto mma2_copies = [&](int q, int op, auto c_c, unsigned slot, unsigned ks_off, bool tail) {
         constexpr int c = decltype(c_c)::value;
-        const int i = big_pair_row(q), j = big_pair_col(q);
+        const int i = order::row(q), j = order::col(q);
         asm volatile("" ::"v"(fb[1][j]), "v"(fa[1][i]));
         big_set_m0(copy_base[c >> 1] + slot);
         SCHED_FENCE();
@@ -283,9 +298,9 @@ void dense_large_kernel(DenseArgs p)
     for (int u = 0; u < BIG_SLOTS - 1; ++u) {
         const int ks = item.first + (u >> 1);
         const unsigned off = (unsigned)ks * (u & 1 ? b_step : a_step);
-        static_for<BIG_COPIES / 2>([&](auto c_c) {
+        static_for<COPIES / 2>([&](auto c_c) {
             constexpr int c = decltype(c_c)::value;
-            big_set_m0(copy_base[c >> 1] + (unsigned)(u * BIG_UNIT));
+            big_set_m0(copy_base[c >> 1] + (unsigned)(u * UNIT));
             asm volatile("s_nop 0");
             copy(u & 1, Int<2 * c>{}, off, ks == nk - 1);
             copy(u & 1, Int<2 * c + 1>{}, off, ks == nk - 1);
@@ -297,8 +312,8 @@ void dense_large_kernel(DenseArgs p)
     constexpr bool REREAD = EPI == EPI_LINEAR || EPI == EPI_POLY;
     auto read_first = [&]() {
 #pragma unroll
-        for (int j = 0; j < 7; ++j) {
-            if (j < 4) {
+        for (int j = 0; j < BLOCKS - 1; ++j) {
+            if (j < BLOCKS / 2) {
                 read_a(ring[0], j);
                 SCHED_FENCE();
             }
@@ -318,40 +333,40 @@ void dense_large_kernel(DenseArgs p)
         asm volatile("" : "+v"(ra[0]), "+v"(ra[1]), "+v"(rb[0]), "+v"(rb[1]), "+s"(copy_base[0]), "+s"(copy_base[1]));
         const bool tail = TAIL && ks == nk - 1;
         const unsigned a_off = (unsigned)ks * a_step, b_off = (unsigned)ks * b_step;
-        static_for<32>([&](auto qc) {
+        static_for<order::HALF>([&](auto qc) {
             constexpr int q = decltype(qc)::value;
-            constexpr int d = big_a_copy_at(1) - big_a_copy_at(0);
-            if constexpr (q >= big_a_copy_at(0) && (q - big_a_copy_at(0)) % d == 0 && q <= big_a_copy_at(BIG_COPIES / 2 - 1))
-                mma2_copies(q, 0, Int<(q - big_a_copy_at(0)) / d>{}, ring[4], a_off, tail);
+            constexpr int a0 = order::a_copy_at(0), d = order::a_copy_at(1) - a0;
+            if constexpr (q >= a0 && (q - a0) % d == 0 && q <= order::a_copy_at(COPIES / 2 - 1))
+                mma2_copies(q, 0, Int<(q - a0) / d>{}, ring[4], a_off, tail);
             else
                 mma2(q);
-            if constexpr (q == BIG_B7_READ)
-                read_b(ring[1], 7);
+            if constexpr (q == order::LAST_B_READ)
+                read_b(ring[1], BLOCKS - 1);
 #pragma unroll
-            for (int i = 4; i < 8; ++i)
-                if (q == big_a_read_at(i))
+            for (int i = BLOCKS / 2; i < BLOCKS; ++i)
+                if (q == order::a_read_at(i))
                     read_a(ring[0], i);
             SCHED_VALU_ONLY();
         });
         wait_reads();
         if constexpr (!first)
-            wait_copies_le<BIG_COPIES>();
+            wait_copies_le<COPIES>();
         lds_barrier();
         SCHED_FENCE();
-        static_for<32>([&](auto qc) {
-            constexpr int q = 32 + decltype(qc)::value;
-            constexpr int b0 = big_b_copy_at(0, last), d = big_b_copy_at(1, last) - b0;
-            if constexpr (q >= b0 && (q - b0) % d == 0 && q <= big_b_copy_at(BIG_COPIES / 2 - 1, last))
+        static_for<order::HALF>([&](auto qc) {
+            constexpr int q = order::HALF + decltype(qc)::value;
+            constexpr int b0 = order::b_copy_at(0, last), d = order::b_copy_at(1, last) - b0;
+            if constexpr (q >= b0 && (q - b0) % d == 0 && q <= order::b_copy_at(COPIES / 2 - 1, last))
                 mma2_copies(q, 1, Int<(q - b0) / d>{}, ring[0], b_off, tail);
             else
                 mma2(q);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (q == big_a_read_at(i))
+            for (int i = 0; i < BLOCKS / 2; ++i)
+                if (q == order::a_read_at(i))
                     read_a(ring[2], i);
 #pragma unroll
-            for (int j = 0; j < 7; ++j)
-                if (q == big_b_read_at(j))
+            for (int j = 0; j < BLOCKS - 1; ++j)
+                if (q == order::b_read_at(j))
                     read_b(ring[3], j);
             SCHED_VALU_ONLY();
         });
@@ -362,9 +377,9 @@ void dense_large_kernel(DenseArgs p)
     for (;;) {
         // accumulators written to zero in place (see gemm_bf16.hpp)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < BLOCKS; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < BLOCKS; ++j) {
                 float zero;
                 asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
                 acc[i][j] = f32x4{zero, zero, zero, zero};
@@ -384,13 +399,13 @@ void dense_large_kernel(DenseArgs p)
         wait_all_copies();
 
         const int ln = fresh_lane();
-        if (item.steps < nk) {
+        if (BLOCKS == 8 && item.steps < nk) {
             f32x4 *ws = reinterpret_cast<f32x4 *>(p.ws) + (size_t)(item.at - p.whole) * (BIG_FLOATS / 4) + wave * 64 * 64 + ln;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < BLOCKS; ++i) {
                 hold_row(acc[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < BLOCKS; ++j)
                     ws[(i * 8 + j) * 64] = acc[i][j];
             }
         } else {
@@ -401,26 +416,26 @@ void dense_large_kernel(DenseArgs p)
             if (p.batch > 1)
                 enter_batch(q, b);
             const Views v = make_views<EPI>(q);
-            const int m0 = tm * BIG + 128 * wm;
-            const int col = tn * big_columns(EPI) + big_columns(EPI) / 2 * wn;
+            const int m0 = tm * SIDE + SIDE / 2 * wm;
+            const int col = tn * COLS + COLS / 2 * wn;
             with_epilogue<EPI>(q, [&](auto act_c, auto extra_c) {
                 constexpr int ACT = decltype(act_c)::value, EXTRA = decltype(extra_c)::value;
-                u32x2 bias[8];
+                u32x2 bias[BLOCKS];
                 load_bias_row<EPI, EXTRA>(q, v, col, ln, bias);
                 // residual rows are asked for AHEAD rows before their use, and
                 // before the stores of the row at hand
                 constexpr int AHEAD = 3;
-                u32x4 res[AHEAD][4];
+                u32x4 res[AHEAD][BLOCKS / 2];
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i)
-                    load_res_row<EPI, EXTRA, 8>(q, v, m0 + 16 * i + (ln & 15), col, ln, res[i]);
+                    load_res_row<EPI, EXTRA, BLOCKS>(q, v, m0 + 16 * i + (ln & 15), col, ln, res[i]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < BLOCKS; ++i) {
                     hold_row(acc[i]);
-                    PackedRow<EPI, 8> row;
+                    PackedRow<EPI, BLOCKS> row;
                     finish_row<EPI, TO, ACT, EXTRA>(q, acc[i], m0 + 16 * i + (ln & 15), col, ln, bias, res[i % AHEAD], row);
-                    if (i + AHEAD < 8)
-                        load_res_row<EPI, EXTRA, 8>(q, v, m0 + 16 * (i + AHEAD) + (ln & 15), col, ln, res[i % AHEAD]);
+                    if (i + AHEAD < BLOCKS)
+                        load_res_row<EPI, EXTRA, BLOCKS>(q, v, m0 + 16 * (i + AHEAD) + (ln & 15), col, ln, res[i % AHEAD]);
                     store_row<EXTRA>(q, v, row, m0 + 16 * i + (ln & 15), col, ln);
                     if constexpr (EPI >= EPI_STORE_SYM)
                         if ((i & 1) && tm != tn)

@@ -1,7 +1,8 @@
 // dense_ops.hip -- host side of the dense layer's fused operators: argument
 // checks, plans, workspace layout and launches of the kernels in
-// dense_tile.hpp, dense_grad.hpp and newton_schulz.hpp. The C ABI is declared
-// in include/gemm355.h. Nothing here allocates memory.
+// dense_large.hpp, dense_tile.hpp, dense_small.hpp, dense_grad.hpp and
+// newton_schulz.hpp. The C ABI is declared in include/gemm355.h. Nothing here
+// allocates memory.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -34,13 +35,14 @@ struct Shape {
     int batch;
     bool symmetric;
     bool gated;
+    bool row_k;       // both operands
 };
 
 // How a product runs on tiles of one size, in rounds of `grid` workgroups: the
 // first `whole` tiles one workgroup each, the K steps of the rest (fewer than a
 // round) split over as many workgroups as a round has.
 struct TilePlan {
-    int tiles_m, tiles_n, tiles, grid, whole, splits, steps_per_split;
+    int side, tiles_m, tiles_n, tiles, grid, whole, splits, steps_per_split;
     size_t workspace_bytes;
     double steps;     // of the busiest workgroup
 };
@@ -49,6 +51,7 @@ constexpr int kMaxSplits = 16;
 TilePlan plan_tiles(const Shape &s, int side, int cus, int min_steps, bool split)
 {
     TilePlan t = {};
+    t.side = side;
     t.tiles_m = (int)ceil_div(s.M, side);
     t.tiles_n = (int)ceil_div(s.N, s.gated ? side / 2 : side);
     t.tiles = s.symmetric ? t.tiles_m * (t.tiles_m + 1) / 2 : t.tiles_m * t.tiles_n;
@@ -75,7 +78,6 @@ TilePlan plan_tiles(const Shape &s, int side, int cus, int min_steps, bool split
 }
 
 TilePlan plan_tile(const Shape &s, int cus) { return plan_tiles(s, d::TILE, cus, 4, true); }
-TilePlan plan_large(const Shape &s, int cus, bool split) { return plan_tiles(s, d::BIG, cus, d::BIG_MIN_STEPS, split); }
 
 // The small-tile kernel's tile, in blocks of 16 rows of A and of B, and its
 // waves (8, or 4 with two workgroups per compute unit).
@@ -146,13 +148,28 @@ struct TileTimes {
     double fixed, step, step_full, round, split, split_mb;
 };
 constexpr TileTimes kTile = {2.2, 0.31, 0.22, 4.3, 5.1, 0.46}, kBig = {4.0, 1.19, 0.42, 6.0, 0.0, 0.0},
-                    kBigSplit = {1.6, 1.25, 0.0, 13.4, 1.6, 0.30};
+                    kBigSplit = {1.6, 1.25, 0.0, 13.4, 1.6, 0.30}, kMid = {4.0, 0.70, 0.25, 5.0, 0.0, 0.0};
 double time_tiles(const TilePlan &t, int batch, const TileTimes &c)
 {
     const int64_t items = t.whole + (int64_t(t.tiles) * batch - t.whole) * t.splits;
     const double fill = std::min(1.0, double(items) / t.grid);
     return c.fixed + t.steps * (c.step + c.step_full * fill) + double(ceil_div(items, t.grid)) * c.round +
            (t.splits > 1 ? c.split + c.split_mb * 1e-6 * double(t.workspace_bytes) : 0.0);
+}
+
+// 256 x 256 tiles; for a symmetric product that is not split 192 x 192 ones
+// where they are estimated faster. A K step of theirs takes two thirds of the
+// larger ones' time for 9/16 of the work, so they serve where the larger leave
+// units idle: 4096 x 4096 has 136 of those for 256 units and 253 of these (its
+// square 94 -> 66 us, X X^T of 4096 x 8192 169 -> 122). Other products fill a
+// round or have their last one split, without the factor of a triangle.
+TilePlan plan_large(const Shape &s, int cus, bool split)
+{
+    const TilePlan t = plan_tiles(s, d::BIG, cus, d::BIG_MIN_STEPS, split);
+    if (split || !s.symmetric || !s.row_k)
+        return t;
+    const TilePlan u = plan_tiles(s, d::MID, cus, d::BIG_MIN_STEPS, false);
+    return time_tiles(u, s.batch, kMid) < time_tiles(t, s.batch, kBig) ? u : t;
 }
 
 struct Choice {
@@ -178,7 +195,8 @@ Choice choose_kernel(const Shape &s, bool layer, int cus)
     offer(KERNEL_SMALL, time_small(plan_small_waves(s, layer, false, cus), nk, s.batch, cus));
     offer(KERNEL_NARROW, time_small(plan_small(s, layer, true, cus), nk, s.batch, cus));
     if (big_ok) {
-        offer(KERNEL_WHOLE, time_tiles(plan_large(s, cus, false), s.batch, kBig));
+        const TilePlan w = plan_large(s, cus, false);
+        offer(KERNEL_WHOLE, time_tiles(w, s.batch, w.side == d::MID ? kMid : kBig));
         const TilePlan b = plan_large(s, cus, true);
         if (b.splits > 1)
             offer(KERNEL_SPLIT, time_tiles(b, s.batch, kBigSplit));
@@ -262,9 +280,13 @@ int product_large(DenseArgs p, const TilePlan &t, hipStream_t stream)
     const int64_t tail = int64_t(t.tiles) * p.batch - t.whole;
     // persistent: a workgroup per compute unit at most, each an item per round
     p.grid = (int)std::min<int64_t>(t.grid, ceil_div(t.whole + tail * t.splits, 8) * 8);
-    int st = p.K % d::BIG_BK != 0
-        ? launch_kernel(d::dense_large_kernel<T, LA, LB, EPI, TO, true>, (unsigned)p.grid, (unsigned)d::BIG_THREADS, p, stream)
-        : launch_kernel(d::dense_large_kernel<T, LA, LB, EPI, TO, false>, (unsigned)p.grid, (unsigned)d::BIG_THREADS, p, stream);
+    const bool ragged = p.K % d::BIG_BK != 0;
+    auto kernel = ragged ? d::dense_large_kernel<T, LA, LB, EPI, TO, true> : d::dense_large_kernel<T, LA, LB, EPI, TO, false>;
+    if constexpr (EPI >= d::EPI_STORE_SYM && LA == d::ROW_K && LB == d::ROW_K)
+        if (t.side == d::MID)
+            kernel = ragged ? d::dense_large_kernel<T, LA, LB, EPI, TO, true, 6>
+                            : d::dense_large_kernel<T, LA, LB, EPI, TO, false, 6>;
+    int st = launch_kernel(kernel, (unsigned)p.grid, (unsigned)d::BIG_THREADS, p, stream);
     if (st == GEMM355_OK && tail > 0)
         st = launch_kernel(d::dense_large_reduce_kernel<EPI, TO>, (unsigned)ceil_div(tail * 16, d::BIG_REDUCE_WAVES),
                            64u * d::BIG_REDUCE_WAVES, p, stream);
@@ -606,8 +628,8 @@ OrthoPlan plan_ortho(int batch, int rows, int cols, int cus)
     const int m = std::min(rows, cols), n = std::max(rows, cols);
     const size_t x = align_up(size_t(batch) * rows * cols * 2), s = align_up(size_t(batch) * m * m * 2);
     OrthoPlan o = {};
-    o.gram = plan_product({m, m, n, batch, true, false}, false, cus);
-    o.square = plan_product({m, m, m, batch, true, false}, false, cus);
+    o.gram = plan_product({m, m, n, batch, true, false, rows <= cols}, false, cus);
+    o.square = plan_product({m, m, m, batch, true, false, true}, false, cus);
     o.update = plan_product({rows, cols, m, batch, false, false}, false, cus);
     o.norm_blocks = (int)std::min<int64_t>(d::NS_BLOCKS, ceil_div(int64_t(rows) * cols, d::NS_THREADS * 8));
     o.x1_at = x;

@@ -17,13 +17,15 @@
  *  - All array pointers are DEVICE pointers owned by the caller. The library
  *    allocates no memory, keeps no per-call state and never synchronises: it
  *    enqueues the work on `stream` and returns. The only scratch memory, the
- *    FP32 partials of a split K or the decoded operands of the decode-first
- *    NVFP4 path, is a workspace the caller passes to the *_ws entry points,
+ *    FP32 partials of a split K, the decoded operands of the decode-first
+ *    NVFP4 path or what the layer calls keep between their kernels, is a
+ *    workspace the caller passes to the *_ws entry points and the layer calls,
  *    or, for gemm_bf16_nt_noalloc only, a fixed static device array.
  *    `stream` is a hipStream_t passed as void*; NULL means the default (null)
  *    stream.
  *  - Arrays are dense, row-major, with no padding between rows (the leading
- *    dimension of A and B is K, that of C is N). C must not overlap any input.
+ *    dimension of A and B is K, that of C is N). C must not overlap any input
+ *    (but for the residual of gemm_bf16_nt_bias_act_res).
  *  - Only the M x N elements of C are written.
  *  - Results for inputs holding NaN or infinity are unspecified.
  *  - Every argument check happens before the first HIP runtime call, so a
@@ -36,11 +38,12 @@
  *  - Calls are thread-safe: the library holds no mutable state apart from a
  *    per-device cache of the compute-unit count, filled once under a lock,
  *    the overrides set by gemm355_force_instance, gemm355_force_supergroup,
- *    gemm355_force_schedule and gemm355_force_fp4_path (process-wide
- *    diagnostics), and two static device arrays that only opt-in paths use:
- *    the scratch of gemm_bf16_nt_noalloc and the tile counters of the
- *    dynamic tile order (gemm355_force_schedule(1)); calls that use either
- *    and overlap on one GPU race. Calls may be captured into HIP graphs.
+ *    gemm355_force_schedule, gemm355_force_fp4_path and
+ *    gemm355_force_layer_kernel (process-wide diagnostics), and two static
+ *    device arrays that only opt-in paths use: the scratch of
+ *    gemm_bf16_nt_noalloc and the tile counters of the dynamic tile order
+ *    (gemm355_force_schedule(1)); calls that use either and overlap on one GPU
+ *    race. Calls may be captured into HIP graphs.
  */
 #ifndef GEMM355_H
 #define GEMM355_H
@@ -445,8 +448,9 @@ int gemm_mxfp4_nt_bias_act(int M, int N, int K, const void *Aq, const void *SA, 
  *                    GEMM355_ERR_UNSUPPORTED, with nothing enqueued (that
  *                    call gives UNSUPPORTED for arrays that are too large
  *                    and otherwise the errors of
- *                    gemm_bf16_nt_workspace_size). NULL with 0 bytes is accepted where that is 0; NULL with
- *                    workspace_bytes > 0 is GEMM355_ERR_INVALID_ARG.
+ *                    gemm_bf16_nt_workspace_size). NULL with 0 bytes is
+ *                    accepted where that is 0; NULL with workspace_bytes > 0
+ *                    is GEMM355_ERR_INVALID_ARG.
  * Every output must be apart from every input, from the workspace and from the
  * other outputs, else GEMM355_ERR_INVALID_ARG (one exception: C may be R).
  * All arrays 16-byte aligned, sizes that are a row's length multiples of 8
@@ -571,11 +575,13 @@ int gemm355_newton_schulz_workspace_size(int batch, int rows, int cols, size_t *
  * gemm355_force_layer_kernel -- override the choice of kernel for the products
  * of the layer calls (gemm_bf16_nt_bias_act_res and those after it), a
  * process-wide diagnostic for tests and measurements: 0 (the default) by size,
- * 1 = 256 x 256 tiles, 2 = the same with the K steps of the last round's tiles
- * split over the workgroups, 3 = 128 x 128 tiles, 4 = 64 x 64 tiles, 5 = 32 x 32
- * tiles and, for few tokens, narrower ones. Products with K <= 192 take 128 x 128 tiles for 1 and 2. The workspace sizes follow the setting. Returns
- * GEMM355_OK, or GEMM355_ERR_INVALID_ARG for another value (setting
- * unchanged). No HIP call is made.
+ * 1 = 256 x 256 tiles (for symmetric products 192 x 192 ones where those take
+ * less time), 2 = 256 x 256 with the K steps of the last round's tiles split
+ * over the workgroups, 3 = 128 x 128 tiles, 4 = 64 x 64 tiles, 5 = 32 x 32 tiles
+ * and, for few tokens, narrower ones. Products with K <= 192 take 128 x 128
+ * tiles for 1 and 2. The workspace sizes follow the setting. Returns GEMM355_OK,
+ * or GEMM355_ERR_INVALID_ARG for another value (setting unchanged). No HIP call
+ * is made.
  */
 int gemm355_force_layer_kernel(int kernel);
 

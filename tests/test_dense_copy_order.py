@@ -25,13 +25,13 @@ COPIES, SLOTS, MIN_STEPS = 8, 5, 4
 def test_large_constants_match_the_kernel():
     s = _src("dense_large.hpp")
     assert "constexpr int BIG_SLOTS = %d;" % SLOTS in s
-    assert "constexpr int BIG_COPIES = %d;" % COPIES in s
+    assert "COPIES = BLOCKS," in s and "bool TAIL, int BLOCKS = %d>" % COPIES in s
     assert re.search(r"constexpr int BIG_MIN_STEPS = %d;" % MIN_STEPS, s)
-    assert re.search(r"if constexpr \(!first\)\s*wait_copies_le<BIG_COPIES>\(\);\s*lds_barrier\(\);", s)
-    assert "mma2_copies(q, 0, Int<(q - big_a_copy_at(0)) / d>{}, ring[4], a_off, tail);" in s
+    assert re.search(r"if constexpr \(!first\)\s*wait_copies_le<COPIES>\(\);\s*lds_barrier\(\);", s)
+    assert "mma2_copies(q, 0, Int<(q - a0) / d>{}, ring[4], a_off, tail);" in s
     assert "mma2_copies(q, 1, Int<(q - b0) / d>{}, ring[0], b_off, tail);" in s
     assert "read_a(ring[2], i);" in s and "read_b(ring[3], j);" in s
-    assert "read_a(ring[0], i);" in s and "read_b(ring[1], 7);" in s
+    assert "read_a(ring[0], i);" in s and "read_b(ring[1], BLOCKS - 1);" in s
     assert "read_a(ring[0], j);" in s and "read_b(ring[1], j);" in s      # read_first
     # an item: its first step, those in between, the last two; then every copy, the epilogue, the reads again
     assert re.search(r"step\(item.first \+ 2, Int<1>\{\}, Int<0>\{\}\);\s*for \(int s = 1; s < item.steps - 2; \+\+s\)", s)
@@ -41,18 +41,18 @@ def test_large_constants_match_the_kernel():
                      r"ring\[3\] = r0;\s*ring\[4\] = r1;", s)
 
 
-def large_run(items, reread):
-    w = Wave(SLOTS)
+def large_run(items, reread, blocks=COPIES):
+    w, copies = Wave(SLOTS), blocks
     A, B = (lambda t, k: ("A", t, k)), (lambda t, k: ("B", t, k))
     ring = list(range(SLOTS))
 
     def first(t):
-        for j in range(7):
-            if j < 4:
+        for j in range(blocks - 1):
+            if j < blocks // 2:
                 w.read(A(t, 0), ring[0])
             w.read(B(t, 0), ring[1])
     for u, unit in enumerate((A(0, 0), B(0, 0), A(0, 1), B(0, 1))):
-        w.copy(unit, u, COPIES)
+        w.copy(unit, u, copies)
     w.wait(0)
     w.barrier()
     first(0)
@@ -60,20 +60,20 @@ def large_run(items, reread):
         for s in range(n):
             kt, ks = (t, s + 2) if s + 2 < n else (t + 1, s + 2 - n)
             nt, nx = (t, s + 1) if s + 1 < n else (t + 1, 0)
-            w.copy(A(kt, ks), ring[4], COPIES)
+            w.copy(A(kt, ks), ring[4], copies)
             w.read(B(t, s), ring[1])
-            for _ in range(4):
+            for _ in range(blocks // 2):
                 w.read(A(t, s), ring[0])
             w.wait_reads()
             if s:
-                w.wait(COPIES)
+                w.wait(copies)
             w.barrier()
-            w.copy(B(kt, ks), ring[0], COPIES)
-            for _ in range(4):
+            w.copy(B(kt, ks), ring[0], copies)
+            for _ in range(blocks // 2):
                 w.read(A(nt, nx), ring[2])
-            for _ in range(7):
+            for _ in range(blocks - 1):
                 w.read(B(nt, nx), ring[3])
-            ring = [ring[2], ring[3], ring[4], ring[0], ring[1]]
+            ring = ring[2:] + ring[:2]
         w.wait(0)
         w.tick()            # the epilogue's stores: not ordered against copies
         if reread:
@@ -83,12 +83,41 @@ def large_run(items, reread):
 
 @pytest.mark.parametrize("reread", [False, True])
 @pytest.mark.parametrize("items", [[4], [4, 4, 4], [5, 9, 4], [40, 4, 17], [6, 6], [128, 9]])
-def test_large_order(items, reread):
-    large_run(items, reread)
+@pytest.mark.parametrize("blocks", [8, 6])
+def test_large_order(items, reread, blocks):
+    large_run(items, reread, blocks)
+
+
+@pytest.mark.parametrize("blocks", [8, 6])
+def test_large_fragments_are_read_between_their_uses(blocks):
+    # after the last pair that uses a fragment's registers, eight pairs before
+    # the next that does; from a unit whose copies the middle of the step waits for
+    s = _src("dense_large.hpp")
+    half, rows = blocks * blocks // 2, blocks // 2
+    for text in ("row(int q) { return (q < HALF ? 0 : ROWS) + q % ROWS; }", "col(int q) { return q % HALF / ROWS; }",
+                 "BLOCKS == 8 ? (i < 4 ? 34 + 4 * i : 8 + 6 * (i - 4)) : i < 3 ? 19 + 3 * i : 5 + 3 * (i - 3);",
+                 "BLOCKS == 8 ? 36 + 4 * j : 21 + 3 * j; }", "LAST_B_READ = 2;",
+                 "return BLOCKS * c + 2; }", "return HALF + (last ? 2 : BLOCKS) * c; }"):
+        assert text in s, text
+    pairs = 2 * half
+    uses = [((0 if q < half else rows) + q % rows, q % half // rows) for q in range(pairs)]
+    assert sorted(uses) == [(i, j) for i in range(blocks) for j in range(blocks)]
+    a_read = [(34 + 4 * i if i < 4 else 8 + 6 * (i - 4)) if blocks == 8 else (19 + 3 * i if i < 3 else 5 + 3 * (i - 3))
+              for i in range(blocks)]
+    b_read = [36 + 4 * j if blocks == 8 else 21 + 3 * j for j in range(blocks - 1)] + [2]
+    for at, which in [(a, ("A", i)) for i, a in enumerate(a_read)] + [(b, ("B", j)) for j, b in enumerate(b_read)]:
+        used = [q for q, (i, j) in enumerate(uses) if which in (("A", i), ("B", j))]
+        if at >= half:     # the next step's
+            assert max(used) <= at < pairs and min(used) + pairs - at >= 8
+        else:              # this step's
+            assert min(used) - at >= 8 and max(used) - pairs <= at
+    for last in (False, True):     # every copy has its pair, in the half that may overwrite the slot
+        assert 2 + blocks * (blocks // 2 - 1) < half and (2 if last else blocks) * (blocks // 2 - 1) < half
 
 
 def test_large_model_catches_a_looser_wait():
     _fails_with_looser_waits(lambda nk, tiles: large_run([nk] * tiles, True), 8)
+    _fails_with_looser_waits(lambda nk, tiles: large_run([nk] * tiles, True, 6), 8)
 
 
 # ---- 128 x 128 -------------------------------------------------------------------

@@ -49,6 +49,24 @@ def test_newton_schulz(kernel, shape):
     assert rel <= 15 ** 0.5 * 2.0 ** -11 * 2 + 2.0 ** -8 / 3 ** 0.5, rel
 
 
+@pytest.mark.parametrize("batch,side", [(20, 784), (5, 1160)], ids=["256-tiles", "192-tiles"])
+def test_newton_schulz_whole_symmetric_tiles(batch, side):
+    # whole 256 x 256 tiles where 192 x 192 ones need another round, and those
+    # over more than one round's and with ragged edges
+    need_gpu()
+    gen = gen_of(batch, side, 39)
+    G = torch.randn(batch, side, side, generator=gen)
+    g.force_layer_kernel(g.LAYER_LARGE)
+    try:
+        print("newton schulz", batch, side, flush=True)
+        got = run_ortho(G, 2)
+    finally:
+        g.force_layer_kernel(g.LAYER_AUTO)
+    want = ortho_exact(G.cuda(), 2, (3.4445, -4.7750, 2.0315), 1e-7).cpu()
+    rel = ((got - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)).max().item()
+    assert rel <= 6 ** 0.5 * 2.0 ** -11 * 2 + 2.0 ** -8 / 3 ** 0.5, rel
+
+
 def whole(gen, *shape, top=2):
     return torch.randint(-top, top + 1, shape, generator=gen, device="cuda").to(torch.bfloat16)
 
