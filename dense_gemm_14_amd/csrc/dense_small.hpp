@@ -20,6 +20,13 @@
 //   * Tiles: 64 x 64; 32 x 32 where those leave compute units idle; for few tokens
 //     16 or 32 rows against 16 columns of weights (16 + 16 of a gated layer), so
 //     that every compute unit has weights to stream.
+//
+// Measured (BF16, operands in cache, one launch behind the other, which alone
+// takes 2.6 us): 1 x 1024 x 1024 3.5 us; 1 x 4096 x 4096 5.2, and 7.4 with the
+// weights in HBM, 4.5 TB/s; 64 x 512 x 512 3.7; 333 x 1032 x 2056 8.9; 1024^3
+// 6.8. Both products of a backward pass of 301 tokens, 1384 gated columns and K =
+// 512 in one launch: 13 us. Bounded by latency: the launch, then the memory's
+// once per slice that a wave takes.
 #pragma once
 
 #include "dense_common.hpp"
