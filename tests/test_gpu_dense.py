@@ -284,6 +284,6 @@ def test_feed_forward_block_runs_together():
     close(dW1.get(), *r["dB"], "dW1")
     for O, G in ((U1, dW1), (U2, dW2)):
         want = ortho_exact(G.get()[None], 5, (3.4445, -4.7750, 2.0315), 1e-7)[0]
-        # the gradients of few tokens have a wide spectrum: the small
-        # directions carry the FP16 rounding of the large ones
-        assert ((O.get() - want).norm() / want.norm()).item() <= 2e-2
+        # as in test_newton_schulz: these gradients' singular values, 0.003 to 0.2
+        # of the norm, all grow to about 1 within the five steps
+        assert ((O.get() - want).norm() / want.norm()).item() <= 15 ** 0.5 * 2.0 ** -11 * 2 + 2.0 ** -8 / 3 ** 0.5
