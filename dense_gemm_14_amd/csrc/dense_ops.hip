@@ -80,7 +80,7 @@ TilePlan plan_tiles(const Shape &s, int side, int cus, int min_steps, bool split
 TilePlan plan_tile(const Shape &s, int cus) { return plan_tiles(s, d::TILE, cus, 4, true); }
 
 // The small-tile kernel's tile, in blocks of 16 rows of A and of B, and its
-// waves (8, or 4 with two workgroups per compute unit).
+// waves (8, or fewer with more workgroups per compute unit).
 struct SmallPlan {
     int mb, nb, waves, tiles_m, tiles_n, tiles;
 };
@@ -131,18 +131,30 @@ double time_small(const SmallPlan &t, int nk, int batch, int cus)
     const double tiles = double(t.tiles) * batch, slots = small_slots(t, cus);
     return kStart + ceil(tiles / slots) * time_small_tile(t, nk, std::min(1.0, tiles / slots));
 }
-// 64 x 64 tiles with four waves where that is estimated faster: two workgroups
-// then share a compute unit, so a second round begins at twice as many tiles.
-// Measured, eight waves against four (us): 1024 x 1152 x 1024, 288 tiles, 11.8
-// against 8.7; 64 x 18000 x 512 9.7 against 6.6; a backward pass of 170 x 1528 x
-// 1608 15.1 against 9.8. Eight waves keep long contractions of few tiles, where
-// a wave's share of K is what takes the time (1024 x 1024 x 1024: 6.9).
+// 64 x 64 tiles with fewer waves, and so more workgroups to a unit, where that is
+// estimated faster; two waves or one only for what is more than a round of the
+// next larger. Measured, before and after (us): eight waves and four, 1024 x 1152
+// x 1024, 288 tiles, 11.8 and 8.7; 64 x 18000 x 512 9.7 and 6.6; a backward pass
+// of 170 x 1528 x 1608 15.1 and 9.8. Four waves and fewer: 1310 x 6288 x 168, 2079
+// tiles of three slices, 18.6 and 12.6; a gated layer of 877 x 2344 x 72 10.0 and
+// 6.8. Eight waves keep long contractions of few tiles, where a wave's share of K
+// is what takes the time (1024 x 1024 x 1024: 6.9), and four the short ones: eight
+// matrices of 64 x 512 orthogonalised in 53.6, with one wave 57.4.
 SmallPlan plan_small_waves(const Shape &s, bool layer, bool narrow, int cus)
 {
-    SmallPlan t = plan_small(s, layer, narrow, cus), u = t;
-    u.waves = 4;
+    SmallPlan best = plan_small(s, layer, narrow, cus);
     const int nk = (int)ceil_div(s.K, d::SMALL_BK);
-    return !narrow && time_small(u, nk, s.batch, cus) < time_small(t, nk, s.batch, cus) ? u : t;
+    if (!narrow)
+        for (int waves = 4; waves >= 1; waves /= 2) {
+            SmallPlan t = best;
+            t.waves = 2 * waves;
+            if (waves < 4 && int64_t(t.tiles) * s.batch <= small_slots(t, cus))
+                break;
+            t.waves = waves;
+            if (time_small(t, nk, s.batch, cus) < time_small(best, nk, s.batch, cus))
+                best = t;
+        }
+    return best;
 }
 struct TileTimes {
     double fixed, step, step_full, round, split, split_mb;
@@ -244,8 +256,12 @@ int product_small(DenseArgs p, const SmallPlan &t, hipStream_t stream)
     }
     if (t.mb == 2)
         return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 2, 8>, blocks, threads, p, stream);
-    return t.waves == 8 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 8>, blocks, threads, p, stream)
-                        : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 4>, blocks, threads, p, stream);
+    switch (t.waves) {
+    case 1: return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 1>, blocks, threads, p, stream);
+    case 2: return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 2>, blocks, threads, p, stream);
+    case 4: return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 4>, blocks, threads, p, stream);
+    default: return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 8>, blocks, threads, p, stream);
+    }
 }
 
 void set_plan(DenseArgs &p, const TilePlan &t)

@@ -6,8 +6,9 @@
 //     WAVES, ... and computes the whole tile for them, so no LDS byte is read twice
 //     and the waves never wait for each other until they add their sums. Eight
 //     waves fill a compute unit; where there are more tiles than units, 64 x 64
-//     tiles also run with four, two workgroups to a unit, so that the last tiles
-//     do not wait for a unit of their own.
+//     tiles also run with four, two or one, as many more workgroups to a unit, so
+//     that the last tiles do not wait for a unit of their own and short
+//     contractions leave no wave idle.
 //   * A wave copies its slices through the memory pipeline into its own LDS
 //     ring (SMALL_STAGES stages of 2 KiB per block and slice): it waits for a
 //     stage, reads the whole slice into registers, refills the stage at once and

@@ -94,10 +94,12 @@ def test_many_tiles_are_exact(kernel, M, N, K):
 
 
 @pytest.mark.parametrize("choice", [g.LAYER_AUTO, g.LAYER_SMALL], ids=["auto", "small"])
-@pytest.mark.parametrize("M,N,K", [(1100, 1104, 1104), (64, 18000, 520), (2001, 664, 104), (170, 1528, 1608)])
+@pytest.mark.parametrize("M,N,K", [(1100, 1104, 1104), (64, 18000, 520), (2001, 664, 104), (170, 1528, 1608),
+                                   (1310, 6288, 168), (4100, 4104, 72)])
 def test_small_tiles_around_one_per_unit_are_exact(choice, M, N, K):
     # between one and two 64 x 64 tiles per compute unit, in one product or in
-    # both of a backward pass: workgroups of four waves, two to a unit
+    # both of a backward pass: workgroups of four waves, two to a unit; the last
+    # two, about eight and sixteen of a short contraction: of one
     need_gpu()
     gen = torch.Generator(device="cuda")
     gen.manual_seed(M)
