@@ -475,10 +475,14 @@ int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const
 
 // Whether a backward pass runs as one launch of small tiles (KERNEL_SMALL or
 // KERNEL_NARROW; 0: its products one by one); pa, pb: the plans of the products
-// that are wanted. Together the tiles fill the compute units better and two
-// launches of about 3 us fall away. Estimate: the tiles' time shared out over
-// the units, and no less than the longest tile.
-constexpr double kLaunches = 6.0;
+// that are wanted. Together the tiles fill the compute units better and launches
+// fall away, the bias gradient's too. Estimate: the tiles' time shared out over
+// the units, and no less than the longest tile; it comes out a tenth too short,
+// and what separate launches cost is in each one's own estimate already. (Over
+// 140 backward passes of up to 4096 tokens: ten vectors of 7336 x 328 weights,
+// 115 slices of which one tile of dA takes every eighth, 22 us together, 14 apart;
+// 170 x 1528 x 1608 10.5 together, 28 as two products of 128 x 128 tiles.)
+constexpr double kTogether = 1.1, kBiasLaunch = 1.0;
 Together backward_together(const Shape &a, const ProductPlan *pa, const Shape &b, const ProductPlan *pb, int cus)
 {
     const bool small = (!pa || pa->kernel >= KERNEL_SMALL) && (!pb || pb->kernel >= KERNEL_SMALL);
@@ -488,7 +492,7 @@ Together backward_together(const Shape &a, const ProductPlan *pa, const Shape &b
     const bool forced = pa->us == 0.0;
     if (forced && !small)
         return {0, 0};
-    double best_us = forced ? 1e30 : kLaunches + pa->us + pb->us;
+    double best_us = forced ? 1e30 : (pa->us + pb->us) / kTogether + kBiasLaunch;
     Together best = {0, 0};
     for (const Together &how : {Together{KERNEL_SMALL, 8}, Together{KERNEL_SMALL, 4}, Together{KERNEL_NARROW, 8}}) {
         if (forced && how.kernel != pa->kernel)
