@@ -237,30 +237,37 @@ ProductPlan plan_product(const Shape &s, bool layer, int cus)
     return p;
 }
 
+// One instance of the small-tile kernel; its threads are the instance's own.
+template <class T, int LA, int LB, int EPI, class TO, int MB, int NB, int WAVES>
+int launch_small(unsigned blocks, DenseArgs &p, hipStream_t stream)
+{
+    return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, MB, NB, WAVES>, blocks, 64u * WAVES, p, stream);
+}
+
 template <class T, int LA, int LB, int EPI, class TO>
 int product_small(DenseArgs p, const SmallPlan &t, hipStream_t stream)
 {
     p.tiles_m = t.tiles_m;
     p.tiles_n = t.tiles_n;
     p.tiles = t.tiles;
-    const unsigned blocks = (unsigned)(ceil_div(int64_t(t.tiles) * p.batch, 8) * 8), threads = 64u * t.waves;
+    const unsigned blocks = (unsigned)(ceil_div(int64_t(t.tiles) * p.batch, 8) * 8);
     if constexpr (EPI == d::EPI_LINEAR) {
         if (t.nb == 1)
-            return t.mb == 1 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 1, 8>, blocks, threads, p, stream)
-                             : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 1, 8>, blocks, threads, p, stream);
+            return t.mb == 1 ? launch_small<T, LA, LB, EPI, TO, 1, 1, 8>(blocks, p, stream)
+                             : launch_small<T, LA, LB, EPI, TO, 2, 1, 8>(blocks, p, stream);
     }
     if constexpr (EPI == d::EPI_LINEAR || EPI == d::EPI_GATED) {
         if (t.mb == 1)
-            return t.nb == 2 ? launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 2, 8>, blocks, threads, p, stream)
-                             : launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 1, 4, 8>, blocks, threads, p, stream);
+            return t.nb == 2 ? launch_small<T, LA, LB, EPI, TO, 1, 2, 8>(blocks, p, stream)
+                             : launch_small<T, LA, LB, EPI, TO, 1, 4, 8>(blocks, p, stream);
     }
     if (t.mb == 2)
-        return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 2, 2, 8>, blocks, threads, p, stream);
+        return launch_small<T, LA, LB, EPI, TO, 2, 2, 8>(blocks, p, stream);
     switch (t.waves) {
-    case 1: return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 1>, blocks, threads, p, stream);
-    case 2: return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 2>, blocks, threads, p, stream);
-    case 4: return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 4>, blocks, threads, p, stream);
-    default: return launch_kernel(d::dense_small_kernel<T, LA, LB, EPI, TO, 4, 4, 8>, blocks, threads, p, stream);
+    case 1: return launch_small<T, LA, LB, EPI, TO, 4, 4, 1>(blocks, p, stream);
+    case 2: return launch_small<T, LA, LB, EPI, TO, 4, 4, 2>(blocks, p, stream);
+    case 4: return launch_small<T, LA, LB, EPI, TO, 4, 4, 4>(blocks, p, stream);
+    default: return launch_small<T, LA, LB, EPI, TO, 4, 4, 8>(blocks, p, stream);
     }
 }
 
@@ -447,8 +454,15 @@ struct Together {
     int kernel, waves;
 };
 
+template <int BLOCKS, int WAVES>
+int launch_small_bwd(unsigned blocks, d::SmallBwdArgs &g, hipStream_t s)
+{
+    return launch_kernel(d::dense_small_bwd_kernel<BLOCKS, WAVES>, blocks, 64u * WAVES, g, s);
+}
+
 // A backward pass whose products are small, in one launch: 32 x 32 tiles, or
-// 64 x 64 with eight or four waves.
+// 64 x 64 with eight or four waves (there are no other instances; what plans
+// fewer waves runs product by product).
 int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const d::BiasArgs &bias, int bias_blocks,
                    const Together &how, int cus, hipStream_t s)
 {
@@ -467,10 +481,10 @@ int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const
     g.bias = bias;
     g.bias_blocks = bias_blocks;
     g.first_b = pb.K > pa.K;
-    const unsigned blocks = (unsigned)(pa.tiles + pb.tiles + bias_blocks), threads = 64u * how.waves;
-    return how.kernel == KERNEL_NARROW ? launch_kernel(d::dense_small_bwd_kernel<2, 8>, blocks, threads, g, s)
-           : how.waves == 8            ? launch_kernel(d::dense_small_bwd_kernel<4, 8>, blocks, threads, g, s)
-                                       : launch_kernel(d::dense_small_bwd_kernel<4, 4>, blocks, threads, g, s);
+    const unsigned blocks = (unsigned)(pa.tiles + pb.tiles + bias_blocks);
+    if (how.kernel == KERNEL_NARROW)
+        return launch_small_bwd<2, 8>(blocks, g, s);
+    return how.waves == 8 ? launch_small_bwd<4, 8>(blocks, g, s) : launch_small_bwd<4, 4>(blocks, g, s);
 }
 
 // Whether a backward pass runs as one launch of small tiles (KERNEL_SMALL or
@@ -485,11 +499,16 @@ int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const
 constexpr double kTogether = 1.1, kBiasLaunch = 1.0;
 Together backward_together(const Shape &a, const ProductPlan *pa, const Shape &b, const ProductPlan *pb, int cus)
 {
-    const bool small = (!pa || pa->kernel >= KERNEL_SMALL) && (!pb || pb->kernel >= KERNEL_SMALL);
-    if (!pa || !pb)   // alone, a product runs as it would anywhere
-        return !small ? Together{0, 0} : pa ? Together{pa->kernel, pa->small.waves} : pb ? Together{pb->kernel, pb->small.waves}
-                                                                                         : Together{KERNEL_SMALL, 8};
-    const bool forced = pa->us == 0.0;
+    if (!pa && !pb)   // the bias gradient alone
+        return {KERNEL_SMALL, 8};
+    if (!pa || !pb) {
+        // alone, a product runs as it would anywhere: beside the bias gradient in
+        // one launch where that has the planned tiles and waves, else by itself
+        const ProductPlan &one = pa ? *pa : *pb;
+        const bool has = one.kernel == KERNEL_NARROW || (one.kernel == KERNEL_SMALL && one.small.waves >= 4);
+        return has ? Together{one.kernel, one.small.waves} : Together{0, 0};
+    }
+    const bool small = pa->kernel >= KERNEL_SMALL && pb->kernel >= KERNEL_SMALL, forced = pa->us == 0.0;
     if (forced && !small)
         return {0, 0};
     double best_us = forced ? 1e30 : (pa->us + pb->us) / kTogether + kBiasLaunch;
