@@ -655,6 +655,9 @@ int layer_backward_workspace(int M, int N, int K, int act, size_t *bytes)
 // stored: the Gram matrix is X X^T of a wide and X^T X of a tall matrix, and
 // the update P X or X P.
 constexpr float kPolyScale = 256.0f;   // S and P are held times this
+// X is held times this, as large as loses nothing at the top: an element of 16,
+// FP16's largest value then, makes a diagonal element of S overflow too.
+constexpr float kIterateScale = 4096.0f;
 
 struct OrthoPlan {
     ProductPlan gram, square, update;
@@ -692,14 +695,14 @@ int ortho_start(const d::NormArgs &n, int batch, hipStream_t s)
 // One Newton-Schulz step from x to out (BF16 and unscaled after the last).
 template <bool WIDE, class TO>
 int ortho_step(const OrthoPlan &o, int batch, int rows, int cols, const void *x, uint8_t *ws, void *out, float a, float b,
-               float c, float scale, bool last, hipStream_t s)
+               float c, bool last, hipStream_t s)
 {
     typedef _Float16 h;
     const int m = WIDE ? rows : cols, n = WIDE ? cols : rows;
     void *S = ws + o.s_at, *P = ws + o.p_at, *partials = ws + o.partials_at;
     DenseArgs p = args_of(m, m, n, x, x, S);
     p.batch = batch;
-    p.alpha = kPolyScale / (scale * scale);
+    p.alpha = kPolyScale / (kIterateScale * kIterateScale);
     int st = WIDE ? product<h, d::ROW_K, d::ROW_K, d::EPI_STORE_SYM>(p, o.gram, partials, s)
                   : product<h, d::COL_K, d::COL_K, d::EPI_STORE_SYM>(p, o.gram, partials, s);
     if (st != GEMM355_OK)
@@ -715,7 +718,7 @@ int ortho_step(const OrthoPlan &o, int batch, int rows, int cols, const void *x,
         return st;
     p = WIDE ? args_of(rows, cols, m, P, x, out) : args_of(rows, cols, m, x, P, out);
     p.batch = batch;
-    p.alpha = (last ? 1.0f / scale : 1.0f) / kPolyScale;
+    p.alpha = (last ? 1.0f / kIterateScale : 1.0f) / kPolyScale;
     // P = P^T: as the right-hand operand its rows are its columns
     return WIDE ? product<h, d::ROW_K, d::COL_K, d::EPI_STORE, TO>(p, o.update, partials, s)
                 : product<h, d::ROW_K, d::ROW_K, d::EPI_STORE, TO>(p, o.update, partials, s);
@@ -832,15 +835,13 @@ extern "C" int gemm355_newton_schulz(int batch, int rows, int cols, int g_type, 
 
     const hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    // a power of two near sqrt(min(rows, cols)): exact to scale by
-    const float scale = exp2f(ceilf(0.5f * log2f((float)std::min(rows, cols))));
     d::NormArgs n = {};
     n.g = G;
     n.partial = reinterpret_cast<double *>(ws + o.norm_at);
     n.x = reinterpret_cast<uint16_t *>(ws);
     n.elements = elements;
     n.blocks = o.norm_blocks;
-    n.scale = scale;
+    n.scale = kIterateScale;
     n.eps = eps;
     int st = g_type == GEMM355_FP32 ? ortho_start<true>(n, batch, s) : ortho_start<false>(n, batch, s);
     uint8_t *x = ws, *next = ws + o.x1_at;
@@ -848,7 +849,7 @@ extern "C" int gemm355_newton_schulz(int batch, int rows, int cols, int g_type, 
         const bool last = i == steps - 1, wide = rows <= cols;
         auto step = wide ? (last ? ortho_step<true, __bf16> : ortho_step<true, _Float16>)
                          : (last ? ortho_step<false, __bf16> : ortho_step<false, _Float16>);
-        st = step(o, batch, rows, cols, x, ws, last ? O : next, a, b, c, scale, last, s);
+        st = step(o, batch, rows, cols, x, ws, last ? O : next, a, b, c, last, s);
         std::swap(x, next);
     }
     return st;

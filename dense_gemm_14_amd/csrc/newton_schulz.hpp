@@ -8,8 +8,11 @@
 // FP16, not BF16, carries the iterates: both have the same matrix rate, the
 // singular values stay below about 1.3, and three more bits keep five steps'
 // rounding at 1.5e-3 of the result where BF16 iterates lose 1e-2. X is held
-// times 2^e, about sqrt(min(rows, cols)), which makes its elements of order
-// 1 / sqrt(max(rows, cols)) at the start: FP16's normal range.
+// times 2^12: that puts the elements, about |G| / (|G| + eps) / sqrt(rows cols)
+// at the start, into FP16's normal range also where eps outweighs the norm (down
+// to a share of 2^-26 sqrt(rows cols) of it; with a scale of sqrt(min(rows,
+// cols)) a share of 1e-4 of 256 x 1032 lost 6e-3 and of 1e-5 6e-2), and X reaches
+// FP16's largest value no earlier than X X^T does.
 //
 // Bound by memory: 4096 x 8192 of FP32 are read in 28 us (4.8 TB/s, what a copy
 // reaches) and read again and written in 30, of 1970 to 2050 for all five steps.

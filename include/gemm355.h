@@ -559,12 +559,13 @@ typedef enum gemm355_type {
  *          are safe); (3.4445, -4.7750, 2.0315) is a common choice
  *   eps    >= 0, finite; a zero matrix gives zeros
  * The norm is taken in FP64. X, S and a I + b S + c S^2 are rounded to FP16
- * between the products, X held times a power of two near sqrt(min(rows, cols))
- * and the other two times 256 so that they stay in its normal range; sums are
- * FP32. For matrices of independent entries that is within 2e-3 of the exact
- * result (2-norm, relative) before O's own rounding; directions whose singular
- * value is far below the norm carry more. The symmetric S and S^2 are computed
- * on and below the diagonal only.
+ * between the products, X held times 4096 and the other two times 256 so that
+ * they stay in its normal range; sums are FP32. For matrices of independent
+ * entries that is within 2e-3 of the exact result (2-norm, relative) before O's
+ * own rounding, as long as ||G||_F is at least 2^-26 sqrt(rows cols) times
+ * ||G||_F + eps (below, X starts among FP16's subnormals); directions whose
+ * singular value is far below the norm carry more. The symmetric S and S^2 are
+ * computed on and below the diagonal only.
  * rows and cols multiples of 8; batch 0, rows 0 or cols 0 does nothing.
  */
 int gemm355_newton_schulz(int batch, int rows, int cols, int g_type, const void *G, int steps, float a, float b,
