@@ -498,9 +498,17 @@ def _layers():
     return _bound
 
 
+def _int32(v) -> int:
+    """A number for a C int (ctypes would cut it to its low 32 bits)."""
+    v = int(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise OverflowError("size beyond 32 bits")
+    return v
+
+
 def _size_of(fn, *args) -> int:
     out = ctypes.c_size_t(0)
-    _check(getattr(load(), fn)(*args, ctypes.byref(out)), fn)
+    _check(getattr(load(), fn)(*map(_int32, args), ctypes.byref(out)), fn)
     return out.value
 
 
@@ -519,7 +527,7 @@ def gemm_bf16_nt_bias_act_res(M: int, N: int, K: int, A, B, bias, activation: in
 
 def bias_act_res_workspace_size(M: int, N: int, K: int) -> int:
     """Workspace bytes of gemm_bf16_nt_bias_act_res on the current device."""
-    return _size_of("gemm_bf16_nt_bias_act_res_workspace_size", int(M), int(N), int(K))
+    return _size_of("gemm_bf16_nt_bias_act_res_workspace_size", M, N, K)
 
 
 def gemm_bf16_nt_bias_act_bwd(M: int, N: int, K: int, A, B, Z, activation: int, dC, dA, dB, dbias, workspace=None,
@@ -536,7 +544,7 @@ def gemm_bf16_nt_bias_act_bwd(M: int, N: int, K: int, A, B, Z, activation: int, 
 
 def bias_act_bwd_workspace_size(M: int, N: int, K: int, activation: int) -> int:
     """Workspace bytes of gemm_bf16_nt_bias_act_bwd on the current device."""
-    return _size_of("gemm_bf16_nt_bias_act_bwd_workspace_size", int(M), int(N), int(K), int(activation))
+    return _size_of("gemm_bf16_nt_bias_act_bwd_workspace_size", M, N, K, activation)
 
 
 def gemm_bf16_nt_gated(M: int, N: int, K: int, A, B, bias, activation: int, Z, C, workspace=None,
@@ -553,7 +561,7 @@ def gemm_bf16_nt_gated(M: int, N: int, K: int, A, B, bias, activation: int, Z, C
 
 def gated_workspace_size(M: int, N: int, K: int) -> int:
     """Workspace bytes of gemm_bf16_nt_gated on the current device."""
-    return _size_of("gemm_bf16_nt_gated_workspace_size", int(M), int(N), int(K))
+    return _size_of("gemm_bf16_nt_gated_workspace_size", M, N, K)
 
 
 def gemm_bf16_nt_gated_bwd(M: int, N: int, K: int, A, B, Z, activation: int, dC, dA, dB, dbias, workspace=None,
@@ -569,7 +577,7 @@ def gemm_bf16_nt_gated_bwd(M: int, N: int, K: int, A, B, Z, activation: int, dC,
 
 def gated_bwd_workspace_size(M: int, N: int, K: int) -> int:
     """Workspace bytes of gemm_bf16_nt_gated_bwd on the current device."""
-    return _size_of("gemm_bf16_nt_gated_bwd_workspace_size", int(M), int(N), int(K))
+    return _size_of("gemm_bf16_nt_gated_bwd_workspace_size", M, N, K)
 
 
 def newton_schulz(batch: int, rows: int, cols: int, G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
@@ -579,33 +587,34 @@ def newton_schulz(batch: int, rows: int, cols: int, G, O, steps: int = 5, coeffi
     X <- a X + (b X X^T + c (X X^T)^2) X with coefficients (a, b, c). G's type
     is its tensor's (g_type, BF16 or FP32, names it for a raw address). The
     workspace holds newton_schulz_workspace_size(batch, rows, cols) bytes."""
-    batch, rows, cols = int(batch), int(rows), int(cols)
+    batch, rows, cols, steps = _int32(batch), _int32(rows), _int32(cols), _int32(steps)
     if g_type is None:
         import torch
         types = {torch.bfloat16: BF16, torch.int16: BF16, torch.uint16: BF16, torch.float32: FP32}
         if not isinstance(G, torch.Tensor) or G.dtype not in types:
             raise TypeError("G: expected a BF16 or FP32 tensor, or an address with g_type")
         g_type = types[G.dtype]
+    g_type = _int32(g_type)
     dev = _device()
     n = batch * rows * cols if min(batch, rows, cols) > 0 else 0
     gg = _addr(G, n * (4 if g_type == FP32 else 2), "G", dev)
     o = _addr(O, n * 2, "O", dev)
     w, nb = _workspace(workspace, workspace_bytes, dev)
     a, b, c = coefficients
-    _check(load().gemm355_newton_schulz(batch, rows, cols, int(g_type), gg, int(steps), a, b, c, eps, o, w, nb,
+    _check(load().gemm355_newton_schulz(batch, rows, cols, g_type, gg, steps, a, b, c, eps, o, w, nb,
                                         _stream(stream, dev)), "gemm355_newton_schulz")
 
 
 def newton_schulz_workspace_size(batch: int, rows: int, cols: int) -> int:
     """Workspace bytes of newton_schulz on the current device."""
-    return _size_of("gemm355_newton_schulz_workspace_size", int(batch), int(rows), int(cols))
+    return _size_of("gemm355_newton_schulz_workspace_size", batch, rows, cols)
 
 
 def force_layer_kernel(kernel: int) -> None:
     """Kernel of the layer calls' products for the whole process: LAYER_AUTO
     (default), LAYER_LARGE, LAYER_SPLIT, LAYER_TILE, LAYER_SMALL or
     LAYER_NARROW (a diagnostic)."""
-    _check(load().gemm355_force_layer_kernel(int(kernel)), "gemm355_force_layer_kernel")
+    _check(load().gemm355_force_layer_kernel(_int32(kernel)), "gemm355_force_layer_kernel")
 
 
 def force_instance(instance: int) -> None:

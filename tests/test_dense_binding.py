@@ -1,0 +1,30 @@
+"""The Python binding of the layer calls without a GPU: what it refuses before it
+asks for a device."""
+import pytest
+
+import dense_gemm_14_amd as g
+
+SIZES = [(g.bias_act_res_workspace_size, 3, ()), (g.gated_workspace_size, 3, ()), (g.gated_bwd_workspace_size, 3, ()),
+         (g.bias_act_bwd_workspace_size, 3, (g.ACT_NONE,)), (g.newton_schulz_workspace_size, 3, ())]
+
+
+@pytest.mark.parametrize("far", [1 << 31, 1 << 32, (1 << 32) + 8, -(1 << 32) + 8, 1 << 70])
+@pytest.mark.parametrize("fn,count,rest", SIZES, ids=[s[0].__name__ for s in SIZES])
+def test_sizes_beyond_32_bits_are_refused(fn, count, rest, far):
+    # (cut to 32 bits, 2^32 would be an empty product that needs no workspace)
+    for i in range(count):
+        sizes = [far if j == i else 0 for j in range(count)]
+        with pytest.raises(OverflowError):
+            fn(*sizes, *rest)
+
+
+def test_newton_schulz_refuses_numbers_beyond_32_bits():
+    ok = dict(batch=1, rows=64, cols=64, G=1 << 40, O=1 << 41, steps=5, workspace=1 << 42, workspace_bytes=1 << 30,
+              stream=1 << 43, g_type=g.BF16)
+    for name in ("batch", "rows", "cols", "steps", "g_type"):
+        with pytest.raises(OverflowError):
+            g.newton_schulz(**{**ok, name: 1 << 32})
+    with pytest.raises(OverflowError):
+        g.bias_act_bwd_workspace_size(8, 8, 8, 1 << 32)
+    with pytest.raises(OverflowError):
+        g.force_layer_kernel(1 << 32)
