@@ -290,6 +290,13 @@ def gemm_bf16_nt_bias_act(M: int, N: int, K: int, A, B, bias, activation: int, C
            "gemm_bf16_nt_bias_act")
 
 
+def _unsigned(nbytes) -> int:
+    """A workspace's size for a C size_t (ctypes would make -1 the largest)."""
+    if int(nbytes) < 0:
+        raise ValueError("workspace_bytes is negative: %d" % int(nbytes))
+    return int(nbytes)
+
+
 def _workspace(ws, nbytes, device=None):
     """(address, bytes) of a workspace tensor, int address or None."""
     if ws is None:
@@ -297,9 +304,9 @@ def _workspace(ws, nbytes, device=None):
     if isinstance(ws, int):
         if nbytes is None:
             raise ValueError("workspace_bytes is needed with a raw workspace address")
-        return ws, int(nbytes)
+        return ws, _unsigned(nbytes)
     have = ws.nbytes
-    nb = have if nbytes is None else int(nbytes)
+    nb = have if nbytes is None else _unsigned(nbytes)
     if nb > have:
         raise ValueError("workspace holds %d bytes, workspace_bytes says %d" % (have, nb))
     return _addr(ws, nb, "workspace", device), nb

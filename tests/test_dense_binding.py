@@ -28,3 +28,15 @@ def test_newton_schulz_refuses_numbers_beyond_32_bits():
         g.bias_act_bwd_workspace_size(8, 8, 8, 1 << 32)
     with pytest.raises(OverflowError):
         g.force_layer_kernel(1 << 32)
+
+
+def test_a_negative_workspace_size_is_refused():
+    # (as an unsigned size it would pass for any need)
+    with pytest.raises(ValueError, match="workspace_bytes"):
+        g._workspace(1 << 42, -1)
+
+    class Held:
+        nbytes = 64
+
+    with pytest.raises(ValueError, match="workspace_bytes"):
+        g._workspace(Held(), -1)
