@@ -46,7 +46,9 @@ The functions mirror the C entry points declared in ``include/gemm355.h``:
 
 Operands may be torch tensors on a ROCm device (their storage is checked
 against the sizes before the call, since the C side cannot see it) or raw
-device addresses as ints (unchecked). ``stream`` is a ``torch.cuda.Stream``,
+device addresses as ints (unchecked). The layer calls (gemm_bf16_nt_bias_act_res
+and those after it) also refuse tensors of another floating type than they
+compute with; integer tensors are taken as the values' bits. ``stream`` is a ``torch.cuda.Stream``,
 a raw hipStream_t as int, or None for torch's current stream.
 """
 from __future__ import annotations
@@ -238,6 +240,17 @@ def _addr(x, need_bytes: int, what: str, device=None):
     if x.nbytes < need_bytes:
         raise ValueError("%s holds %d bytes, the sizes need %d" % (what, x.nbytes, need_bytes))
     return x.data_ptr()
+
+
+def _typed_addr(x, need_bytes: int, what: str, device=None, dtype=None):
+    """_addr of an array of BF16 (or `dtype`) values: a tensor of another
+    floating type is refused, one of integers holds the values' bits."""
+    if x is not None and not isinstance(x, int):
+        torch = _torch or _import_torch()
+        dtype = dtype or torch.bfloat16
+        if isinstance(x, torch.Tensor) and x.dtype != dtype and (x.dtype.is_floating_point or x.dtype.is_complex):
+            raise TypeError("%s: expected %s values, got %s" % (what, dtype, x.dtype))
+    return _addr(x, need_bytes, what, device)
 
 
 def _stream(stream, device=None):
@@ -497,7 +510,7 @@ def _layers():
         if not os.path.exists(_build.MARSHAL_PATH):
             _build.build_marshal()
         from . import _marshal as m
-        m.bind(_tensor, _current_device, _raw_stream, _addr, _workspace, _stream,
+        m.bind(_tensor, _current_device, _raw_stream, _typed_addr, _workspace, _stream, _torch.bfloat16, _torch.int16,
                *[ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in (
                    "gemm_bf16_nt_bias_act_res", "gemm_bf16_nt_gated", "gemm_bf16_nt_bias_act_bwd",
                    "gemm_bf16_nt_gated_bwd")])
@@ -604,8 +617,9 @@ def newton_schulz(batch: int, rows: int, cols: int, G, O, steps: int = 5, coeffi
     g_type = _int32(g_type)
     dev = _device()
     n = batch * rows * cols if min(batch, rows, cols) > 0 else 0
-    gg = _addr(G, n * (4 if g_type == FP32 else 2), "G", dev)
-    o = _addr(O, n * 2, "O", dev)
+    fp32 = g_type == FP32
+    gg = _typed_addr(G, n * (4 if fp32 else 2), "G", dev, _torch.float32 if fp32 else None)
+    o = _typed_addr(O, n * 2, "O", dev)
     w, nb = _workspace(workspace, workspace_bytes, dev)
     a, b, c = coefficients
     _check(load().gemm355_newton_schulz(batch, rows, cols, g_type, gg, steps, a, b, c, eps, o, w, nb,

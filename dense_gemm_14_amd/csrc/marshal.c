@@ -1,13 +1,13 @@
 /*
  * marshal.c -- argument marshalling of the layer calls (CPython C API): the
- * checks of __init__.py's _ptr, _workspace and _stream and the call itself,
+ * checks of __init__.py's _typed_addr, _workspace and _stream and the call itself,
  * without the interpreter between them. A small product's launch takes 2.3 us;
  * marshalled in Python its call took 4.9 us, and that, not the kernel, was the
  * time of every layer of up to about a million weights.
  *
- * What is not an exact torch.Tensor on the current device, large enough and
- * contiguous, goes to the Python functions, which know the other kinds of
- * arguments and word the refusals.
+ * What is not an exact torch.Tensor of BF16 values or their bits on the current
+ * device, large enough and contiguous, goes to the Python functions, which know
+ * the other kinds of arguments and word the refusals.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -23,8 +23,8 @@ typedef int (*backward_fn)(int, int, int, const void *, const void *, const void
 static linear_fn linear_call;
 static gated_fn gated_call;
 static backward_fn backward_call[2];   /* linear, gated */
-static PyObject *tensor_type, *current_device, *raw_stream, *slow_ptr, *slow_workspace, *slow_stream;
-static PyObject *s_get_device, *s_nbytes, *s_is_contiguous, *s_data_ptr;
+static PyObject *tensor_type, *current_device, *raw_stream, *slow_ptr, *slow_workspace, *slow_stream, *bf16, *bits16;
+static PyObject *s_get_device, *s_nbytes, *s_is_contiguous, *s_data_ptr, *s_dtype;
 
 static int to_int(PyObject *o, int *out)
 {
@@ -88,6 +88,16 @@ static int fits(PyObject *x, size_t need, long device, long long *bytes)
     return c == Py_True;
 }
 
+/* Whether the tensor x holds BF16 values, under that type or as 16-bit integers. */
+static int holds_bf16(PyObject *x)
+{
+    PyObject *t = PyObject_GetAttr(x, s_dtype);
+    if (!t)
+        return -1;
+    Py_DECREF(t);   /* torch keeps its types */
+    return t == bf16 || t == bits16;
+}
+
 static int pointer(PyObject *x, size_t need, const char *what, long device, void **out)
 {
     long long bytes;
@@ -96,6 +106,8 @@ static int pointer(PyObject *x, size_t need, const char *what, long device, void
     if (x == Py_None)
         return 0;
     ok = fits(x, need, device, &bytes);
+    if (ok > 0)
+        ok = holds_bf16(x);
     if (ok < 0)
         return -1;
     if (ok)
@@ -214,14 +226,15 @@ static PyObject *backward(PyObject *self, PyObject *const *a, Py_ssize_t count)
     return PyLong_FromLong(status);
 }
 
-/* bind(tensor type, current_device, raw_stream, _ptr, _workspace, _stream, four addresses) */
+/* bind(tensor type, current_device, raw_stream, _typed_addr, _workspace, _stream, bfloat16, int16, four addresses) */
 static PyObject *bind(PyObject *self, PyObject *args)
 {
     unsigned long long f[4];
-    PyObject *o[6];
-    if (!PyArg_ParseTuple(args, "OOOOOOKKKK", &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &f[0], &f[1], &f[2], &f[3]))
+    PyObject *o[8];
+    if (!PyArg_ParseTuple(args, "OOOOOOOOKKKK", &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &o[6], &o[7], &f[0], &f[1],
+                          &f[2], &f[3]))
         return NULL;
-    for (int i = 0; i < 6; ++i)
+    for (int i = 0; i < 8; ++i)
         Py_INCREF(o[i]);   /* kept for the life of the process */
     tensor_type = o[0];
     current_device = o[1];
@@ -229,6 +242,8 @@ static PyObject *bind(PyObject *self, PyObject *args)
     slow_ptr = o[3];
     slow_workspace = o[4];
     slow_stream = o[5];
+    bf16 = o[6];
+    bits16 = o[7];
     linear_call = (linear_fn)(uintptr_t)f[0];
     gated_call = (gated_fn)(uintptr_t)f[1];
     backward_call[0] = (backward_fn)(uintptr_t)f[2];
@@ -250,7 +265,8 @@ PyMODINIT_FUNC PyInit__marshal(void)
     s_nbytes = PyUnicode_InternFromString("nbytes");
     s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
-    if (!s_get_device || !s_nbytes || !s_is_contiguous || !s_data_ptr)
+    s_dtype = PyUnicode_InternFromString("dtype");
+    if (!s_get_device || !s_nbytes || !s_is_contiguous || !s_data_ptr || !s_dtype)
         return NULL;
     return PyModule_Create(&module);
 }

@@ -40,3 +40,19 @@ def test_a_negative_workspace_size_is_refused():
 
     with pytest.raises(ValueError, match="workspace_bytes"):
         g._workspace(Held(), -1)
+
+
+def test_tensors_of_another_type_are_refused():
+    import torch
+    for t in (torch.float32, torch.float16, torch.float64, torch.complex64, torch.float8_e4m3fn):
+        with pytest.raises(TypeError, match="A: expected"):
+            g._typed_addr(torch.zeros(8, dtype=t), 0, "A")
+    # BF16, and integers as its bits, get as far as the device check
+    for t in (torch.bfloat16, torch.int16, torch.uint8):
+        with pytest.raises(ValueError, match="on the GPU"):
+            g._typed_addr(torch.zeros(8, dtype=t), 0, "A")
+    with pytest.raises(ValueError, match="on the GPU"):
+        g._typed_addr(torch.zeros(8), 0, "G", None, torch.float32)
+    with pytest.raises(TypeError, match="float32"):
+        g._typed_addr(torch.zeros(8, dtype=torch.bfloat16), 0, "G", None, torch.float32)
+    assert g._typed_addr(None, 8, "A") is None and g._typed_addr(64, 8, "A") == 64
