@@ -78,6 +78,8 @@ def build(verbose: bool = False) -> str:
 def stale() -> bool:
     if not os.path.exists(LIB_PATH) or not os.path.exists(MARSHAL_PATH):
         return True
+    if os.path.getmtime(MARSHAL_SOURCE) > os.path.getmtime(MARSHAL_PATH):
+        return True
     t = os.path.getmtime(LIB_PATH)
     return any(os.path.getmtime(s) > t for s in SOURCES + HEADERS)
 
