@@ -1,5 +1,5 @@
 """Build libgemm355.so in-tree with hipcc for gfx950 (no GPU needed to compile),
-and the binding's _marshal.so with gcc."""
+and the binding's _marshal module with gcc."""
 from __future__ import annotations
 
 import os
@@ -21,7 +21,8 @@ HEADERS = [os.path.join(CSRC, f) for f in ("common.hpp", "gemm_bf16.hpp", "gemm_
     [os.path.join(INCLUDE, "gemm355.h")]
 
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.c")
-MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
+# (the tag keeps another interpreter from loading it)
+MARSHAL_PATH = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
