@@ -673,7 +673,9 @@ OrthoPlan plan_ortho(int batch, int rows, int cols, int cus)
     o.gram = plan_product({m, m, n, batch, true, false, rows <= cols}, false, cus);
     o.square = plan_product({m, m, m, batch, true, false, true}, false, cus);
     o.update = plan_product({rows, cols, m, batch, false, false}, false, cus);
-    o.norm_blocks = (int)std::min<int64_t>(d::NS_BLOCKS, ceil_div(int64_t(rows) * cols, d::NS_THREADS * 8));
+    // (a launch has fewer than 2^32 threads, whatever the batch)
+    o.norm_blocks = (int)std::min<int64_t>({d::NS_BLOCKS, ceil_div(int64_t(rows) * cols, d::NS_THREADS * 8),
+                                            ((int64_t(1) << 32) - 1) / d::NS_THREADS / batch});
     o.x1_at = x;
     o.s_at = 2 * x;
     o.p_at = o.s_at + s;

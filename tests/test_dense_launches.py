@@ -62,7 +62,7 @@ class Recorder:
             self.seen[name, threads] = self.seen.get((name, threads), 0) + 1
 
     # addresses far apart, never read
-    A, B, BIAS, R, Z, C, DC, DA, DB, DBIAS, WS = (i << 40 for i in range(1, 12))
+    A, B, BIAS, R, Z, C, DC, DA, DB, DBIAS, WS = (i << 44 for i in range(1, 12))
 
     def forward(self, gated, M, N, K, act):
         call = "gemm_bf16_nt_gated" if gated else "gemm_bf16_nt_bias_act_res"
@@ -102,6 +102,11 @@ def run(shim, seed, count):
             rec.forward(gated, M, N, K, act)
             for wanted in GRADIENTS:
                 rec.backward(gated, M, N, K, act, wanted)
+    # the most matrices of the largest size that the card holds: more elements
+    # than one launch may have work-items
+    for sizes in ((65535, 16, 32776), (65535, 32, 16384), (40000, 72, 11656)):
+        rec.lib.gemm355_force_layer_kernel(0)
+        rec.ortho(*sizes, False)
     for _ in range(count // 4):
         rec.lib.gemm355_force_layer_kernel(rng.choice([0, 0, 1, 2, 3, 4, 5]))
         rec.ortho(rng.choice([1, 2, 5, 12]), log_size(rng, 8, 4096, 8), log_size(rng, 8, 4096, 8), rng.random() < 0.5)
