@@ -10,10 +10,10 @@
 // lanes side by side (512 contiguous bytes of a row), 8 rows at a time. A
 // workgroup walks a block of rows and leaves one row of FP32 column sums; a
 // second kernel adds those rows in order, so the sums do not depend on timing.
-// Measured: 4096 x 8192 in 45 us, 4.5 TB/s, gated (4096 x 16384 pre-activations)
-// in 63 us, 5.3 TB/s; a copy reaches 4.8. It is a pass of its own because both
-// products read dZ, a tile of it as often as there are tiles beside it:
-// recomputing it there would read Z and dC as often and take the activation's
+// Measured: 4096 x 8192 in 40 to 45 us, 4.5 to 5.0 TB/s, gated (4096 x 16384
+// pre-activations) in 63 us, 5.3 TB/s; a copy reaches 4.8. It is a pass of its own
+// because both products read dZ, a tile of it as often as there are tiles beside
+// it: recomputing it there would read Z and dC as often and take the activation's
 // instructions between the matrix ones.
 #pragma once
 
@@ -119,7 +119,10 @@ __global__ __launch_bounds__(GRAD_THREADS) void dense_grad_kernel(GradArgs p)
 
 // The bias gradient of 64 columns by THREADS threads: from the workgroups'
 // column sums, or, where nothing else has to pass over dC (the identity), from dC
-// itself. `part`: THREADS / 8 x 65 floats of LDS.
+// itself. `part`: THREADS / 8 x 65 floats of LDS. From dC it takes cols / 64
+// workgroups whatever the rows, and so grows with them where the columns are few:
+// 4096 x 4096 in 9 us, 8192 x 1024 in 11, 65536 x 64 in 114 (alone, with the
+// launch).
 struct BiasArgs {
     const float *sums;     // [blocks][cols], or NULL
     const uint16_t *dc;    // else: blocks x cols BF16

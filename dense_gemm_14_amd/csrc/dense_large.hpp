@@ -24,11 +24,12 @@
 //     without bias, residual or Z) a copy of the code without branches: with
 //     them the accumulators spilled (394 us instead of 362 below).
 //
-// Measured (BF16): layer of 8192 x 4096 with K = 8192 362 us, 1520 TFLOP/s, and
-// 384 with a residual read; gated layer of 8192 x 8192 with K = 4096 768 us, 1430,
-// and 798 with its pre-activations stored; input and weight gradients of 4096 x
-// 8192 x 4096 181 and 186 us, 1520 and 1480. Bounded by the matrix cores at the
-// clock that the power limit leaves (1544 TFLOP/s for a large library product).
+// Measured (BF16; cards and runs differ by 6 %): layer of 8192 x 4096 with K =
+// 8192 362 to 371 us, 1520 to 1480 TFLOP/s, and 382 to 406 with a residual read;
+// gated layer of 8192 x 8192 with K = 4096 768 us, 1430, and 788 to 843 with its
+// pre-activations stored; input and weight gradients of 4096 x 8192 x 4096 181 to
+// 186 and 186 to 193 us, 1520 to 1420. Bounded by the matrix cores at the clock
+// that the power limit leaves (1544 TFLOP/s for a large library product).
 // 192 x 192: the LDS reads and writes of a step take as many cycles as its
 // matrix instructions; a ring of six units, three steps ahead, gained nothing.
 #pragma once

@@ -29,10 +29,10 @@
 // would leave most units idle. Measured (BF16): 4096^3 in 144 us as a layer and
 // 165 as a weight gradient, 950 and 830 TFLOP/s, the matrix cores busy 43 % of
 // the time. What bounds it is the barrier of each step: 16 instructions per
-// wave stand between two of them, against about 300 cycles of waiting; without
-// the copies the same loop takes 109 us. Tried instead: 256 x 128 tiles (5 %
-// faster on 4096^3 alone), two workgroups of four waves per unit (137 to 188 us),
-// copies or reads spread over the step (no change).
+// wave stand between two of them, against about 300 cycles of waiting; a variant
+// without the copies, for measurement only, took 109 us. Tried instead: 256 x 128
+// tiles (5 % faster on 4096^3 alone), two workgroups of four waves per unit (137
+// to 188 us), copies or reads spread over the step (no change).
 #pragma once
 
 #include "dense_common.hpp"

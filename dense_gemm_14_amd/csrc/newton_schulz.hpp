@@ -15,7 +15,7 @@
 // FP16's largest value no earlier than X X^T does.
 //
 // Bound by memory: 4096 x 8192 of FP32 are read in 28 us (4.8 TB/s, what a copy
-// reaches) and read again and written in 30, of 1970 to 2050 for all five steps.
+// reaches) and read again and written in 30, of 1970 to 2110 for all five steps.
 #pragma once
 
 #include "dense_common.hpp"

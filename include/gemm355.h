@@ -477,6 +477,9 @@ enum { GEMM355_ACT_SILU = 3 };
  *   R     M x N BF16, or NULL for zeros; may be C itself (in-place addition)
  *   Z     M x N BF16 output for gemm_bf16_nt_bias_act_bwd, or NULL
  * M == 0 or N == 0 does nothing; K == 0 gives z = bias.
+ * With R and Z NULL and no SiLU this is gemm_bf16_nt_bias_act's product through
+ * other kernels: faster for up to a few hundred rows (one row against 4096 x 4096
+ * weights 5.6 us, there 15.5), slower for large ones (8192^3 752 us, there 705).
  */
 int gemm_bf16_nt_bias_act_res(int M, int N, int K, const void *A, const void *B, const void *bias, int activation,
                               const void *R, void *Z, void *C, void *workspace, size_t workspace_bytes, void *stream);
