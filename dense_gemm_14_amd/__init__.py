@@ -36,6 +36,13 @@ The functions mirror the C entry points declared in ``include/gemm355.h``:
     gated_workspace_size(M, N, K)
     gated_bwd_workspace_size(M, N, K)
     newton_schulz_workspace_size(batch, rows, cols)
+    embedding(tokens, vocab, cols, ids, E, Y, scale=1.0, stream=None)
+    embedding_bwd(tokens, vocab, cols, ids, dY, R, dE, scale=1.0, workspace=None, workspace_bytes=None, stream=None)
+    embedding_bwd_workspace_size(tokens, vocab, cols)
+    layer_norm(rows, cols, X, gamma, beta, Y, mean, rstd, eps=1e-5, stream=None)
+    layer_norm_bwd(rows, cols, X, gamma, mean, rstd, dY, R, dX, dgamma, dbeta, workspace=None, workspace_bytes=None,
+                   stream=None)
+    layer_norm_bwd_workspace_size(rows, cols)
     force_layer_kernel(kernel)        # kernel of these calls' products (diagnostic)
     force_instance(instance)          # BF16 instance override (diagnostic)
     force_supergroup(width)           # band width of the tile order (diagnostic)
@@ -73,8 +80,10 @@ ACT_RELU = 1
 ACT_GELU_TANH = 2
 ACT_SILU = 3         # the layer calls only (gemm_bf16_nt_bias_act_res and those after it)
 
-BF16 = 0             # input types of newton_schulz
+BF16 = 0             # types of newton_schulz's input and of the row calls' arrays
 FP32 = 1
+INT32 = 0            # types of ids and targets
+INT64 = 1
 
 INSTANCE_AUTO = 0    # gemm_bf16_nt picks the instance by shape
 INSTANCE_LARGE = 1   # 256 x 256 output tiles
@@ -170,6 +179,18 @@ def load() -> ctypes.CDLL:
     lib.gemm355_newton_schulz.restype = i
     lib.gemm355_newton_schulz_workspace_size.argtypes = [i, i, i, psz]
     lib.gemm355_newton_schulz_workspace_size.restype = i
+    lib.gemm355_embedding.argtypes = [i, i, i, i, p, i, p, f, i, p, p]
+    lib.gemm355_embedding.restype = i
+    lib.gemm355_embedding_bwd.argtypes = [i, i, i, i, p, i, p, f, i, p, p, p, sz, p]
+    lib.gemm355_embedding_bwd.restype = i
+    lib.gemm355_embedding_bwd_workspace_size.argtypes = [i, i, i, psz]
+    lib.gemm355_embedding_bwd_workspace_size.restype = i
+    lib.gemm355_layer_norm.argtypes = [i, i, i, p, i, p, p, f, p, p, p, p]
+    lib.gemm355_layer_norm.restype = i
+    lib.gemm355_layer_norm_bwd.argtypes = [i, i, i, p, i, p, p, p, p, p, p, p, p, p, sz, p]
+    lib.gemm355_layer_norm_bwd.restype = i
+    lib.gemm355_layer_norm_bwd_workspace_size.argtypes = [i, i, psz]
+    lib.gemm355_layer_norm_bwd_workspace_size.restype = i
     lib.gemm355_force_layer_kernel.argtypes = [i]
     lib.gemm355_force_layer_kernel.restype = i
     lib.gemm355_status_string.argtypes = [i]
@@ -629,6 +650,159 @@ def newton_schulz(batch: int, rows: int, cols: int, G, O, steps: int = 5, coeffi
 def newton_schulz_workspace_size(batch: int, rows: int, cols: int) -> int:
     """Workspace bytes of newton_schulz on the current device."""
     return _size_of("gemm355_newton_schulz_workspace_size", batch, rows, cols)
+
+
+# ---- the ends of a network ---------------------------------------------------
+
+def _is_tensor(x) -> bool:
+    return x is not None and not isinstance(x, int) and isinstance(x, (_torch or _import_torch()).Tensor)
+
+
+def _type_of(given, what: str, *arrays) -> int:
+    """BF16 or FP32: `given`, or the type of the first tensor among `arrays`
+    (integers of 16 bits hold BF16 values' bits); BF16 if there is none to tell."""
+    if given is not None:
+        given = _int32(given)
+        if given not in (BF16, FP32):
+            raise ValueError("%s: expected BF16 or FP32, got %d" % (what, given))
+        return given
+    for x in arrays:
+        if _is_tensor(x):
+            t = _torch
+            kind = {t.float32: FP32, t.bfloat16: BF16, t.int16: BF16, t.uint16: BF16}.get(x.dtype)
+            if kind is None:
+                raise TypeError("%s: expected bfloat16 or float32 values, got %s" % (what, x.dtype))
+            return kind
+    if any(x is not None for x in arrays):
+        raise ValueError("%s: its type has to be given with a raw address" % what)
+    return BF16
+
+
+def _values(x, kind: int, count: int, what: str, device):
+    """Address of `count` values of a type that _type_of has given."""
+    t = _torch or _import_torch()
+    if kind == FP32:
+        return _floats(x, count, what, device)
+    if _is_tensor(x) and x.dtype not in (t.bfloat16, t.int16, t.uint16):
+        raise TypeError("%s: expected torch.bfloat16 values, got %s" % (what, x.dtype))
+    return _addr(x, 2 * count, what, device)
+
+
+def _floats(x, count: int, what: str, device):
+    """Address of `count` FP32 values."""
+    if _is_tensor(x) and x.dtype != _torch.float32:
+        raise TypeError("%s: expected torch.float32 values, got %s" % (what, x.dtype))
+    return _addr(x, 4 * count, what, device)
+
+
+def _ids(x, given, count: int, what: str, device):
+    """(address, type) of `count` ids."""
+    if _is_tensor(x):
+        kind = {_torch.int32: INT32, _torch.int64: INT64}.get(x.dtype)
+        if kind is None:
+            raise TypeError("%s: expected int32 or int64 values, got %s" % (what, x.dtype))
+    elif given is None and x is not None:
+        raise ValueError("%s: its type has to be given with a raw address" % what)
+    else:
+        kind = _int32(given or 0)
+    return _addr(x, count * (8 if kind == INT64 else 4), what, device), kind
+
+
+def _count(*sizes) -> int:
+    """Elements of an array of these sizes (none where the call refuses them)."""
+    n = 1
+    for s in sizes:
+        n *= max(0, s)
+    return n
+
+
+def embedding(tokens: int, vocab: int, cols: int, ids, E, Y, scale: float = 1.0, stream=None, id_type=None,
+              e_type=None, y_type=None) -> None:
+    """Y[t] = scale * E[ids[t]] (tokens x cols), zeros where ids[t] lies outside
+    0 .. vocab - 1.
+
+    E (vocab x cols) and Y are BF16 or FP32 each, ids (tokens) int32 or int64;
+    id_type (INT32, INT64), e_type and y_type (BF16, FP32) name the types of raw
+    addresses."""
+    tokens, vocab, cols = _int32(tokens), _int32(vocab), _int32(cols)
+    dev = _device()
+    i, it = _ids(ids, id_type, _count(tokens), "ids", dev)
+    et, yt = _type_of(e_type, "E", E), _type_of(y_type, "Y", Y)
+    e = _values(E, et, _count(vocab, cols), "E", dev)
+    y = _values(Y, yt, _count(tokens, cols), "Y", dev)
+    _check(load().gemm355_embedding(tokens, vocab, cols, it, i, et, e, scale, yt, y, _stream(stream, dev)),
+           "gemm355_embedding")
+
+
+def embedding_bwd(tokens: int, vocab: int, cols: int, ids, dY, R, dE, scale: float = 1.0, workspace=None,
+                  workspace_bytes=None, stream=None, id_type=None, y_type=None, e_type=None) -> None:
+    """dE[v] = R[v] + scale * the sum of dY[t] over the tokens with ids[t] = v.
+
+    dY (tokens x cols) and dE (vocab x cols) are BF16 or FP32 each; R, of dE's
+    type, may be None for zeros, or dE itself: only rows that occur are then read
+    and written. The workspace holds embedding_bwd_workspace_size(tokens, vocab,
+    cols) bytes."""
+    tokens, vocab, cols = _int32(tokens), _int32(vocab), _int32(cols)
+    dev = _device()
+    i, it = _ids(ids, id_type, _count(tokens), "ids", dev)
+    yt, et = _type_of(y_type, "dY", dY), _type_of(e_type, "dE", dE)
+    y = _values(dY, yt, _count(tokens, cols), "dY", dev)
+    r = _values(R, et, _count(vocab, cols), "R", dev)
+    e = _values(dE, et, _count(vocab, cols), "dE", dev)
+    w, nb = _workspace(workspace, workspace_bytes, dev)
+    _check(load().gemm355_embedding_bwd(tokens, vocab, cols, it, i, yt, y, scale, et, r, e, w, nb, _stream(stream, dev)),
+           "gemm355_embedding_bwd")
+
+
+def embedding_bwd_workspace_size(tokens: int, vocab: int, cols: int) -> int:
+    """Workspace bytes of embedding_bwd on the current device."""
+    return _size_of("gemm355_embedding_bwd_workspace_size", tokens, vocab, cols)
+
+
+def layer_norm(rows: int, cols: int, X, gamma, beta, Y, mean, rstd, eps: float = 1e-5, stream=None, x_type=None,
+               w_type=None) -> None:
+    """Y (BF16) = (X - mean) * rstd * gamma + beta with each row's mean and
+    rstd = 1 / sqrt(variance + eps).
+
+    X (rows x cols) is BF16 or FP32, gamma and beta (cols, or None) likewise;
+    mean and rstd (rows, FP32) are outputs for layer_norm_bwd, or None."""
+    rows, cols = _int32(rows), _int32(cols)
+    dev = _device()
+    xt, wt = _type_of(x_type, "X", X), _type_of(w_type, "gamma", gamma, beta)
+    x = _values(X, xt, _count(rows, cols), "X", dev)
+    ga = _values(gamma, wt, _count(cols), "gamma", dev)
+    be = _values(beta, wt, _count(cols), "beta", dev)
+    y = _values(Y, BF16, _count(rows, cols), "Y", dev)
+    m, s = _floats(mean, _count(rows), "mean", dev), _floats(rstd, _count(rows), "rstd", dev)
+    _check(load().gemm355_layer_norm(rows, cols, xt, x, wt, ga, be, eps, y, m, s, _stream(stream, dev)),
+           "gemm355_layer_norm")
+
+
+def layer_norm_bwd(rows: int, cols: int, X, gamma, mean, rstd, dY, R, dX, dgamma, dbeta, workspace=None,
+                   workspace_bytes=None, stream=None, x_type=None, w_type=None) -> None:
+    """Gradients of layer_norm: dX (of X's type) from dY (rows x cols, BF16) and
+    the forward call's mean and rstd, plus R (of X's type, None for zeros; may be
+    dX itself), and dgamma and dbeta (of gamma's type). Each output may be None if
+    it is not wanted. The workspace holds layer_norm_bwd_workspace_size(rows, cols)
+    bytes (None where that is 0)."""
+    rows, cols = _int32(rows), _int32(cols)
+    dev = _device()
+    xt, wt = _type_of(x_type, "X", X, dX), _type_of(w_type, "gamma", gamma, dgamma, dbeta)
+    n, c = _count(rows, cols), _count(cols)
+    x = _values(X, xt, n, "X", dev)
+    ga = _values(gamma, wt, c, "gamma", dev)
+    m, s = _floats(mean, _count(rows), "mean", dev), _floats(rstd, _count(rows), "rstd", dev)
+    dy = _values(dY, BF16, n, "dY", dev)
+    r, dx = _values(R, xt, n, "R", dev), _values(dX, xt, n, "dX", dev)
+    dg, db = _values(dgamma, wt, c, "dgamma", dev), _values(dbeta, wt, c, "dbeta", dev)
+    w, nb = _workspace(workspace, workspace_bytes, dev)
+    _check(load().gemm355_layer_norm_bwd(rows, cols, xt, x, wt, ga, m, s, dy, r, dx, dg, db, w, nb, _stream(stream, dev)),
+           "gemm355_layer_norm_bwd")
+
+
+def layer_norm_bwd_workspace_size(rows: int, cols: int) -> int:
+    """Workspace bytes of layer_norm_bwd on the current device."""
+    return _size_of("gemm355_layer_norm_bwd_workspace_size", rows, cols)
 
 
 def force_layer_kernel(kernel: int) -> None:

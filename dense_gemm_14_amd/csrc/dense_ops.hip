@@ -12,6 +12,7 @@
 
 #include "gemm355.h"
 #include "host.hpp"
+#include "checks.hpp"
 #include "dense_large.hpp"
 #include "dense_small.hpp"
 #include "dense_tile.hpp"
@@ -23,9 +24,6 @@ namespace {
 using namespace gemm355::host;
 namespace d = gemm355::dense;
 using d::DenseArgs;
-
-constexpr size_t kAlign = 256;
-size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
 // ---- products --------------------------------------------------------------
 
@@ -343,34 +341,6 @@ DenseArgs args_of(int M, int N, int K, const void *a, const void *b, void *c)
 }
 
 // ---- argument checks -------------------------------------------------------
-
-// An array of a call: its address, size and required alignment.
-struct Array {
-    const void *p;
-    size_t bytes;
-};
-
-// Whether any output overlaps an input, the workspace or another output.
-bool any_overlap(const Array *out, int outs, const Array *in, int ins)
-{
-    for (int i = 0; i < outs; ++i) {
-        for (int j = 0; j < ins; ++j)
-            if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
-                return true;
-        for (int j = i + 1; j < outs; ++j)
-            if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
-                return true;
-    }
-    return false;
-}
-
-bool all_aligned(const Array *a, int n)
-{
-    for (int i = 0; i < n; ++i)
-        if (!aligned(a[i].p, 16))
-            return false;
-    return true;
-}
 
 bool act_ok(int act) { return act >= GEMM355_ACT_NONE && act <= GEMM355_ACT_SILU; }
 

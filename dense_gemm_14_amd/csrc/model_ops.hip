@@ -1,0 +1,395 @@
+// model_ops.hip -- host side of the calls around a network's layers that pass
+// over rows: embedding, layer norm and their gradients (embedding.hpp,
+// layer_norm.hpp). Argument checks, workspace layout and launches. The C ABI is
+// declared in include/gemm355.h. Nothing here allocates memory.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <math.h>
+#include <stdint.h>
+
+#include "gemm355.h"
+#include "checks.hpp"
+#include "embedding.hpp"
+#include "layer_norm.hpp"
+
+namespace {
+
+using namespace gemm355::host;
+namespace r = gemm355::rows;
+using gemm355::Int;
+
+bool type_ok(int t) { return t == GEMM355_BF16 || t == GEMM355_FP32; }
+bool id_type_ok(int t) { return t == GEMM355_INT32 || t == GEMM355_INT64; }
+size_t size_of(int type) { return type == GEMM355_FP32 ? 4 : 2; }
+size_t id_size(int type) { return type == GEMM355_INT64 ? 8 : 4; }
+
+// Elements of an array; arrays beyond this are refused, so that no product of
+// sizes runs over.
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+bool elements_ok(int64_t rows, int64_t cols) { return rows * cols <= kMaxElements; }
+
+// f(T{}) for a type of the C ABI.
+template <class F>
+int with_type(int type, F &&f)
+{
+    return type == GEMM355_FP32 ? f(float{}) : f(__bf16{});
+}
+
+int ceil_log2(int64_t n)
+{
+    int l = 0;
+    while ((int64_t(1) << l) < n)
+        ++l;
+    return l;
+}
+
+// ---- embedding -------------------------------------------------------------
+
+constexpr int64_t kMaxBlocks = int64_t(1) << 20;
+
+template <int PER>
+int launch_embed(r::EmbedArgs &p, int e_type, int y_type, int64_t blocks, hipStream_t s)
+{
+    return with_type(e_type, [&](auto e) {
+        return with_type(y_type, [&](auto y) {
+            return launch_kernel(r::embed_kernel<decltype(e), decltype(y), PER>, (unsigned)std::min(blocks, kMaxBlocks),
+                                 (unsigned)r::EMBED_THREADS, p, s);
+        });
+    });
+}
+
+// ---- embedding's gradient ----------------------------------------------------
+
+struct EmbedBwdPlan {
+    int range, groups;          // ids per workgroup of the order, workgroups
+    int block, blocks, pieces;
+    size_t sorted_at, partial_at, bytes;
+};
+
+EmbedBwdPlan plan_embed_bwd(int tokens, int vocab, int cols, int cus)
+{
+    EmbedBwdPlan e = {};
+    e.range = (int)std::min<int64_t>(r::ORDER_MAX_RANGE, ceil_div(vocab, cus));
+    e.groups = (int)ceil_div(vocab, e.range);
+    e.pieces = (int)ceil_div(cols, 512);
+    // blocks of up to 32 tokens, fewer where that leaves fewer waves than run
+    // at a time
+    e.block = 32;
+    while (e.block > 4 && ceil_div(tokens, e.block) * e.pieces < 16 * int64_t(cus))
+        e.block /= 2;
+    e.blocks = (int)ceil_div(tokens, e.block);
+    e.sorted_at = align_up((size_t(vocab) + 1) * sizeof(int));
+    e.partial_at = e.sorted_at + align_up(size_t(tokens) * 8);
+    e.bytes = e.partial_at + (tokens > e.block ? size_t(e.blocks) * 2 * cols * sizeof(float) : 0);
+    return e;
+}
+
+// ---- layer norm --------------------------------------------------------------
+
+// The kernel that holds rows of `cols` columns: f(Int<waves>{}, Int<eights of
+// columns per lane>{}), or f(Int<0>{}, Int<0>{}) for wider rows, which are read
+// again. A wave holds up to 4096 columns where there are rows for every wave of
+// the card, four waves otherwise.
+template <class F>
+int with_rows(int cols, bool many, F &&f)
+{
+    const int64_t per_wave = ceil_div(cols, 512), per_four = ceil_div(cols, 2048);
+    if (per_wave <= 1)
+        return f(Int<1>{}, Int<1>{});
+    if (many) {
+        if (per_wave <= 2)
+            return f(Int<1>{}, Int<2>{});
+        if (per_wave <= 4)
+            return f(Int<1>{}, Int<4>{});
+        if (per_wave <= 8)
+            return f(Int<1>{}, Int<8>{});
+    }
+    if (per_four <= 1)
+        return f(Int<4>{}, Int<1>{});
+    if (per_four <= 2)
+        return f(Int<4>{}, Int<2>{});
+    if (per_four <= 4)
+        return f(Int<4>{}, Int<4>{});
+    if (per_four <= 8)
+        return f(Int<4>{}, Int<8>{});
+    return f(Int<0>{}, Int<0>{});
+}
+
+// Whether the gradients of few or very wide rows take one launch.
+bool norm_direct(int rows, int cols) { return rows <= 256 || cols > 16384; }
+
+// Waves that hold a row where there are many, and the workgroups that walk them.
+int norm_bwd_waves(int cols) { return cols <= 2048 ? 1 : cols <= 8192 ? 4 : 8; }
+int norm_bwd_blocks(int rows, int cols, int cus)
+{
+    return (int)std::min<int64_t>(cus, ceil_div(rows, r::NORM_BWD_THREADS / 64 / norm_bwd_waves(cols)));
+}
+template <class F>
+int with_bwd_rows(int cols, F &&f)
+{
+    return cols <= 512     ? f(Int<1>{}, Int<1>{})
+           : cols <= 1024  ? f(Int<1>{}, Int<2>{})
+           : cols <= 2048  ? f(Int<1>{}, Int<4>{})
+           : cols <= 4096  ? f(Int<4>{}, Int<2>{})
+           : cols <= 8192  ? f(Int<4>{}, Int<4>{})
+                           : f(Int<8>{}, Int<4>{});
+}
+
+} // namespace
+
+extern "C" int gemm355_embedding(int tokens, int vocab, int cols, int id_type, const void *ids, int e_type, const void *E,
+                                 float scale, int y_type, void *Y, void *stream)
+{
+    if (tokens < 0 || vocab < 0 || cols < 0 || !id_type_ok(id_type) || !type_ok(e_type) || !type_ok(y_type) ||
+        !isfinite(scale))
+        return GEMM355_ERR_INVALID_ARG;
+    if (tokens == 0 || cols == 0)
+        return GEMM355_OK;
+    if (!ids || !Y || (vocab > 0 && !E))
+        return GEMM355_ERR_INVALID_ARG;
+    if (cols % 8 != 0 || !elements_ok(tokens, cols) || !elements_ok(vocab, cols))
+        return GEMM355_ERR_UNSUPPORTED;
+    const Array out[] = {{Y, size_t(tokens) * cols * size_of(y_type)}};
+    const Array in[] = {{E, size_t(vocab) * cols * size_of(e_type)}, {ids, size_t(tokens) * id_size(id_type)}};
+    if (any_overlap(out, 1, in, 2))
+        return GEMM355_ERR_INVALID_ARG;
+    if (!all_aligned(out, 1) || !all_aligned(in, 1) || !aligned(ids, id_size(id_type)))
+        return GEMM355_ERR_UNSUPPORTED;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc != GEMM355_OK)
+        return rc;
+    r::EmbedArgs p = {};
+    p.ids = ids;
+    p.e = E;
+    p.y = Y;
+    p.tokens = tokens;
+    p.vocab = vocab;
+    p.cols = cols;
+    p.scale = scale;
+    p.wide = id_type == GEMM355_INT64;
+    p.lanes_log2 = std::min(6, ceil_log2(cols / 8));
+    p.pieces = (int)ceil_div(cols / 8, int64_t(1) << p.lanes_log2);
+    const int64_t groups = r::EMBED_THREADS >> p.lanes_log2;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    // four tokens per lane where that leaves eight workgroups for every unit
+    const int64_t four = ceil_div(tokens, groups * 4) * p.pieces;
+    if (four >= 8 * int64_t(cus)) {
+        p.items = four;
+        return launch_embed<4>(p, e_type, y_type, p.items, s);
+    }
+    p.items = ceil_div(tokens, groups) * p.pieces;
+    return launch_embed<1>(p, e_type, y_type, p.items, s);
+}
+
+extern "C" int gemm355_embedding_bwd_workspace_size(int tokens, int vocab, int cols, size_t *bytes)
+{
+    if (tokens < 0 || vocab < 0 || cols < 0 || !bytes)
+        return GEMM355_ERR_INVALID_ARG;
+    if (!elements_ok(tokens, cols) || !elements_ok(vocab, cols))
+        return GEMM355_ERR_UNSUPPORTED;
+    *bytes = 0;
+    if (vocab == 0 || cols == 0)
+        return GEMM355_OK;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc == GEMM355_OK)
+        *bytes = plan_embed_bwd(tokens, vocab, cols, cus).bytes;
+    return rc;
+}
+
+extern "C" int gemm355_embedding_bwd(int tokens, int vocab, int cols, int id_type, const void *ids, int y_type,
+                                     const void *dY, float scale, int e_type, const void *R, void *dE, void *workspace,
+                                     size_t workspace_bytes, void *stream)
+{
+    if (tokens < 0 || vocab < 0 || cols < 0 || !id_type_ok(id_type) || !type_ok(e_type) || !type_ok(y_type) ||
+        !isfinite(scale))
+        return GEMM355_ERR_INVALID_ARG;
+    if (vocab == 0 || cols == 0)
+        return GEMM355_OK;
+    if (!dE || !workspace || (tokens > 0 && (!ids || !dY)))
+        return GEMM355_ERR_INVALID_ARG;
+    if (cols % 8 != 0 || !elements_ok(tokens, cols) || !elements_ok(vocab, cols))
+        return GEMM355_ERR_UNSUPPORTED;
+    const size_t e_bytes = size_t(vocab) * cols * size_of(e_type);
+    const Array out[] = {{dE, e_bytes}, {workspace, workspace_bytes}};
+    // dE may be R itself: every element is read before it is written, by the same lane
+    const Array in[] = {{dY, size_t(tokens) * cols * size_of(y_type)}, {R == dE ? nullptr : R, e_bytes},
+                        {ids, size_t(tokens) * id_size(id_type)}};
+    if (any_overlap(out, 2, in, 3))
+        return GEMM355_ERR_INVALID_ARG;
+    if (!all_aligned(out, 2) || !all_aligned(in, 2) || !aligned(ids, id_size(id_type)))
+        return GEMM355_ERR_UNSUPPORTED;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc != GEMM355_OK)
+        return rc;
+    const EmbedBwdPlan e = plan_embed_bwd(tokens, vocab, cols, cus);
+    if (workspace_bytes < e.bytes)
+        return GEMM355_ERR_UNSUPPORTED;
+
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    r::EmbedBwdArgs p = {};
+    p.ids = ids;
+    p.dy = dY;
+    p.r = R;
+    p.de = dE;
+    p.start = reinterpret_cast<int *>(ws);
+    p.sorted = reinterpret_cast<int2 *>(ws + e.sorted_at);
+    p.partial = reinterpret_cast<float *>(ws + e.partial_at);
+    p.tokens = tokens;
+    p.vocab = vocab;
+    p.cols = cols;
+    p.range = e.range;
+    p.block = e.block;
+    p.blocks = e.blocks;
+    p.pieces = e.pieces;
+    p.scale = scale;
+    p.wide = id_type == GEMM355_INT64;
+    int st = launch_kernel(r::embed_order_kernel, (unsigned)e.groups, (unsigned)r::ORDER_THREADS, p, s);
+    if (st != GEMM355_OK)
+        return st;
+    constexpr int per = r::EMBED_THREADS / 64;
+    const int64_t sum_groups = std::min<int64_t>(ceil_div(int64_t(e.blocks) * e.pieces, per), 16 * int64_t(cus));
+    const int64_t fill_groups = R == dE ? 0 : std::min<int64_t>(ceil_div(int64_t(vocab) * e.pieces, per), 8 * int64_t(cus));
+    p.sum_waves = (int)(sum_groups * per);
+    return with_type(e_type, [&](auto te) {
+        return with_type(y_type, [&](auto ty) {
+            typedef decltype(te) TE;
+            if (sum_groups + fill_groups > 0) {
+                const int st = launch_kernel(r::embed_sums_kernel<TE, decltype(ty)>, (unsigned)(sum_groups + fill_groups),
+                                             (unsigned)r::EMBED_THREADS, p, s);
+                if (st != GEMM355_OK)
+                    return st;
+            }
+            if (tokens <= e.block)      // no id can have more
+                return (int)GEMM355_OK;
+            return launch_kernel(r::embed_join_kernel<TE>,
+                                 (unsigned)std::min<int64_t>(int64_t(e.blocks) * e.pieces, 16 * int64_t(cus)),
+                                 (unsigned)r::JOIN_THREADS, p, s);
+        });
+    });
+}
+
+extern "C" int gemm355_layer_norm(int rows, int cols, int x_type, const void *X, int w_type, const void *gamma,
+                                  const void *beta, float eps, void *Y, float *mean, float *rstd, void *stream)
+{
+    if (rows < 0 || cols < 0 || !type_ok(x_type) || !type_ok(w_type) || !isfinite(eps) || eps < 0.0f)
+        return GEMM355_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0)
+        return GEMM355_OK;
+    if (!X || !Y)
+        return GEMM355_ERR_INVALID_ARG;
+    if (cols % 8 != 0 || !elements_ok(rows, cols))
+        return GEMM355_ERR_UNSUPPORTED;
+    const size_t n = size_t(rows) * cols, w = size_t(cols) * size_of(w_type);
+    const Array out[] = {{Y, n * 2}, {mean, size_t(rows) * 4}, {rstd, size_t(rows) * 4}};
+    const Array in[] = {{X, n * size_of(x_type)}, {gamma, w}, {beta, w}};
+    if (any_overlap(out, 3, in, 3))
+        return GEMM355_ERR_INVALID_ARG;
+    if (!all_aligned(out, 1) || !all_aligned(in, 3) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return GEMM355_ERR_UNSUPPORTED;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc != GEMM355_OK)
+        return rc;
+    r::NormArgs p = {X, gamma, beta, Y, mean, rstd, rows, cols, eps};
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return with_type(x_type, [&](auto tx) {
+        return with_type(w_type, [&](auto tw) {
+            return with_rows(cols, rows >= 4 * cus, [&](auto waves_c, auto vpt_c) {
+                constexpr int WAVES = decltype(waves_c)::value, VPT = decltype(vpt_c)::value;
+                if constexpr (WAVES == 0) {
+                    return launch_kernel(r::norm_wide_kernel<decltype(tx), decltype(tw)>,
+                                         (unsigned)std::min<int64_t>(rows, 2 * int64_t(cus)),
+                                         (unsigned)r::NORM_WIDE_THREADS, p, s);
+                } else {
+                    return launch_kernel(r::norm_kernel<decltype(tx), decltype(tw), WAVES, VPT>,
+                                         (unsigned)std::min<int64_t>(ceil_div(int64_t(rows) * WAVES, 4), 8 * int64_t(cus)),
+                                         (unsigned)r::NORM_THREADS, p, s);
+                }
+            });
+        });
+    });
+}
+
+extern "C" int gemm355_layer_norm_bwd_workspace_size(int rows, int cols, size_t *bytes)
+{
+    if (rows < 0 || cols < 0 || !bytes)
+        return GEMM355_ERR_INVALID_ARG;
+    if (!elements_ok(rows, cols))
+        return GEMM355_ERR_UNSUPPORTED;
+    *bytes = 0;
+    if (rows == 0 || cols == 0 || norm_direct(rows, cols))
+        return GEMM355_OK;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc == GEMM355_OK)
+        *bytes = size_t(norm_bwd_blocks(rows, cols, cus)) * 2 * cols * sizeof(float);
+    return rc;
+}
+
+extern "C" int gemm355_layer_norm_bwd(int rows, int cols, int x_type, const void *X, int w_type, const void *gamma,
+                                      const float *mean, const float *rstd, const void *dY, const void *R, void *dX,
+                                      void *dgamma, void *dbeta, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (rows < 0 || cols < 0 || !type_ok(x_type) || !type_ok(w_type))
+        return GEMM355_ERR_INVALID_ARG;
+    const bool wants_columns = dgamma || dbeta, wants_x = dX && rows > 0;
+    if (cols == 0 || (!wants_x && !wants_columns))
+        return GEMM355_OK;
+    if (rows > 0 && (!X || !mean || !rstd || !dY))
+        return GEMM355_ERR_INVALID_ARG;
+    if (workspace_bytes > 0 && !workspace)
+        return GEMM355_ERR_INVALID_ARG;
+    if (cols % 8 != 0 || !elements_ok(rows, cols))
+        return GEMM355_ERR_UNSUPPORTED;
+    const size_t n = size_t(rows) * cols, w = size_t(cols) * size_of(w_type);
+    const Array out[] = {{dX, n * size_of(x_type)}, {dgamma, w}, {dbeta, w}, {workspace, workspace_bytes}};
+    // dX may be R itself: every element is read before it is written, by the same lane
+    const Array in[] = {{X, n * size_of(x_type)}, {dY, n * 2}, {gamma, w}, {dX == R ? nullptr : R, n * size_of(x_type)},
+                        {mean, size_t(rows) * 4}, {rstd, size_t(rows) * 4}};
+    if (any_overlap(out, 4, in, 6))
+        return GEMM355_ERR_INVALID_ARG;
+    if (!all_aligned(out, 4) || !all_aligned(in, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return GEMM355_ERR_UNSUPPORTED;
+    int cus = 0;
+    const int rc = compute_units(&cus);
+    if (rc != GEMM355_OK)
+        return rc;
+    r::NormBwdArgs p = {X, gamma, mean, rstd, dY, R, wants_x ? dX : nullptr, dgamma, dbeta, static_cast<float *>(workspace),
+                        rows, cols, 0, wants_columns};
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (norm_direct(rows, cols)) {      // (no rows: the column blocks write zeros)
+        const unsigned columns = wants_columns ? (unsigned)ceil_div(cols, 64) : 0u;
+        return with_type(x_type, [&](auto tx) {
+            return with_type(w_type, [&](auto tw) {
+                auto go = [&](auto vpt_c) {
+                    constexpr int VPT = decltype(vpt_c)::value;
+                    p.blocks = wants_x ? (int)std::min<int64_t>(rows, (VPT ? 8 : 2) * int64_t(cus)) : 0;
+                    return launch_kernel(r::norm_bwd_direct_kernel<decltype(tx), decltype(tw), VPT>,
+                                         (unsigned)p.blocks + columns, (unsigned)r::norm_direct_threads<VPT>(), p, s);
+                };
+                return cols <= 2048 ? go(Int<1>{}) : cols <= 4096 ? go(Int<2>{}) : cols <= 8192 ? go(Int<4>{}) : go(Int<0>{});
+            });
+        });
+    }
+    p.blocks = norm_bwd_blocks(rows, cols, cus);
+    if (workspace_bytes < size_t(p.blocks) * 2 * cols * sizeof(float))
+        return GEMM355_ERR_UNSUPPORTED;
+    return with_type(x_type, [&](auto tx) {
+        return with_type(w_type, [&](auto tw) {
+            typedef decltype(tw) TW;
+            const int st = with_bwd_rows(cols, [&](auto waves_c, auto vpt_c) {
+                return launch_kernel(r::norm_bwd_kernel<decltype(tx), TW, decltype(waves_c)::value, decltype(vpt_c)::value>,
+                                     (unsigned)p.blocks, (unsigned)r::NORM_BWD_THREADS, p, s);
+            });
+            if (st != GEMM355_OK || !wants_columns)
+                return st;
+            return launch_kernel(r::norm_sums_kernel<TW>, (unsigned)ceil_div(2 * int64_t(cols), r::NORM_SUM_COLS),
+                                 (unsigned)r::NORM_SUM_THREADS, p, s);
+        });
+    });
+}

@@ -589,6 +589,101 @@ int gemm355_newton_schulz_workspace_size(int batch, int rows, int cols, size_t *
  */
 int gemm355_force_layer_kernel(int kernel);
 
+/*
+ * ---- The ends of a network: embedding, normalisation, loss --------------------
+ *
+ * What stands around the layers: the lookup of the tokens' rows, the layer norm
+ * before each layer, and the loss over the vocabulary, each with its gradients.
+ * The conventions are those of the layer calls (device pointers, dense row-major
+ * arrays, one stream, no allocation, no synchronisation, deterministic; they may
+ * be captured into graphs; outputs apart from inputs, the workspace and each
+ * other). Sums, statistics and states are FP32, and every stored value is rounded
+ * once. Arrays of rows are 16-byte aligned and their row length (cols, K) is a
+ * multiple of 8; arrays of one number per row or token (ids, targets, mean, rstd,
+ * lse, loss, dloss) need only their own type's alignment; else
+ * GEMM355_ERR_UNSUPPORTED. Arrays of rows may pass 2^31 bytes unless a call says
+ * otherwise (2^40 elements are the limit).
+ *
+ * An id or target outside 0 .. vocab - 1 (such as -1 or -100) marks a place that
+ * is left out: it gives a row of zeros, a loss of zero and no gradient.
+ */
+typedef enum gemm355_id_type {
+    GEMM355_INT32 = 0,
+    GEMM355_INT64 = 1
+} gemm355_id_type;
+
+/*
+ * gemm355_embedding -- Y[t][c] = scale * E[ids[t]][c], rounded to Y's type; zeros
+ * for a token whose id is left out.
+ *
+ *   ids   tokens ids of type id_type (a gemm355_id_type)
+ *   E     vocab x cols of type e_type (GEMM355_BF16 or GEMM355_FP32)
+ *   scale finite
+ *   Y     tokens x cols of type y_type
+ * tokens == 0 or cols == 0 does nothing.
+ */
+int gemm355_embedding(int tokens, int vocab, int cols, int id_type, const void *ids, int e_type, const void *E,
+                      float scale, int y_type, void *Y, void *stream);
+
+/*
+ * gemm355_embedding_bwd -- the table's gradient:
+ *
+ *   dE[v][c] = R[v][c] + scale * sum over the tokens t with ids[t] == v of dY[t][c]
+ *
+ *   dY    tokens x cols of type y_type
+ *   R     vocab x cols of type e_type, or NULL for zeros. R may be dE itself, as
+ *         for a table that is also the output projection, whose gradient the
+ *         loss has left there: only the rows that occur are then read and
+ *         written.
+ *   dE    vocab x cols of type e_type
+ * The tokens of one id are added in an order that depends on the ids and sizes
+ * alone. The workspace (gemm355_embedding_bwd_workspace_size bytes) is as for the
+ * layer calls; it is always needed, but for vocab == 0 or cols == 0, which do
+ * nothing.
+ */
+int gemm355_embedding_bwd(int tokens, int vocab, int cols, int id_type, const void *ids, int y_type, const void *dY,
+                          float scale, int e_type, const void *R, void *dE, void *workspace, size_t workspace_bytes,
+                          void *stream);
+int gemm355_embedding_bwd_workspace_size(int tokens, int vocab, int cols, size_t *bytes);
+
+/*
+ * gemm355_layer_norm -- normalises each row:
+ *
+ *   mean = sum x / cols,  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *   Y = bf16((x - mean) * rstd * gamma + beta)
+ *
+ *   X      rows x cols of type x_type (GEMM355_BF16 or GEMM355_FP32)
+ *   gamma, beta  cols values of type w_type, or NULL for ones and zeros
+ *   eps    >= 0, finite
+ *   Y      rows x cols BF16, the layers' operand
+ *   mean, rstd  rows FP32 values for gemm355_layer_norm_bwd, or NULL
+ * rows == 0 or cols == 0 does nothing.
+ */
+int gemm355_layer_norm(int rows, int cols, int x_type, const void *X, int w_type, const void *gamma, const void *beta,
+                       float eps, void *Y, float *mean, float *rstd, void *stream);
+
+/*
+ * gemm355_layer_norm_bwd -- its gradients, with u = (x - mean) * rstd and
+ * g = dY * gamma:
+ *
+ *   dX = R + rstd * (g - sum g / cols - u * sum (g u) / cols)
+ *   dgamma[c] = sum over rows of dY * u,   dbeta[c] = sum over rows of dY
+ *
+ *   mean, rstd  as the forward call left them
+ *   dY     rows x cols BF16
+ *   R      rows x cols of type x_type, the gradient that reaches X past the
+ *          layer (a residual's), or NULL for zeros; may be dX itself
+ *   dX     rows x cols of type x_type
+ *   dgamma, dbeta  cols values of type w_type
+ * Each output may be NULL if it is not wanted. rows == 0 writes zeros to dgamma
+ * and dbeta. The workspace (gemm355_layer_norm_bwd_workspace_size bytes, NULL
+ * where that is 0) is as for the layer calls.
+ */
+int gemm355_layer_norm_bwd(int rows, int cols, int x_type, const void *X, int w_type, const void *gamma,
+                           const float *mean, const float *rstd, const void *dY, const void *R, void *dX, void *dgamma,
+                           void *dbeta, void *workspace, size_t workspace_bytes, void *stream);
+int gemm355_layer_norm_bwd_workspace_size(int rows, int cols, size_t *bytes);
+
 /* Human-readable text for a status code (static storage; never NULL). */
 const char *gemm355_status_string(int status);
 
