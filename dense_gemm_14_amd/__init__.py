@@ -43,6 +43,11 @@ The functions mirror the C entry points declared in ``include/gemm355.h``:
     layer_norm_bwd(rows, cols, X, gamma, mean, rstd, dY, R, dX, dgamma, dbeta, workspace=None, workspace_bytes=None,
                    stream=None)
     layer_norm_bwd_workspace_size(rows, cols)
+    gemm_bf16_nt_cross_entropy(M, V, K, A, B, targets, loss, lse, workspace, workspace_bytes=None, stream=None)
+    gemm_bf16_nt_cross_entropy_bwd(M, V, K, A, B, targets, lse, dloss, dA, dB, workspace, workspace_bytes=None,
+                                   stream=None)
+    cross_entropy_workspace_size(M, V, K)
+    cross_entropy_bwd_workspace_size(M, V, K)
     force_layer_kernel(kernel)        # kernel of these calls' products (diagnostic)
     force_instance(instance)          # BF16 instance override (diagnostic)
     force_supergroup(width)           # band width of the tile order (diagnostic)
@@ -191,6 +196,14 @@ def load() -> ctypes.CDLL:
     lib.gemm355_layer_norm_bwd.restype = i
     lib.gemm355_layer_norm_bwd_workspace_size.argtypes = [i, i, psz]
     lib.gemm355_layer_norm_bwd_workspace_size.restype = i
+    lib.gemm_bf16_nt_cross_entropy.argtypes = [i, i, i, p, p, i, p, p, p, p, sz, p]
+    lib.gemm_bf16_nt_cross_entropy.restype = i
+    lib.gemm_bf16_nt_cross_entropy_workspace_size.argtypes = [i, i, i, psz]
+    lib.gemm_bf16_nt_cross_entropy_workspace_size.restype = i
+    lib.gemm_bf16_nt_cross_entropy_bwd.argtypes = [i, i, i, p, p, i, p, p, p, p, p, p, sz, p]
+    lib.gemm_bf16_nt_cross_entropy_bwd.restype = i
+    lib.gemm_bf16_nt_cross_entropy_bwd_workspace_size.argtypes = [i, i, i, psz]
+    lib.gemm_bf16_nt_cross_entropy_bwd_workspace_size.restype = i
     lib.gemm355_force_layer_kernel.argtypes = [i]
     lib.gemm355_force_layer_kernel.restype = i
     lib.gemm355_status_string.argtypes = [i]
@@ -803,6 +816,53 @@ def layer_norm_bwd(rows: int, cols: int, X, gamma, mean, rstd, dY, R, dX, dgamma
 def layer_norm_bwd_workspace_size(rows: int, cols: int) -> int:
     """Workspace bytes of layer_norm_bwd on the current device."""
     return _size_of("gemm355_layer_norm_bwd_workspace_size", rows, cols)
+
+
+def gemm_bf16_nt_cross_entropy(M: int, V: int, K: int, A, B, targets, loss, lse, workspace=None, workspace_bytes=None,
+                               stream=None, target_type=None) -> None:
+    """loss[m] = lse[m] - z[m][targets[m]] and lse[m] = log sum exp z[m] of the
+    logits z = A @ B^T, which are not kept.
+
+    A (M x K) and B (V x K) are BF16, targets (M) int32 or int64 (target_type,
+    INT32 or INT64, names the type of a raw address), loss and lse (M) FP32
+    outputs. A row whose target lies outside 0 .. V - 1 is left out: zeros. The
+    workspace holds cross_entropy_workspace_size(M, V, K) bytes."""
+    M, V, K = _int32(M), _int32(V), _int32(K)
+    dev = _device()
+    a, b = _values(A, BF16, _count(M, K), "A", dev), _values(B, BF16, _count(V, K), "B", dev)
+    t, tt = _ids(targets, target_type, _count(M), "targets", dev)
+    lo, ls = _floats(loss, _count(M), "loss", dev), _floats(lse, _count(M), "lse", dev)
+    w, nb = _workspace(workspace, workspace_bytes, dev)
+    _check(load().gemm_bf16_nt_cross_entropy(M, V, K, a, b, tt, t, lo, ls, w, nb, _stream(stream, dev)),
+           "gemm_bf16_nt_cross_entropy")
+
+
+def cross_entropy_workspace_size(M: int, V: int, K: int) -> int:
+    """Workspace bytes of gemm_bf16_nt_cross_entropy on the current device."""
+    return _size_of("gemm_bf16_nt_cross_entropy_workspace_size", M, V, K)
+
+
+def gemm_bf16_nt_cross_entropy_bwd(M: int, V: int, K: int, A, B, targets, lse, dloss, dA, dB, workspace=None,
+                                   workspace_bytes=None, stream=None, target_type=None) -> None:
+    """Gradients of gemm_bf16_nt_cross_entropy: dA (M x K) and dB (V x K), BF16,
+    each None if it is not wanted, from the forward call's lse and dloss (M, FP32;
+    None for ones), the gradient of each row's loss. Rows that are left out get
+    zeros in dA and add nothing to dB. The workspace holds
+    cross_entropy_bwd_workspace_size(M, V, K) bytes."""
+    M, V, K = _int32(M), _int32(V), _int32(K)
+    dev = _device()
+    a, b = _values(A, BF16, _count(M, K), "A", dev), _values(B, BF16, _count(V, K), "B", dev)
+    t, tt = _ids(targets, target_type, _count(M), "targets", dev)
+    ls, dl = _floats(lse, _count(M), "lse", dev), _floats(dloss, _count(M), "dloss", dev)
+    da, db = _values(dA, BF16, _count(M, K), "dA", dev), _values(dB, BF16, _count(V, K), "dB", dev)
+    w, nb = _workspace(workspace, workspace_bytes, dev)
+    _check(load().gemm_bf16_nt_cross_entropy_bwd(M, V, K, a, b, tt, t, ls, dl, da, db, w, nb, _stream(stream, dev)),
+           "gemm_bf16_nt_cross_entropy_bwd")
+
+
+def cross_entropy_bwd_workspace_size(M: int, V: int, K: int) -> int:
+    """Workspace bytes of gemm_bf16_nt_cross_entropy_bwd on the current device."""
+    return _size_of("gemm_bf16_nt_cross_entropy_bwd_workspace_size", M, V, K)
 
 
 def force_layer_kernel(kernel: int) -> None:

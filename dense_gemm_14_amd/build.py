@@ -14,11 +14,11 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libgemm355.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("gemm355.hip", "dense_ops.hip", "model_ops.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("gemm355.hip", "dense_ops.hip", "loss_ops.hip", "model_ops.hip")]
 HEADERS = [os.path.join(CSRC, f) for f in ("common.hpp", "gemm_bf16.hpp", "gemm_bf16_small.hpp", "gemm_bf16_small_long.hpp", "gemm_bf16_splitk.hpp",
                                            "gemm_fp4.hpp", "fp4_decode.hpp", "gemm_mxfp4.hpp", "schedule.hpp", "host.hpp",
                                            "dense_common.hpp", "dense_large.hpp", "dense_small.hpp", "dense_tile.hpp", "dense_grad.hpp", "newton_schulz.hpp",
-                                           "checks.hpp", "vector8.hpp", "embedding.hpp", "layer_norm.hpp")] + \
+                                           "checks.hpp", "dense_plan.hpp", "dense_loss.hpp", "cross_entropy.hpp", "vector8.hpp", "embedding.hpp", "layer_norm.hpp")] + \
     [os.path.join(INCLUDE, "gemm355.h")]
 
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.c")

@@ -1,0 +1,220 @@
+// cross_entropy.hpp -- softmax cross entropy over a vocabulary, and its gradient,
+// without keeping the logits z = A B^T (M tokens, V rows of the vocabulary).
+//
+//   lse[m] = log sum exp z[m][v],  loss[m] = lse[m] - z[m][target[m]]
+//   dz[m][v] = (exp(z[m][v] - lse[m]) - [v = target[m]]) dloss[m]
+//   dA = dz B,  dB = dz^T A
+//
+// Forward: one product whose epilogue leaves, for each row and run of 64 or 128
+// columns, the largest z and the sum of the exponentials under it, and the
+// target's z (dense_loss.hpp); a second kernel joins the runs. 8 bytes for every
+// 128 logits go through memory.
+// Backward: for a piece of the vocabulary at a time z again, with dz as its
+// epilogue's result, and both products of that piece; dA's sums are kept in FP32
+// between the pieces. A piece's dz, in BF16, is what the workspace has to hold.
+//
+// Rows that are left out (padding, prompts) cost nothing: the kept rows are moved
+// together beforehand, and the products take their number from device memory.
+// That also keeps whatever the other rows hold, infinities included, out of dB.
+//
+// dz enters the products in BF16. The rows' weights dloss are taken relative to
+// the largest, and that one multiplies the FP32 results: with equal weights, a
+// mean's, dz is rounded as if there were none (2^-8 of a weight at most, the same
+// for every element, would otherwise be in both gradients).
+#pragma once
+
+#include "dense_loss.hpp"
+
+namespace gemm355 {
+namespace dense {
+
+constexpr int CE_THREADS = 256, CE_WAVES = CE_THREADS / 64;
+
+struct CePrepArgs {
+    const void *ids;          // the targets
+    const void *a;
+    const float *lse, *dloss; // backward (dloss may be NULL: ones)
+    int *rows;                // number of kept rows
+    int *map, *target;        // of each kept row: where it was, its target
+    float *klse, *weight;     // backward: its lse, its weight relative to *scale
+    float *scale;             // backward
+    void *ka;                 // the kept rows of A, zeros behind them
+    float *loss0, *lse0;      // forward: zeros for rows that are left out
+    void *da;                 // backward: zeros for their gradient, or NULL
+    void *dz;                 // backward: zeros behind the kept rows
+    int M, V, K;
+    int chunk;                // rows per workgroup
+    int dz_pitch;
+    int splits[2], min_steps[2];   // backward: of the products over the rows
+    bool wide;
+};
+
+// Rows of dz and A that a product over them reads: whole K steps for a kernel
+// that needs some (min_steps > 0), else those that there are.
+__host__ __device__ inline int64_t ce_depth(int64_t rows, int splits, int min_steps)
+{
+    if (min_steps == 0)
+        return rows;
+    const int64_t steps = ((rows + 63) / 64 + splits - 1) / splits;
+    return 64 * splits * (steps > min_steps ? steps : min_steps);
+}
+
+template <bool BWD>
+__global__ __launch_bounds__(CE_THREADS) void ce_prep_kernel(CePrepArgs p)
+{
+    __shared__ int part[3][CE_WAVES], place[CE_THREADS];
+    __shared__ float top[CE_WAVES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t r0 = (int64_t)blockIdx.x * p.chunk, r1 = min((int64_t)p.M, r0 + p.chunk);
+
+    // every workgroup looks at all targets, and so waits for no other
+    int before = 0, kept = 0;
+    float largest = 0.0f;
+#pragma unroll 4
+    for (int64_t m = tid; m < p.M; m += CE_THREADS) {
+        const bool in = rows::id_at(p.ids, p.wide, (size_t)m, p.V) >= 0;
+        before += in && m < r0;
+        kept += in;
+        if constexpr (BWD)
+            if (p.dloss && in) {
+                const float w = fabsf(p.dloss[m]);
+                largest = fmaxf(largest, w < __builtin_inff() ? w : 0.0f);
+            }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        before += __shfl_xor(before, d);
+        kept += __shfl_xor(kept, d);
+        if constexpr (BWD)
+            largest = fmaxf(largest, __shfl_xor(largest, d));
+    }
+    if (lane == 0) {
+        part[0][wave] = before;
+        part[1][wave] = kept;
+        top[wave] = largest;
+    }
+    __syncthreads();
+    before = kept = 0;
+    largest = 0.0f;
+#pragma unroll
+    for (int w = 0; w < CE_WAVES; ++w) {
+        before += part[0][w];
+        kept += part[1][w];
+        largest = fmaxf(largest, top[w]);
+    }
+    const float scale = BWD && p.dloss && largest > 0.0f ? largest : 1.0f;
+    if (blockIdx.x == 0 && tid == 0) {
+        *p.rows = kept;
+        if constexpr (BWD)
+            *p.scale = scale;
+    }
+
+    const uint16_t *a = static_cast<const uint16_t *>(p.a);
+    uint16_t *ka = static_cast<uint16_t *>(p.ka);
+    for (int64_t first = r0; first < r1; first += CE_THREADS) {
+        const int64_t m = first + tid;
+        const int target = m < r1 ? rows::id_at(p.ids, p.wide, (size_t)m, p.V) : -1;
+        const unsigned long long in = __ballot(target >= 0);
+        if (lane == 0)
+            part[2][wave] = __popcll(in);
+        __syncthreads();
+        int at = before + __popcll(in & ((1ull << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < CE_WAVES; ++w) {
+            at += w < wave ? part[2][w] : 0;
+            before += part[2][w];
+        }
+        place[tid] = target >= 0 ? at : -1;
+        if (target >= 0) {
+            p.map[at] = (int)m;
+            p.target[at] = target;
+            if constexpr (BWD) {
+                p.klse[at] = p.lse[m];
+                p.weight[at] = p.dloss ? p.dloss[m] / scale : 1.0f;
+            }
+        } else if (!BWD && m < r1) {
+            p.loss0[m] = 0.0f;
+            p.lse0[m] = 0.0f;
+        }
+        __syncthreads();
+        for (int i = wave; i < CE_THREADS && first + i < r1; i += CE_WAVES) {
+            const int to = __builtin_amdgcn_readfirstlane(place[i]);
+            if (to >= 0) {
+                const uint16_t *from = a + (size_t)(first + i) * (size_t)p.K;
+#pragma unroll 8
+                for (int c = 8 * lane; c < p.K; c += 512)
+                    *reinterpret_cast<u32x4 *>(ka + (size_t)to * (size_t)p.K + (size_t)c) = *reinterpret_cast<const u32x4 *>(from + c);
+            } else if (BWD && p.da) {
+                for (int c = 8 * lane; c < p.K; c += 512)
+                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.da) + (size_t)(first + i) * (size_t)p.K + (size_t)c) = u32x4{};
+            }
+        }
+    }
+    if constexpr (BWD) {
+        // zeros behind the kept rows, up to the last step of the products over them
+        const int64_t depth = max(ce_depth(kept, p.splits[0], p.min_steps[0]), ce_depth(kept, p.splits[1], p.min_steps[1]));
+        for (int64_t row = kept + (int64_t)blockIdx.x * CE_WAVES + wave; row < depth; row += (int64_t)gridDim.x * CE_WAVES) {
+            for (int c = 8 * lane; c < p.K; c += 512)
+                *reinterpret_cast<u32x4 *>(ka + (size_t)row * (size_t)p.K + (size_t)c) = u32x4{};
+            for (int c = 8 * lane; c < p.dz_pitch; c += 512)
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.dz) + (size_t)row * (size_t)p.dz_pitch + (size_t)c) = u32x4{};
+        }
+    }
+}
+
+// Joins the runs of ROWS rows: as many lanes side by side, the others share out
+// the runs.
+struct CeJoinArgs {
+    const f32x2 *stats;      // [run][stride]: {largest, sum}
+    const float *picked;
+    const int *rows, *map;   // or NULL: M rows, in place, whose targets say which are left out
+    const void *ids;
+    float *loss, *lse;
+    int M, V, stride, runs;
+    bool wide;
+};
+
+struct CeSum {
+    float top, sum, rest;    // the largest finite value, the sum under it, and what was not finite
+};
+__device__ inline CeSum ce_join(const CeSum &a, const CeSum &b)
+{
+    // (a side without a finite value has top -inf and sum 0)
+    const float base = loss_base(fmaxf(a.top, b.top));
+    return CeSum{fmaxf(a.top, b.top), a.sum * loss_exp(a.top, base) + b.sum * loss_exp(b.top, base), a.rest + b.rest};
+}
+
+template <int ROWS>
+__global__ __launch_bounds__(CE_THREADS) void ce_join_kernel(CeJoinArgs p)
+{
+    constexpr int LANES = CE_THREADS / ROWS;
+    __shared__ CeSum part[LANES][ROWS];
+    const int tx = threadIdx.x % ROWS, ty = threadIdx.x / ROWS;
+    const int M = p.rows ? __builtin_amdgcn_readfirstlane(*p.rows) : p.M;
+    const int m = (int)blockIdx.x * ROWS + tx;
+    CeSum s = {-__builtin_inff(), 0.0f, 0.0f};
+    if (m < M)
+#pragma unroll 8
+        for (int i = ty; i < p.runs; i += LANES) {
+            const f32x2 t = p.stats[(size_t)i * (size_t)p.stride + (size_t)m];
+            s = ce_join(s, __builtin_isinf(t[0]) ? CeSum{-__builtin_inff(), 0.0f, t[1]} : CeSum{t[0], t[1], 0.0f});
+        }
+    part[ty][tx] = s;
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d /= 2) {
+        __syncthreads();
+        if (ty < d)
+            part[ty][tx] = s = ce_join(s, part[ty + d][tx]);
+    }
+    if (ty == 0 && m < M) {
+        const float base = loss_base(s.top), rest = logf(s.sum + s.rest);
+        const int row = p.map ? p.map[m] : m;
+        const bool out = !p.map && rows::id_at(p.ids, p.wide, (size_t)m, p.V) < 0;
+        p.lse[row] = out ? 0.0f : base + rest;
+        p.loss[row] = out ? 0.0f : (base - p.picked[m]) + rest;
+    }
+}
+
+} // namespace dense
+} // namespace gemm355

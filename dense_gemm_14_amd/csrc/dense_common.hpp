@@ -24,8 +24,13 @@ enum Epilogue {
     EPI_GATED = 2,   // gate and up sums of one column: C = round(act(zg) zu), Z = round of both if wanted
     EPI_STORE_SYM = 3,   // EPI_STORE of a symmetric product: tiles on and below the diagonal, FP16,
                          // those below it stored a second time, mirrored
-    EPI_POLY = 4         // C = round(alpha acc + beta R + gamma [row == column]), symmetric likewise
+    EPI_POLY = 4,        // C = round(alpha acc + beta R + gamma [row == column]), symmetric likewise
+    EPI_CE = 5,          // the loss over a vocabulary (dense_loss.hpp)
+    EPI_CE_GRAD = 6,
+    EPI_ACC = 7
 };
+constexpr bool epi_symmetric(int epi) { return epi == EPI_STORE_SYM || epi == EPI_POLY; }
+constexpr bool epi_loss(int epi) { return epi >= EPI_CE; }
 // Activations (the values of gemm355_activation).
 enum { A_NONE = 0, A_RELU = 1, A_GELU = 2, A_SILU = 3 };
 
@@ -45,7 +50,51 @@ struct DenseArgs {
     int batch;
     int grid;            // workgroups of a round
     float alpha, beta, gamma;
+
+    int lda;             // elements from one stored row of A to the next
+    // Sizes that only the device knows: *rows replaces M or, with rows_in_k, K. A
+    // kernel that takes whole K steps has min_steps > 0: every split then gets at
+    // least as many, and the operands have zeros behind their rows.
+    const int *rows;
+    int rows_in_k, min_steps;
+    const float *scale;  // EPI_STORE, EPI_ACC: factor of the result, or (EPI_STORE) NULL
+    // EPI_CE, EPI_CE_GRAD: B's rows are v0 .. v0 + N - 1 of the vocabulary
+    const int *target;   // the rows' targets; NULL: ids, as the caller has them, of `vocab` ones
+    const void *ids;
+    int wide, vocab;
+    const float *lse, *weight;
+    int v0;
+    int ldc;             // EPI_CE_GRAD: elements from one row of C to the next
+    f32x2 *stats;        // EPI_CE: {largest, sum} [run of columns][stats_rows]
+    float *picked;       // the targets' values
+    int stats_rows;
+    // EPI_ACC
+    float *acc;          // M x N sums of the pieces before (add), of this one too (!last)
+    const int *map;      // C's row of each row, or NULL
+    int c_rows;          // rows of C
+    int add, last;
 };
+
+__device__ inline int device_rows(const DenseArgs &p) { return __builtin_amdgcn_readfirstlane(*p.rows); }
+
+// Takes the sizes that only the device knows; `side`: rows of a tile. The split
+// tiles stay as many, or all that are left.
+__device__ inline void take_rows(DenseArgs &p, int side)
+{
+    if (!p.rows)
+        return;
+    const int n = device_rows(p);
+    if (p.rows_in_k) {
+        p.steps_per_split = max(p.min_steps, ((n + 63) / 64 + p.splits - 1) / p.splits);
+        p.K = p.min_steps > 0 ? 64 * p.steps_per_split * p.splits : n;
+    } else {
+        const int tail = p.tiles - p.whole;
+        p.M = n;
+        p.tiles_m = (n + side - 1) / side;
+        p.tiles = p.tiles_m * p.tiles_n;
+        p.whole = max(0, p.tiles - tail);
+    }
+}
 
 // Asks for all arguments at the kernel's start, at once: left to the compiler
 // they are fetched in three dependent steps, which a product of a few
@@ -196,7 +245,7 @@ __device__ inline void triangle_tile(int p, int &tm, int &tn)
 template <int EPI>
 __device__ inline void dense_tile(const DenseArgs &p, int pos, int &tm, int &tn)
 {
-    if constexpr (EPI >= EPI_STORE_SYM)
+    if constexpr (epi_symmetric(EPI))
         triangle_tile(pos, tm, tn);
     else
         supergroup_tile(pos, p.tiles_m, p.tiles_n, p.supergroup, tm, tn);
@@ -404,10 +453,11 @@ __device__ inline void finish_row(const DenseArgs &p, f32x4 (&x)[BJ], int m, int
                 x[j + 1] += r1;
             }
     } else {
+        const float alpha = EPI == EPI_STORE && p.scale ? p.alpha * *p.scale : p.alpha;
 #pragma unroll
         for (int j = 0; j < BJ; j += 2) {
-            x[j] *= p.alpha;
-            x[j + 1] *= p.alpha;
+            x[j] *= alpha;
+            x[j + 1] *= alpha;
             if constexpr (EPI == EPI_POLY) {
                 f32x4 r0, r1;
                 unpack_pair<TO>(res[j / 2], r0, r1);

@@ -171,10 +171,11 @@ __device__ inline void bias_block(const BiasArgs &p, int block, float *part)
     }
 }
 
-__global__ __launch_bounds__(BIAS_THREADS) void dense_bias_kernel(BiasArgs p)
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void dense_bias_kernel(BiasArgs p)
 {
-    __shared__ float part[BIAS_THREADS / 8 * BIAS_PITCH];
-    bias_block<BIAS_THREADS>(p, (int)blockIdx.x, part);
+    __shared__ float part[THREADS / 8 * BIAS_PITCH];
+    bias_block<THREADS>(p, (int)blockIdx.x, part);
 }
 
 } // namespace dense

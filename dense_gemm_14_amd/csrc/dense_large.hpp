@@ -35,6 +35,7 @@
 #pragma once
 
 #include "dense_common.hpp"
+#include "dense_loss.hpp"
 
 namespace gemm355 {
 namespace dense {
@@ -123,6 +124,7 @@ void dense_large_kernel(DenseArgs p)
     constexpr int SIDE = 32 * BLOCKS, UNIT = big_unit(BLOCKS), COPIES = BLOCKS, COLS = big_columns(EPI, SIDE);
     __shared__ __attribute__((aligned(1024))) uint8_t lds[BIG_SLOTS * UNIT];
 
+    take_rows(p, SIDE);
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -132,9 +134,9 @@ void dense_large_kernel(DenseArgs p)
     const int nk = (p.K + BIG_BK - 1) / BIG_BK;
 
     const unsigned lds_base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
-    const unsigned a_step = LA == ROW_K ? BIG_BK * 2u : (unsigned)BIG_BK * (unsigned)p.M * 2u;
+    const unsigned a_step = LA == ROW_K ? BIG_BK * 2u : (unsigned)BIG_BK * (unsigned)p.lda * 2u;
     const unsigned b_step = LB == ROW_K ? BIG_BK * 2u : (unsigned)BIG_BK * (unsigned)p.N * 2u;
-    const unsigned a_bytes = (unsigned)p.M * (unsigned)p.K * 2u;
+    const unsigned a_bytes = (unsigned)(LA == ROW_K ? p.M : p.K) * (unsigned)p.lda * 2u;
     const unsigned b_bytes = (unsigned)p.N * (unsigned)p.K * 2u * (EPI == EPI_GATED ? 2u : 1u);
 
     // The workgroup's items: one per round.
@@ -163,7 +165,7 @@ void dense_large_kernel(DenseArgs p)
     // (COL_K) to the last eight: they only feed outputs that are not stored.
     unsigned long long ga, gb;
     unsigned voff[2][COPIES];
-    auto place_rows = [&](auto layout_c, unsigned (&o)[COPIES], int row0, int rows, bool gated) {
+    auto place_rows = [&](auto layout_c, unsigned (&o)[COPIES], int row0, int rows, int pitch, bool gated) {
         constexpr int L = decltype(layout_c)::value;
         const int ln = fresh_lane();
 #pragma unroll
@@ -176,12 +178,12 @@ void dense_large_kernel(DenseArgs p)
                 // its last four the up columns of the same outputs
                 const int row = gated ? ((r & 64) ? rows : 0) + min(row0 + 64 * (r >> 7) + (r & 63), rows - 1)
                                       : min(row0 + r, rows - 1);
-                o[j] = ((unsigned)row * (unsigned)p.K + 8u * (unsigned)c) * 2u + BIG_SHIFT - 1024u * (j & 3);
+                o[j] = ((unsigned)row * (unsigned)pitch + 8u * (unsigned)c) * 2u + BIG_SHIFT - 1024u * (j & 3);
             } else {
                 const int k = 2 * block + (ln >> 5), pos = ln & 31;
                 const int c = (((pos >> 1) ^ key_col(k)) << 1) | (pos & 1);
-                const int col = min(row0 + 8 * c, rows - 8);
-                o[j] = ((unsigned)k * (unsigned)rows + (unsigned)col) * 2u + BIG_SHIFT - 1024u * (j & 3);
+                const int col = min(row0 + 8 * c, (rows - 1) & ~7);
+                o[j] = ((unsigned)k * (unsigned)pitch + (unsigned)col) * 2u + BIG_SHIFT - 1024u * (j & 3);
             }
         }
     };
@@ -191,8 +193,8 @@ void dense_large_kernel(DenseArgs p)
         dense_tile<EPI>(p, tile - b * p.tiles, tm, tn);
         ga = reinterpret_cast<unsigned long long>(p.a) + (unsigned long long)b * a_bytes - BIG_SHIFT;
         gb = reinterpret_cast<unsigned long long>(p.b) + (unsigned long long)b * b_bytes - BIG_SHIFT;
-        place_rows(Int<LA>{}, voff[0], tm * SIDE, p.M, false);
-        place_rows(Int<LB>{}, voff[1], tn * COLS, p.N, EPI == EPI_GATED);
+        place_rows(Int<LA>{}, voff[0], tm * SIDE, p.M, p.lda, false);
+        place_rows(Int<LB>{}, voff[1], tn * COLS, p.N, LB == ROW_K ? p.K : p.N, EPI == EPI_GATED);
     };
     place_copies(item.tile);
     // ROW_K, per block parity: this lane's chunk of the last K step lies below K
@@ -320,7 +322,7 @@ void dense_large_kernel(DenseArgs p)
     // The fragments of an item's first step that are not read within it. The
     // last step of the item before reads them too; where the epilogue needs the
     // registers (REREAD) they are read again behind it.
-    constexpr bool REREAD = EPI == EPI_LINEAR || EPI == EPI_POLY;
+    constexpr bool REREAD = EPI == EPI_LINEAR || EPI == EPI_POLY || epi_loss(EPI);
     auto read_first = [&]() {
 #pragma unroll
         for (int j = 0; j < BLOCKS - 1; ++j) {
@@ -426,9 +428,12 @@ void dense_large_kernel(DenseArgs p)
             dense_tile<EPI>(p, item.tile - b * p.tiles, tm, tn);
             if (p.batch > 1)
                 enter_batch(q, b);
-            const Views v = make_views<EPI>(q);
             const int m0 = tm * SIDE + SIDE / 2 * wm;
             const int col = tn * COLS + COLS / 2 * wn;
+            if constexpr (epi_loss(EPI))
+                loss_rows<EPI>(q, acc, m0, col, ln, [&](int i) { hold_row(acc[i]); });
+            else {
+            const Views v = make_views<EPI>(q);
             with_epilogue<EPI>(q, [&](auto act_c, auto extra_c) {
                 constexpr int ACT = decltype(act_c)::value, EXTRA = decltype(extra_c)::value;
                 u32x2 bias[BLOCKS];
@@ -448,11 +453,12 @@ void dense_large_kernel(DenseArgs p)
                     if (i + AHEAD < BLOCKS)
                         load_res_row<EPI, EXTRA, BLOCKS>(q, v, m0 + 16 * (i + AHEAD) + (ln & 15), col, ln, res[i % AHEAD]);
                     store_row<EXTRA>(q, v, row, m0 + 16 * i + (ln & 15), col, ln);
-                    if constexpr (EPI >= EPI_STORE_SYM)
+                    if constexpr (epi_symmetric(EPI))
                         if ((i & 1) && tm != tn)
                             store_mirrored(q, v, acc[i - 1], acc[i], m0 + 16 * (i - 1), col, ln);
                 }
             });
+            }
         }
         if constexpr (REREAD)
             read_first();
@@ -472,6 +478,7 @@ constexpr int BIG_REDUCE_WAVES = 4;
 template <int EPI, class TO>
 __global__ __launch_bounds__(64 * BIG_REDUCE_WAVES) void dense_large_reduce_kernel(DenseArgs p)
 {
+    take_rows(p, BIG);
     const int lane = threadIdx.x & 63;
     const int unit = (int)blockIdx.x * BIG_REDUCE_WAVES + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int tail = p.tiles * p.batch - p.whole, t = unit >> 4;
@@ -496,9 +503,13 @@ __global__ __launch_bounds__(64 * BIG_REDUCE_WAVES) void dense_large_reduce_kern
     DenseArgs q = p;
     if (p.batch > 1)
         enter_batch(q, b);
-    const Views v = make_views<EPI>(q);
     const int m0 = tm * BIG + 128 * (wave & 1) + 16 * i0;
     const int col = tn * big_columns(EPI) + big_columns(EPI) / 2 * (wave >> 1);
+    if constexpr (epi_loss(EPI)) {
+        loss_rows<EPI>(q, x, m0, col, lane, [](int) {});
+        return;
+    } else {
+    const Views v = make_views<EPI>(q);
     with_epilogue<EPI>(q, [&](auto act_c, auto extra_c) {
         constexpr int ACT = decltype(act_c)::value, EXTRA = decltype(extra_c)::value;
         u32x2 bias[8];
@@ -514,9 +525,10 @@ __global__ __launch_bounds__(64 * BIG_REDUCE_WAVES) void dense_large_reduce_kern
             store_row<EXTRA>(q, v, row, m0 + 16 * i + (lane & 15), col, lane);
         }
     });
-    if constexpr (EPI >= EPI_STORE_SYM)
+    if constexpr (epi_symmetric(EPI))
         if (tm != tn)
             store_mirrored(q, v, x[0], x[1], m0, col, lane);
+    }
 }
 
 } // namespace dense

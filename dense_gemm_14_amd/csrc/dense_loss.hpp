@@ -1,0 +1,323 @@
+// dense_loss.hpp -- epilogues of the products around the softmax cross entropy
+// over a vocabulary (cross_entropy.hpp has the other kernels and the whole):
+//
+//   EPI_CE       z = A B^T of a tile. Nothing of it is stored but, for each row
+//                and run of columns, the largest z and the sum of exp(z - largest),
+//                and the target's z where the run holds it.
+//   EPI_CE_GRAD  z again, C = round((exp(z - lse) - [column = target]) weight),
+//                zeros in the columns between N and the next multiple of 8
+//   EPI_ACC      sums over pieces of the contraction: FP32 sums, added to those
+//                of the pieces before, rounded to C by the last piece
+//
+// Work per element: an exponential, at a quarter of the vector rate, and about
+// five plain instructions, 4 % of a tile's time at K = 4096; a compare with the
+// target only in the runs that hold one.
+#pragma once
+
+#include "dense_common.hpp"
+#include "vector8.hpp"
+
+namespace gemm355 {
+namespace dense {
+
+constexpr float LOG2E = 1.4426950408889634f;
+
+// Variants of a tile's epilogue. EPI_CE, EPI_CE_GRAD: LOSS_EDGE, the run has
+// columns past N. EPI_ACC: LOSS_ADD, there is a piece before; LOSS_LAST, there is
+// none after.
+enum { LOSS_EDGE = 1, LOSS_ADD = 1, LOSS_LAST = 2 };
+
+template <int EPI, class F>
+__device__ inline void with_loss(const DenseArgs &p, int col, int width, F &&f)
+{
+    if constexpr (EPI == EPI_ACC) {
+        if (p.add)
+            p.last ? f(Int<LOSS_ADD | LOSS_LAST>{}) : f(Int<LOSS_ADD>{});
+        else
+            p.last ? f(Int<LOSS_LAST>{}) : f(Int<0>{});
+    } else {
+        if (col + width > p.N)
+            f(Int<LOSS_EDGE>{});
+        else
+            f(Int<0>{});
+    }
+}
+
+// What an epilogue needs to know of row m: EPI_CE the target's column, EPI_CE_GRAD
+// that and the row's lse and weight, EPI_ACC (last piece) the row of C.
+struct LossRow {
+    int at;
+    float lse, weight;
+};
+// Column of row m's target; below 0 for a row that is left out.
+__device__ inline int loss_target(const DenseArgs &p, int m)
+{
+    return (p.target ? p.target[m] : rows::id_at(p.ids, p.wide, (size_t)m, p.vocab)) - p.v0;
+}
+template <int EPI, int MODE>
+__device__ inline LossRow loss_row_of(const DenseArgs &p, int m)
+{
+    LossRow r = {-1, 0.0f, 0.0f};
+    if (m < p.M) {
+        if constexpr (EPI == EPI_ACC) {
+            if constexpr (MODE & LOSS_LAST)
+                r.at = p.map ? p.map[m] : m;
+        } else {
+            r.at = loss_target(p, m);
+            if constexpr (EPI == EPI_CE_GRAD) {
+                r.lse = p.lse[m];
+                r.weight = p.weight[m];
+            }
+        }
+    }
+    return r;
+}
+
+// Largest and sum over the four lanes that hold a row (l16, 16 + l16, ...): a swap
+// of a value with itself leaves each lane both halves' values.
+struct Two {
+    float a, b;
+};
+__device__ inline Two swap_halves(float x)
+{
+    const unsigned w = __builtin_bit_cast(unsigned, x);
+    const auto s = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    const unsigned a = s[0], b = s[1];
+    return Two{__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+__device__ inline Two swap_rows(float x)
+{
+    const unsigned w = __builtin_bit_cast(unsigned, x);
+    const auto s = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    const unsigned a = s[0], b = s[1];
+    return Two{__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+__device__ inline float row_max(float x)
+{
+    const Two h = swap_halves(x), r = swap_rows(fmaxf(h.a, h.b));
+    return fmaxf(r.a, r.b);
+}
+__device__ inline float row_add(float x)
+{
+    const Two h = swap_halves(x), r = swap_rows(h.a + h.b);
+    return r.a + r.b;
+}
+
+// What the exponentials' arguments are taken from: the largest value, or 0 where
+// it is infinite (all -inf then give a sum of 0, and +inf one of +inf; NaN is in
+// the sum in any case).
+__device__ inline float loss_base(float top) { return __builtin_isinf(top) ? 0.0f : top; }
+// The difference is taken first: as one multiply-add with top * log2(e) rounded
+// beforehand every term would be off by the same 2^-24 top log2(e).
+__device__ inline float loss_exp(float z, float base) { return __builtin_amdgcn_exp2f((z - base) * LOG2E); }
+__device__ inline float loss_softmax(float z, float lse) { return __builtin_amdgcn_exp2f(z * LOG2E - lse * LOG2E); }
+
+// What a row of blocks reads besides its sums (EPI_ACC: the pieces' before).
+template <int EPI, int MODE, int BJ>
+__device__ inline void load_acc_row(const DenseArgs &p, int m, int col, int lane, f32x4 (&add)[BJ])
+{
+    if constexpr (EPI == EPI_ACC && (MODE & LOSS_ADD))
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) {
+            const int n = col + 16 * j + 4 * (lane >> 4);
+            add[j] = m < p.M && n < p.N ? *reinterpret_cast<const f32x4 *>(p.acc + (size_t)m * (size_t)p.N + (size_t)n) : f32x4{};
+        }
+}
+
+// The epilogue of one row of blocks: x[0 .. BJ - 1], BJ blocks side by side at
+// column `col`, this lane's row m.
+template <int EPI, int MODE, int BJ>
+__device__ inline void loss_row(const DenseArgs &p, const __amdgpu_buffer_rsrc_t &rc, f32x4 (&x)[BJ], int m, int col,
+                                int lane, const LossRow &row, const f32x4 (&add)[BJ])
+{
+    const int n0 = col + 4 * (lane >> 4);
+    if constexpr (EPI == EPI_CE) {
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (MODE & LOSS_EDGE)
+                    x[j][e] = n0 + 16 * j + e < p.N ? x[j][e] : -__builtin_inff();
+                top = fmaxf(top, x[j][e]);
+            }
+        top = row_max(top);
+        const float base = loss_base(top);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) {
+            float t[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                t[e] = loss_exp(x[j][e], base);
+            sum += (t[0] + t[1]) + (t[2] + t[3]);
+        }
+        sum = row_add(sum);
+        if (lane < 16 && m < p.M && col < p.N)
+            p.stats[(size_t)(col / (16 * BJ)) * (size_t)p.stats_rows + (size_t)m] = f32x2{top, sum};
+        const int d = row.at - n0;
+        if (__ballot(row.at >= col && row.at < col + 16 * BJ) != 0) {
+#pragma unroll
+            for (int j = 0; j < BJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (d == 16 * j + e)
+                        p.picked[m] = x[j][e];
+        }
+    }
+    if constexpr (EPI == EPI_CE_GRAD) {
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[j][e] = loss_softmax(x[j][e], row.lse);
+        const int d = row.at - n0;
+        if (__ballot(row.at >= col && row.at < col + 16 * BJ) != 0) {
+#pragma unroll
+            for (int j = 0; j < BJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[j][e] -= d == 16 * j + e ? 1.0f : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[j][e] *= row.weight;
+                if constexpr (MODE & LOSS_EDGE)
+                    x[j][e] = n0 + 16 * j + e < p.N ? x[j][e] : 0.0f;
+            }
+#pragma unroll
+        for (int j = 0; j < BJ; j += 2)
+            store16(pack_pair<__bf16>(x[j], x[j + 1]), rc, pair_offset(p, m, col + 16 * j, p.ldc, 0, lane));
+    }
+    if constexpr (EPI == EPI_ACC) {
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+            if constexpr (MODE & LOSS_ADD)
+                x[j] += add[j];
+        if constexpr (MODE & LOSS_LAST) {
+            const float scale = *p.scale;
+#pragma unroll
+            for (int j = 0; j < BJ; j += 2) {
+                const u32x4 w = pack_pair<__bf16>(x[j] * scale, x[j + 1] * scale);
+                const int n = col + 16 * j + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
+                store16(w, rc, m < p.M && n < p.N ? (int)(((unsigned)row.at * (unsigned)p.N + (unsigned)n) * 2u) : OOB);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < BJ; ++j)
+                if (m < p.M && n0 + 16 * j < p.N)
+                    *reinterpret_cast<f32x4 *>(p.acc + (size_t)m * (size_t)p.N + (size_t)(n0 + 16 * j)) = x[j];
+        }
+    }
+}
+
+// Where the epilogue stores 16-bit values.
+template <int EPI>
+__device__ inline __amdgpu_buffer_rsrc_t loss_rsrc(const DenseArgs &p)
+{
+    const unsigned bytes = EPI == EPI_CE_GRAD ? (unsigned)p.M * (unsigned)p.ldc * 2u
+                           : EPI == EPI_ACC   ? (unsigned)p.c_rows * (unsigned)p.N * 2u : 0u;
+    return make_rsrc(p.c, bytes);
+}
+
+// Rows of blocks m0 + 16 i, i < R, of a wave's tile, BJ blocks wide at `col`;
+// hold(i) before row i's sums are used.
+template <int EPI, int R, int BJ, class Hold>
+__device__ inline void loss_rows(const DenseArgs &p, f32x4 (&x)[R][BJ], int m0, int col, int lane, Hold &&hold)
+{
+    const __amdgpu_buffer_rsrc_t rc = loss_rsrc<EPI>(p);
+    with_loss<EPI>(p, col, 16 * BJ, [&](auto mode_c) {
+        constexpr int MODE = decltype(mode_c)::value;
+        constexpr int AHEAD = EPI == EPI_ACC && (MODE & LOSS_ADD) ? (R < 2 ? R : 2) : 1;
+        LossRow row[R];
+        f32x4 add[AHEAD][BJ];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            row[i] = loss_row_of<EPI, MODE>(p, m0 + 16 * i + (lane & 15));
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            load_acc_row<EPI, MODE>(p, m0 + 16 * i + (lane & 15), col, lane, add[i]);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            hold(i);
+            loss_row<EPI, MODE>(p, rc, x[i], m0 + 16 * i + (lane & 15), col, lane, row[i], add[i % AHEAD]);
+            if (i + AHEAD < R)
+                load_acc_row<EPI, MODE>(p, m0 + 16 * (i + AHEAD) + (lane & 15), col, lane, add[i % AHEAD]);
+        }
+    });
+}
+
+// The same for eight consecutive columns n .. n + 7 of row m, one of the RUNS
+// neighbouring lanes that hold a tile's row (small tiles). All of them call it,
+// in or out of C.
+template <int EPI, int RUNS>
+__device__ inline void loss_eight(const DenseArgs &p, float (&x)[8], int m, int n, int part)
+{
+    const bool in = m < p.M && n < p.N;
+    if constexpr (EPI == EPI_CE) {
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = in && n + e < p.N ? x[e] : -__builtin_inff();
+            top = fmaxf(top, x[e]);
+        }
+#pragma unroll
+        for (int d = 1; d < RUNS; d *= 2)
+            top = fmaxf(top, __shfl_xor(top, d));
+        const float base = loss_base(top);
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            sum += loss_exp(x[e], base);
+#pragma unroll
+        for (int d = 1; d < RUNS; d *= 2)
+            sum += __shfl_xor(sum, d);
+        if (!in)
+            return;
+        if (((int)threadIdx.x & (RUNS - 1)) == 0)
+            p.stats[(size_t)part * (size_t)p.stats_rows + (size_t)m] = f32x2{top, sum};
+        const int d = loss_target(p, m) - n;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (d == e && n + e < p.N)
+                p.picked[m] = x[e];
+    } else {
+        if (!in)
+            return;
+        if constexpr (EPI == EPI_CE_GRAD) {
+            const float lse = p.lse[m], weight = p.weight[m];
+            const int d = loss_target(p, m) - n;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = n + e < p.N ? (loss_softmax(x[e], lse) - (d == e ? 1.0f : 0.0f)) * weight : 0.0f;
+            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + (size_t)m * (size_t)p.ldc + (size_t)n) =
+                u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+        }
+        if constexpr (EPI == EPI_ACC) {
+            f32x4 *acc = reinterpret_cast<f32x4 *>(p.acc + (size_t)m * (size_t)p.N + (size_t)n);
+            if (p.add) {
+                const f32x4 lo = acc[0], hi = acc[1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] += lo[e];
+                    x[4 + e] += hi[e];
+                }
+            }
+            if (p.last) {
+                const float scale = *p.scale;
+                const int row = p.map ? p.map[m] : m;
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + (size_t)row * (size_t)p.N + (size_t)n) =
+                    u32x4{pack_bf16(x[0] * scale, x[1] * scale), pack_bf16(x[2] * scale, x[3] * scale),
+                          pack_bf16(x[4] * scale, x[5] * scale), pack_bf16(x[6] * scale, x[7] * scale)};
+            } else {
+                acc[0] = f32x4{x[0], x[1], x[2], x[3]};
+                acc[1] = f32x4{x[4], x[5], x[6], x[7]};
+            }
+        }
+    }
+}
+
+} // namespace dense
+} // namespace gemm355

@@ -32,6 +32,7 @@
 
 #include "dense_common.hpp"
 #include "dense_grad.hpp"
+#include "dense_loss.hpp"
 
 namespace gemm355 {
 namespace dense {
@@ -69,10 +70,12 @@ struct SmallOperand {
         return RB == 4 ? ((k >> 1) & 1) | ((k >> 2) & 2) : RB == 2 ? (k >> 3) & 1 : 0;
     }
 
-    __device__ inline void init(const void *base, int rows, int row0, int K, int gate_rows, unsigned ring, int lane)
+    // pitch: elements from one stored row to the next
+    __device__ inline void init(const void *base, int rows, int row0, int K, int pitch, int gate_rows, unsigned ring,
+                                int lane)
     {
         const int l16 = lane & 15, grp = lane >> 4;
-        const unsigned extent = (unsigned)(GATED ? 2 * gate_rows : rows) * (unsigned)K * 2u;
+        const unsigned extent = (unsigned)(GATED ? 2 * gate_rows : LAYOUT == ROW_K ? rows : K) * (unsigned)pitch * 2u;
         rsrc = rsrc_words(static_cast<const uint8_t *>(base) - COPY_SHIFT, base ? extent + COPY_SHIFT : 0u);
         lds = ring;
 #pragma unroll
@@ -81,12 +84,12 @@ struct SmallOperand {
                 const int r = 8 * t + (lane >> 3);
                 const int c = swizzle_row(r, lane & 7);
                 const int row = row0 + (GATED ? (t < RB ? 0 : gate_rows - 8 * RB) : 0) + r;
-                off[t] = ((unsigned)row * (unsigned)K + 8u * (unsigned)c) * 2u + COPY_SHIFT - 1024u * (t & 1);
+                off[t] = ((unsigned)row * (unsigned)pitch + 8u * (unsigned)c) * 2u + COPY_SHIFT - 1024u * (t & 1);
                 chunk_k[t & 1] = 8 * c;   // the same for every second copy; rows past the operand: past its range
             } else {
                 const int k = t * (32 / RB) + lane / (2 * RB), pos = lane % (2 * RB);
                 const int col = row0 + 16 * ((pos >> 1) ^ key(k)) + 8 * (pos & 1);
-                off[t] = ((unsigned)k * (unsigned)rows + (unsigned)col) * 2u + COPY_SHIFT - 1024u * (t & 1);
+                off[t] = ((unsigned)k * (unsigned)pitch + (unsigned)col) * 2u + COPY_SHIFT - 1024u * (t & 1);
                 chunk_k[t] = col < rows ? 0 : NEVER;   // K rows past the operand lie past its range
             }
         }
@@ -95,7 +98,7 @@ struct SmallOperand {
             read_at[0] = (unsigned)(l16 * 128 + (swizzle_row(l16, grp) << 4));
             read_at[1] = (unsigned)(l16 * 128 + (swizzle_row(l16, 4 + grp) << 4));
         } else {
-            step = (unsigned)SMALL_BK * (unsigned)rows * 2u;
+            step = (unsigned)SMALL_BK * (unsigned)pitch * 2u;
             read_at[0] = (unsigned)((8 * grp + (l16 >> 2)) * 32 * RB + (l16 & 3) * 8);
             read_at[1] = (unsigned)(key(8 * grp + (l16 >> 2)) << 5);
         }
@@ -193,9 +196,10 @@ __device__ inline void finish8(const DenseArgs &p, float (&x)[8], float (&u)[8],
                 x[e] += b[e];
         }
     } else {
+        const float alpha = EPI == EPI_STORE && p.scale ? p.alpha * *p.scale : p.alpha;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            x[e] *= p.alpha;
+            x[e] *= alpha;
         if constexpr (EPI == EPI_POLY) {
             float r[8];
             unpack_eight<TO>(*at16(p.r, at), r);
@@ -226,8 +230,8 @@ __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *
     const unsigned ring = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + (unsigned)(wave * STAGES * STAGE);
     SmallOperand<T, LA, false, MB> oa;
     SmallOperand<T, LB, EPI == EPI_GATED, NB> ob;
-    oa.init(p.a, p.M, tm * 16 * MB, p.K, 0, ring, lane);
-    ob.init(p.b, p.N, tn * small_columns(EPI, NB), p.K, p.N, ring + 2048 * MB, lane);
+    oa.init(p.a, p.M, tm * 16 * MB, p.K, p.lda, 0, ring, lane);
+    ob.init(p.b, p.N, tn * small_columns(EPI, NB), p.K, LB == ROW_K ? p.K : p.N, p.N, ring + 2048 * MB, lane);
 
     const int nk = (p.K + SMALL_BK - 1) / SMALL_BK;
     auto copies = [&](int s, unsigned slot) {
@@ -309,13 +313,17 @@ __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *
     for (int q = threadIdx.x; q < 16 * MB * RUNS; q += 64 * WAVES) {
         const int r = q / RUNS, c = 8 * (q % RUNS);
         const int m = tm * 16 * MB + r, n = tn * COLS + c;
-        if (m < p.M && n < p.N) {
+        if constexpr (epi_loss(EPI)) {
+            float x[8];
+            eight(r, c, x);
+            loss_eight<EPI, RUNS>(p, x, m, n, tn);
+        } else if (m < p.M && n < p.N) {
             float x[8], u[8];
             eight(r, c, x);
             if constexpr (EPI == EPI_GATED)
                 eight(r, COLS + c, u);
             finish8<EPI, TO>(p, x, u, m, n);
-            if constexpr (EPI >= EPI_STORE_SYM)
+            if constexpr (epi_symmetric(EPI))
                 if (tm != tn) {   // for the mirror image, one element at a time
                     const u32x4 w = pack_eight<TO>(x);
 #pragma unroll
@@ -340,6 +348,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void dense_small_kernel(DenseArgs p)
     static_assert(small_lds(MB, NB, WAVES) * (8 / WAVES) <= 163840, "8 / WAVES workgroups share a compute unit's LDS");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[small_lds(MB, NB, WAVES)];
     fetch_args(p);
+    take_rows(p, 16 * MB);
     const int item = small_item(p.tiles * p.batch);
     if (item < 0)
         return;

@@ -36,6 +36,7 @@
 #pragma once
 
 #include "dense_common.hpp"
+#include "dense_loss.hpp"
 
 namespace gemm355 {
 namespace dense {
@@ -68,11 +69,12 @@ struct TileOperand {
     unsigned read_lds;   // this lane's place of the wave's first block
     unsigned flip;       // COL_K: segment of block 0, to be flipped by the block's number
 
-    __device__ inline void init(const void *base, int rows, int row0, int K, int gate_rows, unsigned lds, int wave,
-                                int lane, int half, int k_half)
+    // pitch: elements from one stored row to the next
+    __device__ inline void init(const void *base, int rows, int row0, int K, int pitch, int gate_rows, unsigned lds,
+                                int wave, int lane, int half, int k_half)
     {
         const int l16 = lane & 15, grp = lane >> 4;
-        const unsigned extent = (unsigned)(GATED ? 2 * gate_rows : rows) * (unsigned)K * 2u;
+        const unsigned extent = (unsigned)(GATED ? 2 * gate_rows : LAYOUT == ROW_K ? rows : K) * (unsigned)pitch * 2u;
         rsrc = rsrc_words(static_cast<const uint8_t *>(base) - COPY_SHIFT, base ? extent + COPY_SHIFT : 0u);
         copy_lds = lds + (unsigned)(2048 * wave);
 #pragma unroll
@@ -82,12 +84,12 @@ struct TileOperand {
                 const int r = 8 * block + (lane >> 3);
                 const int c = swizzle_row(r, lane & 7);
                 const int row = GATED ? ((r & 32) ? gate_rows : 0) + row0 + 32 * (r >> 6) + (r & 31) : row0 + r;
-                off[t] = ((unsigned)row * (unsigned)K + 8u * (unsigned)c) * 2u + COPY_SHIFT - 1024u * t;
+                off[t] = ((unsigned)row * (unsigned)pitch + 8u * (unsigned)c) * 2u + COPY_SHIFT - 1024u * t;
                 chunk_k[t] = 8 * c;   // rows past the operand lie past its range
             } else {
                 const int k = 4 * block + (lane >> 4), pos = lane & 15;
                 const int col = row0 + 8 * ((((pos >> 1) ^ key_col(k)) << 1) | (pos & 1));
-                off[t] = ((unsigned)k * (unsigned)rows + (unsigned)col) * 2u + COPY_SHIFT - 1024u * t;
+                off[t] = ((unsigned)k * (unsigned)pitch + (unsigned)col) * 2u + COPY_SHIFT - 1024u * t;
                 chunk_k[t] = col < rows ? 0 : NEVER;   // K rows past the operand lie past its range
             }
         }
@@ -96,7 +98,7 @@ struct TileOperand {
             read_lds = lds + (unsigned)((64 * half + l16) * 128 + (swizzle_row(l16, 4 * k_half + grp) << 4));
             flip = 0;
         } else {
-            step = (unsigned)TILE_BK * (unsigned)rows * 2u;
+            step = (unsigned)TILE_BK * (unsigned)pitch * 2u;
             read_lds = lds + (unsigned)((32 * k_half + 8 * grp + (l16 >> 2)) * 256 + (l16 & 3) * 8);
             flip = (unsigned)(((4 * half) ^ ((l16 >> 2) | ((grp & 1) << 2))) << 5);
         }
@@ -144,9 +146,13 @@ __device__ inline int tile_item(const DenseArgs &p)
 template <int EPI, class TO>
 __device__ inline void tile_store(const DenseArgs &p, f32x4 (&x)[2][4], int tm, int tn, int wm, int wn, int i0, int lane)
 {
-    const Views v = make_views<EPI>(p);
     const int m0 = tm * TILE + 64 * wm + 16 * i0;
     const int col = tn * tile_columns(EPI) + tile_columns(EPI) / 2 * wn;
+    if constexpr (epi_loss(EPI)) {
+        loss_rows<EPI>(p, x, m0, col, lane, [](int) {});
+        return;
+    } else {
+    const Views v = make_views<EPI>(p);
     with_epilogue<EPI>(p, [&](auto act_c, auto extra_c) {
         constexpr int ACT = decltype(act_c)::value, EXTRA = decltype(extra_c)::value;
         u32x2 bias[4];
@@ -162,9 +168,10 @@ __device__ inline void tile_store(const DenseArgs &p, f32x4 (&x)[2][4], int tm, 
             store_row<EXTRA>(p, v, row, m0 + 16 * i + (lane & 15), col, lane);
         }
     });
-    if constexpr (EPI >= EPI_STORE_SYM)
+    if constexpr (epi_symmetric(EPI))
         if (tm != tn)
             store_mirrored(p, v, x[0], x[1], m0, col, lane);
+    }
 }
 
 template <class T, int LA, int LB, int EPI, class TO>
@@ -182,6 +189,7 @@ void dense_tile_kernel(DenseArgs p)
     const int wn = (wave >> 1) & 1;  // 64-column half
 
     fetch_args(p);
+    take_rows(p, TILE);
     const int item = tile_item(p);
     if (item < 0)
         return;
@@ -196,8 +204,8 @@ void dense_tile_kernel(DenseArgs p)
     const unsigned lds_base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
     TileOperand<T, LA, false> oa;
     TileOperand<T, LB, EPI == EPI_GATED> ob;
-    oa.init(p.a, p.M, tm * TILE, p.K, 0, lds_base, wave, lane, wm, kh);
-    ob.init(p.b, p.N, tn * tile_columns(EPI), p.K, p.N, lds_base + TILE_STAGES * TILE_UNIT, wave, lane, wn, kh);
+    oa.init(p.a, p.M, tm * TILE, p.K, p.lda, 0, lds_base, wave, lane, wm, kh);
+    ob.init(p.b, p.N, tn * tile_columns(EPI), p.K, LB == ROW_K ? p.K : p.N, p.N, lds_base + TILE_STAGES * TILE_UNIT, wave, lane, wn, kh);
 
     const int nk = (p.K + TILE_BK - 1) / TILE_BK;
     const int first = parts ? w.split * p.steps_per_split : 0;
@@ -300,6 +308,7 @@ constexpr int REDUCE_WAVES = 4;
 template <int EPI, class TO>
 __global__ __launch_bounds__(64 * REDUCE_WAVES) void dense_reduce_kernel(DenseArgs p)
 {
+    take_rows(p, TILE);
     const int lane = threadIdx.x & 63;
     const int unit = (int)blockIdx.x * REDUCE_WAVES + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int tail = p.tiles * p.batch - p.whole, q = unit >> 3;

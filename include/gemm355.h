@@ -577,7 +577,8 @@ int gemm355_newton_schulz_workspace_size(int batch, int rows, int cols, size_t *
 
 /*
  * gemm355_force_layer_kernel -- override the choice of kernel for the products
- * of the layer calls (gemm_bf16_nt_bias_act_res and those after it), a
+ * of the layer calls (gemm_bf16_nt_bias_act_res and those after it) and of the
+ * cross entropy over a vocabulary, a
  * process-wide diagnostic for tests and measurements: 0 (the default) by size,
  * 1 = 256 x 256 tiles (for symmetric products 192 x 192 ones where those take
  * less time), 2 = 256 x 256 with the K steps of the last round's tiles split
@@ -683,6 +684,55 @@ int gemm355_layer_norm_bwd(int rows, int cols, int x_type, const void *X, int w_
                            const float *mean, const float *rstd, const void *dY, const void *R, void *dX, void *dgamma,
                            void *dbeta, void *workspace, size_t workspace_bytes, void *stream);
 int gemm355_layer_norm_bwd_workspace_size(int rows, int cols, size_t *bytes);
+
+/*
+ * gemm_bf16_nt_cross_entropy -- softmax cross entropy over a vocabulary, straight
+ * from the last layer's output; the logits are not kept:
+ *
+ *   z[m][v] = sum_k A[m][k] * B[v][k]
+ *   lse[m] = log(sum_v exp(z[m][v])),   loss[m] = lse[m] - z[m][targets[m]]
+ *
+ *   A        M x K BF16 (tokens), B  V x K BF16 (the vocabulary's rows, which may
+ *            be an embedding's table); V is any, K a multiple of 8
+ *   targets  M ids of type target_type (a gemm355_id_type); a row whose target
+ *            lies outside 0 .. V - 1 is left out: loss and lse 0
+ *   loss     M FP32 values; their mean or weighted sum is the caller's, who hands
+ *            its gradient to the backward call
+ *   lse      M FP32 values for gemm_bf16_nt_cross_entropy_bwd
+ * Products exact, sums and exponentials FP32; infinities and NaN among the logits
+ * go where the formula takes them, within their row. A row that is left out costs
+ * nothing from 65 tokens up. M == 0 does nothing; with K == 0 every z is 0.
+ * A padded to 256 rows and 256 rows of B stay below 2^31 bytes each, else
+ * GEMM355_ERR_UNSUPPORTED; B as a whole may be larger. The workspace
+ * (gemm_bf16_nt_cross_entropy_workspace_size bytes) is as for the layer calls and
+ * always needed.
+ */
+int gemm_bf16_nt_cross_entropy(int M, int V, int K, const void *A, const void *B, int target_type, const void *targets,
+                               float *loss, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+int gemm_bf16_nt_cross_entropy_workspace_size(int M, int V, int K, size_t *bytes);
+
+/*
+ * gemm_bf16_nt_cross_entropy_bwd -- its gradients:
+ *
+ *   dz[m][v] = (exp(z[m][v] - lse[m]) - [v == targets[m]]) * dloss[m]
+ *   dA = dz B  (M x K),  dB = dz^T A  (V x K),  BF16
+ *
+ *   lse    as the forward call left it
+ *   dloss  M FP32 values, the gradient of each row's loss, or NULL for ones
+ *   dA, dB  outputs; each may be NULL if it is not wanted
+ * z is computed again, in pieces of the vocabulary; a piece's dz, rounded to BF16
+ * (as a layer's gradient is), is in the workspace. dloss enters as dloss[m] /
+ * max |dloss| before that rounding and as the maximum after the FP32 sums, so that
+ * equal weights add no rounding. Rows that are left out get zeros in dA and add
+ * nothing to dB, whatever A holds there. M == 0 writes zeros to dB, V == 0 to dA;
+ * K == 0 does nothing. Sizes and workspace
+ * (gemm_bf16_nt_cross_entropy_bwd_workspace_size bytes: about 256 MB of dz for a
+ * large batch, FP32 sums and a copy of A) as above.
+ */
+int gemm_bf16_nt_cross_entropy_bwd(int M, int V, int K, const void *A, const void *B, int target_type,
+                                   const void *targets, const float *lse, const float *dloss, void *dA, void *dB,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+int gemm_bf16_nt_cross_entropy_bwd_workspace_size(int M, int V, int K, size_t *bytes);
 
 /* Human-readable text for a status code (static storage; never NULL). */
 const char *gemm355_status_string(int status);

@@ -1,0 +1,380 @@
+"""Softmax cross entropy over a vocabulary and its gradients against 64-bit
+references on the GPU: every kernel forced, odd vocabularies and numbers of tokens,
+rows that are left out, one and several pieces of the vocabulary, infinities,
+missing outputs, repeatability.
+
+Bounds, with u = 2^-8 and v = 2^-24 the half-steps of BF16 and FP32:
+  z        K products in FP32, any order: e_z = (K + 1) v sum |a b|
+  lse      the largest e_z of the row; the exponentials' arguments, differences
+           d from a run's and then from the row's largest z, times log2(e): 3 v d
+           each, weighted by the softmax; the exponential itself and the chain of
+           additions (64 in a lane and its neighbours, 16 and a sixteenth of the
+           runs): 4 v and (100 + runs / 16) v; the logarithm and the last sums
+           3 v (|lse| + |largest|)
+  loss     that and e_z of the target's logit, v (|z| + |largest|)
+  dz       p (e_z + 2 v (|z| + |lse|) + 6 v) + 3 v |dz|, times the weight, and u
+           |dz| for its rounding
+  dA, dB   those errors through the product, its sums, and u of the result
+"""
+import pytest
+import torch
+
+import dense_gemm_14_amd as g
+from tests.dense_util import close
+from tests.gpu_util import need_gpu
+from tests.rows_util import V as v32, Array, randn
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+KERNELS = [g.LAYER_AUTO, g.LAYER_LARGE, g.LAYER_SPLIT, g.LAYER_TILE, g.LAYER_SMALL, g.LAYER_NARROW]
+
+
+def gen_of(seed):
+    gen = torch.Generator()
+    gen.manual_seed(seed)
+    return gen
+
+
+def inputs(M, V, K, seed=0, skip=0.2, spread=2.0, id_type=torch.int64):
+    gen = gen_of(M * 3 + V * 5 + K + seed)
+    A, B = randn(gen, M, K), randn(gen, V, K, std=spread * max(K, 1) ** -0.5)
+    t = torch.randint(0, max(V, 1), (M,), generator=gen)
+    t[torch.rand(M, generator=gen) < 0.5] = max(V - 1, 0)
+    out = torch.rand(M, generator=gen) < skip
+    t[out] = torch.where(torch.rand(M, generator=gen) < 0.5, -100, V)[out]
+    # tokens whose target is likely
+    A = torch.where((torch.arange(M) % 3 == 0)[:, None] & ~out[:, None] & (V > 0),
+                    A + 2 * B[t.clamp(0, max(V - 1, 0))] if V else A, A)
+    w = torch.randn(M, generator=gen)
+    return A, B, t.to(id_type), w
+
+
+def reference(A, B, t):
+    a, b = A.double(), B.double()
+    M, K = a.shape
+    z = a @ b.t()
+    ez = (K + 1) * v32 * (a.abs() @ b.abs().t())
+    kept = (t >= 0) & (t < len(b))
+    at = t.long().clamp(0, max(len(b) - 1, 0))[:, None]
+    return z, ez, kept, at
+
+
+def forward_reference(A, B, t):
+    z, ez, kept, at = reference(A, B, t)
+    top = z.amax(1)
+    lse = torch.logsumexp(z, 1)
+    p = torch.exp(z - lse[:, None])
+    d = (p * (top[:, None] - z)).sum(1)
+    runs = B.shape[0] / 16
+    e = ez.amax(1) + v32 * (6 * d + 104 + runs / 16 + 3 * (lse.abs() + top.abs()))
+    zt, ezt = z.gather(1, at)[:, 0], ez.gather(1, at)[:, 0]
+    loss = lse - zt
+    e_loss = e + ezt + v32 * (zt.abs() + top.abs())
+    nil = torch.zeros_like(lse)
+    return {k: (torch.where(kept, x, nil), torch.where(kept, y, nil))
+            for k, (x, y) in {"loss": (loss, e_loss), "lse": (lse, e)}.items()}
+
+
+def backward_reference(A, B, t, lse, w):
+    z, ez, kept, at = reference(A, B, t)
+    a, b, l = A.double(), B.double(), lse.double()[:, None]
+    w = torch.where(kept, w.double(), torch.zeros(()).double().to(w.device))[:, None]
+    a = torch.where(kept[:, None], a, torch.zeros_like(a))
+    p = torch.where(kept[:, None], torch.exp(z - l), torch.zeros_like(z))
+    e = p * (ez + 2 * v32 * (z.abs() + l.abs()) + 6 * v32)
+    dz = p.clone()
+    dz.scatter_add_(1, at, torch.full_like(at, -1, dtype=torch.float64))
+    dz = dz * w
+    e = (e * w.abs() + 3 * v32 * dz.abs())
+    e = torch.where(kept[:, None], e + U * (dz.abs() + e) + 1e-37, torch.zeros_like(e))
+
+    def prod(x, ex, y):
+        out = x @ y
+        err = ex @ y.abs() + (x.shape[1] + 2) * v32 * ((x.abs() + ex) @ y.abs())
+        return out, err + U * (out.abs() + err)
+    return {"dA": prod(dz, e, b), "dB": prod(dz.t().contiguous(), e.t().contiguous(), a)}
+
+
+def workspace(nbytes):
+    buf = torch.full((nbytes + 4096,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN in every type
+
+    def check():
+        assert (buf[nbytes:] == 0xFF).all(), "write past the workspace"
+    return buf, check
+
+
+def run(A, B, t):
+    M, K, V = *A.shape, len(B)
+    loss, lse = Array(M, dtype=torch.float32), Array(M, dtype=torch.float32)
+    nb = g.cross_entropy_workspace_size(M, V, K)
+    ws, check = workspace(nb)
+    g.gemm_bf16_nt_cross_entropy(M, V, K, A.cuda(), B.cuda(), t.cuda(), loss.t, lse.t, ws, nb)
+    torch.cuda.synchronize()
+    check()
+    return {"loss": loss.get(), "lse": lse.get()}
+
+
+def run_bwd(A, B, t, lse, w, want=("dA", "dB")):
+    M, K, V = *A.shape, len(B)
+    outs = {"dA": Array(M, K), "dB": Array(V, K)}
+    nb = g.cross_entropy_bwd_workspace_size(M, V, K)
+    ws, check = workspace(nb)
+    g.gemm_bf16_nt_cross_entropy_bwd(M, V, K, A.cuda(), B.cuda(), t.cuda(), lse.cuda(), None if w is None else w.cuda(),
+                                     *[outs[k].t if k in want else None for k in outs], ws, nb)
+    torch.cuda.synchronize()
+    check()
+    return {k: outs[k].get() for k in want}
+
+
+def check(got, want):
+    for k in got:
+        close(got[k], *[x.cpu() for x in want[k]], k)
+
+
+def lse_of(A, B, t):
+    return forward_reference(A, B, t)["lse"][0].float()
+
+
+SIZES = [(1, 1, 8), (1, 50, 64), (3, 257, 72), (17, 1000, 136), (64, 515, 264), (65, 100, 64), (130, 515, 264),
+         (300, 1031, 520), (257, 264, 1032), (700, 2057, 328)]
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("M,V,K", SIZES)
+def test_forward(M, V, K, kernel):
+    need_gpu()
+    print("ce", M, V, K, kernel, flush=True)
+    g.force_layer_kernel(kernel)
+    try:
+        for id_type, spread in ((torch.int64, 2.0), (torch.int32, 20.0)):
+            A, B, t, _ = inputs(M, V, K, spread=spread, id_type=id_type)
+            check(run(A, B, t), forward_reference(A, B, t))
+    finally:
+        g.force_layer_kernel(g.LAYER_AUTO)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("M,V,K", SIZES)
+def test_gradients(M, V, K, kernel):
+    need_gpu()
+    print("ce_bwd", M, V, K, kernel, flush=True)
+    g.force_layer_kernel(kernel)
+    try:
+        for id_type, weighted in ((torch.int64, True), (torch.int32, False)):
+            A, B, t, w = inputs(M, V, K, id_type=id_type)
+            lse = lse_of(A, B, t)
+            want = backward_reference(A, B, t, lse, w if weighted else torch.ones(M))
+            check(run_bwd(A, B, t, lse, w if weighted else None), want)
+    finally:
+        g.force_layer_kernel(g.LAYER_AUTO)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("M,V,K", [(1100, 700, 264), (600, 1300, 1544)])
+@pytest.mark.parametrize("kept", [0, 1, 63, 64, 65, 300])
+def test_rows_left_out(M, V, K, kept, kernel):
+    # A holds NaN and infinities where rows are left out, dloss NaN
+    need_gpu()
+    print("ce left out", M, V, K, kept, kernel, flush=True)
+    A, B, t, w = inputs(M, V, K, skip=0.0)
+    out = torch.randperm(M, generator=gen_of(kept))[kept:]
+    t[out] = torch.where(out % 2 == 0, -1, V + 7)
+    clean, bad, bw = A.clone(), A.clone(), w.clone()
+    clean[out] = 0
+    bad[out] = float("nan")
+    bad[out[::2]] = float("inf")
+    bw[out] = float("nan")
+    g.force_layer_kernel(kernel)
+    try:
+        want = forward_reference(clean, B, t)
+        got = run(bad, B, t)
+        check(got, want)
+        lse = want["lse"][0].float()
+        grads = run_bwd(bad, B, t, lse, bw)
+        check(grads, backward_reference(clean, B, t, lse, w))
+        assert not grads["dA"][out].any()
+    finally:
+        g.force_layer_kernel(g.LAYER_AUTO)
+
+
+def test_empty_sizes():
+    need_gpu()
+    A, B, t, w = inputs(9, 40, 72)
+    # an empty vocabulary: every row is left out
+    e = torch.zeros(0, 72, dtype=torch.bfloat16)
+    for M in (9, 100):
+        a, tt = A[:1].expand(M, 72).contiguous(), torch.zeros(M, dtype=torch.int64)
+        got = run(a, e, tt)
+        assert not got["loss"].any() and not got["lse"].any()
+        assert not run_bwd(a, e, tt, torch.zeros(M), None)["dA"].any()
+    # no tokens
+    none = torch.zeros(0, 72, dtype=torch.bfloat16)
+    got = run_bwd(none, B, torch.zeros(0, dtype=torch.int64), torch.zeros(0), None)
+    assert got["dB"].shape == (40, 72) and not got["dB"].any()
+    # K == 0: every logit is 0
+    for M in (9, 100):
+        t = torch.arange(M) % 40
+        got = run(torch.zeros(M, 0, dtype=torch.bfloat16), torch.zeros(40, 0, dtype=torch.bfloat16), t)
+        log40 = torch.log(torch.tensor(40.0, dtype=torch.float64)).expand(M)
+        close(got["loss"], log40, torch.full((M,), 16 * v32 * 4, dtype=torch.float64), "loss")
+
+
+@pytest.mark.parametrize("M,V,K", [(8192, 20001, 72), (20000, 17000, 64), (300, 600000, 64)])
+def test_several_pieces(M, V, K):
+    # (references on the GPU: products of plain matrices in 64 bits)
+    need_gpu()
+    A, B, t, w = (x.cuda() for x in inputs(M, V, K, skip=0.1))
+    torch.cuda.synchronize()
+    print("ce pieces", M, V, K, flush=True)
+    got = run(A, B, t)
+    lse, parts = torch.empty(M, device="cuda"), []
+    dB = eB = None
+    for i in range(0, M, 2048):
+        want = forward_reference(A[i:i + 2048], B, t[i:i + 2048])
+        for k in got:
+            close(got[k][i:i + 2048], *[x.cpu() for x in want[k]], k)
+        lse[i:i + 2048] = want["lse"][0].float()
+    grads = run_bwd(A, B, t, lse, w)
+    for i in range(0, M, 2048):
+        s = slice(i, i + 2048)
+        want = backward_reference(A[s], B, t[s], lse[s], w[s])
+        close(grads["dA"][s], *[x.cpu() for x in want["dA"]], "dA")
+        value, bound = want["dB"]
+        # (the sum of the parts' bounds covers theirs; M v of the sums across them)
+        dB, eB = (value, bound) if dB is None else (dB + value, eB + bound + U * value.abs())
+    close(grads["dB"], dB.cpu(), eB.cpu(), "dB")
+
+
+def test_equal_weights_add_no_rounding():
+    # dloss the same everywhere: the gradients are those of ones, times it
+    need_gpu()
+    A, B, t, _ = inputs(200, 300, 136, skip=0.0)
+    lse = lse_of(A, B, t)
+    ones = run_bwd(A, B, t, lse, None)
+    for c in (2.0 ** -11, -0.25, 3.0):
+        got = run_bwd(A, B, t, lse, torch.full((200,), c))
+        for k in got:
+            # one rounding of each to BF16
+            close(got[k], ones[k] * c, 2 * U * (ones[k] * c).abs(), k)
+    zero = run_bwd(A, B, t, lse, torch.zeros(200))
+    assert not zero["dA"].any() and not zero["dB"].any()
+
+
+@pytest.mark.parametrize("M", [5, 200])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_infinite_logits(M, kernel):
+    need_gpu()
+    V, K, inf = 300, 264, float("inf")
+    A, B, t, w = inputs(M, V, K, skip=0.0)
+    A[:, 0], B[:, 0] = 0, 0
+    B[7, 0] = 3e38
+    A[1, 0] = 3e38       # z[1][7] overflows to +inf
+    A[2, 0] = -3e38      # z[2][7] is -inf
+    A[3, 5] = float("nan")
+    t[1], t[2], t[4] = 5, 8, 7
+    g.force_layer_kernel(kernel)
+    try:
+        got = run(A, B, t)
+    finally:
+        g.force_layer_kernel(g.LAYER_AUTO)
+    assert got["lse"][1] == inf and got["loss"][1] == inf
+    assert got["lse"][3].isnan() and got["loss"][3].isnan()
+    keep = torch.ones(M, dtype=torch.bool)
+    keep[[1, 3]] = False
+    B2 = B.clone()
+    B2[7, 0] = 0
+    A2 = A.clone()
+    A2[:, 0] = 0
+    want = forward_reference(A2[keep], B2, t[keep])
+    # row 2 without the logit that is -inf
+    rest = torch.cat([B2[:7], B2[8:]])
+    two = forward_reference(A2[2:3], rest, t[2:3] - 1)
+    for k in got:
+        x, e = want[k]
+        x[1], e[1] = two[k][0][0], two[k][1][0]
+        close(got[k][keep], x, e, k)
+
+
+def test_one_output_of_two():
+    need_gpu()
+    for M, V, K in ((33, 300, 72), (600, 1000, 264), (8200, 20000, 64)):
+        A, B, t, w = inputs(M, V, K)
+        lse = torch.randn(M, generator=gen_of(1)) + 8
+        both = run_bwd(A, B, t, lse, w)
+        for k in both:
+            assert torch.equal(run_bwd(A, B, t, lse, w, (k,))[k], both[k]), (M, k)
+
+
+def test_the_same_every_time():
+    need_gpu()
+    for M, V, K in ((33, 1000, 520), (700, 2057, 1032)):
+        A, B, t, w = inputs(M, V, K)
+        first = run(A, B, t)
+        lse = first["lse"].float()
+        grads = run_bwd(A, B, t, lse, w)
+        for _ in range(4):
+            again = run(A, B, t)
+            assert all(torch.equal(first[k], again[k]) for k in first)
+            again = run_bwd(A, B, t, lse, w)
+            assert all(torch.equal(grads[k], again[k]) for k in grads)
+
+
+def test_gradients_against_differences():
+    # of the loss in 64 bits, along random directions of A and B
+    need_gpu()
+    M, V, K, h = 12, 45, 16, 1e-6
+    A, B, t, w = inputs(M, V, K)
+    got = run_bwd(A, B, t, lse_of(A, B, t), w)
+    kept = (t >= 0) & (t < V)
+    at = t.clamp(0, V - 1)[:, None]
+
+    def total(a, b):
+        z = a @ b.t()
+        return (torch.where(kept, torch.logsumexp(z, 1) - z.gather(1, at)[:, 0], 0.0) * w.double()).sum()
+    gen = gen_of(2)
+    for k in ("dA", "dB"):
+        for _ in range(4):
+            base = [A.double(), B.double()]
+            i = 0 if k == "dA" else 1
+            d = torch.randn(base[i].shape, generator=gen, dtype=torch.float64)
+            ends = []
+            for s in (h, -h):
+                moved = list(base)
+                moved[i] = base[i] + s * d
+                ends.append(total(*moved))
+            slope = (ends[0] - ends[1]) / (2 * h)
+            # dz is rounded to BF16 and the result again: 2 u of what is summed
+            want = backward_reference(A, B, t, lse_of(A, B, t), w)[k]
+            assert abs(slope - (got[k] * d).sum()) <= (want[1] * d.abs()).sum() + 1e-6
+
+
+def test_far_offsets():
+    # a vocabulary of more than 2^31 bytes, its rows all the same but a few
+    need_gpu()
+    V, K, M = 140000, 8192, 70
+    B = torch.zeros(V, K, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, 1, 65535, 131071, 131072, 131073, 139999], device="cuda")
+    B[rows, torch.arange(len(rows), device="cuda")] = 8
+    t = rows[torch.arange(M, device="cuda") % len(rows)]
+    t[3::9] = 77777
+    A = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    A[torch.arange(M, device="cuda"), torch.arange(M, device="cuda") % len(rows)] = 1
+    # one logit of 8, all others 0
+    lse = torch.log(torch.tensor(V - 1 + torch.e ** 8, dtype=torch.float64))
+    z = torch.where(t == 77777, 0.0, 8.0).double().cpu()
+    got = run(A, B, t)
+    bound = torch.full((M,), v32 * (200 + V / 256 + 100), dtype=torch.float64)
+    close(got["lse"], lse.expand(M), bound, "lse")
+    close(got["loss"], lse - z, bound, "loss")
+    grads = run_bwd(A, B, t, got["lse"].float(), None)
+    want = backward_reference(A[:, :8].cpu(), B[rows][:, :8].cpu(), torch.searchsorted(rows, t).cpu(), got["lse"].float(),
+                              torch.ones(M))
+    # (dA has terms of the rows with a value alone; B's other rows are zeros)
+    keep = (t != 77777).cpu()
+    close(grads["dA"][keep][:, :8], want["dA"][0][keep], 2 * want["dA"][1][keep] + 1e-12, "dA")
+    p0 = torch.exp(-lse)
+    plain = torch.zeros(8, dtype=torch.float64)
+    plain[:7] = torch.bincount(torch.arange(M) % 7, minlength=7).double() * p0
+    assert (grads["dB"][100, :8] - plain).abs().max() <= 3 * U * plain.max()
+    assert torch.equal(grads["dB"][100], grads["dB"][131074]) and torch.equal(grads["dB"][100], grads["dB"][139998])
+    assert grads["dB"][139999, 6] < -0.9 and not grads["dB"][:, 8:].any()
