@@ -548,6 +548,10 @@ def _layers():
                *[ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in (
                    "gemm_bf16_nt_bias_act_res", "gemm_bf16_nt_gated", "gemm_bf16_nt_bias_act_bwd",
                    "gemm_bf16_nt_gated_bwd")])
+        m.bind_ends(_torch.nn.Parameter, _torch.float32, _torch.int32, _torch.int64,
+                    *[ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in (
+                        "gemm355_embedding", "gemm355_embedding_bwd", "gemm355_layer_norm", "gemm355_layer_norm_bwd",
+                        "gemm_bf16_nt_cross_entropy", "gemm_bf16_nt_cross_entropy_bwd")])
         _bound = m
     return _bound
 
@@ -737,6 +741,12 @@ def embedding(tokens: int, vocab: int, cols: int, ids, E, Y, scale: float = 1.0,
     E (vocab x cols) and Y are BF16 or FP32 each, ids (tokens) int32 or int64;
     id_type (INT32, INT64), e_type and y_type (BF16, FP32) name the types of raw
     addresses."""
+    if id_type is None and e_type is None and y_type is None:
+        status = (_bound or _layers()).embedding(tokens, vocab, cols, ids, E, Y, scale, stream)
+        if status is not None:      # (None: something that the long way knows about)
+            if status:
+                raise Gemm355Error(status, "gemm355_embedding")
+            return
     tokens, vocab, cols = _int32(tokens), _int32(vocab), _int32(cols)
     dev = _device()
     i, it = _ids(ids, id_type, _count(tokens), "ids", dev)
@@ -755,6 +765,13 @@ def embedding_bwd(tokens: int, vocab: int, cols: int, ids, dY, R, dE, scale: flo
     type, may be None for zeros, or dE itself: only rows that occur are then read
     and written. The workspace holds embedding_bwd_workspace_size(tokens, vocab,
     cols) bytes."""
+    if id_type is None and y_type is None and e_type is None:
+        status = (_bound or _layers()).embedding_bwd(tokens, vocab, cols, ids, dY, R, dE, scale, workspace, workspace_bytes,
+                                                     stream)
+        if status is not None:      # (None: something that the long way knows about)
+            if status:
+                raise Gemm355Error(status, "gemm355_embedding_bwd")
+            return
     tokens, vocab, cols = _int32(tokens), _int32(vocab), _int32(cols)
     dev = _device()
     i, it = _ids(ids, id_type, _count(tokens), "ids", dev)
@@ -779,6 +796,12 @@ def layer_norm(rows: int, cols: int, X, gamma, beta, Y, mean, rstd, eps: float =
 
     X (rows x cols) is BF16 or FP32, gamma and beta (cols, or None) likewise;
     mean and rstd (rows, FP32) are outputs for layer_norm_bwd, or None."""
+    if x_type is None and w_type is None:
+        status = (_bound or _layers()).layer_norm(rows, cols, X, gamma, beta, Y, mean, rstd, eps, stream)
+        if status is not None:      # (None: something that the long way knows about)
+            if status:
+                raise Gemm355Error(status, "gemm355_layer_norm")
+            return
     rows, cols = _int32(rows), _int32(cols)
     dev = _device()
     xt, wt = _type_of(x_type, "X", X), _type_of(w_type, "gamma", gamma, beta)
@@ -798,6 +821,13 @@ def layer_norm_bwd(rows: int, cols: int, X, gamma, mean, rstd, dY, R, dX, dgamma
     dX itself), and dgamma and dbeta (of gamma's type). Each output may be None if
     it is not wanted. The workspace holds layer_norm_bwd_workspace_size(rows, cols)
     bytes (None where that is 0)."""
+    if x_type is None and w_type is None:
+        status = (_bound or _layers()).layer_norm_bwd(rows, cols, X, gamma, mean, rstd, dY, R, dX, dgamma, dbeta, workspace,
+                                                      workspace_bytes, stream)
+        if status is not None:      # (None: something that the long way knows about)
+            if status:
+                raise Gemm355Error(status, "gemm355_layer_norm_bwd")
+            return
     rows, cols = _int32(rows), _int32(cols)
     dev = _device()
     xt, wt = _type_of(x_type, "X", X, dX), _type_of(w_type, "gamma", gamma, dgamma, dbeta)
@@ -827,6 +857,12 @@ def gemm_bf16_nt_cross_entropy(M: int, V: int, K: int, A, B, targets, loss, lse,
     INT32 or INT64, names the type of a raw address), loss and lse (M) FP32
     outputs. A row whose target lies outside 0 .. V - 1 is left out: zeros. The
     workspace holds cross_entropy_workspace_size(M, V, K) bytes."""
+    if target_type is None:
+        status = (_bound or _layers()).entropy(M, V, K, A, B, targets, loss, lse, workspace, workspace_bytes, stream)
+        if status is not None:      # (None: something that the long way knows about)
+            if status:
+                raise Gemm355Error(status, "gemm_bf16_nt_cross_entropy")
+            return
     M, V, K = _int32(M), _int32(V), _int32(K)
     dev = _device()
     a, b = _values(A, BF16, _count(M, K), "A", dev), _values(B, BF16, _count(V, K), "B", dev)
@@ -849,6 +885,13 @@ def gemm_bf16_nt_cross_entropy_bwd(M: int, V: int, K: int, A, B, targets, lse, d
     None for ones), the gradient of each row's loss. Rows that are left out get
     zeros in dA and add nothing to dB. The workspace holds
     cross_entropy_bwd_workspace_size(M, V, K) bytes."""
+    if target_type is None:
+        status = (_bound or _layers()).entropy_bwd(M, V, K, A, B, targets, lse, dloss, dA, dB, workspace, workspace_bytes,
+                                                   stream)
+        if status is not None:      # (None: something that the long way knows about)
+            if status:
+                raise Gemm355Error(status, "gemm_bf16_nt_cross_entropy_bwd")
+            return
     M, V, K = _int32(M), _int32(V), _int32(K)
     dev = _device()
     a, b = _values(A, BF16, _count(M, K), "A", dev), _values(B, BF16, _count(V, K), "B", dev)
