@@ -6,7 +6,7 @@
 //   dA = dz B,  dB = dz^T A
 //
 // Forward: one product whose epilogue leaves, for each row and run of 64 or 128
-// columns, the largest z and the sum of the exponentials under it, and the
+// columns, the sum of the exponentials under a base near the largest z, and the
 // target's z (dense_loss.hpp); a second kernel joins the runs. 8 bytes for every
 // 128 logits go through memory.
 // Backward: for a piece of the vocabulary at a time z again, with dz as its
@@ -36,7 +36,7 @@ struct CePrepArgs {
     const float *lse, *dloss; // backward (dloss may be NULL: ones)
     int *rows;                // number of kept rows
     int *map, *target;        // of each kept row: where it was, its target
-    float *klse, *weight;     // backward: its lse, its weight relative to *scale
+    float *klse, *weight;     // backward: its lse times log2(e), its weight relative to *scale
     float *scale;             // backward
     void *ka;                 // the kept rows of A, zeros behind them
     float *loss0, *lse0;      // forward: zeros for rows that are left out
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(CE_THREADS) void ce_prep_kernel(CePrepArgs p)
             p.map[at] = (int)m;
             p.target[at] = target;
             if constexpr (BWD) {
-                p.klse[at] = p.lse[m];
+                p.klse[at] = p.lse[m] * LOG2E;
                 p.weight[at] = p.dloss ? p.dloss[m] / scale : 1.0f;
             }
         } else if (!BWD && m < r1) {
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(CE_THREADS) void ce_prep_kernel(CePrepArgs p)
 // Joins the runs of ROWS rows: as many lanes side by side, the others share out
 // the runs.
 struct CeJoinArgs {
-    const f32x2 *stats;      // [run][stride]: {largest, sum}
+    const f32x2 *stats;      // [run][stride]: {base, sum}
     const float *picked;
     const int *rows, *map;   // or NULL: M rows, in place, whose targets say which are left out
     const void *ids;
@@ -176,13 +176,13 @@ struct CeJoinArgs {
 };
 
 struct CeSum {
-    float top, sum, rest;    // the largest finite value, the sum under it, and what was not finite
+    float base, sum;         // a sum of powers of two under a base that is a whole number, -inf and 0 if there is none
+    float rest;              // what was not finite
 };
 __device__ inline CeSum ce_join(const CeSum &a, const CeSum &b)
 {
-    // (a side without a finite value has top -inf and sum 0)
-    const float base = loss_base(fmaxf(a.top, b.top));
-    return CeSum{fmaxf(a.top, b.top), a.sum * loss_exp(a.top, base) + b.sum * loss_exp(b.top, base), a.rest + b.rest};
+    const float base = fmaxf(a.base, b.base), ref = __builtin_isinf(base) ? 0.0f : base;
+    return CeSum{base, a.sum * __builtin_amdgcn_exp2f(a.base - ref) + b.sum * __builtin_amdgcn_exp2f(b.base - ref), a.rest + b.rest};
 }
 
 template <int ROWS>
@@ -208,11 +208,13 @@ __global__ __launch_bounds__(CE_THREADS) void ce_join_kernel(CeJoinArgs p)
             part[ty][tx] = s = ce_join(s, part[ty + d][tx]);
     }
     if (ty == 0 && m < M) {
-        const float base = loss_base(s.top), rest = logf(s.sum + s.rest);
+        // base log(2) in 64 bits: rounded to 32 it would be the largest error of all
+        const double base = __builtin_isinf(s.base) ? 0.0 : (double)s.base * 0.69314718055994530942;
+        const float rest = logf(s.sum + s.rest);
         const int row = p.map ? p.map[m] : m;
         const bool out = !p.map && rows::id_at(p.ids, p.wide, (size_t)m, p.V) < 0;
-        p.lse[row] = out ? 0.0f : base + rest;
-        p.loss[row] = out ? 0.0f : (base - p.picked[m]) + rest;
+        p.lse[row] = out ? 0.0f : (float)(base + rest);
+        p.loss[row] = out ? 0.0f : (float)(base - p.picked[m] + rest);
     }
 }
 

@@ -2,16 +2,19 @@
 // over a vocabulary (cross_entropy.hpp has the other kernels and the whole):
 //
 //   EPI_CE       z = A B^T of a tile. Nothing of it is stored but, for each row
-//                and run of columns, the largest z and the sum of exp(z - largest),
+//                and run of columns, the sum of 2^(z log2(e) - base) with its base,
 //                and the target's z where the run holds it.
 //   EPI_CE_GRAD  z again, C = round((exp(z - lse) - [column = target]) weight),
 //                zeros in the columns between N and the next multiple of 8
 //   EPI_ACC      sums over pieces of the contraction: FP32 sums, added to those
 //                of the pieces before, rounded to C by the last piece
 //
-// Work per element: an exponential, at a quarter of the vector rate, and about
-// five plain instructions, 4 % of a tile's time at K = 4096; a compare with the
-// target only in the runs that hold one.
+// Work per element: an exponential, at a quarter of the vector rate, and three or
+// four plain instructions (maximum, multiply-add, sum; or multiply-add, factor,
+// conversion), 4 % of a tile's time at K = 4096; a compare with the target only in
+// the runs that hold one. Measured, forward of 8192 x 128000 with K = 4096: 6.0 ms,
+// a library product of these sizes 5.9; 6.06 with an epilogue that stores one value
+// a row, so what is left of it hides behind the power limit.
 #pragma once
 
 #include "dense_common.hpp"
@@ -24,7 +27,9 @@ constexpr float LOG2E = 1.4426950408889634f;
 
 // Variants of a tile's epilogue. EPI_CE, EPI_CE_GRAD: LOSS_EDGE, the run has
 // columns past N. EPI_ACC: LOSS_ADD, there is a piece before; LOSS_LAST, there is
-// none after.
+// none after. Copies of the code, not branches in each row: with those the
+// compiler moved accumulators about in the main loop (8192 x 128000, K = 4096:
+// 6250 us instead of 6020).
 enum { LOSS_EDGE = 1, LOSS_ADD = 1, LOSS_LAST = 2 };
 
 template <int EPI, class F>
@@ -36,10 +41,7 @@ __device__ inline void with_loss(const DenseArgs &p, int col, int width, F &&f)
         else
             p.last ? f(Int<LOSS_LAST>{}) : f(Int<0>{});
     } else {
-        if (col + width > p.N)
-            f(Int<LOSS_EDGE>{});
-        else
-            f(Int<0>{});
+        col + width > p.N ? f(Int<LOSS_EDGE>{}) : f(Int<0>{});
     }
 }
 
@@ -65,7 +67,7 @@ __device__ inline LossRow loss_row_of(const DenseArgs &p, int m)
         } else {
             r.at = loss_target(p, m);
             if constexpr (EPI == EPI_CE_GRAD) {
-                r.lse = p.lse[m];
+                r.lse = p.lse[m];      // (times log2(e))
                 r.weight = p.weight[m];
             }
         }
@@ -103,14 +105,19 @@ __device__ inline float row_add(float x)
     return r.a + r.b;
 }
 
-// What the exponentials' arguments are taken from: the largest value, or 0 where
-// it is infinite (all -inf then give a sum of 0, and +inf one of +inf; NaN is in
-// the sum in any case).
-__device__ inline float loss_base(float top) { return __builtin_isinf(top) ? 0.0f : top; }
-// The difference is taken first: as one multiply-add with top * log2(e) rounded
-// beforehand every term would be off by the same 2^-24 top log2(e).
-__device__ inline float loss_exp(float z, float base) { return __builtin_amdgcn_exp2f((z - base) * LOG2E); }
-__device__ inline float loss_softmax(float z, float lse) { return __builtin_amdgcn_exp2f(z * LOG2E - lse * LOG2E); }
+// Exponentials are powers of two: exp(z) = 2^(z log2(e)). What their arguments are
+// taken from is a whole number near the largest argument (0 where that is
+// infinite: all -inf then give a sum of 0, and +inf one of +inf; NaN is in the sum
+// in any case), so that an argument is one multiply-add with one rounding of its
+// small result, and joining two sums multiplies by a power of two, exactly.
+__device__ inline float loss_base(float top) { return __builtin_isinf(top) ? 0.0f : __builtin_rintf(top * LOG2E); }
+__device__ inline float loss_exp(float z, float base) { return __builtin_amdgcn_exp2f(__builtin_fmaf(z, LOG2E, -base)); }
+// {base, sum} as it is stored: base -inf where no value was finite, the sum then 0,
+// +inf or NaN.
+__device__ inline f32x2 loss_stat(float top, float base, float sum)
+{
+    return f32x2{__builtin_isinf(top) ? -__builtin_inff() : base, sum};
+}
 
 // What a row of blocks reads besides its sums (EPI_ACC: the pieces' before).
 template <int EPI, int MODE, int BJ>
@@ -131,18 +138,37 @@ __device__ inline void loss_row(const DenseArgs &p, const __amdgpu_buffer_rsrc_t
                                 int lane, const LossRow &row, const f32x4 (&add)[BJ])
 {
     const int n0 = col + 4 * (lane >> 4);
+    // (a real branch, for what one run in a hundred needs: the statement in it
+    // keeps the compiler from computing both sides and choosing)
+    const bool hit = __ballot(row.at >= col && row.at < col + 16 * BJ) != 0;
+    const int d = row.at - n0;
     if constexpr (EPI == EPI_CE) {
+        if constexpr (MODE & LOSS_EDGE) {
+#pragma unroll
+            for (int j = 0; j < BJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[j][e] = n0 + 16 * j + e < p.N ? x[j][e] : -__builtin_inff();
+        }
         float top = -__builtin_inff();
 #pragma unroll
         for (int j = 0; j < BJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (MODE & LOSS_EDGE)
-                    x[j][e] = n0 + 16 * j + e < p.N ? x[j][e] : -__builtin_inff();
+            for (int e = 0; e < 4; ++e)
                 top = fmaxf(top, x[j][e]);
-            }
         top = row_max(top);
         const float base = loss_base(top);
+        if (hit) {
+            float picked = 0.0f;
+            asm volatile("");
+#pragma unroll
+            for (int j = 0; j < BJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    picked = d == 16 * j + e ? x[j][e] : picked;
+            if (d >= 0 && d < 16 * BJ && (d & 12) == 0)
+                p.picked[m] = picked;
+        }
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < BJ; ++j) {
@@ -154,25 +180,16 @@ __device__ inline void loss_row(const DenseArgs &p, const __amdgpu_buffer_rsrc_t
         }
         sum = row_add(sum);
         if (lane < 16 && m < p.M && col < p.N)
-            p.stats[(size_t)(col / (16 * BJ)) * (size_t)p.stats_rows + (size_t)m] = f32x2{top, sum};
-        const int d = row.at - n0;
-        if (__ballot(row.at >= col && row.at < col + 16 * BJ) != 0) {
-#pragma unroll
-            for (int j = 0; j < BJ; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (d == 16 * j + e)
-                        p.picked[m] = x[j][e];
-        }
+            p.stats[(size_t)(col / (16 * BJ)) * (size_t)p.stats_rows + (size_t)m] = loss_stat(top, base, sum);
     }
     if constexpr (EPI == EPI_CE_GRAD) {
 #pragma unroll
         for (int j = 0; j < BJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                x[j][e] = loss_softmax(x[j][e], row.lse);
-        const int d = row.at - n0;
-        if (__ballot(row.at >= col && row.at < col + 16 * BJ) != 0) {
+                x[j][e] = loss_exp(x[j][e], row.lse);
+        if (hit) {
+            asm volatile("");
 #pragma unroll
             for (int j = 0; j < BJ; ++j)
 #pragma unroll
@@ -182,11 +199,15 @@ __device__ inline void loss_row(const DenseArgs &p, const __amdgpu_buffer_rsrc_t
 #pragma unroll
         for (int j = 0; j < BJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4; ++e)
                 x[j][e] *= row.weight;
-                if constexpr (MODE & LOSS_EDGE)
+        if constexpr (MODE & LOSS_EDGE) {
+#pragma unroll
+            for (int j = 0; j < BJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
                     x[j][e] = n0 + 16 * j + e < p.N ? x[j][e] : 0.0f;
-            }
+        }
 #pragma unroll
         for (int j = 0; j < BJ; j += 2)
             store16(pack_pair<__bf16>(x[j], x[j + 1]), rc, pair_offset(p, m, col + 16 * j, p.ldc, 0, lane));
@@ -277,7 +298,7 @@ __device__ inline void loss_eight(const DenseArgs &p, float (&x)[8], int m, int 
         if (!in)
             return;
         if (((int)threadIdx.x & (RUNS - 1)) == 0)
-            p.stats[(size_t)part * (size_t)p.stats_rows + (size_t)m] = f32x2{top, sum};
+            p.stats[(size_t)part * (size_t)p.stats_rows + (size_t)m] = loss_stat(top, base, sum);
         const int d = loss_target(p, m) - n;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -291,7 +312,7 @@ __device__ inline void loss_eight(const DenseArgs &p, float (&x)[8], int m, int 
             const int d = loss_target(p, m) - n;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                x[e] = n + e < p.N ? (loss_softmax(x[e], lse) - (d == e ? 1.0f : 0.0f)) * weight : 0.0f;
+                x[e] = n + e < p.N ? (loss_exp(x[e], lse) - (d == e ? 1.0f : 0.0f)) * weight : 0.0f;
             *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + (size_t)m * (size_t)p.ldc + (size_t)n) =
                 u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
         }

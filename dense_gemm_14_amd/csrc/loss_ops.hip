@@ -23,7 +23,7 @@ int64_t columns_within(int64_t row_bytes)
     return ((int64_t(1) << 31) - 1) / std::max<int64_t>(row_bytes, 1) / kPieceUnit * kPieceUnit;
 }
 
-// V cut into pieces of at most `most` columns, all but the last of one size.
+// V cut into pieces of at most `most` columns, all but the last of that size.
 struct Pieces {
     int count, width, last;
 };
@@ -32,12 +32,8 @@ Pieces cut(int V, int64_t most)
     Pieces p = {};
     if (V == 0)
         return p;
-    p.count = (int)ceil_div(V, most);
-    p.width = V;
-    if (p.count > 1) {
-        p.width = (int)(ceil_div(ceil_div(V, p.count), kPieceUnit) * kPieceUnit);
-        p.count = (int)ceil_div(V, p.width);
-    }
+    p.width = (int)std::min<int64_t>(V, most);
+    p.count = (int)ceil_div(V, p.width);
     p.last = V - (p.count - 1) * p.width;
     return p;
 }
@@ -126,7 +122,14 @@ BackwardPlan plan_backward(int M, int V, int K, int cus)
     // (rows of dz: up to a few K steps more than there are tokens)
     const int64_t fit = columns_within((int64_t(rows) + 64 * 4 * kMaxSplits) * 2);
     const int64_t want = std::max<int64_t>(8192, kPieceBytes / 2 / rows / kPieceUnit * kPieceUnit);
-    w.pieces = cut(V, std::min({want, fit, columns_within(int64_t(K) * 2)}));
+    // Pieces of sixteen tiles' columns: with a multiple of sixteen tiles of rows
+    // (4096 tokens or values of K) a piece's products fill whole rounds of 256 units,
+    // and only the last one leaves some idle (4096 x 128000, K = 4096: 31.25 rounds in
+    // all, 32 for four equal pieces).
+    int64_t most = std::min({want, fit, columns_within(int64_t(K) * 2)});
+    if (most >= 16 * kPieceUnit)
+        most = most / (16 * kPieceUnit) * (16 * kPieceUnit);
+    w.pieces = cut(V, most);
     w.pitch = (int)(ceil_div(w.pieces.width, 8) * 8);
     size_t partials = 0;
     int64_t depth = 0;
