@@ -71,16 +71,21 @@ __global__ __launch_bounds__(CE_THREADS) void ce_prep_kernel(CePrepArgs p)
     // every workgroup looks at all targets, and so waits for no other
     int before = 0, kept = 0;
     float largest = 0.0f;
-#pragma unroll 4
-    for (int64_t m = tid; m < p.M; m += CE_THREADS) {
-        const bool in = rows::id_at(p.ids, p.wide, (size_t)m, p.V) >= 0;
-        before += in && m < r0;
-        kept += in;
-        if constexpr (BWD)
-            if (p.dloss && in) {
-                const float w = fabsf(p.dloss[m]);
-                largest = fmaxf(largest, w < __builtin_inff() ? w : 0.0f);
-            }
+    constexpr int AHEAD = 4;
+    for (int64_t m0 = tid; m0 < p.M; m0 += AHEAD * CE_THREADS) {
+        int id[AHEAD];
+        float w[AHEAD] = {};
+        rows::ids_at<AHEAD>(p.ids, p.wide, m0, CE_THREADS, p.M, p.V, id);
+        if (BWD && p.dloss)
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                w[k] = p.dloss[min(m0 + k * CE_THREADS, (int64_t)p.M - 1)];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            before += id[k] >= 0 && m0 + k * CE_THREADS < r0;
+            kept += id[k] >= 0;
+            largest = id[k] >= 0 && fabsf(w[k]) < __builtin_inff() ? fmaxf(largest, fabsf(w[k])) : largest;
+        }
     }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {

@@ -54,15 +54,12 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_kernel(EmbedArgs p)
             continue;
         const int64_t t0 = block * groups * PER + group;
         Raw8<TE> row[PER];
-        bool in[PER];
+        int id[PER];
+        ids_at<PER>(p.ids, p.wide, t0, groups, p.tokens, p.vocab, id);
+        if (p.vocab > 0)
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int64_t t = t0 + (int64_t)i * groups;
-            const int id = t < p.tokens ? id_at(p.ids, p.wide, (size_t)t, p.vocab) : -1;
-            in[i] = id >= 0;
-            if (in[i])
-                row[i].load(p.e, (size_t)id * (size_t)p.cols + (size_t)c);
-        }
+            for (int i = 0; i < PER; ++i)
+                row[i].load(p.e, (size_t)max(id[i], 0) * (size_t)p.cols + (size_t)c);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int64_t t = t0 + (int64_t)i * groups;
@@ -71,7 +68,7 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_kernel(EmbedArgs p)
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                x[e] = in[i] ? p.scale * row[i].get(e) : 0.0f;
+                x[e] = id[i] >= 0 ? p.scale * row[i].get(e) : 0.0f;
             Raw8<TY> out;
             out.set(x);
             out.store(p.y, (size_t)t * (size_t)p.cols + (size_t)c);
@@ -99,32 +96,41 @@ struct EmbedBwdArgs {
     bool wide;
 };
 
+constexpr int FILL_ROWS = 16;
 constexpr int ORDER_THREADS = 1024, ORDER_WAVES = ORDER_THREADS / 64;
-constexpr int ORDER_MAX_RANGE = 512;
+constexpr int ORDER_MAX_RANGE = 512, ORDER_AHEAD = 8;
 
 __global__ __launch_bounds__(ORDER_THREADS) void embed_order_kernel(EmbedBwdArgs p)
 {
-    // [id of the range][wave]: first its tokens, then where the next one goes
-    __shared__ int count[ORDER_MAX_RANGE * ORDER_WAVES];
+    // [wave][id of the range]: first its tokens, then where the next one goes
+    __shared__ int count[ORDER_WAVES][ORDER_MAX_RANGE];
     __shared__ int before[ORDER_WAVES], total[ORDER_WAVES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int v0 = (int)blockIdx.x * p.range, range = min(p.range, p.vocab - v0);
-    for (int i = threadIdx.x; i < range * ORDER_WAVES; i += ORDER_THREADS)
-        count[i] = 0;
+    for (int i = threadIdx.x; i < ORDER_MAX_RANGE * ORDER_WAVES; i += ORDER_THREADS)
+        (&count[0][0])[i] = 0;
     __syncthreads();
 
     // this wave's run of tokens, whole groups of 64
     const int64_t run = ((int64_t)p.tokens + ORDER_THREADS - 1) / ORDER_THREADS * 64;
     const int64_t first = wave * run, last = min((int64_t)p.tokens, first + run);
+    // (loads of eight groups at a time: one after the other they took the time)
+    auto each_group = [&](auto &&f) {
+        for (int64_t t0 = first; t0 < last; t0 += 64 * ORDER_AHEAD) {
+            int id[ORDER_AHEAD];
+            ids_at<ORDER_AHEAD>(p.ids, p.wide, t0 + lane, 64, last, p.vocab, id);
+#pragma unroll
+            for (int k = 0; k < ORDER_AHEAD; ++k)
+                f((int)(t0 + 64 * k) + lane, id[k]);
+        }
+    };
     int less = 0;
-#pragma unroll 4
-    for (int64_t t = first + lane; t < last; t += 64) {
-        const int id = id_at(p.ids, p.wide, (size_t)t, p.vocab);
+    each_group([&](int, int id) {
         less += id >= 0 && id < v0;
         if (id >= v0 && id < v0 + range)
-            atomicAdd(&count[(id - v0) * ORDER_WAVES + wave], 1);
-    }
+            atomicAdd(&count[wave][id - v0], 1);
+    });
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
         less += __shfl_xor(less, d);
@@ -143,7 +149,7 @@ __global__ __launch_bounds__(ORDER_THREADS) void embed_order_kernel(EmbedBwdArgs
         if (i < range)
 #pragma unroll
             for (int w = 0; w < ORDER_WAVES; ++w)
-                mine += count[i * ORDER_WAVES + w];
+                mine += count[w][i];
         int upto = mine;     // of the lanes up to this one
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -163,8 +169,8 @@ __global__ __launch_bounds__(ORDER_THREADS) void embed_order_kernel(EmbedBwdArgs
             p.start[v0 + i] = at;
 #pragma unroll
             for (int w = 0; w < ORDER_WAVES; ++w) {
-                const int n = count[i * ORDER_WAVES + w];
-                count[i * ORDER_WAVES + w] = at;
+                const int n = count[w][i];
+                count[w][i] = at;
                 at += n;
             }
         }
@@ -174,56 +180,50 @@ __global__ __launch_bounds__(ORDER_THREADS) void embed_order_kernel(EmbedBwdArgs
         p.start[p.vocab] = base;
 
     // place: tokens of one id in their own order
-    for (int64_t t0 = first; t0 < last; t0 += 64) {
-        const int64_t t = t0 + lane;
-        const int id = t < last ? id_at(p.ids, p.wide, (size_t)t, p.vocab) : -1;
+    each_group([&](int t, int id) {
         const int i = id >= v0 && id < v0 + range ? id - v0 : -1;
         for (unsigned long long left = __ballot(i >= 0); left != 0;) {
             const int lead = __builtin_ctzll(left);
             const int which = __builtin_amdgcn_readlane(i, lead);
             const unsigned long long same = __ballot(i == which);
-            const int at = count[which * ORDER_WAVES + wave];
+            const int at = count[wave][which];
             if (i == which)
-                p.sorted[at + __popcll(same & ((1ull << lane) - 1))] = make_int2(id, (int)t);
+                p.sorted[at + __popcll(same & ((1ull << lane) - 1))] = make_int2(id, t);
             if (lane == lead)
-                count[which * ORDER_WAVES + wave] = at + __popcll(same);
+                count[wave][which] = at + __popcll(same);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the next turn reads what this lane wrote
             left &= ~same;
         }
-    }
+    });
 }
 
-// Adds the rows of the sorted tokens a .. b - 1 of one id.
-template <class TY>
-__device__ inline void embed_add(const EmbedBwdArgs &p, int a, int b, int c, float (&x)[8])
+// x += the rows of dY of the tokens token(0) .. token(n - 1), asked for in that
+// order; after(i) once row i is in. (Rows past the last are the last again: a load
+// under a condition would wait for the one before.)
+template <class TY, class Token, class After>
+__device__ inline void embed_add(const EmbedBwdArgs &p, int n, int c, float (&x)[8], Token &&token, After &&after)
 {
-    constexpr int AHEAD = 4;
-    if (c >= p.cols)
-        return;
-    int i = a;
-    for (; i + AHEAD <= b; i += AHEAD) {
+    constexpr int AHEAD = 8;
+    const int cc = min(c, p.cols - 8);
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
         Raw8<TY> row[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k)
-            row[k].load(p.dy, (size_t)p.sorted[i + k].y * (size_t)p.cols + (size_t)c);
+            row[k].load(p.dy, (size_t)token(min(i0 + k, n - 1)) * (size_t)p.cols + (size_t)cc);
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k)
+            if (i0 + k < n) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] += row[k].get(e);
-    }
-    for (; i < b; ++i) {
-        Raw8<TY> row;
-        row.load(p.dy, (size_t)p.sorted[i].y * (size_t)p.cols + (size_t)c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] += row.get(e);
+                for (int e = 0; e < 8; ++e)
+                    x[e] += row[k].get(e);
+                after(i0 + k);
+            }
     }
 }
 
 // dE[v] from the sum of its rows of dY.
 template <class TE>
-__device__ inline void embed_finish(const EmbedBwdArgs &p, int v, int c, float (&x)[8])
+__device__ inline void embed_finish(const EmbedBwdArgs &p, int v, int c, const float (&x)[8])
 {
     if (c >= p.cols)
         return;
@@ -232,11 +232,44 @@ __device__ inline void embed_finish(const EmbedBwdArgs &p, int v, int c, float (
     r.fill(0.0f);
     if (p.r)
         r.load(p.r, at);
+    float y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        x[e] = p.scale * x[e] + r.get(e);
-    r.set(x);
+        y[e] = p.scale * x[e] + r.get(e);
+    r.set(y);
     r.store(p.de, at);
+}
+
+// This lane's eight columns at c of the rows v0 + i, i in `rows`, that no token
+// has: R or zeros, several rows at a time.
+template <class TE>
+__device__ inline void embed_fill(const EmbedBwdArgs &p, int v0, unsigned long long rows, int c)
+{
+    constexpr int AHEAD = 8;
+    if (p.r == p.de)
+        return;
+    const int cc = min(c, p.cols - 8);
+    while (rows != 0) {
+        Raw8<TE> r[AHEAD];
+        size_t at[AHEAD];
+        const int n = min(AHEAD, __popcll(rows));
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            // (past the last row: that one again)
+            at[k] = k < n ? (size_t)(v0 + __builtin_ctzll(rows)) * (size_t)p.cols : at[k > 0 ? k - 1 : 0];
+            rows = k < n ? rows & (rows - 1) : rows;
+            r[k].fill(0.0f);
+        }
+        if (p.r)
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                r[k].load(p.r, at[k] + (size_t)cc);
+        if (c < p.cols)
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (k < n)
+                    r[k].store(p.de, at[k] + (size_t)c);
+    }
 }
 
 __device__ inline void embed_partial(const EmbedBwdArgs &p, int block, int which, int c, const float (&x)[8])
@@ -248,7 +281,8 @@ __device__ inline void embed_partial(const EmbedBwdArgs &p, int block, int which
     out.store(p.partial, ((size_t)block * 2 + (size_t)which) * (size_t)p.cols + (size_t)c);
 }
 
-// An id with more tokens than a block's is cut.
+// An id with more tokens than a block's (at most 32) is cut.
+constexpr int SUMS_BLOCK = 32;
 template <class TE, class TY>
 __global__ __launch_bounds__(EMBED_THREADS) void embed_sums_kernel(EmbedBwdArgs p)
 {
@@ -256,16 +290,14 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_sums_kernel(EmbedBwdArgs 
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int at = (int)blockIdx.x * (EMBED_THREADS / 64) + wave, waves = (int)gridDim.x * (EMBED_THREADS / 64);
     if (at >= p.sum_waves) {
-        // rows without a token
-        if (p.r == p.de)
-            return;
-        const int64_t items = (int64_t)p.vocab * p.pieces;
+        // rows without a token, looked for among sixteen at a time
+        const int64_t items = (((int64_t)p.vocab + FILL_ROWS - 1) / FILL_ROWS) * p.pieces;
         for (int64_t item = at - p.sum_waves; item < items; item += waves - p.sum_waves) {
-            const int v = (int)(item / p.pieces), c = 512 * (int)(item - (int64_t)v * p.pieces) + 8 * lane;
-            if (p.start[v] != p.start[v + 1])
-                continue;
-            float x[8] = {};
-            embed_finish<TE>(p, v, c, x);
+            const int group = (int)(item / p.pieces), c = 512 * (int)(item - (int64_t)group * p.pieces) + 8 * lane;
+            const int v0 = group * FILL_ROWS, v = min(v0 + lane, p.vocab);
+            const int next = p.start[min(v + 1, p.vocab)];
+            const bool none = lane < FILL_ROWS && v < p.vocab && p.start[v] == next;
+            embed_fill<TE>(p, v0, __ballot(none), c);
         }
         return;
     }
@@ -273,39 +305,54 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_sums_kernel(EmbedBwdArgs 
     const int64_t items = (int64_t)p.blocks * p.pieces;
     for (int64_t item = at; item < items; item += p.sum_waves) {
         const int b = (int)(item / p.pieces), c = 512 * (int)(item - (int64_t)b * p.pieces) + 8 * lane;
-        const int64_t begin = (int64_t)b * p.block;
-        if (begin >= kept)
+        if ((int64_t)b * p.block >= kept)
             break;
-        const int end = (int)min((int64_t)kept, begin + p.block);
-        int i = (int)begin;
-        const int v0 = p.sorted[i].x;
-        if (p.start[v0] < i) {      // begun in an earlier block
-            const int stop = p.start[v0 + 1];
-            if (stop - p.start[v0] > p.block) {
+        const int begin = b * p.block, n = min(kept - begin, p.block);
+        // lane l: sorted token begin + l, two blocks' worth: an id that is not cut
+        // ends within them
+        int2 mine = make_int2(-1, 0);
+        if (lane < kept - begin)
+            mine = p.sorted[begin + lane];
+        auto id_of = [&](int i) { return __builtin_amdgcn_readlane(mine.x, i); };
+        auto token_of = [&](int i) { return __builtin_amdgcn_readlane(mine.y, i); };
+        const int v0 = id_of(0), v1 = id_of(n - 1);
+        const int start0 = p.start[v0], stop0 = p.start[v0 + 1], start1 = p.start[v1], stop1 = p.start[v1 + 1];
+        int i = 0, end = stop1 - begin;          // of the ids that are added up here
+        if (start0 < begin) {                    // begun in an earlier block
+            const int stop = min(stop0 - begin, n);
+            if (stop0 - start0 > p.block) {
                 float x[8] = {};
-                embed_add<TY>(p, i, min(stop, end), c, x);
+                embed_add<TY>(p, stop, c, x, token_of, [](int) {});
                 embed_partial(p, b, 0, c, x);
             }
-            i = stop;
+            i = stop0 - begin;
         }
-        while (i < end) {
-            const int v = p.sorted[i].x, stop = p.start[v + 1];
+        if (i >= n)
+            continue;
+        if (stop1 - start1 > p.block) {          // goes on into the next blocks
+            end = start1 - begin;
             float x[8] = {};
-            if (stop - i > p.block) {
-                embed_add<TY>(p, i, end, c, x);
-                embed_partial(p, b, 1, c, x);
-            } else {
-                embed_add<TY>(p, i, stop, c, x);
-                embed_finish<TE>(p, v, c, x);
-            }
-            i = stop;
+            embed_add<TY>(p, n - end, c, x, [&](int k) { return token_of(end + k); }, [](int) {});
+            embed_partial(p, b, 1, c, x);
         }
+        float x[8] = {};
+        embed_add<TY>(p, end - i, c, x, [&](int k) { return token_of(i + k); },
+                      [&](int k) {
+                          const int v = id_of(i + k);
+                          if (i + k + 1 == end || id_of(i + k + 1) != v) {
+                              embed_finish<TE>(p, v, c, x);
+#pragma unroll
+                              for (int e = 0; e < 8; ++e)
+                                  x[e] = 0.0f;
+                          }
+                      });
     }
 }
 
-// Joins the partial rows of the id that was cut and begins in a block: 512
-// columns by a workgroup, whose waves each add a run of the blocks.
-constexpr int JOIN_THREADS = 512;
+// Joins the partial rows of the ids that were cut: a workgroup takes 512 columns
+// of the ids that begin in JOIN_BLOCKS blocks, one after the other, its waves each
+// a run of an id's blocks.
+constexpr int JOIN_THREADS = 512, JOIN_BLOCKS = 8;
 template <class TE>
 __global__ __launch_bounds__(JOIN_THREADS) void embed_join_kernel(EmbedBwdArgs p)
 {
@@ -314,39 +361,155 @@ __global__ __launch_bounds__(JOIN_THREADS) void embed_join_kernel(EmbedBwdArgs p
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int kept = p.start[p.vocab];
-    const int64_t items = (int64_t)p.blocks * p.pieces;
+    const int64_t items = (((int64_t)p.blocks + JOIN_BLOCKS - 1) / JOIN_BLOCKS) * p.pieces;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int b = (int)(item / p.pieces), c = 512 * (int)(item - (int64_t)b * p.pieces) + 8 * lane;
-        const int64_t next = ((int64_t)b + 1) * p.block;
-        if (next >= kept)
-            break;
-        const int v = p.sorted[next - 1].x, begin = p.start[v], stop = p.start[v + 1];
-        if (stop - begin <= p.block || begin < next - p.block)
-            continue;        // not cut, or begun before
-        // block b's part, then those of blocks b + 1 .. last
-        const int last = (stop - 1) / p.block, parts = last - b + 1, per = (parts + WAVES - 1) / WAVES;
-        float x[8] = {};
-        if (c < p.cols)
+        const int group = (int)(item / p.pieces), c = 512 * (int)(item - (int64_t)group * p.pieces) + 8 * lane;
+        const int b0 = group * JOIN_BLOCKS;
+        // lane l < JOIN_BLOCKS: whether an id is cut that begins in block b0 + l
+        const int64_t next = ((int64_t)b0 + lane + 1) * p.block;
+        int v = 0, begin = 0, stop = 0;
+        if (lane < JOIN_BLOCKS && next < kept) {
+            v = p.sorted[next - 1].x;
+            begin = p.start[v];
+            stop = p.start[v + 1];
+        }
+        const bool cut = stop - begin > p.block && begin >= next - p.block;
+        for (unsigned long long left = __ballot(cut); left != 0; left &= left - 1) {
+            const int l = __builtin_ctzll(left), b = b0 + l;
+            // block b's part, then those of blocks b + 1 .. last
+            const int last = (__builtin_amdgcn_readlane(stop, l) - 1) / p.block, parts = last - b + 1;
+            const int per = (parts + WAVES - 1) / WAVES;
+            float x[8] = {};
+            if (c < p.cols)
 #pragma unroll 4
-            for (int k = wave * per; k < min(parts, (wave + 1) * per); ++k) {
-                Raw8<float> row;
-                row.load(p.partial, ((size_t)(b + k) * 2 + (k == 0 ? 1 : 0)) * (size_t)p.cols + (size_t)c);
+                for (int k = wave * per; k < min(parts, (wave + 1) * per); ++k) {
+                    Raw8<float> row;
+                    row.load(p.partial, ((size_t)(b + k) * 2 + (k == 0 ? 1 : 0)) * (size_t)p.cols + (size_t)c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    x[e] += row.get(e);
+                    for (int e = 0; e < 8; ++e)
+                        x[e] += row.get(e);
+                }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                part[wave][e][lane] = x[e];
+            __syncthreads();
+            if (wave == 0) {
+#pragma unroll
+                for (int w = 1; w < WAVES; ++w)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] += part[w][e][lane];
+                embed_finish<TE>(p, __builtin_amdgcn_readlane(v, l), c, x);
             }
-        __syncthreads();
+        }
+    }
+}
+
+// ---- few tokens ----------------------------------------------------------------
+//
+// Up to 1024 tokens take one launch: a workgroup owns a range of ids and 512
+// columns, lists the tokens of its ids, and writes its rows, with and without
+// tokens. An id with more than a few tokens is added up by its four waves.
+constexpr int FEW_TOKENS = 1024, FEW_RANGE = 512, FEW_CUT = 16;
+
+template <class TE, class TY>
+__global__ __launch_bounds__(EMBED_THREADS) void embed_few_kernel(EmbedBwdArgs p)
+{
+    constexpr int WAVES = EMBED_THREADS / 64, GROUPS = FEW_TOKENS / EMBED_THREADS;
+    __shared__ int token[FEW_TOKENS], which[FEW_TOKENS], count[FEW_RANGE], before[GROUPS][WAVES];
+    __shared__ float part[WAVES][8][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int owner = (int)blockIdx.x / p.pieces, c = 512 * ((int)blockIdx.x - owner * p.pieces) + 8 * lane;
+    const int v0 = owner * p.range, range = min(p.range, p.vocab - v0);
+
+    // the tokens of the range's ids, in order
+    int id[GROUPS];
+    unsigned long long in[GROUPS];
+    ids_at<GROUPS>(p.ids, p.wide, tid, EMBED_THREADS, p.tokens, p.vocab, id);
+    for (int i = tid; i < range; i += EMBED_THREADS)
+        count[i] = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            part[wave][e][lane] = x[e];
-        __syncthreads();
-        if (wave == 0) {
+    for (int k = 0; k < GROUPS; ++k) {
+        id[k] -= v0;
+        in[k] = __ballot(id[k] >= 0 && id[k] < range);
+        if (lane == 0)
+            before[k][wave] = __popcll(in[k]);
+    }
+    __syncthreads();
+    int at = 0;
 #pragma unroll
-            for (int w = 1; w < WAVES; ++w)
+    for (int k = 0; k < GROUPS; ++k)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    x[e] += part[w][e][lane];
-            embed_finish<TE>(p, v, c, x);
+        for (int w = 0; w < WAVES; ++w) {
+            if (w == wave && (in[k] >> lane & 1)) {
+                const int place = at + __popcll(in[k] & ((1ull << lane) - 1));
+                token[place] = k * EMBED_THREADS + tid;
+                which[place] = id[k];
+                atomicAdd(&count[id[k]], 1);
+            }
+            at += before[k][w];
+        }
+    const int listed = at;
+    __syncthreads();
+
+    // x += the tokens of id v0 + i that are among its from-th to its to-th
+    auto add = [&](int i, int from, int to, float (&x)[8]) {
+        int seen = 0;
+        for (int l0 = 0; l0 < listed && seen < to; l0 += 64) {
+            const int l = l0 + lane;
+            unsigned long long of_id = __ballot(l < listed && which[min(l, FEW_TOKENS - 1)] == i);
+            const int n = __popcll(of_id);
+            const int skip = min(n, max(0, from - seen));
+            for (int k = 0; k < skip; ++k)
+                of_id &= of_id - 1;
+            const int take = min(n, to - seen) - skip, mine = token[min(l, FEW_TOKENS - 1)];
+            unsigned long long rest = of_id;
+            // (the matches one after the other, as their rows are asked for)
+            int asked = 0, t = 0;
+            embed_add<TY>(p, max(take, 0), c, x, [&](int k) {
+                if (asked <= k) {
+                    t = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rest));
+                    rest &= rest - 1;
+                    ++asked;
+                }
+                return t;
+            }, [](int) {});
+            seen += n;
+        }
+    };
+    for (int i0 = 64 * wave; i0 < range; i0 += 64 * WAVES) {
+        const int n = i0 + lane < range ? count[i0 + lane] : -1;
+        embed_fill<TE>(p, v0 + i0, __ballot(n == 0), c);
+        for (unsigned long long left = __ballot(n > 0 && n <= FEW_CUT); left != 0; left &= left - 1) {
+            const int l = __builtin_ctzll(left);
+            float x[8] = {};
+            add(i0 + l, 0, __builtin_amdgcn_readlane(n, l), x);
+            embed_finish<TE>(p, v0 + i0 + l, c, x);
+        }
+    }
+    if (listed <= FEW_CUT)
+        return;
+    for (int i0 = 0; i0 < range; i0 += 64) {
+        const int n = i0 + lane < range ? count[i0 + lane] : -1;
+        for (unsigned long long left = __ballot(n > FEW_CUT); left != 0; left &= left - 1) {
+            const int l = __builtin_ctzll(left), all = __builtin_amdgcn_readlane(n, l), per = (all + WAVES - 1) / WAVES;
+            float x[8] = {};
+            add(i0 + l, wave * per, min(all, (wave + 1) * per), x);
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                part[wave][e][lane] = x[e];
+            __syncthreads();
+            if (wave == 0) {
+#pragma unroll
+                for (int w = 1; w < WAVES; ++w)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] += part[w][e][lane];
+                embed_finish<TE>(p, v0 + i0 + l, c, x);
+            }
         }
     }
 }

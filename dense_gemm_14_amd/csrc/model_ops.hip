@@ -61,8 +61,11 @@ int launch_embed(r::EmbedArgs &p, int e_type, int y_type, int64_t blocks, hipStr
 
 // ---- embedding's gradient ----------------------------------------------------
 
+constexpr int kMaxVocab = 1 << 30;     // (a launch has fewer than 2^32 threads)
+
 struct EmbedBwdPlan {
-    int range, groups;          // ids per workgroup of the order, workgroups
+    bool few;                   // tokens, in one launch
+    int range, groups;          // ids per workgroup (few: of all; else: of the order), workgroups
     int block, blocks, pieces;
     size_t sorted_at, partial_at, bytes;
 };
@@ -70,18 +73,25 @@ struct EmbedBwdPlan {
 EmbedBwdPlan plan_embed_bwd(int tokens, int vocab, int cols, int cus)
 {
     EmbedBwdPlan e = {};
+    e.pieces = (int)ceil_div(cols, 512);
+    e.few = tokens <= r::FEW_TOKENS;
+    if (e.few) {
+        // four workgroups for every unit, or as many as there are ids
+        e.range = (int)std::min<int64_t>(r::FEW_RANGE, ceil_div(int64_t(vocab) * e.pieces, 4 * int64_t(cus)));
+        e.groups = (int)ceil_div(vocab, e.range);
+        return e;
+    }
     e.range = (int)std::min<int64_t>(r::ORDER_MAX_RANGE, ceil_div(vocab, cus));
     e.groups = (int)ceil_div(vocab, e.range);
-    e.pieces = (int)ceil_div(cols, 512);
     // blocks of up to 32 tokens, fewer where that leaves fewer waves than run
     // at a time
-    e.block = 32;
+    e.block = r::SUMS_BLOCK;
     while (e.block > 4 && ceil_div(tokens, e.block) * e.pieces < 16 * int64_t(cus))
         e.block /= 2;
     e.blocks = (int)ceil_div(tokens, e.block);
     e.sorted_at = align_up((size_t(vocab) + 1) * sizeof(int));
     e.partial_at = e.sorted_at + align_up(size_t(tokens) * 8);
-    e.bytes = e.partial_at + (tokens > e.block ? size_t(e.blocks) * 2 * cols * sizeof(float) : 0);
+    e.bytes = e.partial_at + size_t(e.blocks) * 2 * cols * sizeof(float);
     return e;
 }
 
@@ -187,7 +197,7 @@ extern "C" int gemm355_embedding_bwd_workspace_size(int tokens, int vocab, int c
 {
     if (tokens < 0 || vocab < 0 || cols < 0 || !bytes)
         return GEMM355_ERR_INVALID_ARG;
-    if (!elements_ok(tokens, cols) || !elements_ok(vocab, cols))
+    if (!elements_ok(tokens, cols) || !elements_ok(vocab, cols) || vocab > kMaxVocab)
         return GEMM355_ERR_UNSUPPORTED;
     *bytes = 0;
     if (vocab == 0 || cols == 0)
@@ -208,9 +218,9 @@ extern "C" int gemm355_embedding_bwd(int tokens, int vocab, int cols, int id_typ
         return GEMM355_ERR_INVALID_ARG;
     if (vocab == 0 || cols == 0)
         return GEMM355_OK;
-    if (!dE || !workspace || (tokens > 0 && (!ids || !dY)))
+    if (!dE || (workspace_bytes > 0 && !workspace) || (tokens > 0 && (!ids || !dY)))
         return GEMM355_ERR_INVALID_ARG;
-    if (cols % 8 != 0 || !elements_ok(tokens, cols) || !elements_ok(vocab, cols))
+    if (cols % 8 != 0 || !elements_ok(tokens, cols) || !elements_ok(vocab, cols) || vocab > kMaxVocab)
         return GEMM355_ERR_UNSUPPORTED;
     const size_t e_bytes = size_t(vocab) * cols * size_of(e_type);
     const Array out[] = {{dE, e_bytes}, {workspace, workspace_bytes}};
@@ -248,26 +258,29 @@ extern "C" int gemm355_embedding_bwd(int tokens, int vocab, int cols, int id_typ
     p.pieces = e.pieces;
     p.scale = scale;
     p.wide = id_type == GEMM355_INT64;
+    if (e.few)
+        return with_type(e_type, [&](auto te) {
+            return with_type(y_type, [&](auto ty) {
+                return launch_kernel(r::embed_few_kernel<decltype(te), decltype(ty)>, (unsigned)(int64_t(e.groups) * e.pieces),
+                                     (unsigned)r::EMBED_THREADS, p, s);
+            });
+        });
     int st = launch_kernel(r::embed_order_kernel, (unsigned)e.groups, (unsigned)r::ORDER_THREADS, p, s);
     if (st != GEMM355_OK)
         return st;
     constexpr int per = r::EMBED_THREADS / 64;
     const int64_t sum_groups = std::min<int64_t>(ceil_div(int64_t(e.blocks) * e.pieces, per), 16 * int64_t(cus));
-    const int64_t fill_groups = R == dE ? 0 : std::min<int64_t>(ceil_div(int64_t(vocab) * e.pieces, per), 8 * int64_t(cus));
+    const int64_t fill_groups = R == dE ? 0 : std::min<int64_t>(ceil_div(ceil_div(vocab, r::FILL_ROWS) * e.pieces, per), 8 * int64_t(cus));
     p.sum_waves = (int)(sum_groups * per);
     return with_type(e_type, [&](auto te) {
         return with_type(y_type, [&](auto ty) {
             typedef decltype(te) TE;
-            if (sum_groups + fill_groups > 0) {
-                const int st = launch_kernel(r::embed_sums_kernel<TE, decltype(ty)>, (unsigned)(sum_groups + fill_groups),
-                                             (unsigned)r::EMBED_THREADS, p, s);
-                if (st != GEMM355_OK)
-                    return st;
-            }
-            if (tokens <= e.block)      // no id can have more
-                return (int)GEMM355_OK;
+            const int st = launch_kernel(r::embed_sums_kernel<TE, decltype(ty)>, (unsigned)(sum_groups + fill_groups),
+                                         (unsigned)r::EMBED_THREADS, p, s);
+            if (st != GEMM355_OK)
+                return st;
             return launch_kernel(r::embed_join_kernel<TE>,
-                                 (unsigned)std::min<int64_t>(int64_t(e.blocks) * e.pieces, 16 * int64_t(cus)),
+                                 (unsigned)std::min<int64_t>(ceil_div(e.blocks, r::JOIN_BLOCKS) * e.pieces, 16 * int64_t(cus)),
                                  (unsigned)r::JOIN_THREADS, p, s);
         });
     });

@@ -58,6 +58,26 @@ __device__ inline int id_at(const void *ids, bool wide, size_t i, int count)
     return v >= 0 && v < count ? (int)v : -1;
 }
 
+// Ids first, first + step, ... below last, N at once; -1 from there on. (The choice of
+// type stands outside the loads, which would else wait for each other.)
+template <int N>
+__device__ inline void ids_at(const void *ids, bool wide, int64_t first, int64_t step, int64_t last, int count, int (&id)[N])
+{
+    long long v[N];
+    if (wide) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] = first + k * step < last ? static_cast<const long long *>(ids)[first + k * step] : -1;
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] = first + k * step < last ? static_cast<const int *>(ids)[first + k * step] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        id[k] = v[k] >= 0 && v[k] < count ? (int)v[k] : -1;
+}
+
 // One step of a sum over lanes: x of the lane that CTRL names, 0 where there is
 // none or ROWS (a mask of the wave's four rows of 16 lanes) leaves it out.
 template <int CTRL, int ROWS>

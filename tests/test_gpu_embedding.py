@@ -71,8 +71,8 @@ def test_lookup_keeps_infinities_and_an_empty_table():
     assert (Y.get() == 0).all()
 
 
-SIZES = [(1, 1, 8), (3, 1000, 520), (33, 7, 24), (64, 129, 4096), (777, 5001, 1000), (5000, 300, 136), (2050, 3, 1032),
-         (9000, 70001, 72)]
+SIZES = [(1, 1, 8), (3, 1000, 520), (33, 7, 24), (64, 129, 4096), (777, 5001, 1000), (1024, 640, 520), (1025, 640, 520),
+         (5000, 300, 136), (2050, 3, 1032), (9000, 70001, 72), (33000, 130001, 24)]
 
 
 def run_bwd(tokens, vocab, cols, ids, dY, R, scale, e_type, in_place=False):

@@ -51,7 +51,7 @@ def test_embedding_refusals():
 
 def test_embedding_gradient_refusals():
     for bad in (dict(tokens=-1), dict(vocab=-1), dict(cols=-8), dict(it=2), dict(et=2), dict(yt=2), dict(scale=NAN),
-                dict(ids=None), dict(dy=None), dict(de=None), dict(ws=None), dict(ws=None, nb=0), dict(de=DY + 64),
+                dict(ids=None), dict(dy=None), dict(de=None), dict(ws=None), dict(de=DY + 64),
                 dict(r=E + 64), dict(de=IDS), dict(ws=E), dict(ws=DY), dict(ws=R), dict(ws=IDS), dict(r=E, ws=E)):
         assert embed_bwd(**bad) == g.ERR_INVALID_ARG, bad
     for bad in (dict(cols=12), dict(dy=DY + 8), dict(de=E + 8), dict(r=R + 8), dict(ws=WS + 8), dict(ids=IDS + 4),
@@ -60,7 +60,7 @@ def test_embedding_gradient_refusals():
     assert embed_bwd(vocab=0, ids=None, dy=None, r=None, de=None, ws=None, nb=0) == g.OK
     assert embed_bwd(cols=0, ids=None, dy=None, r=None, de=None, ws=None, nb=0) == g.OK
     if no_gpu():
-        for ok in ({}, dict(r=E), dict(r=None), dict(tokens=0, ids=None, dy=None)):
+        for ok in ({}, dict(r=E), dict(r=None), dict(tokens=0, ids=None, dy=None), dict(ws=None, nb=0)):
             assert embed_bwd(**ok) == g.ERR_NO_DEVICE, ok
 
 
