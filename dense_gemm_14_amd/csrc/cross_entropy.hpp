@@ -193,25 +193,41 @@ __device__ inline CeSum ce_join(const CeSum &a, const CeSum &b)
 template <int ROWS>
 __global__ __launch_bounds__(CE_THREADS) void ce_join_kernel(CeJoinArgs p)
 {
-    constexpr int LANES = CE_THREADS / ROWS;
-    __shared__ CeSum part[LANES][ROWS];
+    constexpr int LANES = CE_THREADS / ROWS, AHEAD = 8;
+    __shared__ CeSum part[CE_WAVES][ROWS];
     const int tx = threadIdx.x % ROWS, ty = threadIdx.x / ROWS;
     const int M = p.rows ? __builtin_amdgcn_readfirstlane(*p.rows) : p.M;
     const int m = (int)blockIdx.x * ROWS + tx;
     CeSum s = {-__builtin_inff(), 0.0f, 0.0f};
     if (m < M)
-#pragma unroll 8
-        for (int i = ty; i < p.runs; i += LANES) {
-            const f32x2 t = p.stats[(size_t)i * (size_t)p.stride + (size_t)m];
-            s = ce_join(s, __builtin_isinf(t[0]) ? CeSum{-__builtin_inff(), 0.0f, t[1]} : CeSum{t[0], t[1], 0.0f});
-        }
-    part[ty][tx] = s;
+        for (int i0 = ty; i0 < p.runs; i0 += AHEAD * LANES) {
+            f32x2 t[AHEAD];
+            float base = -__builtin_inff();
 #pragma unroll
-    for (int d = LANES / 2; d > 0; d /= 2) {
-        __syncthreads();
-        if (ty < d)
-            part[ty][tx] = s = ce_join(s, part[ty + d][tx]);
-    }
+            for (int k = 0; k < AHEAD; ++k) {
+                t[k] = p.stats[(size_t)min(i0 + k * LANES, p.runs - 1) * (size_t)p.stride + (size_t)m];
+                base = fmaxf(base, t[k][0]);
+            }
+            CeSum x = {base, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (i0 + k * LANES < p.runs) {
+                    const bool finite = !__builtin_isinf(t[k][0]);
+                    x.sum += finite ? t[k][1] * __builtin_amdgcn_exp2f(t[k][0] - base) : 0.0f;
+                    x.rest += finite ? 0.0f : t[k][1];
+                }
+            s = ce_join(s, x);
+        }
+    // the lanes of a row within a wave, then the waves
+#pragma unroll
+    for (int d = ROWS; d < 64; d *= 2)
+        s = ce_join(s, CeSum{__shfl_xor(s.base, d), __shfl_xor(s.sum, d), __shfl_xor(s.rest, d)});
+    if ((threadIdx.x & 63) < ROWS)
+        part[threadIdx.x >> 6][tx] = s;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < CE_WAVES; ++w)
+        s = w == 0 ? part[0][tx] : ce_join(s, part[w][tx]);
     if (ty == 0 && m < M) {
         // base log(2) in 64 bits: rounded to 32 it would be the largest error of all
         const double base = __builtin_isinf(s.base) ? 0.0 : (double)s.base * 0.69314718055994530942;

@@ -35,25 +35,30 @@ struct EmbedArgs {
     void *y;
     int64_t items;       // groups of `per` tokens times pieces of a row
     int tokens, vocab, cols;
-    int lanes_log2;      // lanes side by side in a row: 1 << lanes_log2, of 8 columns each
+    int lanes_log2;      // lanes side by side in a row: 1 << lanes_log2, of embed_width columns each
     int pieces;          // of that many columns in a row
     float scale;
     bool wide;           // 64-bit ids
 };
 
+// Columns of a lane: eight BF16 values, or four where FP32 ones are written, so that
+// a wave's store is whole lines either way.
+constexpr int embed_width(bool fp32) { return fp32 ? 4 : 8; }
+
 // PER tokens by one group of lanes.
 template <class TE, class TY, int PER>
 __global__ __launch_bounds__(EMBED_THREADS) void embed_kernel(EmbedArgs p)
 {
+    constexpr int W = embed_width(sizeof(TY) == 4);
     const int groups = EMBED_THREADS >> p.lanes_log2;
     const int group = (int)threadIdx.x >> p.lanes_log2, lane = (int)threadIdx.x & ((1 << p.lanes_log2) - 1);
     for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
         const int64_t block = item / p.pieces;
-        const int c = 8 * (lane + ((int)(item - block * p.pieces) << p.lanes_log2));
+        const int c = W * (lane + ((int)(item - block * p.pieces) << p.lanes_log2));
         if (c >= p.cols)
             continue;
         const int64_t t0 = block * groups * PER + group;
-        Raw8<TE> row[PER];
+        typename RawOf<TE, W>::type row[PER];
         int id[PER];
         ids_at<PER>(p.ids, p.wide, t0, groups, p.tokens, p.vocab, id);
         if (p.vocab > 0)
@@ -65,11 +70,11 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_kernel(EmbedArgs p)
             const int64_t t = t0 + (int64_t)i * groups;
             if (t >= p.tokens)
                 break;
-            float x[8];
+            float x[W];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < W; ++e)
                 x[e] = id[i] >= 0 ? p.scale * row[i].get(e) : 0.0f;
-            Raw8<TY> out;
+            typename RawOf<TY, W>::type out;
             out.set(x);
             out.store(p.y, (size_t)t * (size_t)p.cols + (size_t)c);
         }

@@ -126,24 +126,39 @@ int with_rows(int cols, bool many, F &&f)
     return f(Int<0>{}, Int<0>{});
 }
 
-// Whether the gradients of few or very wide rows take one launch.
-bool norm_direct(int rows, int cols) { return rows <= 256 || cols > 16384; }
+// Whether the gradients of few or very wide rows take one launch: its workgroups
+// for dgamma and dbeta each pass over all rows of their columns, 5 ns a row, the
+// other form pays for a second launch and for workgroups' sums. Measured, one launch
+// and two (us): 301 x 1000 5.0 and 8.1, 301 x 4096 5.1 and 11.9, 600 x 1000 6.7 and
+// 9.1, 1200 x 512 9.2 and 7.7, 1200 x 2048 FP32 13.9 and 17.8, 2000 x 2048 FP32 21.5
+// and 19.6, 4000 x 8192 FP32 146 and 96, 2000 x 16384 77 and 76.
+bool norm_direct(int rows, int cols, bool fp32) { return rows <= 800 || cols > (fp32 ? 8192 : 16384); }
 
-// Waves that hold a row where there are many, and the workgroups that walk them.
-int norm_bwd_waves(int cols) { return cols <= 2048 ? 1 : cols <= 8192 ? 4 : 8; }
-int norm_bwd_blocks(int rows, int cols, int cus)
+// Waves that hold a row where there are many, and the workgroups that walk them. A
+// lane holds eight columns of FP32 rows, sixteen of BF16 ones.
+int norm_bwd_waves(int cols, bool fp32)
 {
-    return (int)std::min<int64_t>(cus, ceil_div(rows, r::NORM_BWD_THREADS / 64 / norm_bwd_waves(cols)));
+    const int64_t waves = fp32 ? ceil_div(cols, 512) : cols <= 512 ? 1 : ceil_div(cols, 1024);
+    return 1 << ceil_log2(waves);
 }
-template <class F>
+int norm_bwd_blocks(int rows, int cols, bool fp32, int cus)
+{
+    return (int)std::min<int64_t>(cus, ceil_div(rows, r::NORM_BWD_THREADS / 64 / norm_bwd_waves(cols, fp32)));
+}
+template <class X, class F>
 int with_bwd_rows(int cols, F &&f)
 {
-    return cols <= 512     ? f(Int<1>{}, Int<1>{})
-           : cols <= 1024  ? f(Int<1>{}, Int<2>{})
-           : cols <= 2048  ? f(Int<1>{}, Int<4>{})
-           : cols <= 4096  ? f(Int<4>{}, Int<2>{})
-           : cols <= 8192  ? f(Int<4>{}, Int<4>{})
-                           : f(Int<8>{}, Int<4>{});
+    constexpr bool FP32 = sizeof(X) == 4;
+    typedef Int<FP32 ? 1 : 2> Vpt;
+    if (!FP32 && cols <= 512)
+        return f(Int<1>{}, Int<1>{});
+    switch (norm_bwd_waves(cols, FP32)) {
+    case 1: return f(Int<1>{}, Vpt{});
+    case 2: return f(Int<2>{}, Vpt{});
+    case 4: return f(Int<4>{}, Vpt{});
+    case 8: return f(Int<8>{}, Vpt{});
+    default: return f(Int<16>{}, Vpt{});
+    }
 }
 
 } // namespace
@@ -179,8 +194,9 @@ extern "C" int gemm355_embedding(int tokens, int vocab, int cols, int id_type, c
     p.cols = cols;
     p.scale = scale;
     p.wide = id_type == GEMM355_INT64;
-    p.lanes_log2 = std::min(6, ceil_log2(cols / 8));
-    p.pieces = (int)ceil_div(cols / 8, int64_t(1) << p.lanes_log2);
+    const int units = cols / r::embed_width(y_type == GEMM355_FP32);
+    p.lanes_log2 = std::min(6, ceil_log2(units));
+    p.pieces = (int)ceil_div(units, int64_t(1) << p.lanes_log2);
     const int64_t groups = r::EMBED_THREADS >> p.lanes_log2;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     // four tokens per lane where that leaves eight workgroups for every unit
@@ -335,12 +351,13 @@ extern "C" int gemm355_layer_norm_bwd_workspace_size(int rows, int cols, size_t 
     if (!elements_ok(rows, cols))
         return GEMM355_ERR_UNSUPPORTED;
     *bytes = 0;
-    if (rows == 0 || cols == 0 || norm_direct(rows, cols))
+    if (rows == 0 || cols == 0 || norm_direct(rows, cols, false))
         return GEMM355_OK;
     int cus = 0;
     const int rc = compute_units(&cus);
-    if (rc == GEMM355_OK)
-        *bytes = size_t(norm_bwd_blocks(rows, cols, cus)) * 2 * cols * sizeof(float);
+    if (rc == GEMM355_OK)   // (of the type that takes more)
+        *bytes = size_t(std::max(norm_bwd_blocks(rows, cols, false, cus), norm_bwd_blocks(rows, cols, true, cus))) * 2 * cols *
+                 sizeof(float);
     return rc;
 }
 
@@ -375,7 +392,8 @@ extern "C" int gemm355_layer_norm_bwd(int rows, int cols, int x_type, const void
     r::NormBwdArgs p = {X, gamma, mean, rstd, dY, R, wants_x ? dX : nullptr, dgamma, dbeta, static_cast<float *>(workspace),
                         rows, cols, 0, wants_columns};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (norm_direct(rows, cols)) {      // (no rows: the column blocks write zeros)
+    const bool fp32 = x_type == GEMM355_FP32;
+    if (norm_direct(rows, cols, fp32)) {      // (no rows: the column blocks write zeros)
         const unsigned columns = wants_columns ? (unsigned)ceil_div(cols, 64) : 0u;
         return with_type(x_type, [&](auto tx) {
             return with_type(w_type, [&](auto tw) {
@@ -389,13 +407,13 @@ extern "C" int gemm355_layer_norm_bwd(int rows, int cols, int x_type, const void
             });
         });
     }
-    p.blocks = norm_bwd_blocks(rows, cols, cus);
+    p.blocks = norm_bwd_blocks(rows, cols, fp32, cus);
     if (workspace_bytes < size_t(p.blocks) * 2 * cols * sizeof(float))
         return GEMM355_ERR_UNSUPPORTED;
     return with_type(x_type, [&](auto tx) {
         return with_type(w_type, [&](auto tw) {
             typedef decltype(tw) TW;
-            const int st = with_bwd_rows(cols, [&](auto waves_c, auto vpt_c) {
+            const int st = with_bwd_rows<decltype(tx)>(cols, [&](auto waves_c, auto vpt_c) {
                 return launch_kernel(r::norm_bwd_kernel<decltype(tx), TW, decltype(waves_c)::value, decltype(vpt_c)::value>,
                                      (unsigned)p.blocks, (unsigned)r::NORM_BWD_THREADS, p, s);
             });

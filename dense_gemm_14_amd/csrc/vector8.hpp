@@ -16,9 +16,12 @@ template <> struct Raw8<__bf16> {
     {
         w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + at);
     }
+    // Past the L2 (a wave's 1 KiB is whole lines, and nothing here reads it again):
+    // norms of 8192 x 4096 in 29.3 us instead of 31.3, a table's gradient of 128000 x
+    // 4096 in 230 instead of 248.
     __device__ inline void store(void *p, size_t at) const
     {
-        *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + at) = w;
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + at));
     }
     __device__ inline float get(int e) const { return e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]); }
     __device__ inline void set(const float (&x)[8])
@@ -36,6 +39,8 @@ template <> struct Raw8<float> {
         lo = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(p) + at);
         hi = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(p) + at + 4);
     }
+    // (through the L2, which joins the two halves of a line: 16384 x 4096 rows looked up
+    // in 85 us, past it in 105)
     __device__ inline void store(void *p, size_t at) const
     {
         *reinterpret_cast<f32x4 *>(static_cast<float *>(p) + at) = lo;
@@ -50,6 +55,37 @@ template <> struct Raw8<float> {
     __device__ inline void fill(float v) { lo = hi = f32x4{v, v, v, v}; }
     __device__ inline void hold() { asm volatile("" : "+v"(lo), "+v"(hi)); }
 };
+
+// Four values, 8 bytes of BF16 or 16 of FP32, each read or written once.
+template <class T> struct Raw4;
+template <> struct Raw4<__bf16> {
+    u32x2 w;
+    __device__ inline void load(const void *p, size_t at)
+    {
+        w = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(p) + at));
+    }
+    __device__ inline void store(void *p, size_t at) const
+    {
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p) + at));
+    }
+    __device__ inline float get(int e) const { return e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]); }
+    __device__ inline void set(const float (&x)[4]) { w = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])}; }
+};
+template <> struct Raw4<float> {
+    f32x4 v;
+    __device__ inline void load(const void *p, size_t at)
+    {
+        v = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(static_cast<const float *>(p) + at));
+    }
+    __device__ inline void store(void *p, size_t at) const
+    {
+        __builtin_nontemporal_store(v, reinterpret_cast<f32x4 *>(static_cast<float *>(p) + at));
+    }
+    __device__ inline float get(int e) const { return v[e]; }
+    __device__ inline void set(const float (&x)[4]) { v = f32x4{x[0], x[1], x[2], x[3]}; }
+};
+template <class T, int N> struct RawOf { typedef Raw8<T> type; };
+template <class T> struct RawOf<T, 4> { typedef Raw4<T> type; };
 
 // Id `i` of an array of 32- or 64-bit ids; -1 for one outside 0 .. count - 1.
 __device__ inline int id_at(const void *ids, bool wide, size_t i, int count)
