@@ -420,10 +420,10 @@ template <int VPT>
 constexpr int norm_direct_threads() { return VPT ? 256 : NORM_WIDE_THREADS; }
 
 template <class X, class W, int THREADS>
-__device__ inline void norm_columns(const NormBwdArgs &p, int block, float (*part)[2][65])
+__device__ inline void norm_columns(const NormBwdArgs &p, int64_t block, float (*part)[2][65])
 {
     const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
-    const int64_t c = (int64_t)block * 64 + 8 * tx;
+    const int64_t c = block * 64 + 8 * tx;
     float dg[8] = {}, db[8] = {};
     if (c < p.cols)
 #pragma unroll 4
@@ -447,7 +447,7 @@ __device__ inline void norm_columns(const NormBwdArgs &p, int block, float (*par
     __syncthreads();
     const int i = threadIdx.x & 63, which = (threadIdx.x >> 6) & 1;
     void *out = which ? p.dbeta : p.dgamma;
-    const int64_t col = (int64_t)block * 64 + i;
+    const int64_t col = block * 64 + i;
     if (threadIdx.x < 128 && col < p.cols && out) {
         float t = 0.0f;
         for (int r = 0; r < THREADS / 8; ++r)
@@ -465,7 +465,10 @@ __global__ __launch_bounds__(norm_direct_threads<VPT>()) void norm_bwd_direct_ke
     constexpr int THREADS = norm_direct_threads<VPT>();
     __shared__ float part[THREADS / 8][2][65];
     if ((int)blockIdx.x >= p.blocks) {
-        norm_columns<X, W, THREADS>(p, (int)blockIdx.x - p.blocks, part);
+        for (int64_t block = (int64_t)blockIdx.x - p.blocks; block * 64 < p.cols; block += (int64_t)gridDim.x - p.blocks) {
+            norm_columns<X, W, THREADS>(p, block, part);
+            __syncthreads();
+        }
         return;
     }
     if constexpr (VPT > 0) {

@@ -61,7 +61,10 @@ struct ForwardPlan {
 ForwardPlan plan_forward(int M, int V, int K, int cus)
 {
     ForwardPlan f = {};
-    f.pieces = cut(V, columns_within(int64_t(K) * 2));
+    // (blocks of 16 x 16, of which no tile has fewer, below 2^27, so that counts of
+    // tiles stay within 32 bits)
+    const int64_t counted = (int64_t(1) << 27) / ceil_div(M, 16) * 16 / kPieceUnit * kPieceUnit;
+    f.pieces = cut(V, std::min(columns_within(int64_t(K) * 2), counted));
     int64_t runs = 0;
     size_t partials = 0;
     for (int i = 0; i < 2 && f.pieces.count > i; ++i) {
@@ -91,11 +94,13 @@ ForwardPlan plan_forward(int M, int V, int K, int cus)
     return f;
 }
 
+constexpr int64_t kMaxTokens = 1 << 26;
+
 // Tokens, and a piece of at least one unit of the vocabulary, within 32-bit
 // offsets.
 bool extents_ok(int64_t M, int64_t K)
 {
-    return extent_ok(std::max<int64_t>(M, 1), K * 2) && columns_within(K * 2) >= kPieceUnit;
+    return M <= kMaxTokens && extent_ok(std::max<int64_t>(M, 1), K * 2) && columns_within(K * 2) >= kPieceUnit;
 }
 
 constexpr size_t kMaxLogits = size_t(1) << 46;   // (M V, so that no size runs over)
@@ -113,14 +118,25 @@ struct BackwardPlan {
     size_t rows_at, scale_at, map_at, target_at, lse_at, weight_at, a_at, dz_at, acc_at, partials_at, bytes;
 };
 
+// Columns that a piece's dz may have. (Its rows: where the product over them may take
+// whole K steps, for each split at least four, more than there are tokens.)
+int64_t piece_columns(int64_t M)
+{
+    const bool whole_steps = M > (d::BIG_MIN_STEPS - 1) * d::BIG_BK;
+    return columns_within((whole_steps ? M + d::BIG_BK * d::BIG_MIN_STEPS * kMaxSplits : ceil_div(M, 256) * 256) * 2);
+}
+bool backward_extents_ok(int64_t M, int64_t K)
+{
+    return extents_ok(M, K) && piece_columns(std::max<int64_t>(M, 1)) >= kPieceUnit;
+}
+
 int splits_of(const ProductPlan &p) { return p.kernel >= KERNEL_SMALL ? 1 : p.tiles.splits; }
 
 BackwardPlan plan_backward(int M, int V, int K, int cus)
 {
     BackwardPlan w = {};
     const int rows = std::max(M, 1);
-    // (rows of dz: up to a few K steps more than there are tokens)
-    const int64_t fit = columns_within((int64_t(rows) + 64 * 4 * kMaxSplits) * 2);
+    const int64_t fit = piece_columns(rows);
     const int64_t want = std::max<int64_t>(8192, kPieceBytes / 2 / rows / kPieceUnit * kPieceUnit);
     // Pieces of sixteen tiles' columns: with a multiple of sixteen tiles of rows
     // (4096 tokens or values of K) a piece's products fill whole rounds of 256 units,
@@ -277,7 +293,7 @@ extern "C" int gemm_bf16_nt_cross_entropy_bwd_workspace_size(int M, int V, int K
 {
     if (M < 0 || V < 0 || K < 0 || !bytes)
         return GEMM355_ERR_INVALID_ARG;
-    if (!extents_ok(M, K) || size_t(M) * size_t(V) > kMaxLogits)
+    if (!backward_extents_ok(M, K) || size_t(M) * size_t(V) > kMaxLogits)
         return GEMM355_ERR_UNSUPPORTED;
     *bytes = 0;
     if (K == 0 || (M == 0 && V == 0))
@@ -300,7 +316,7 @@ extern "C" int gemm_bf16_nt_cross_entropy_bwd(int M, int V, int K, const void *A
         return GEMM355_OK;
     if ((M > 0 && (!A || !targets || !lse)) || (V > 0 && M > 0 && !B) || !workspace)
         return GEMM355_ERR_INVALID_ARG;
-    if (K % 8 != 0 || !extents_ok(M, K) || size_t(M) * size_t(V) > kMaxLogits)
+    if (K % 8 != 0 || !backward_extents_ok(M, K) || size_t(M) * size_t(V) > kMaxLogits)
         return GEMM355_ERR_UNSUPPORTED;
     const size_t a_bytes = size_t(M) * K * 2, b_bytes = size_t(V) * K * 2;
     const Array out[] = {{dA, a_bytes}, {dB, b_bytes}, {workspace, workspace_bytes}};

@@ -394,7 +394,7 @@ extern "C" int gemm355_layer_norm_bwd(int rows, int cols, int x_type, const void
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const bool fp32 = x_type == GEMM355_FP32;
     if (norm_direct(rows, cols, fp32)) {      // (no rows: the column blocks write zeros)
-        const unsigned columns = wants_columns ? (unsigned)ceil_div(cols, 64) : 0u;
+        const unsigned columns = wants_columns ? (unsigned)std::min<int64_t>(ceil_div(cols, 64), kMaxBlocks) : 0u;
         return with_type(x_type, [&](auto tx) {
             return with_type(w_type, [&](auto tw) {
                 auto go = [&](auto vpt_c) {

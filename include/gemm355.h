@@ -703,7 +703,8 @@ int gemm355_layer_norm_bwd_workspace_size(int rows, int cols, size_t *bytes);
  * go where the formula takes them, within their row. A row that is left out costs
  * nothing from 65 tokens up. M == 0 does nothing; with K == 0 every z is 0.
  * A padded to 256 rows and 256 rows of B stay below 2^31 bytes each, else
- * GEMM355_ERR_UNSUPPORTED; B as a whole may be larger. The workspace
+ * GEMM355_ERR_UNSUPPORTED, as are more than 2^26 tokens or 2^46 logits; B as a whole
+ * may be larger. The workspace
  * (gemm_bf16_nt_cross_entropy_workspace_size bytes) is as for the layer calls and
  * always needed.
  */
@@ -725,7 +726,7 @@ int gemm_bf16_nt_cross_entropy_workspace_size(int M, int V, int K, size_t *bytes
  * max |dloss| before that rounding and as the maximum after the FP32 sums, so that
  * equal weights add no rounding. Rows that are left out get zeros in dA and add
  * nothing to dB, whatever A holds there. M == 0 writes zeros to dB, V == 0 to dA;
- * K == 0 does nothing. Sizes and workspace
+ * K == 0 does nothing. M up to 4 million; other sizes and workspace
  * (gemm_bf16_nt_cross_entropy_bwd_workspace_size bytes: about 256 MB of dz for a
  * large batch, FP32 sums and a copy of A) as above.
  */

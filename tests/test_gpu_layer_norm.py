@@ -14,7 +14,8 @@ BF16, FP32 = torch.bfloat16, torch.float32
 TYPES = [(BF16, BF16), (FP32, FP32), (FP32, BF16), (BF16, FP32)]
 SIZES = [(1, 8), (1, 64), (3, 72), (2, 512), (5, 520), (1, 1000), (1, 4096), (7, 1032), (9, 2056), (3, 5000), (2, 8200),
          (3, 16384), (2, 16392), (2, 32776), (1030, 8), (1111, 72), (1025, 520), (1100, 1544), (1030, 4096), (300, 2048),
-         (261, 5000), (270, 8200), (259, 16384)]
+         (261, 5000), (270, 8200), (259, 16384),
+         (800, 1000), (801, 8), (801, 1000), (820, 3000), (900, 5000), (801, 8192), (803, 8200), (805, 16384)]
 
 
 def gen_of(seed):

@@ -1,4 +1,4 @@
-"""Embedding and layer norm of the C ABI without a GPU: every refusal happens
+"""Embedding, layer norm and cross entropy of the C ABI without a GPU: every refusal happens
 before any HIP call, so the addresses here are never dereferenced; and what the
 binding refuses before it asks for a device."""
 import ctypes
@@ -27,6 +27,17 @@ def norm(rows=8, cols=64, xt=0, x=X, wt=0, gamma=GAMMA, beta=BETA, eps=1e-5, y=Y
 def norm_bwd(rows=300, cols=64, xt=0, x=X, wt=0, gamma=GAMMA, mean=MEAN, rstd=RSTD, dy=DY, r=R, dx=DX, dg=DG, db=DB,
              ws=WS, nb=1 << 20):
     return g.load().gemm355_layer_norm_bwd(rows, cols, xt, x, wt, gamma, mean, rstd, dy, r, dx, dg, db, ws, nb, None)
+
+
+A, B, T, LOSS, LSE, DLOSS = ((64 + i) << 24 for i in range(6))
+
+
+def entropy(M=80, V=100, K=64, a=A, b=B, tt=1, t=T, loss=LOSS, lse=LSE, ws=WS, nb=1 << 23):
+    return g.load().gemm_bf16_nt_cross_entropy(M, V, K, a, b, tt, t, loss, lse, ws, nb, None)
+
+
+def entropy_bwd(M=80, V=100, K=64, a=A, b=B, tt=1, t=T, lse=LSE, dloss=DLOSS, da=DX, db=DB, ws=WS, nb=1 << 23):
+    return g.load().gemm_bf16_nt_cross_entropy_bwd(M, V, K, a, b, tt, t, lse, dloss, da, db, ws, nb, None)
 
 
 def no_gpu():
@@ -96,10 +107,47 @@ def test_norm_gradient_refusals():
             assert norm_bwd(**ok) == g.ERR_NO_DEVICE, ok
 
 
+def test_cross_entropy_refusals():
+    for bad in (dict(M=-1), dict(V=-1), dict(K=-8), dict(tt=2), dict(tt=-1), dict(a=None), dict(b=None), dict(t=None),
+                dict(loss=None), dict(lse=None), dict(ws=None), dict(ws=None, nb=0), dict(loss=LSE), dict(loss=A + 16),
+                dict(lse=B), dict(lse=T), dict(ws=A), dict(ws=B), dict(ws=T), dict(ws=LOSS), dict(loss=LSE + 4)):
+        assert entropy(**bad) == g.ERR_INVALID_ARG, bad
+    for bad in (dict(K=12), dict(a=A + 8), dict(b=B + 2), dict(t=T + 4), dict(tt=0, t=T + 2), dict(loss=LOSS + 2),
+                dict(lse=LSE + 1), dict(ws=WS + 8), dict(M=TOP, a=1 << 45, t=1 << 50, loss=1 << 52, lse=1 << 53),
+                dict(K=1 << 22, a=1 << 45, b=1 << 50), dict(M=1 << 24, V=TOP, K=8, a=1 << 45, b=1 << 50, t=1 << 52)):
+        assert entropy(**bad) == g.ERR_UNSUPPORTED, bad
+    assert entropy(M=0, a=None, b=None, t=None, loss=None, lse=None, ws=None, nb=0) == g.OK
+    if no_gpu():
+        for ok in ({}, dict(V=0, b=None), dict(K=0, a=None, b=None), dict(V=101), dict(t=T + 8), dict(tt=0, t=T + 4),
+                   dict(loss=LOSS + 4, lse=LSE + 12)):
+            assert entropy(**ok) == g.ERR_NO_DEVICE, ok
+
+
+def test_cross_entropy_gradient_refusals():
+    for bad in (dict(M=-1), dict(V=-1), dict(K=-8), dict(tt=2), dict(a=None), dict(b=None), dict(t=None), dict(lse=None),
+                dict(ws=None), dict(ws=None, nb=0), dict(da=A), dict(da=B), dict(db=B), dict(db=A), dict(da=DB), dict(da=T),
+                dict(da=LSE), dict(db=DLOSS), dict(ws=A), dict(ws=DX), dict(ws=DB), dict(ws=LSE), dict(ws=DLOSS)):
+        assert entropy_bwd(**bad) == g.ERR_INVALID_ARG, bad
+    for bad in (dict(K=12), dict(a=A + 8), dict(b=B + 2), dict(da=DX + 8), dict(db=DB + 4), dict(t=T + 4), dict(lse=LSE + 2),
+                dict(dloss=DLOSS + 1), dict(ws=WS + 8), dict(M=TOP, a=1 << 45, t=1 << 50, da=None, lse=1 << 52, dloss=None),
+                dict(K=1 << 22, a=1 << 45, b=1 << 50, da=None, db=1 << 55)):
+        assert entropy_bwd(**bad) == g.ERR_UNSUPPORTED, bad
+    none = dict(a=None, b=None, t=None, lse=None, dloss=None, ws=None, nb=0)
+    assert entropy_bwd(da=None, db=None, **none) == g.OK
+    assert entropy_bwd(K=0, **none) == g.OK
+    assert entropy_bwd(M=0, V=0, **none) == g.OK
+    assert entropy_bwd(M=0, db=None, **none) == g.OK and entropy_bwd(V=0, da=None, **none) == g.OK
+    if no_gpu():
+        for ok in ({}, dict(dloss=None), dict(da=None), dict(db=None), dict(V=0, b=None), dict(V=101),
+                   dict(M=0, a=None, b=None, t=None, lse=None, dloss=None), dict(lse=LSE + 4, dloss=DLOSS + 4)):
+            assert entropy_bwd(**ok) == g.ERR_NO_DEVICE, ok
+
+
 def test_workspace_size_refusals():
     lib, n = g.load(), ctypes.c_size_t(7)
-    for name, count in (("embedding_bwd", 3), ("layer_norm_bwd", 2)):
-        fn = getattr(lib, "gemm355_%s_workspace_size" % name)
+    for name, count in (("gemm355_embedding_bwd", 3), ("gemm355_layer_norm_bwd", 2), ("gemm_bf16_nt_cross_entropy", 3),
+                        ("gemm_bf16_nt_cross_entropy_bwd", 3)):
+        fn = getattr(lib, name + "_workspace_size")
         for i in range(count):
             assert fn(*[-1 if j == i else 8 for j in range(count)], ctypes.byref(n)) == g.ERR_INVALID_ARG
         assert fn(*[8] * count, None) == g.ERR_INVALID_ARG
@@ -148,6 +196,15 @@ def test_sizes_beyond_32_bits_are_refused(far):
             g.embedding_bwd(*[far if j == i else 8 for j in range(3)], 64, 64, None, 64, id_type=0, e_type=0, y_type=0)
         with pytest.raises(OverflowError):
             g.embedding_bwd_workspace_size(*[far if j == i else 8 for j in range(3)])
+        with pytest.raises(OverflowError):
+            g.gemm_bf16_nt_cross_entropy(*[far if j == i else 8 for j in range(3)], 64, 64, 64, 64, 64, target_type=0)
+        with pytest.raises(OverflowError):
+            g.gemm_bf16_nt_cross_entropy_bwd(*[far if j == i else 8 for j in range(3)], 64, 64, 64, 64, 64, 64, 64,
+                                             target_type=0)
+        with pytest.raises(OverflowError):
+            g.cross_entropy_workspace_size(*[far if j == i else 8 for j in range(3)])
+        with pytest.raises(OverflowError):
+            g.cross_entropy_bwd_workspace_size(*[far if j == i else 8 for j in range(3)])
     for i in range(2):
         with pytest.raises(OverflowError):
             g.layer_norm(*[far if j == i else 8 for j in range(2)], 64, None, None, 64, None, None, x_type=0)
