@@ -93,6 +93,7 @@ struct EmbedBwdArgs {
     float *partial;        // [blocks][2][cols]: of ids that were cut; 0: begun in an earlier block, 1: beginning here
     int tokens, vocab, cols;
     int range;             // ids per workgroup of the order
+    int order_groups;      // workgroups of the order
     int block;             // tokens per block
     int blocks;            // of the sorted tokens (as many as all tokens would need)
     int pieces;            // of 512 columns in a row
@@ -101,10 +102,74 @@ struct EmbedBwdArgs {
     bool wide;
 };
 
+// This lane's eight columns at c of the rows v0 + i, i in `rows`, that no token
+// has: R or zeros, several rows at a time.
+template <class TE>
+__device__ inline void embed_fill(const EmbedBwdArgs &p, int v0, unsigned long long rows, int c)
+{
+    constexpr int AHEAD = 8;
+    if (p.r == p.de)
+        return;
+    const int cc = min(c, p.cols - 8);
+    while (rows != 0) {
+        Raw8<TE> r[AHEAD];
+        size_t at[AHEAD];
+        const int n = min(AHEAD, __popcll(rows));
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            // (past the last row: that one again)
+            at[k] = k < n ? (size_t)(v0 + __builtin_ctzll(rows)) * (size_t)p.cols : at[k > 0 ? k - 1 : 0];
+            rows = k < n ? rows & (rows - 1) : rows;
+            r[k].fill(0.0f);
+        }
+        if (p.r)
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                r[k].load(p.r, at[k] + (size_t)cc);
+        if (c < p.cols)
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (k < n)
+                    r[k].store(p.de, at[k] + (size_t)c);
+    }
+}
+
 constexpr int FILL_ROWS = 16;
+
+// All rows, R or zeros, by threads that go through memory side by side. Few of them,
+// four waves a unit: 1 GiB of zeros takes 162 us so, with eight times as many 190 to
+// 240, their stores spread over too many of the memory's pages at a time.
+constexpr int FILL_THREADS = 256;
+template <class TE>
+__device__ inline void embed_fill_all(const EmbedBwdArgs &p, int64_t thread, int64_t threads)
+{
+    constexpr int AHEAD = 4;
+    const int64_t n = (int64_t)p.vocab * p.cols, step = 8 * threads;
+    if (!p.r) {      // 16 bytes of either type
+        u32x4 *out = static_cast<u32x4 *>(p.de);
+        for (int64_t i = thread; i < n / (16 / (int)sizeof(TE)); i += threads)
+            __builtin_nontemporal_store(u32x4{}, out + i);
+        return;
+    }
+    for (int64_t i = 8 * thread; i < n; i += AHEAD * step) {
+        Raw8<TE> r[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            r[k].load(p.r, (size_t)min(i + k * step, n - 8));
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (i + k * step < n)
+                r[k].store(p.de, (size_t)(i + k * step));
+    }
+}
+
 constexpr int ORDER_THREADS = 1024, ORDER_WAVES = ORDER_THREADS / 64;
 constexpr int ORDER_MAX_RANGE = 512, ORDER_AHEAD = 8;
 
+// Workgroups from p.order_groups on fill every row, for the sums to write those
+// again that have tokens: where those are few, the ordering then costs no time of
+// its own (16384 tokens of 128000 ids: 250 us, 219 so).
+template <class TE>
 __global__ __launch_bounds__(ORDER_THREADS) void embed_order_kernel(EmbedBwdArgs p)
 {
     // [wave][id of the range]: first its tokens, then where the next one goes
@@ -112,6 +177,12 @@ __global__ __launch_bounds__(ORDER_THREADS) void embed_order_kernel(EmbedBwdArgs
     __shared__ int before[ORDER_WAVES], total[ORDER_WAVES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    if ((int)blockIdx.x >= p.order_groups) {
+        if (threadIdx.x < FILL_THREADS)
+            embed_fill_all<TE>(p, ((int64_t)blockIdx.x - p.order_groups) * FILL_THREADS + threadIdx.x,
+                               ((int64_t)gridDim.x - p.order_groups) * FILL_THREADS);
+        return;
+    }
     const int v0 = (int)blockIdx.x * p.range, range = min(p.range, p.vocab - v0);
     for (int i = threadIdx.x; i < ORDER_MAX_RANGE * ORDER_WAVES; i += ORDER_THREADS)
         (&count[0][0])[i] = 0;
@@ -245,38 +316,6 @@ __device__ inline void embed_finish(const EmbedBwdArgs &p, int v, int c, const f
     r.store(p.de, at);
 }
 
-// This lane's eight columns at c of the rows v0 + i, i in `rows`, that no token
-// has: R or zeros, several rows at a time.
-template <class TE>
-__device__ inline void embed_fill(const EmbedBwdArgs &p, int v0, unsigned long long rows, int c)
-{
-    constexpr int AHEAD = 8;
-    if (p.r == p.de)
-        return;
-    const int cc = min(c, p.cols - 8);
-    while (rows != 0) {
-        Raw8<TE> r[AHEAD];
-        size_t at[AHEAD];
-        const int n = min(AHEAD, __popcll(rows));
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            // (past the last row: that one again)
-            at[k] = k < n ? (size_t)(v0 + __builtin_ctzll(rows)) * (size_t)p.cols : at[k > 0 ? k - 1 : 0];
-            rows = k < n ? rows & (rows - 1) : rows;
-            r[k].fill(0.0f);
-        }
-        if (p.r)
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                r[k].load(p.r, at[k] + (size_t)cc);
-        if (c < p.cols)
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                if (k < n)
-                    r[k].store(p.de, at[k] + (size_t)c);
-    }
-}
-
 __device__ inline void embed_partial(const EmbedBwdArgs &p, int block, int which, int c, const float (&x)[8])
 {
     if (c >= p.cols)
@@ -295,14 +334,12 @@ __global__ __launch_bounds__(EMBED_THREADS) void embed_sums_kernel(EmbedBwdArgs 
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int at = (int)blockIdx.x * (EMBED_THREADS / 64) + wave, waves = (int)gridDim.x * (EMBED_THREADS / 64);
     if (at >= p.sum_waves) {
-        // rows without a token, looked for among sixteen at a time
+        // rows without a token
         const int64_t items = (((int64_t)p.vocab + FILL_ROWS - 1) / FILL_ROWS) * p.pieces;
         for (int64_t item = at - p.sum_waves; item < items; item += waves - p.sum_waves) {
             const int group = (int)(item / p.pieces), c = 512 * (int)(item - (int64_t)group * p.pieces) + 8 * lane;
-            const int v0 = group * FILL_ROWS, v = min(v0 + lane, p.vocab);
-            const int next = p.start[min(v + 1, p.vocab)];
-            const bool none = lane < FILL_ROWS && v < p.vocab && p.start[v] == next;
-            embed_fill<TE>(p, v0, __ballot(none), c);
+            const int v0 = group * FILL_ROWS, v = min(v0 + lane, p.vocab), next = p.start[min(v + 1, p.vocab)];
+            embed_fill<TE>(p, v0, __ballot(lane < FILL_ROWS && v < p.vocab && p.start[v] == next), c);
         }
         return;
     }

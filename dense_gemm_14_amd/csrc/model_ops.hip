@@ -281,18 +281,26 @@ extern "C" int gemm355_embedding_bwd(int tokens, int vocab, int cols, int id_typ
                                      (unsigned)r::EMBED_THREADS, p, s);
             });
         });
-    int st = launch_kernel(r::embed_order_kernel, (unsigned)e.groups, (unsigned)r::ORDER_THREADS, p, s);
-    if (st != GEMM355_OK)
-        return st;
     constexpr int per = r::EMBED_THREADS / 64;
     const int64_t sum_groups = std::min<int64_t>(ceil_div(int64_t(e.blocks) * e.pieces, per), 16 * int64_t(cus));
-    const int64_t fill_groups = R == dE ? 0 : std::min<int64_t>(ceil_div(ceil_div(vocab, r::FILL_ROWS) * e.pieces, per), 8 * int64_t(cus));
+    // Rows without a token are filled beside the ordering, and those with one as well,
+    // where at most a quarter have one; else beside the sums.
+    const bool early = vocab / 4 >= tokens;
+    const bool fills = R != dE;
+    const int64_t early_groups =
+        fills && early ? std::min<int64_t>(ceil_div(int64_t(vocab) * cols, 32 * r::FILL_THREADS), cus) : 0;
+    const int64_t late_groups =
+        fills && !early ? std::min<int64_t>(ceil_div(ceil_div(vocab, r::FILL_ROWS) * e.pieces, per), 8 * int64_t(cus)) : 0;
+    p.order_groups = e.groups;
     p.sum_waves = (int)(sum_groups * per);
     return with_type(e_type, [&](auto te) {
         return with_type(y_type, [&](auto ty) {
             typedef decltype(te) TE;
-            const int st = launch_kernel(r::embed_sums_kernel<TE, decltype(ty)>, (unsigned)(sum_groups + fill_groups),
-                                         (unsigned)r::EMBED_THREADS, p, s);
+            int st = launch_kernel(r::embed_order_kernel<TE>, (unsigned)(e.groups + early_groups), (unsigned)r::ORDER_THREADS, p, s);
+            if (st != GEMM355_OK)
+                return st;
+            st = launch_kernel(r::embed_sums_kernel<TE, decltype(ty)>, (unsigned)(sum_groups + late_groups),
+                               (unsigned)r::EMBED_THREADS, p, s);
             if (st != GEMM355_OK)
                 return st;
             return launch_kernel(r::embed_join_kernel<TE>,

@@ -701,7 +701,7 @@ int gemm355_layer_norm_bwd_workspace_size(int rows, int cols, size_t *bytes);
  *   lse      M FP32 values for gemm_bf16_nt_cross_entropy_bwd
  * Products exact, sums and exponentials FP32; infinities and NaN among the logits
  * go where the formula takes them, within their row. A row that is left out costs
- * nothing from 65 tokens up. M == 0 does nothing; with K == 0 every z is 0.
+ * nothing in a product of more than 2^33 multiplications. M == 0 does nothing; with K == 0 every z is 0.
  * A padded to 256 rows and 256 rows of B stay below 2^31 bytes each, else
  * GEMM355_ERR_UNSUPPORTED, as are more than 2^26 tokens or 2^46 logits; B as a whole
  * may be larger. The workspace
