@@ -121,16 +121,18 @@ struct BackwardPlan {
     size_t rows_at, scale_at, map_at, target_at, lse_at, weight_at, a_at, dz_at, acc_at, partials_at, bytes;
 };
 
-// Columns that a piece's dz may have. (Its rows: where the product over them may take
-// whole K steps, for each split at least four, more than there are tokens.)
-int64_t piece_columns(int64_t M)
+// Rows of dz and of the moved A, for their extents: where the product over them may
+// take whole K steps, up to a step for each split more than there are tokens.
+int64_t padded_rows(int64_t M)
 {
-    const bool whole_steps = M > (d::BIG_MIN_STEPS - 1) * d::BIG_BK;
-    return columns_within((whole_steps ? M + d::BIG_BK * d::BIG_MIN_STEPS * kMaxSplits : ceil_div(M, 256) * 256) * 2);
+    return M > (d::BIG_MIN_STEPS - 1) * d::BIG_BK ? M + d::BIG_BK * kMaxSplits : ceil_div(M, 256) * 256;
 }
+// Columns that a piece's dz may have.
+int64_t piece_columns(int64_t M) { return columns_within(padded_rows(M) * 2); }
 bool backward_extents_ok(int64_t M, int64_t K)
 {
-    return extents_ok(M, K) && piece_columns(std::max<int64_t>(M, 1)) >= kPieceUnit;
+    M = std::max<int64_t>(M, 1);
+    return extents_ok(M, K) && extent_ok(padded_rows(M), K * 2) && piece_columns(M) >= kPieceUnit;
 }
 
 int splits_of(const ProductPlan &p) { return p.kernel >= KERNEL_SMALL ? 1 : p.tiles.splits; }

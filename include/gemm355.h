@@ -726,7 +726,8 @@ int gemm_bf16_nt_cross_entropy_workspace_size(int M, int V, int K, size_t *bytes
  * max |dloss| before that rounding and as the maximum after the FP32 sums, so that
  * equal weights add no rounding. Rows that are left out get zeros in dA and add
  * nothing to dB, whatever A holds there. M == 0 writes zeros to dB, V == 0 to dA;
- * K == 0 does nothing. M up to 4 million; other sizes and workspace
+ * K == 0 does nothing. M up to 4 million, and A with 1024 rows more below 2^31
+ * bytes; other sizes and workspace
  * (gemm_bf16_nt_cross_entropy_bwd_workspace_size bytes: about 256 MB of dz for a
  * large batch, FP32 sums and a copy of A) as above.
  */

@@ -114,10 +114,11 @@ def run(shim, seed, count):
     for M, N in ((2147483647, 8), (2147483647, 512), (1, 1 << 30), (500, 1 << 31 - 9), (100000000, 4096), (1 << 20, 1 << 20)):
         rec.norm(M, N, rng)
     for M, V, K in ((1 << 18, 100000, 2048), (1, 1 << 27, 8), (1, 1000, 1 << 21), (100000, 200000, 512), (0, 100, 64),
-                    (33, 0, 64), (4000000, 1000, 8), (1 << 26, 100, 8), (1 << 26, 300, 0)):
+                    (33, 0, 64), (4000000, 1000, 8), (260000, 300, 4096), (1 << 26, 100, 8), (1 << 26, 300, 0)):
         rec.entropy(M, V, K, rng)
     n = ctypes.c_size_t(7)
-    assert rec.lib.gemm_bf16_nt_cross_entropy_bwd_workspace_size(8000000, 1000, 8, ctypes.byref(n)) == g.ERR_UNSUPPORTED
+    for sizes in ((8000000, 1000, 8), (261500, 300, 4096)):
+        assert rec.lib.gemm_bf16_nt_cross_entropy_bwd_workspace_size(*sizes, ctypes.byref(n)) == g.ERR_UNSUPPORTED, sizes
     # tiles of the logits beyond 32 bits: pieces
     rec.lib.gemm355_force_layer_kernel(5)
     args = (4000000, 1 << 20, 8)
