@@ -271,12 +271,29 @@ __device__ inline void loss_rows(const DenseArgs &p, f32x4 (&x)[R][BJ], int m0, 
 }
 
 // The same for eight consecutive columns n .. n + 7 of row m, one of the RUNS
-// neighbouring lanes that hold a tile's row (small tiles). All of them call it,
-// in or out of C.
+// neighbouring lanes that hold a tile's row (small tiles). All of them call it, in
+// or out of C. What it reads besides its sums is asked for beforehand.
+struct LossEight {
+    LossRow row;
+    f32x4 add[2];
+};
+template <int EPI>
+__device__ inline LossEight loss_eight_of(const DenseArgs &p, int m, int n)
+{
+    LossEight r = {loss_row_of<EPI, LOSS_LAST>(p, m), {}};
+    if constexpr (EPI == EPI_ACC)
+        if (p.add && m < p.M && n < p.N) {
+            const f32x4 *acc = reinterpret_cast<const f32x4 *>(p.acc + (size_t)m * (size_t)p.N + (size_t)n);
+            r.add[0] = acc[0];
+            r.add[1] = acc[1];
+        }
+    return r;
+}
 template <int EPI, int RUNS>
-__device__ inline void loss_eight(const DenseArgs &p, float (&x)[8], int m, int n, int part)
+__device__ inline void loss_eight(const DenseArgs &p, float (&x)[8], int m, int n, int part, const LossEight &r)
 {
     const bool in = m < p.M && n < p.N;
+    const int d = r.row.at - n;
     if constexpr (EPI == EPI_CE) {
         float top = -__builtin_inff();
 #pragma unroll
@@ -299,7 +316,6 @@ __device__ inline void loss_eight(const DenseArgs &p, float (&x)[8], int m, int 
             return;
         if (((int)threadIdx.x & (RUNS - 1)) == 0)
             p.stats[(size_t)part * (size_t)p.stats_rows + (size_t)m] = loss_stat(top, base, sum);
-        const int d = loss_target(p, m) - n;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (d == e && n + e < p.N)
@@ -308,31 +324,26 @@ __device__ inline void loss_eight(const DenseArgs &p, float (&x)[8], int m, int 
         if (!in)
             return;
         if constexpr (EPI == EPI_CE_GRAD) {
-            const float lse = p.lse[m], weight = p.weight[m];
-            const int d = loss_target(p, m) - n;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                x[e] = n + e < p.N ? (loss_exp(x[e], lse) - (d == e ? 1.0f : 0.0f)) * weight : 0.0f;
+                x[e] = n + e < p.N ? (loss_exp(x[e], r.row.lse) - (d == e ? 1.0f : 0.0f)) * r.row.weight : 0.0f;
             *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + (size_t)m * (size_t)p.ldc + (size_t)n) =
                 u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
         }
         if constexpr (EPI == EPI_ACC) {
-            f32x4 *acc = reinterpret_cast<f32x4 *>(p.acc + (size_t)m * (size_t)p.N + (size_t)n);
-            if (p.add) {
-                const f32x4 lo = acc[0], hi = acc[1];
+            if (p.add)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[e] += lo[e];
-                    x[4 + e] += hi[e];
+                    x[e] += r.add[0][e];
+                    x[4 + e] += r.add[1][e];
                 }
-            }
             if (p.last) {
                 const float scale = *p.scale;
-                const int row = p.map ? p.map[m] : m;
-                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + (size_t)row * (size_t)p.N + (size_t)n) =
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + (size_t)r.row.at * (size_t)p.N + (size_t)n) =
                     u32x4{pack_bf16(x[0] * scale, x[1] * scale), pack_bf16(x[2] * scale, x[3] * scale),
                           pack_bf16(x[4] * scale, x[5] * scale), pack_bf16(x[6] * scale, x[7] * scale)};
             } else {
+                f32x4 *acc = reinterpret_cast<f32x4 *>(p.acc + (size_t)m * (size_t)p.N + (size_t)n);
                 acc[0] = f32x4{x[0], x[1], x[2], x[3]};
                 acc[1] = f32x4{x[4], x[5], x[6], x[7]};
             }

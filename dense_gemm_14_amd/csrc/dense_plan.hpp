@@ -337,5 +337,59 @@ inline DenseArgs args_of(int M, int N, int K, const void *a, const void *b, void
     return p;
 }
 
+// ---- backward passes in one launch ------------------------------------------
+
+// How a backward pass runs as one launch (kernel 0: not).
+struct Together {
+    int kernel, waves;
+};
+
+// Whether a backward pass runs as one launch of small tiles (KERNEL_SMALL or
+// KERNEL_NARROW; 0: its products one by one); pa, pb: the plans of the products
+// that are wanted. Together the tiles fill the compute units better and launches
+// fall away, the bias gradient's too. Estimate: the tiles' time shared out over
+// the units, and no less than the longest tile; it comes out a tenth too short,
+// and what separate launches cost is in each one's own estimate already. (Over
+// 140 backward passes of up to 4096 tokens: ten vectors of 7336 x 328 weights,
+// 115 slices of which one tile of dA takes every eighth, 22 us together, 14 apart;
+// 170 x 1528 x 1608 10.5 together, 28 as two products of 128 x 128 tiles.)
+constexpr double kTogether = 1.1, kBiasLaunch = 1.0;
+inline Together backward_together(const Shape &a, const ProductPlan *pa, const Shape &b, const ProductPlan *pb, int cus)
+{
+    if (!pa && !pb)   // the bias gradient alone
+        return {KERNEL_SMALL, 8};
+    if (!pa || !pb) {
+        // alone, a product runs as it would anywhere: beside the bias gradient in
+        // one launch where that has the planned tiles and waves, else by itself
+        const ProductPlan &one = pa ? *pa : *pb;
+        const bool has = one.kernel == KERNEL_NARROW || (one.kernel == KERNEL_SMALL && one.small.waves >= 4);
+        return has ? Together{one.kernel, one.small.waves} : Together{0, 0};
+    }
+    const bool small = pa->kernel >= KERNEL_SMALL && pb->kernel >= KERNEL_SMALL, forced = pa->us == 0.0;
+    if (forced && !small)
+        return {0, 0};
+    double best_us = forced ? 1e30 : (pa->us + pb->us) / kTogether + kBiasLaunch;
+    Together best = {0, 0};
+    for (const Together &how : {Together{KERNEL_SMALL, 8}, Together{KERNEL_SMALL, 4}, Together{KERNEL_NARROW, 8}}) {
+        if (forced && how.kernel != pa->kernel)
+            continue;
+        SmallPlan ta = plan_small(a, false, how.kernel == KERNEL_NARROW, cus), tb = plan_small(b, false, how.kernel == KERNEL_NARROW, cus);
+        ta.waves = tb.waves = how.waves;
+        const double na = ta.tiles, nb = tb.tiles, slots = small_slots(ta, cus), fill = std::min(1.0, (na + nb) / slots);
+        const int ka = (int)ceil_div(a.K, d::SMALL_BK), kb = (int)ceil_div(b.K, d::SMALL_BK);
+        const double one_a = time_small_tile(ta, ka, fill), one_b = time_small_tile(tb, kb, fill);
+        // a long tile goes on when the others are done
+        const double longest = std::max(time_small_tile(ta, ka, std::min(1.0, na / slots)),
+                                        time_small_tile(tb, kb, std::min(1.0, nb / slots)));
+        // (the last tiles end up to one short tile apart)
+        const double us = kStart + std::max(longest, (na * one_a + nb * one_b) / slots + 0.5 * std::min(one_a, one_b));
+        if (us < best_us) {
+            best_us = us;
+            best = how;
+        }
+    }
+    return best;
+}
+
 } // namespace host
 } // namespace gemm355

@@ -278,6 +278,19 @@ __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *
         }
         wait_all_copies();   // none may still write the LDS that the sums use
     }
+    constexpr int COLS = small_columns(EPI, NB);
+    constexpr int RUNS = COLS / 8;   // of eight columns per row
+    // (a loss's rows are looked up while the sums meet: one after the other in the
+    // loop below they took as long as the product)
+    constexpr int TURNS = epi_loss(EPI) ? (16 * MB * RUNS + 64 * WAVES - 1) / (64 * WAVES) : 1;
+    LossEight ahead[TURNS];
+    if constexpr (epi_loss(EPI))
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) {
+            const int q = (int)threadIdx.x + i * 64 * WAVES;
+            if (q < 16 * MB * RUNS)
+                ahead[i] = loss_eight_of<EPI>(p, tm * 16 * MB + q / RUNS, tn * COLS + 8 * (q % RUNS));
+        }
     // Lane (l16, grp) of block (i, j) holds row 16 i + l16, columns 16 j +
     // 4 grp .. + 3 of the tile.
     __syncthreads();
@@ -293,8 +306,6 @@ __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *
     }
     __syncthreads();
 
-    constexpr int COLS = small_columns(EPI, NB);
-    constexpr int RUNS = COLS / 8;   // of eight columns per row
     auto eight = [&](int r, int c, float (&x)[8]) {
         const float *at = sums + r * PITCH + c;
 #pragma unroll
@@ -310,14 +321,22 @@ __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *
             }
         }
     };
+    if constexpr (epi_loss(EPI)) {
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) {
+            const int q = (int)threadIdx.x + i * 64 * WAVES, r = q / RUNS, c = 8 * (q % RUNS);
+            if (q < 16 * MB * RUNS) {
+                float x[8];
+                eight(r, c, x);
+                loss_eight<EPI, RUNS>(p, x, tm * 16 * MB + r, tn * COLS + c, tn, ahead[i]);
+            }
+        }
+        return;
+    }
     for (int q = threadIdx.x; q < 16 * MB * RUNS; q += 64 * WAVES) {
         const int r = q / RUNS, c = 8 * (q % RUNS);
         const int m = tm * 16 * MB + r, n = tn * COLS + c;
-        if constexpr (epi_loss(EPI)) {
-            float x[8];
-            eight(r, c, x);
-            loss_eight<EPI, RUNS>(p, x, m, n, tn);
-        } else if (m < p.M && n < p.N) {
+        if (m < p.M && n < p.N) {
             float x[8], u[8];
             eight(r, c, x);
             if constexpr (EPI == EPI_GATED)
@@ -390,6 +409,35 @@ __global__ __launch_bounds__(64 * WAVES, 2) void dense_small_bwd_kernel(SmallBwd
         small_tile<__bf16, COL_K, COL_K, EPI_STORE, __bf16, BLOCKS, BLOCKS, WAVES>(p.b, 0, tm, tn, lds);
     } else {
         bias_block<64 * WAVES>(p.bias, item - (p.a.tiles + p.b.tiles - ahead), reinterpret_cast<float *>(lds));
+    }
+}
+
+// Both products of a small loss's backward pass in one launch, likewise: dA = dz B
+// and dB = dz^T A. The tiles are those of all rows; what lies past the kept ones
+// returns at once.
+struct SmallLossArgs {
+    DenseArgs a, b;
+    int tiles_a, tiles_b;
+    int first_b;
+};
+
+template <int BLOCKS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void dense_small_loss_kernel(SmallLossArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[small_lds(BLOCKS, BLOCKS, WAVES)];
+    const int ahead = p.first_b ? p.tiles_b : 0;
+    const int item = (int)blockIdx.x - ahead;
+    int tm, tn;
+    if (item >= 0 && item < p.tiles_a) {
+        take_rows(p.a, 16 * BLOCKS);
+        if (item >= p.a.tiles)
+            return;
+        dense_tile<EPI_ACC>(p.a, item, tm, tn);
+        small_tile<__bf16, ROW_K, COL_K, EPI_ACC, __bf16, BLOCKS, BLOCKS, WAVES>(p.a, 0, tm, tn, lds);
+    } else {
+        take_rows(p.b, 16 * BLOCKS);
+        dense_tile<EPI_STORE>(p.b, item < 0 ? item + ahead : item - p.tiles_a, tm, tn);
+        small_tile<__bf16, COL_K, COL_K, EPI_STORE, __bf16, BLOCKS, BLOCKS, WAVES>(p.b, 0, tm, tn, lds);
     }
 }
 

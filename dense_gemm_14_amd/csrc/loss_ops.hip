@@ -108,7 +108,9 @@ bool extents_ok(int64_t M, int64_t K)
 
 constexpr size_t kMaxLogits = size_t(1) << 46;   // (M V, so that no size runs over)
 
-int prep_blocks(int M, int cus) { return (int)std::min<int64_t>(std::max(M, 1), 4 * int64_t(cus)); }
+// Workgroups that move rows, each after a look at all targets: two rows for each of
+// a workgroup's waves, or more than four workgroups to a unit would be.
+int prep_blocks(int M, int cus) { return (int)std::min<int64_t>(std::max<int64_t>(ceil_div(M, 2 * d::CE_WAVES), 1), 4 * int64_t(cus)); }
 
 // Bytes of a piece's gradient of the logits.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
@@ -116,6 +118,7 @@ constexpr int64_t kPieceBytes = int64_t(256) << 20;
 struct BackwardPlan {
     Pieces pieces;
     ProductPlan z[2], a[2], b[2];     // of a piece, of the last one
+    Together together;                // both products of the only piece
     int min_steps[2];
     int pitch;                        // of dz
     size_t rows_at, scale_at, map_at, target_at, lse_at, weight_at, a_at, dz_at, acc_at, partials_at, bytes;
@@ -137,7 +140,7 @@ bool backward_extents_ok(int64_t M, int64_t K)
 
 int splits_of(const ProductPlan &p) { return p.kernel >= KERNEL_SMALL ? 1 : p.tiles.splits; }
 
-BackwardPlan plan_backward(int M, int V, int K, int cus)
+BackwardPlan plan_backward(int M, int V, int K, bool wants_a, bool wants_b, int cus)
 {
     BackwardPlan w = {};
     const int rows = std::max(M, 1);
@@ -163,6 +166,9 @@ BackwardPlan plan_backward(int M, int V, int K, int cus)
         partials = std::max({partials, w.z[i].workspace_bytes, w.a[i].workspace_bytes, w.b[i].workspace_bytes});
         depth = std::max(depth, d::ce_depth(rows, splits_of(w.b[i]), w.min_steps[i]));
     }
+    // (one launch takes none of the partials and whole steps that are set aside)
+    if (w.pieces.count == 1 && M > 0 && wants_a && wants_b)
+        w.together = backward_together({M, K, V, 1, false, false}, &w.a[1], {V, K, M, 1, false, false}, &w.b[1], cus);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -181,6 +187,37 @@ BackwardPlan plan_backward(int M, int V, int K, int cus)
     w.partials_at = take(partials);
     w.bytes = at;
     return w;
+}
+
+template <int BLOCKS, int WAVES>
+int launch_small_loss(unsigned blocks, d::SmallLossArgs &g, hipStream_t s)
+{
+    return launch_kernel(d::dense_small_loss_kernel<BLOCKS, WAVES>, blocks, 64u * WAVES, g, s);
+}
+
+// Both products of the only piece in one launch.
+int both_small(DenseArgs pa, DenseArgs pb, const Together &how, int cus, hipStream_t s)
+{
+    d::SmallLossArgs g = {};
+    auto place = [&](DenseArgs &p) {
+        const SmallPlan t = plan_small({p.M, p.N, p.K, 1, false, false}, false, how.kernel == KERNEL_NARROW, cus);
+        p.tiles_m = t.tiles_m;
+        p.tiles_n = t.tiles_n;
+        p.tiles = p.whole = t.tiles;
+        p.splits = 1;
+        p.supergroup = 8;
+    };
+    place(pa);
+    place(pb);
+    g.a = pa;
+    g.b = pb;
+    g.tiles_a = pa.tiles;
+    g.tiles_b = pb.tiles;
+    g.first_b = pb.K > pa.K;
+    const unsigned blocks = (unsigned)(pa.tiles + pb.tiles);
+    if (how.kernel == KERNEL_NARROW)
+        return launch_small_loss<2, 8>(blocks, g, s);
+    return how.waves == 8 ? launch_small_loss<4, 8>(blocks, g, s) : launch_small_loss<4, 4>(blocks, g, s);
 }
 
 } // namespace
@@ -306,7 +343,7 @@ extern "C" int gemm_bf16_nt_cross_entropy_bwd_workspace_size(int M, int V, int K
     int cus = 0;
     const int rc = compute_units(&cus);
     if (rc == GEMM355_OK)
-        *bytes = plan_backward(M, V, K, cus).bytes;
+        *bytes = plan_backward(M, V, K, false, false, cus).bytes;   // (the same whichever outputs are wanted)
     return rc;
 }
 
@@ -336,7 +373,7 @@ extern "C" int gemm_bf16_nt_cross_entropy_bwd(int M, int V, int K, const void *A
     const int rc = compute_units(&cus);
     if (rc != GEMM355_OK)
         return rc;
-    const BackwardPlan w = plan_backward(M, V, K, cus);
+    const BackwardPlan w = plan_backward(M, V, K, wants_a, wants_b, cus);
     if (workspace_bytes < w.bytes)
         return GEMM355_ERR_UNSUPPORTED;
 
@@ -384,28 +421,33 @@ extern "C" int gemm_bf16_nt_cross_entropy_bwd(int M, int V, int K, const void *A
             p.ldc = w.pitch;
             st = product<__bf16, d::ROW_K, d::ROW_K, d::EPI_CE_GRAD>(p, w.z[which], partials, s);
         }
-        if (wants_b && st == GEMM355_OK) {                      // dB = dz^T A
-            DenseArgs p = args_of(N, K, (int)d::ce_depth(std::max(M, 1), q.splits[which], q.min_steps[which]), q.dz, q.ka,
-                                  static_cast<uint8_t *>(dB) + from);
-            p.rows = q.rows;
-            p.rows_in_k = 1;
-            p.min_steps = q.min_steps[which];
-            p.lda = w.pitch;
-            p.scale = q.scale;
-            st = product<__bf16, d::COL_K, d::COL_K, d::EPI_STORE>(p, w.b[which], partials, s);
+        // dB = dz^T A, dA += dz B
+        const bool one = w.together.kernel != 0;
+        DenseArgs pb = args_of(N, K, one ? M : (int)d::ce_depth(std::max(M, 1), q.splits[which], q.min_steps[which]), q.dz,
+                               q.ka, static_cast<uint8_t *>(dB) + from);
+        pb.rows = q.rows;
+        pb.rows_in_k = 1;
+        pb.min_steps = one ? 0 : q.min_steps[which];
+        pb.lda = w.pitch;
+        pb.scale = q.scale;
+        DenseArgs pa = args_of(M, K, N, q.dz, b, dA);
+        pa.rows = q.rows;
+        pa.lda = w.pitch;
+        pa.scale = q.scale;
+        pa.acc = reinterpret_cast<float *>(ws + w.acc_at);
+        pa.map = q.map;
+        pa.c_rows = M;
+        pa.add = i > 0;
+        pa.last = which;
+        if (one) {
+            if (st == GEMM355_OK)
+                st = both_small(pa, pb, w.together, cus, s);
+            continue;
         }
-        if (wants_a && st == GEMM355_OK) {                      // dA += dz B
-            DenseArgs p = args_of(M, K, N, q.dz, b, dA);
-            p.rows = q.rows;
-            p.lda = w.pitch;
-            p.scale = q.scale;
-            p.acc = reinterpret_cast<float *>(ws + w.acc_at);
-            p.map = q.map;
-            p.c_rows = M;
-            p.add = i > 0;
-            p.last = which;
-            st = product<__bf16, d::ROW_K, d::COL_K, d::EPI_ACC>(p, w.a[which], partials, s);
-        }
+        if (wants_b && st == GEMM355_OK)
+            st = product<__bf16, d::COL_K, d::COL_K, d::EPI_STORE>(pb, w.b[which], partials, s);
+        if (wants_a && st == GEMM355_OK)
+            st = product<__bf16, d::ROW_K, d::COL_K, d::EPI_ACC>(pa, w.a[which], partials, s);
     }
     return st;
 }

@@ -26,7 +26,7 @@ def kernel_of(mangled):
     name = re.match(r"_ZN7gemm355\d[a-z]+?\d+([a-z_]+?_kernel)", mangled).group(1)
     if name == "norm_bwd_direct_kernel":     # the last argument: eights of columns of a lane, 0 for very wide rows
         return name, 256 if int(re.search(r"Li(\d+)EEEv", mangled).group(1)) else 1024
-    if name == "dense_small_kernel":
+    if name in ("dense_small_kernel", "dense_small_loss_kernel"):
         return name, 64 * int(re.search(r"Li(\d+)EEEv", mangled).group(1))
     return name, THREADS[name]
 
@@ -128,13 +128,16 @@ def run(shim, seed, count):
     assert rec.shim.recorder_take() > 100
     rec.lib.gemm355_force_layer_kernel(0)
     for _ in range(count):
+        rec.lib.gemm355_force_layer_kernel(0)
+        rec.entropy(log_size(rng, 1, 3000), log_size(rng, 1, 3000), log_size(rng, 8, 2048, 8), rng)
         rec.embedding(log_size(rng, 1, 100000), log_size(rng, 1, 300000), log_size(rng, 8, 16384, 8), rng)
         rec.norm(log_size(rng, 1, 20000), log_size(rng, 8, 40000, 8), rng)
         rec.lib.gemm355_force_layer_kernel(rng.choice([0, 0, 0, 1, 2, 3, 4, 5]))
         rec.entropy(log_size(rng, 1, 20000), log_size(rng, 1, 300000), log_size(rng, 8, 8192, 8), rng)
     rec.lib.gemm355_force_layer_kernel(0)
     for name, threads in [*THREADS.items(), ("norm_bwd_direct_kernel", 256), ("norm_bwd_direct_kernel", 1024),
-                          *[("dense_small_kernel", 64 * w) for w in (1, 2, 4, 8)]]:
+                          *[("dense_small_kernel", 64 * w) for w in (1, 2, 4, 8)], ("dense_small_loss_kernel", 256),
+                          ("dense_small_loss_kernel", 512)]:
         assert rec.seen.get((name, threads)), (name, threads, rec.seen)
     print("launches", sum(rec.seen.values()))
 
