@@ -27,10 +27,15 @@ enum Epilogue {
     EPI_POLY = 4,        // C = round(alpha acc + beta R + gamma [row == column]), symmetric likewise
     EPI_CE = 5,          // the loss over a vocabulary (dense_loss.hpp)
     EPI_CE_GRAD = 6,
-    EPI_ACC = 7
+    EPI_ACC = 7,
+    EPI_SCALE = 8        // EPI_STORE, times *scale
 };
 constexpr bool epi_symmetric(int epi) { return epi == EPI_STORE_SYM || epi == EPI_POLY; }
-constexpr bool epi_loss(int epi) { return epi >= EPI_CE; }
+constexpr bool epi_loss(int epi) { return epi >= EPI_CE && epi <= EPI_ACC; }
+// Products of the loss take sizes that only the device knows and an A whose rows lie
+// apart. The others' kernels have no code for that: a branch and a pitch more cost the
+// gradients of 4096 x 8192 x 4096 3 to 5 %.
+constexpr bool epi_sized(int epi) { return epi >= EPI_CE; }
 // Activations (the values of gemm355_activation).
 enum { A_NONE = 0, A_RELU = 1, A_GELU = 2, A_SILU = 3 };
 
@@ -51,13 +56,13 @@ struct DenseArgs {
     int grid;            // workgroups of a round
     float alpha, beta, gamma;
 
-    int lda;             // elements from one stored row of A to the next
+    int lda;             // epi_sized: elements from one stored row of A to the next
     // Sizes that only the device knows: *rows replaces M or, with rows_in_k, K. A
     // kernel that takes whole K steps has min_steps > 0: every split then gets at
     // least as many, and the operands have zeros behind their rows.
     const int *rows;
     int rows_in_k, min_steps;
-    const float *scale;  // EPI_STORE, EPI_ACC: factor of the result, or (EPI_STORE) NULL
+    const float *scale;  // EPI_SCALE, EPI_ACC: factor of the result
     // EPI_CE, EPI_CE_GRAD: B's rows are v0 .. v0 + N - 1 of the vocabulary
     const int *target;   // the rows' targets; NULL: ids, as the caller has them, of `vocab` ones
     const void *ids;
@@ -77,11 +82,19 @@ struct DenseArgs {
 
 __device__ inline int device_rows(const DenseArgs &p) { return __builtin_amdgcn_readfirstlane(*p.rows); }
 
+// Elements from one stored row of A to the next.
+template <int EPI, int LA>
+__device__ inline int pitch_a(const DenseArgs &p)
+{
+    return epi_sized(EPI) ? p.lda : LA == ROW_K ? p.K : p.M;
+}
+
 // Takes the sizes that only the device knows; `side`: rows of a tile. The split
 // tiles stay as many, or all that are left.
+template <int EPI>
 __device__ inline void take_rows(DenseArgs &p, int side)
 {
-    if (!p.rows)
+    if (!epi_sized(EPI) || !p.rows)
         return;
     const int n = device_rows(p);
     if (p.rows_in_k) {
@@ -453,7 +466,7 @@ __device__ inline void finish_row(const DenseArgs &p, f32x4 (&x)[BJ], int m, int
                 x[j + 1] += r1;
             }
     } else {
-        const float alpha = EPI == EPI_STORE && p.scale ? p.alpha * *p.scale : p.alpha;
+        const float alpha = EPI == EPI_SCALE ? p.alpha * *p.scale : p.alpha;
 #pragma unroll
         for (int j = 0; j < BJ; j += 2) {
             x[j] *= alpha;

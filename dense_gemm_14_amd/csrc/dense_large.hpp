@@ -124,7 +124,7 @@ void dense_large_kernel(DenseArgs p)
     constexpr int SIDE = 32 * BLOCKS, UNIT = big_unit(BLOCKS), COPIES = BLOCKS, COLS = big_columns(EPI, SIDE);
     __shared__ __attribute__((aligned(1024))) uint8_t lds[BIG_SLOTS * UNIT];
 
-    take_rows(p, SIDE);
+    take_rows<EPI>(p, SIDE);
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -134,9 +134,9 @@ void dense_large_kernel(DenseArgs p)
     const int nk = (p.K + BIG_BK - 1) / BIG_BK;
 
     const unsigned lds_base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
-    const unsigned a_step = LA == ROW_K ? BIG_BK * 2u : (unsigned)BIG_BK * (unsigned)p.lda * 2u;
+    const unsigned a_step = LA == ROW_K ? BIG_BK * 2u : (unsigned)BIG_BK * (unsigned)pitch_a<EPI, LA>(p) * 2u;
     const unsigned b_step = LB == ROW_K ? BIG_BK * 2u : (unsigned)BIG_BK * (unsigned)p.N * 2u;
-    const unsigned a_bytes = (unsigned)(LA == ROW_K ? p.M : p.K) * (unsigned)p.lda * 2u;
+    const unsigned a_bytes = (unsigned)(LA == ROW_K ? p.M : p.K) * (unsigned)pitch_a<EPI, LA>(p) * 2u;
     const unsigned b_bytes = (unsigned)p.N * (unsigned)p.K * 2u * (EPI == EPI_GATED ? 2u : 1u);
 
     // The workgroup's items: one per round.
@@ -182,7 +182,7 @@ void dense_large_kernel(DenseArgs p)
             } else {
                 const int k = 2 * block + (ln >> 5), pos = ln & 31;
                 const int c = (((pos >> 1) ^ key_col(k)) << 1) | (pos & 1);
-                const int col = min(row0 + 8 * c, (rows - 1) & ~7);
+                const int col = min(row0 + 8 * c, epi_sized(EPI) ? (rows - 1) & ~7 : rows - 8);
                 o[j] = ((unsigned)k * (unsigned)pitch + (unsigned)col) * 2u + BIG_SHIFT - 1024u * (j & 3);
             }
         }
@@ -193,7 +193,7 @@ void dense_large_kernel(DenseArgs p)
         dense_tile<EPI>(p, tile - b * p.tiles, tm, tn);
         ga = reinterpret_cast<unsigned long long>(p.a) + (unsigned long long)b * a_bytes - BIG_SHIFT;
         gb = reinterpret_cast<unsigned long long>(p.b) + (unsigned long long)b * b_bytes - BIG_SHIFT;
-        place_rows(Int<LA>{}, voff[0], tm * SIDE, p.M, p.lda, false);
+        place_rows(Int<LA>{}, voff[0], tm * SIDE, p.M, pitch_a<EPI, LA>(p), false);
         place_rows(Int<LB>{}, voff[1], tn * COLS, p.N, LB == ROW_K ? p.K : p.N, EPI == EPI_GATED);
     };
     place_copies(item.tile);
@@ -478,7 +478,7 @@ constexpr int BIG_REDUCE_WAVES = 4;
 template <int EPI, class TO>
 __global__ __launch_bounds__(64 * BIG_REDUCE_WAVES) void dense_large_reduce_kernel(DenseArgs p)
 {
-    take_rows(p, BIG);
+    take_rows<EPI>(p, BIG);
     const int lane = threadIdx.x & 63;
     const int unit = (int)blockIdx.x * BIG_REDUCE_WAVES + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int tail = p.tiles * p.batch - p.whole, t = unit >> 4;

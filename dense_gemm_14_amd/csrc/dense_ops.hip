@@ -119,8 +119,6 @@ int backward_small(DenseArgs pa, bool wants_a, DenseArgs pb, bool wants_b, const
     };
     place(pa, wants_a);
     place(pb, wants_b);
-    pa.lda = pa.K;
-    pb.lda = pb.M;
     g.a = pa;
     g.b = pb;
     g.bias = bias;

@@ -315,7 +315,7 @@ int product(DenseArgs p, const ProductPlan &plan, void *ws, hipStream_t stream)
 {
     p.supergroup = 8;
     p.ws = static_cast<float *>(ws);
-    if (p.lda == 0)
+    if (p.lda == 0)      // (the rows side by side)
         p.lda = LA == d::ROW_K ? p.K : p.M;
     if (plan.kernel >= KERNEL_SMALL)
         return product_small<T, LA, LB, EPI, TO>(p, plan.small, stream);

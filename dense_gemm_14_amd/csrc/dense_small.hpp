@@ -196,7 +196,7 @@ __device__ inline void finish8(const DenseArgs &p, float (&x)[8], float (&u)[8],
                 x[e] += b[e];
         }
     } else {
-        const float alpha = EPI == EPI_STORE && p.scale ? p.alpha * *p.scale : p.alpha;
+        const float alpha = EPI == EPI_SCALE ? p.alpha * *p.scale : p.alpha;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             x[e] *= alpha;
@@ -230,7 +230,7 @@ __device__ inline void small_tile(DenseArgs &p, int b, int tm, int tn, uint8_t *
     const unsigned ring = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + (unsigned)(wave * STAGES * STAGE);
     SmallOperand<T, LA, false, MB> oa;
     SmallOperand<T, LB, EPI == EPI_GATED, NB> ob;
-    oa.init(p.a, p.M, tm * 16 * MB, p.K, p.lda, 0, ring, lane);
+    oa.init(p.a, p.M, tm * 16 * MB, p.K, pitch_a<EPI, LA>(p), 0, ring, lane);
     ob.init(p.b, p.N, tn * small_columns(EPI, NB), p.K, LB == ROW_K ? p.K : p.N, p.N, ring + 2048 * MB, lane);
 
     const int nk = (p.K + SMALL_BK - 1) / SMALL_BK;
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void dense_small_kernel(DenseArgs p)
     static_assert(small_lds(MB, NB, WAVES) * (8 / WAVES) <= 163840, "8 / WAVES workgroups share a compute unit's LDS");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[small_lds(MB, NB, WAVES)];
     fetch_args(p);
-    take_rows(p, 16 * MB);
+    take_rows<EPI>(p, 16 * MB);
     const int item = small_item(p.tiles * p.batch);
     if (item < 0)
         return;
@@ -429,15 +429,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void dense_small_loss_kernel(SmallLo
     const int item = (int)blockIdx.x - ahead;
     int tm, tn;
     if (item >= 0 && item < p.tiles_a) {
-        take_rows(p.a, 16 * BLOCKS);
+        take_rows<EPI_ACC>(p.a, 16 * BLOCKS);
         if (item >= p.a.tiles)
             return;
         dense_tile<EPI_ACC>(p.a, item, tm, tn);
         small_tile<__bf16, ROW_K, COL_K, EPI_ACC, __bf16, BLOCKS, BLOCKS, WAVES>(p.a, 0, tm, tn, lds);
     } else {
-        take_rows(p.b, 16 * BLOCKS);
-        dense_tile<EPI_STORE>(p.b, item < 0 ? item + ahead : item - p.tiles_a, tm, tn);
-        small_tile<__bf16, COL_K, COL_K, EPI_STORE, __bf16, BLOCKS, BLOCKS, WAVES>(p.b, 0, tm, tn, lds);
+        take_rows<EPI_SCALE>(p.b, 16 * BLOCKS);
+        dense_tile<EPI_SCALE>(p.b, item < 0 ? item + ahead : item - p.tiles_a, tm, tn);
+        small_tile<__bf16, COL_K, COL_K, EPI_SCALE, __bf16, BLOCKS, BLOCKS, WAVES>(p.b, 0, tm, tn, lds);
     }
 }
 

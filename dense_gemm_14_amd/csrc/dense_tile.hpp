@@ -189,7 +189,7 @@ void dense_tile_kernel(DenseArgs p)
     const int wn = (wave >> 1) & 1;  // 64-column half
 
     fetch_args(p);
-    take_rows(p, TILE);
+    take_rows<EPI>(p, TILE);
     const int item = tile_item(p);
     if (item < 0)
         return;
@@ -204,7 +204,7 @@ void dense_tile_kernel(DenseArgs p)
     const unsigned lds_base = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
     TileOperand<T, LA, false> oa;
     TileOperand<T, LB, EPI == EPI_GATED> ob;
-    oa.init(p.a, p.M, tm * TILE, p.K, p.lda, 0, lds_base, wave, lane, wm, kh);
+    oa.init(p.a, p.M, tm * TILE, p.K, pitch_a<EPI, LA>(p), 0, lds_base, wave, lane, wm, kh);
     ob.init(p.b, p.N, tn * tile_columns(EPI), p.K, LB == ROW_K ? p.K : p.N, p.N, lds_base + TILE_STAGES * TILE_UNIT, wave, lane, wn, kh);
 
     const int nk = (p.K + TILE_BK - 1) / TILE_BK;
@@ -308,7 +308,7 @@ constexpr int REDUCE_WAVES = 4;
 template <int EPI, class TO>
 __global__ __launch_bounds__(64 * REDUCE_WAVES) void dense_reduce_kernel(DenseArgs p)
 {
-    take_rows(p, TILE);
+    take_rows<EPI>(p, TILE);
     const int lane = threadIdx.x & 63;
     const int unit = (int)blockIdx.x * REDUCE_WAVES + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int tail = p.tiles * p.batch - p.whole, q = unit >> 3;

@@ -445,7 +445,7 @@ extern "C" int gemm_bf16_nt_cross_entropy_bwd(int M, int V, int K, const void *A
             continue;
         }
         if (wants_b && st == GEMM355_OK)
-            st = product<__bf16, d::COL_K, d::COL_K, d::EPI_STORE>(pb, w.b[which], partials, s);
+            st = product<__bf16, d::COL_K, d::COL_K, d::EPI_SCALE>(pb, w.b[which], partials, s);
         if (wants_a && st == GEMM355_OK)
             st = product<__bf16, d::ROW_K, d::COL_K, d::EPI_ACC>(pa, w.a[which], partials, s);
     }
