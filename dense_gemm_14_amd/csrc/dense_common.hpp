@@ -89,11 +89,14 @@ __device__ inline int pitch_a(const DenseArgs &p)
     return epi_sized(EPI) ? p.lda : LA == ROW_K ? p.K : p.M;
 }
 
-// Takes the sizes that only the device knows; `side`: rows of a tile. The split
-// tiles stay as many, or all that are left.
+// Takes the numbers that only the device knows; `side`: rows of a tile. The split
+// tiles stay as many, or all that are left. (The factor once, here: read again for
+// every row of blocks, as the stores between them demand, it took 5 us a tile.)
 template <int EPI>
 __device__ inline void take_rows(DenseArgs &p, int side)
 {
+    if constexpr (EPI == EPI_SCALE || EPI == EPI_ACC)
+        p.alpha = *p.scale;
     if (!epi_sized(EPI) || !p.rows)
         return;
     const int n = device_rows(p);
@@ -466,11 +469,10 @@ __device__ inline void finish_row(const DenseArgs &p, f32x4 (&x)[BJ], int m, int
                 x[j + 1] += r1;
             }
     } else {
-        const float alpha = EPI == EPI_SCALE ? p.alpha * *p.scale : p.alpha;
 #pragma unroll
         for (int j = 0; j < BJ; j += 2) {
-            x[j] *= alpha;
-            x[j + 1] *= alpha;
+            x[j] *= p.alpha;
+            x[j + 1] *= p.alpha;
             if constexpr (EPI == EPI_POLY) {
                 f32x4 r0, r1;
                 unpack_pair<TO>(res[j / 2], r0, r1);

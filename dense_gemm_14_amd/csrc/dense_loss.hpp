@@ -218,10 +218,9 @@ __device__ inline void loss_row(const DenseArgs &p, const __amdgpu_buffer_rsrc_t
             if constexpr (MODE & LOSS_ADD)
                 x[j] += add[j];
         if constexpr (MODE & LOSS_LAST) {
-            const float scale = *p.scale;
 #pragma unroll
             for (int j = 0; j < BJ; j += 2) {
-                const u32x4 w = pack_pair<__bf16>(x[j] * scale, x[j + 1] * scale);
+                const u32x4 w = pack_pair<__bf16>(x[j] * p.alpha, x[j + 1] * p.alpha);
                 const int n = col + 16 * j + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
                 store16(w, rc, m < p.M && n < p.N ? (int)(((unsigned)row.at * (unsigned)p.N + (unsigned)n) * 2u) : OOB);
             }
@@ -338,7 +337,7 @@ __device__ inline void loss_eight(const DenseArgs &p, float (&x)[8], int m, int 
                     x[4 + e] += r.add[1][e];
                 }
             if (p.last) {
-                const float scale = *p.scale;
+                const float scale = p.alpha;
                 *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + (size_t)r.row.at * (size_t)p.N + (size_t)n) =
                     u32x4{pack_bf16(x[0] * scale, x[1] * scale), pack_bf16(x[2] * scale, x[3] * scale),
                           pack_bf16(x[4] * scale, x[5] * scale), pack_bf16(x[6] * scale, x[7] * scale)};

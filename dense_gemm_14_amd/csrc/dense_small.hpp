@@ -196,10 +196,9 @@ __device__ inline void finish8(const DenseArgs &p, float (&x)[8], float (&u)[8],
                 x[e] += b[e];
         }
     } else {
-        const float alpha = EPI == EPI_SCALE ? p.alpha * *p.scale : p.alpha;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            x[e] *= alpha;
+            x[e] *= p.alpha;
         if constexpr (EPI == EPI_POLY) {
             float r[8];
             unpack_eight<TO>(*at16(p.r, at), r);
