@@ -8,8 +8,9 @@
 //
 // Bound by memory, so one pass over it: a row is held in registers between its sums
 // and its results, by one wave (up to 4096 columns, where there are rows for every
-// wave of the card) or four (up to 16384); wider rows are read again, by then from the
-// caches. Measured, BF16: 8192 x 4096 in 24.2 us, 5.5 TB/s, its gradients with a
+// wave of the card) or four (up to 16384), by 8, 16 or 32 lanes up to 64, 128 or 256
+// columns (heads: 262144 x 128 BF16 22.5 us, 64.5 with a wave for a row; gradients 36
+// and 105); wider rows are read again, by then from the caches. Measured, BF16: 8192 x 4096 in 24.2 us, 5.5 TB/s, its gradients with a
 // residual's in 57.5, 4.7 TB/s, of which 8 the second launch; one row of 4096 2.4 us
 // on the card, 4.9 with its call. The variance is that of the
 // differences from the mean, not of the squares, so no large mean cancels in
@@ -45,34 +46,51 @@ __device__ inline Moments join(const Moments &a, const Moments &b)
     return Moments{n, a.mean + d * part, a.m2 + b.m2 + d * d * a.n * part};
 }
 
-// A row in the registers of WAVES waves: lane `i` of them holds the eight
-// columns 8 (i + 64 WAVES v), v < VPT.
-template <int WAVES>
+// A row in the registers of LANES lanes, of which there are 8, 16 or 32 (a wave
+// then has several rows), a wave's or several waves': lane `i` of them holds the
+// eight columns 8 (i + LANES v), v < VPT.
+template <int LANES>
 __device__ inline int norm_col(int i, int v)
 {
-    return 8 * (i + 64 * WAVES * v);
+    return 8 * (i + LANES * v);
+}
+// Sum over a row's lanes of this wave, the same in each of them. (Fewer than 64:
+// each step adds what the lanes at the other end of a pair, four, eight and sixteen hold.)
+template <int LANES>
+__device__ inline float lanes_sum(float x)
+{
+    if constexpr (LANES >= 64)
+        return wave_sum(x);
+    x += dpp_or_zero<0xB1, 0xF>(x);    // lanes 1 0 3 2 of four
+    x += dpp_or_zero<0x4E, 0xF>(x);    // 2 3 0 1
+    x += dpp_or_zero<0x141, 0xF>(x);   // eight, mirrored
+    if constexpr (LANES > 8)
+        x += dpp_or_zero<0x140, 0xF>(x);   // sixteen, mirrored
+    if constexpr (LANES > 16)
+        x += __shfl_xor(x, 16);
+    return x;
 }
 
-template <class X, class W, int WAVES, int VPT>
+template <class X, class W, int LANES, int VPT>
 __global__ __launch_bounds__(NORM_THREADS) void norm_kernel(NormArgs p)
 {
-    constexpr int GROUPS = NORM_THREADS / 64 / WAVES;   // rows at a time
+    constexpr int GROUPS = NORM_THREADS / LANES, WAVES = (LANES + 63) / 64;   // rows at a time; waves of one
     __shared__ Moments part[2][4];
-    const int group = (int)threadIdx.x / (64 * WAVES), lane = (int)threadIdx.x % (64 * WAVES);
+    const int group = (int)threadIdx.x / LANES, lane = (int)threadIdx.x % LANES;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const float n = (float)p.cols;
     Raw8<W> gamma[VPT], beta[VPT];
     float own = 0.0f;     // columns of this wave
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        const int c = norm_col<WAVES>(lane, v);
+        const int c = norm_col<LANES>(lane, v);
         gamma[v].fill(1.0f);
         beta[v].fill(0.0f);
         if (c < p.cols && p.gamma)
             gamma[v].load(p.gamma, c);
         if (c < p.cols && p.beta)
             beta[v].load(p.beta, c);
-        own += (float)min(512, max(0, p.cols - norm_col<WAVES>(lane & ~63, v)));
+        own += (float)min(8 * min(LANES, 64), max(0, p.cols - norm_col<LANES>(lane & ~63, v)));
     }
     int turn = 0;
     for (int64_t row = (int64_t)blockIdx.x * GROUPS + group; row - group < p.rows; row += (int64_t)gridDim.x * GROUPS) {
@@ -82,7 +100,7 @@ __global__ __launch_bounds__(NORM_THREADS) void norm_kernel(NormArgs p)
         float s = 0.0f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int c = norm_col<WAVES>(lane, v);
+            const int c = norm_col<LANES>(lane, v);
             x[v].fill(0.0f);
             if (in && c < p.cols)
                 x[v].load(p.x, base + c);
@@ -92,17 +110,17 @@ __global__ __launch_bounds__(NORM_THREADS) void norm_kernel(NormArgs p)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 s += x[v].get(e);
-        Moments m = {own, own > 0.0f ? wave_sum(s) / own : 0.0f, 0.0f};
+        Moments m = {own, own > 0.0f ? lanes_sum<LANES>(s) / own : 0.0f, 0.0f};
         s = 0.0f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
-            if (norm_col<WAVES>(lane, v) < p.cols)
+            if (norm_col<LANES>(lane, v) < p.cols)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float d = x[v].get(e) - m.mean;
                     s += d * d;
                 }
-        m.m2 = wave_sum(s);
+        m.m2 = lanes_sum<LANES>(s);
         if constexpr (WAVES > 1) {
             // (two sets in turn: a wave may be a row ahead of one that still reads)
             if ((threadIdx.x & 63) == 0)
@@ -122,7 +140,7 @@ __global__ __launch_bounds__(NORM_THREADS) void norm_kernel(NormArgs p)
         }
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int c = norm_col<WAVES>(lane, v);
+            const int c = norm_col<LANES>(lane, v);
             if (c < p.cols) {
                 float y[8];
 #pragma unroll
@@ -227,9 +245,9 @@ struct NormBwdArgs {
     bool wants_columns;             // dgamma or dbeta
 };
 
-// One row of dX by 64 WAVES lanes that hold it, and (COLUMNS) its terms added
+// One row of dX by the LANES lanes that hold it, and (COLUMNS) its terms added
 // to their columns' sums; exchange(a, b) joins the two sums of the lanes.
-template <class X, class W, int WAVES, int VPT, bool COLUMNS, class Exchange>
+template <class X, class W, int LANES, int VPT, bool COLUMNS, class Exchange>
 __device__ inline void norm_bwd_row(const NormBwdArgs &p, int64_t row, bool in, int lane, Raw8<W> (&gamma)[VPT],
                                     float (&dg)[COLUMNS ? VPT : 1][8], float (&db)[COLUMNS ? VPT : 1][8],
                                     Exchange &&exchange)
@@ -244,7 +262,7 @@ __device__ inline void norm_bwd_row(const NormBwdArgs &p, int64_t row, bool in, 
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        const int c = norm_col<WAVES>(lane, v);
+        const int c = norm_col<LANES>(lane, v);
         x[v].fill(0.0f);
         dy[v].fill(0.0f);
         if (in && c < p.cols) {
@@ -284,7 +302,7 @@ __device__ inline void norm_bwd_row(const NormBwdArgs &p, int64_t row, bool in, 
     su /= (float)p.cols;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        const int c = norm_col<WAVES>(lane, v);
+        const int c = norm_col<LANES>(lane, v);
         if (c < p.cols) {
             Raw8<X> r;
             r.fill(0.0f);
@@ -303,23 +321,24 @@ __device__ inline void norm_bwd_row(const NormBwdArgs &p, int64_t row, bool in, 
     }
 }
 
-template <class W, int WAVES, int VPT>
+template <class W, int LANES, int VPT>
 __device__ inline void norm_gamma(const NormBwdArgs &p, int lane, Raw8<W> (&gamma)[VPT])
 {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         gamma[v].fill(1.0f);
-        if (norm_col<WAVES>(lane, v) < p.cols && p.gamma)
-            gamma[v].load(p.gamma, norm_col<WAVES>(lane, v));
+        if (norm_col<LANES>(lane, v) < p.cols && p.gamma)
+            gamma[v].load(p.gamma, norm_col<LANES>(lane, v));
     }
 }
 
-// Joins the sums of the WAVES waves that hold a row (two sets in turn, as above).
-template <int WAVES>
+// Joins the sums of the lanes that hold a row (two sets in turn, as above).
+template <int LANES>
 __device__ inline void norm_exchange(float &a, float &b, f32x2 *part, int &turn, int wave)
 {
-    a = wave_sum(a);
-    b = wave_sum(b);
+    constexpr int WAVES = LANES / 64;
+    a = lanes_sum<LANES>(a);
+    b = lanes_sum<LANES>(b);
     if constexpr (WAVES > 1) {
         f32x2 *mine = part + (wave / WAVES * 2 + turn) * WAVES;
         if ((threadIdx.x & 63) == 0)
@@ -335,28 +354,28 @@ __device__ inline void norm_exchange(float &a, float &b, f32x2 *part, int &turn,
     }
 }
 
-// Many rows: a workgroup walks rows (sixteen waves: sixteen rows down to one at a
-// time), its lanes keep the sums of their columns, the workgroup's rows are joined
+// Many rows: a workgroup walks rows (sixteen waves: 128 rows of up to
+// 64 columns down to one at a time), its lanes keep the sums of their columns, the workgroup's rows are joined
 // through LDS and leave one row of column sums each for dgamma and dbeta. One
 // workgroup per unit, so that those rows are few; sixteen waves, each with so few
 // columns that 128 registers hold them, so that loads are always in flight (8192 x
 // 4096: 57.5 us; with eight waves and up to 256 registers 67).
 constexpr int NORM_BWD_THREADS = 1024;
-template <class X, class W, int WAVES, int VPT>
+template <class X, class W, int LANES, int VPT>
 __global__ __launch_bounds__(NORM_BWD_THREADS) void norm_bwd_kernel(NormBwdArgs p)
 {
-    constexpr int GROUPS = NORM_BWD_THREADS / 64 / WAVES;
+    constexpr int GROUPS = NORM_BWD_THREADS / LANES;
     __shared__ f32x2 part[2 * NORM_BWD_THREADS / 64];
-    __shared__ float join[GROUPS][64 * WAVES * 16];
-    const int group = (int)threadIdx.x / (64 * WAVES), lane = (int)threadIdx.x % (64 * WAVES);
+    __shared__ float join[GROUPS][LANES * 16];
+    const int group = (int)threadIdx.x / LANES, lane = (int)threadIdx.x % LANES;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     Raw8<W> gamma[VPT];
-    norm_gamma<W, WAVES, VPT>(p, lane, gamma);
+    norm_gamma<W, LANES, VPT>(p, lane, gamma);
     float dg[VPT][8] = {}, db[VPT][8] = {};
     int turn = 0;
     for (int64_t row = (int64_t)blockIdx.x * GROUPS + group; row - group < p.rows; row += (int64_t)p.blocks * GROUPS)
-        norm_bwd_row<X, W, WAVES, VPT, true>(p, row, row < p.rows, lane, gamma, dg, db,
-                                             [&](float &a, float &b) { norm_exchange<WAVES>(a, b, part, turn, wave); });
+        norm_bwd_row<X, W, LANES, VPT, true>(p, row, row < p.rows, lane, gamma, dg, db,
+                                             [&](float &a, float &b) { norm_exchange<LANES>(a, b, part, turn, wave); });
     if (!p.wants_columns)
         return;
     float *out = p.sums + (size_t)blockIdx.x * 2 * (size_t)p.cols;
@@ -366,17 +385,17 @@ __global__ __launch_bounds__(NORM_BWD_THREADS) void norm_bwd_kernel(NormBwdArgs 
         // [which][element][lane]: neighbouring lanes, neighbouring banks
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            join[group][e * 64 * WAVES + lane] = dg[v][e];
-            join[group][(8 + e) * 64 * WAVES + lane] = db[v][e];
+            join[group][e * LANES + lane] = dg[v][e];
+            join[group][(8 + e) * LANES + lane] = db[v][e];
         }
         __syncthreads();
-        for (int i = (int)threadIdx.x; i < 16 * 64 * WAVES; i += NORM_BWD_THREADS) {
+        for (int i = (int)threadIdx.x; i < 16 * LANES; i += NORM_BWD_THREADS) {
             float t = 0.0f;
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
                 t += join[g][i];
-            const int which = i / (8 * 64 * WAVES), e = i / (64 * WAVES) & 7, l = i % (64 * WAVES);
-            const int c = norm_col<WAVES>(l, v) + e;
+            const int which = i / (8 * LANES), e = i / LANES & 7, l = i % LANES;
+            const int c = norm_col<LANES>(l, v) + e;
             if (c < p.cols)
                 out[(size_t)which * p.cols + c] = t;
         }
@@ -477,13 +496,13 @@ __global__ __launch_bounds__(norm_direct_threads<VPT>()) void norm_bwd_direct_ke
     if constexpr (VPT > 0) {
         const int lane = (int)threadIdx.x, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         Raw8<W> gamma[VPT];
-        norm_gamma<W, 4, VPT>(p, lane, gamma);
+        norm_gamma<W, 256, VPT>(p, lane, gamma);
         f32x2 *xch = reinterpret_cast<f32x2 *>(part);
         int turn = 0;
         float none[1][8];
         for (int64_t row = blockIdx.x; row < p.rows; row += p.blocks)
-            norm_bwd_row<X, W, 4, VPT, false>(p, row, true, lane, gamma, none, none,
-                                              [&](float &a, float &b) { norm_exchange<4>(a, b, xch, turn, wave); });
+            norm_bwd_row<X, W, 256, VPT, false>(p, row, true, lane, gamma, none, none,
+                                              [&](float &a, float &b) { norm_exchange<256>(a, b, xch, turn, wave); });
     } else {
         float *sums = &part[0][0][0];
         for (int64_t row = blockIdx.x; row < p.rows; row += p.blocks) {

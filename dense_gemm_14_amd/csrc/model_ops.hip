@@ -97,7 +97,21 @@ EmbedBwdPlan plan_embed_bwd(int tokens, int vocab, int cols, int cus)
 
 // ---- layer norm --------------------------------------------------------------
 
-// The kernel that holds rows of `cols` columns: f(Int<waves>{}, Int<eights of
+// f(Int<lanes>{}, Int<1>{}) with the lanes, a wave's at most, that hold rows of up
+// to 512 columns.
+template <class F>
+int with_lanes(int cols, F &&f)
+{
+    if (cols <= 64)
+        return f(Int<8>{}, Int<1>{});
+    if (cols <= 128)
+        return f(Int<16>{}, Int<1>{});
+    if (cols <= 256)
+        return f(Int<32>{}, Int<1>{});
+    return f(Int<64>{}, Int<1>{});
+}
+
+// The kernel that holds rows of `cols` columns: f(Int<lanes>{}, Int<eights of
 // columns per lane>{}), or f(Int<0>{}, Int<0>{}) for wider rows, which are read
 // again. A wave holds up to 4096 columns where there are rows for every wave of
 // the card, four waves otherwise.
@@ -106,23 +120,23 @@ int with_rows(int cols, bool many, F &&f)
 {
     const int64_t per_wave = ceil_div(cols, 512), per_four = ceil_div(cols, 2048);
     if (per_wave <= 1)
-        return f(Int<1>{}, Int<1>{});
+        return with_lanes(cols, f);
     if (many) {
         if (per_wave <= 2)
-            return f(Int<1>{}, Int<2>{});
+            return f(Int<64>{}, Int<2>{});
         if (per_wave <= 4)
-            return f(Int<1>{}, Int<4>{});
+            return f(Int<64>{}, Int<4>{});
         if (per_wave <= 8)
-            return f(Int<1>{}, Int<8>{});
+            return f(Int<64>{}, Int<8>{});
     }
     if (per_four <= 1)
-        return f(Int<4>{}, Int<1>{});
+        return f(Int<256>{}, Int<1>{});
     if (per_four <= 2)
-        return f(Int<4>{}, Int<2>{});
+        return f(Int<256>{}, Int<2>{});
     if (per_four <= 4)
-        return f(Int<4>{}, Int<4>{});
+        return f(Int<256>{}, Int<4>{});
     if (per_four <= 8)
-        return f(Int<4>{}, Int<8>{});
+        return f(Int<256>{}, Int<8>{});
     return f(Int<0>{}, Int<0>{});
 }
 
@@ -134,30 +148,30 @@ int with_rows(int cols, bool many, F &&f)
 // and 19.6, 4000 x 8192 FP32 146 and 96, 2000 x 16384 77 and 76.
 bool norm_direct(int rows, int cols, bool fp32) { return rows <= 800 || cols > (fp32 ? 8192 : 16384); }
 
-// Waves that hold a row where there are many, and the workgroups that walk them. A
-// lane holds eight columns of FP32 rows, sixteen of BF16 ones.
-int norm_bwd_waves(int cols, bool fp32)
+// Lanes that hold a row where there are many, and the workgroups that walk them. A
+// lane holds eight columns of FP32 rows and of short ones, sixteen of others.
+int norm_bwd_lanes(int cols, bool fp32)
 {
-    const int64_t waves = fp32 ? ceil_div(cols, 512) : cols <= 512 ? 1 : ceil_div(cols, 1024);
-    return 1 << ceil_log2(waves);
+    const int64_t lanes = ceil_div(cols, fp32 || cols <= 512 ? 8 : 16);
+    return std::max(8, 1 << ceil_log2(lanes));
 }
 int norm_bwd_blocks(int rows, int cols, bool fp32, int cus)
 {
-    return (int)std::min<int64_t>(cus, ceil_div(rows, r::NORM_BWD_THREADS / 64 / norm_bwd_waves(cols, fp32)));
+    return (int)std::min<int64_t>(cus, ceil_div(rows, r::NORM_BWD_THREADS / norm_bwd_lanes(cols, fp32)));
 }
 template <class X, class F>
 int with_bwd_rows(int cols, F &&f)
 {
     constexpr bool FP32 = sizeof(X) == 4;
     typedef Int<FP32 ? 1 : 2> Vpt;
-    if (!FP32 && cols <= 512)
-        return f(Int<1>{}, Int<1>{});
-    switch (norm_bwd_waves(cols, FP32)) {
-    case 1: return f(Int<1>{}, Vpt{});
-    case 2: return f(Int<2>{}, Vpt{});
-    case 4: return f(Int<4>{}, Vpt{});
-    case 8: return f(Int<8>{}, Vpt{});
-    default: return f(Int<16>{}, Vpt{});
+    if (cols <= 512)
+        return with_lanes(cols, f);
+    switch (norm_bwd_lanes(cols, FP32)) {
+    case 64: return f(Int<64>{}, Vpt{});
+    case 128: return f(Int<128>{}, Vpt{});
+    case 256: return f(Int<256>{}, Vpt{});
+    case 512: return f(Int<512>{}, Vpt{});
+    default: return f(Int<1024>{}, Vpt{});
     }
 }
 
@@ -336,15 +350,15 @@ extern "C" int gemm355_layer_norm(int rows, int cols, int x_type, const void *X,
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return with_type(x_type, [&](auto tx) {
         return with_type(w_type, [&](auto tw) {
-            return with_rows(cols, rows >= 4 * cus, [&](auto waves_c, auto vpt_c) {
-                constexpr int WAVES = decltype(waves_c)::value, VPT = decltype(vpt_c)::value;
-                if constexpr (WAVES == 0) {
+            return with_rows(cols, rows >= 4 * cus, [&](auto lanes_c, auto vpt_c) {
+                constexpr int LANES = decltype(lanes_c)::value, VPT = decltype(vpt_c)::value;
+                if constexpr (LANES == 0) {
                     return launch_kernel(r::norm_wide_kernel<decltype(tx), decltype(tw)>,
                                          (unsigned)std::min<int64_t>(rows, 2 * int64_t(cus)),
                                          (unsigned)r::NORM_WIDE_THREADS, p, s);
                 } else {
-                    return launch_kernel(r::norm_kernel<decltype(tx), decltype(tw), WAVES, VPT>,
-                                         (unsigned)std::min<int64_t>(ceil_div(int64_t(rows) * WAVES, 4), 8 * int64_t(cus)),
+                    return launch_kernel(r::norm_kernel<decltype(tx), decltype(tw), LANES, VPT>,
+                                         (unsigned)std::min<int64_t>(ceil_div(int64_t(rows) * LANES, r::NORM_THREADS), 8 * int64_t(cus)),
                                          (unsigned)r::NORM_THREADS, p, s);
                 }
             });
@@ -421,8 +435,8 @@ extern "C" int gemm355_layer_norm_bwd(int rows, int cols, int x_type, const void
     return with_type(x_type, [&](auto tx) {
         return with_type(w_type, [&](auto tw) {
             typedef decltype(tw) TW;
-            const int st = with_bwd_rows<decltype(tx)>(cols, [&](auto waves_c, auto vpt_c) {
-                return launch_kernel(r::norm_bwd_kernel<decltype(tx), TW, decltype(waves_c)::value, decltype(vpt_c)::value>,
+            const int st = with_bwd_rows<decltype(tx)>(cols, [&](auto lanes_c, auto vpt_c) {
+                return launch_kernel(r::norm_bwd_kernel<decltype(tx), TW, decltype(lanes_c)::value, decltype(vpt_c)::value>,
                                      (unsigned)p.blocks, (unsigned)r::NORM_BWD_THREADS, p, s);
             });
             if (st != GEMM355_OK || !wants_columns)

@@ -15,6 +15,7 @@ TYPES = [(BF16, BF16), (FP32, FP32), (FP32, BF16), (BF16, FP32)]
 SIZES = [(1, 8), (1, 64), (3, 72), (2, 512), (5, 520), (1, 1000), (1, 4096), (7, 1032), (9, 2056), (3, 5000), (2, 8200),
          (3, 16384), (2, 16392), (2, 32776), (1030, 8), (1111, 72), (1025, 520), (1100, 1544), (1030, 4096), (300, 2048),
          (261, 5000), (270, 8200), (259, 16384),
+         (1, 136), (5, 256), (2003, 64), (9000, 128), (4099, 136), (1037, 256), (1029, 264), (805, 136),
          (800, 1000), (801, 8), (801, 1000), (820, 3000), (900, 5000), (801, 8192), (803, 8200), (805, 16384)]
 
 
@@ -134,7 +135,7 @@ def test_rows_that_are_hard(cols):
     check(run(X[[0, 3, 5]], None, None, 0.0), norm(X[[0, 3, 5]], None, None, 0.0))
 
 
-@pytest.mark.parametrize("rows,cols", [(9, 72), (1100, 520), (6, 5000), (3, 16392)])
+@pytest.mark.parametrize("rows,cols", [(9, 72), (1100, 64), (900, 136), (1100, 520), (6, 5000), (3, 16392)])
 def test_infinities_stay_in_their_row(rows, cols):
     need_gpu()
     X, gamma, beta, gen = inputs(rows, cols, BF16, BF16)
