@@ -13,6 +13,7 @@
 //     token against the 8 KiB of its row of dY) and so knows by itself how many
 //     come before its range: no workgroup waits for another, and no pass over
 //     digits is needed. Its sixteen waves each count, then place, a run of tokens.
+//     (From about 100000 tokens on they are dealt out to buckets of ids first.)
 //   * sums: the sorted tokens are cut into blocks of a few. A wave takes a block
 //     and 512 columns and adds the rows of every id whose tokens begin in its
 //     block, to their end; an id with many tokens is instead cut at the blocks'
@@ -103,6 +104,12 @@ struct EmbedBwdArgs {
     int sum_waves;         // workgroups' waves that add; the rest of the launch fills
     float scale;
     bool wide;
+    // many tokens, ordered by bucket (id >> shift) first
+    int *counts;           // [chunks][buckets] tokens of a chunk; then of the chunks before
+    int *total;            // [buckets]
+    int *bucket_start;     // [buckets + 1]; where a bucket is one id, `start`
+    int2 *bucketed;        // [tokens] {id, token} by bucket; where a bucket is one id, `sorted`
+    int shift, buckets, chunks;
 };
 
 // This lane's eight columns at c of the rows v0 + i, i in `rows`, that no token
@@ -169,10 +176,23 @@ __device__ inline void embed_fill_all(const EmbedBwdArgs &p, int64_t thread, int
 constexpr int ORDER_THREADS = 1024, ORDER_WAVES = ORDER_THREADS / 64;
 constexpr int ORDER_MAX_RANGE = 512, ORDER_AHEAD = 8;
 
+// The workgroups past a launch's first `first` fill all rows; whether this is one.
+template <class TE>
+__device__ inline bool embed_fills(const EmbedBwdArgs &p, int first)
+{
+    if ((int)blockIdx.x < first)
+        return false;
+    if (threadIdx.x < FILL_THREADS)
+        embed_fill_all<TE>(p, ((int64_t)blockIdx.x - first) * FILL_THREADS + threadIdx.x,
+                           ((int64_t)gridDim.x - first) * FILL_THREADS);
+    return true;
+}
+
 // Workgroups from p.order_groups on fill every row, for the sums to write those
 // again that have tokens: where those are few, the ordering then costs no time of
-// its own (16384 tokens of 128000 ids: 250 us, 219 so).
-template <class TE>
+// its own (16384 tokens of 128000 ids: 250 us, 219 so). BUCKETED: a workgroup's range
+// is a bucket, whose tokens are listed already, and none fills.
+template <class TE, bool BUCKETED>
 __global__ __launch_bounds__(ORDER_THREADS) void embed_order_kernel(EmbedBwdArgs p)
 {
     // [wave][id of the range]: first its tokens, then where the next one goes
@@ -180,28 +200,38 @@ __global__ __launch_bounds__(ORDER_THREADS) void embed_order_kernel(EmbedBwdArgs
     __shared__ int before[ORDER_WAVES], total[ORDER_WAVES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    if ((int)blockIdx.x >= p.order_groups) {
-        if (threadIdx.x < FILL_THREADS)
-            embed_fill_all<TE>(p, ((int64_t)blockIdx.x - p.order_groups) * FILL_THREADS + threadIdx.x,
-                               ((int64_t)gridDim.x - p.order_groups) * FILL_THREADS);
+    if (!BUCKETED && embed_fills<TE>(p, p.order_groups))
         return;
-    }
     const int v0 = (int)blockIdx.x * p.range, range = min(p.range, p.vocab - v0);
     for (int i = threadIdx.x; i < ORDER_MAX_RANGE * ORDER_WAVES; i += ORDER_THREADS)
         (&count[0][0])[i] = 0;
     __syncthreads();
 
     // this wave's run of tokens, whole groups of 64
-    const int64_t run = ((int64_t)p.tokens + ORDER_THREADS - 1) / ORDER_THREADS * 64;
-    const int64_t first = wave * run, last = min((int64_t)p.tokens, first + run);
+    const int64_t from = BUCKETED ? p.bucket_start[blockIdx.x] : 0, to = BUCKETED ? p.bucket_start[blockIdx.x + 1] : p.tokens;
+    const int64_t run = (to - from + ORDER_THREADS - 1) / ORDER_THREADS * 64;
+    const int64_t first = from + wave * run, last = min(to, first + run);
     // (loads of eight groups at a time: one after the other they took the time)
     auto each_group = [&](auto &&f) {
         for (int64_t t0 = first; t0 < last; t0 += 64 * ORDER_AHEAD) {
-            int id[ORDER_AHEAD];
-            ids_at<ORDER_AHEAD>(p.ids, p.wide, t0 + lane, 64, last, p.vocab, id);
+            int id[ORDER_AHEAD], token[ORDER_AHEAD];
+            if constexpr (BUCKETED) {
+#pragma unroll
+                for (int k = 0; k < ORDER_AHEAD; ++k) {
+                    const int64_t i = t0 + 64 * k + lane;
+                    const int2 x = i < last ? p.bucketed[i] : make_int2(-1, 0);
+                    id[k] = x.x;
+                    token[k] = x.y;
+                }
+            } else {
+                ids_at<ORDER_AHEAD>(p.ids, p.wide, t0 + lane, 64, last, p.vocab, id);
+#pragma unroll
+                for (int k = 0; k < ORDER_AHEAD; ++k)
+                    token[k] = (int)(t0 + 64 * k) + lane;
+            }
 #pragma unroll
             for (int k = 0; k < ORDER_AHEAD; ++k)
-                f((int)(t0 + 64 * k) + lane, id[k]);
+                f(token[k], id[k]);
         }
     };
     int less = 0;
@@ -218,10 +248,11 @@ __global__ __launch_bounds__(ORDER_THREADS) void embed_order_kernel(EmbedBwdArgs
     __syncthreads();
 
     // prefix sums over the range's ids and, within an id, over the waves
-    int base = 0;
+    int base = BUCKETED ? (int)from : 0;
+    if constexpr (!BUCKETED)
 #pragma unroll
-    for (int w = 0; w < ORDER_WAVES; ++w)
-        base += before[w];
+        for (int w = 0; w < ORDER_WAVES; ++w)
+            base += before[w];
     for (int i0 = 0; i0 < range; i0 += ORDER_THREADS) {
         const int i = i0 + (int)threadIdx.x;
         int mine = 0;
@@ -274,6 +305,154 @@ __global__ __launch_bounds__(ORDER_THREADS) void embed_order_kernel(EmbedBwdArgs
             left &= ~same;
         }
     });
+}
+
+// Many tokens: with all ids read by every workgroup, the order would take longer than
+// the rows (1048576 tokens of as many ids x 64: 2020 us, 181 so). They are then dealt out to buckets of neighbouring ids, in their own order,
+// which takes three launches that read them twice in all: the tokens of each chunk
+// and bucket counted, the counts added up over the chunks, the tokens placed. Buckets
+// of one id are then in order, others are ordered as above, each by a workgroup.
+constexpr int CHUNK = 4096, CHUNK_AHEAD = CHUNK / ORDER_THREADS, BUCKETS_LOG2 = 11, MAX_BUCKETS = 1 << BUCKETS_LOG2;
+
+// This wave's tokens of chunk blockIdx.x, 64 for each k.
+__device__ inline int64_t chunk_first(int wave, int lane) { return (int64_t)blockIdx.x * CHUNK + wave * (CHUNK / ORDER_WAVES) + lane; }
+
+template <class TE>
+__global__ __launch_bounds__(ORDER_THREADS) void embed_count_kernel(EmbedBwdArgs p)
+{
+    __shared__ int count[MAX_BUCKETS];
+    if (embed_fills<TE>(p, p.chunks))
+        return;
+    int id[CHUNK_AHEAD];
+    ids_at<CHUNK_AHEAD>(p.ids, p.wide, (int64_t)blockIdx.x * CHUNK + threadIdx.x, ORDER_THREADS, p.tokens, p.vocab, id);
+    for (int b = threadIdx.x; b < p.buckets; b += ORDER_THREADS)
+        count[b] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < CHUNK_AHEAD; ++k)
+        if (id[k] >= 0)
+            atomicAdd(&count[id[k] >> p.shift], 1);
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.buckets; b += ORDER_THREADS)
+        p.counts[(size_t)blockIdx.x * (size_t)p.buckets + (size_t)b] = count[b];
+}
+
+// 64 buckets a workgroup; its waves take sixteen chunks each at a time.
+__global__ __launch_bounds__(ORDER_THREADS) void embed_scan_kernel(EmbedBwdArgs p)
+{
+    constexpr int AHEAD = 16;
+    __shared__ int part[ORDER_WAVES][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int b = (int)blockIdx.x * 64 + lane;
+    int base = 0;
+    for (int64_t c0 = 0; c0 < p.chunks; c0 += AHEAD * ORDER_WAVES) {
+        const int64_t c = c0 + AHEAD * wave;
+        int n[AHEAD], sum = 0;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            n[k] = b < p.buckets && c + k < p.chunks ? p.counts[(size_t)(c + k) * (size_t)p.buckets + (size_t)b] : 0;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            sum += n[k];
+        part[wave][lane] = sum;
+        __syncthreads();
+        int at = base;
+#pragma unroll
+        for (int w = 0; w < ORDER_WAVES; ++w) {
+            at += w < wave ? part[w][lane] : 0;
+            base += part[w][lane];
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (b < p.buckets && c + k < p.chunks)
+                p.counts[(size_t)(c + k) * (size_t)p.buckets + (size_t)b] = at;
+            at += n[k];
+        }
+        __syncthreads();
+    }
+    if (wave == 0 && b < p.buckets)
+        p.total[b] = base;
+}
+
+__global__ __launch_bounds__(ORDER_THREADS) void embed_place_kernel(EmbedBwdArgs p)
+{
+    constexpr int PER = MAX_BUCKETS / ORDER_THREADS;
+    // [wave][bucket]: first its tokens, then where the next one goes
+    __shared__ int count[ORDER_WAVES][MAX_BUCKETS];
+    __shared__ int total[ORDER_WAVES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int id[CHUNK_AHEAD];
+    ids_at<CHUNK_AHEAD>(p.ids, p.wide, chunk_first(wave, lane), 64, p.tokens, p.vocab, id);
+    // this thread's buckets: their tokens, and those of the chunks before
+    int all[PER], earlier[PER], mine = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int b = PER * tid + k;
+        all[k] = b < p.buckets ? p.total[b] : 0;
+        earlier[k] = b < p.buckets ? p.counts[(size_t)blockIdx.x * (size_t)p.buckets + (size_t)b] : 0;
+        mine += all[k];
+    }
+    for (int i = tid; i < MAX_BUCKETS * ORDER_WAVES; i += ORDER_THREADS)
+        (&count[0][0])[i] = 0;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int x = __shfl_up(upto, d);
+        upto += lane >= d ? x : 0;
+    }
+    if (lane == 63)
+        total[wave] = upto;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < CHUNK_AHEAD; ++k)
+        if (id[k] >= 0)
+            atomicAdd(&count[wave][id[k] >> p.shift], 1);
+    int at = upto - mine, kept = 0;
+#pragma unroll
+    for (int w = 0; w < ORDER_WAVES; ++w) {
+        at += w < wave ? total[w] : 0;
+        kept += total[w];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int b = PER * tid + k;
+        if (blockIdx.x == 0 && b < p.buckets)
+            p.bucket_start[b] = at;
+        int next = at + earlier[k];
+#pragma unroll
+        for (int w = 0; w < ORDER_WAVES; ++w) {
+            const int n = count[w][b];
+            count[w][b] = next;
+            next += n;
+        }
+        at += all[k];
+    }
+    if (blockIdx.x == 0 && tid == 0)
+        p.bucket_start[p.buckets] = kept;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < CHUNK_AHEAD; ++k) {
+        // the lanes whose tokens share a bucket, a bit of its number at a time
+        const int b = max(id[k], 0) >> p.shift;
+        unsigned long long same = __ballot(id[k] >= 0);
+#pragma unroll
+        for (int i = 0; i < BUCKETS_LOG2; ++i) {
+            const bool bit = b >> i & 1;
+            const unsigned long long with = __ballot(bit);
+            same &= bit ? with : ~with;
+        }
+        if (id[k] >= 0) {
+            const int next = count[wave][b], rank = __popcll(same & ((1ull << lane) - 1)), n = __popcll(same);
+            p.bucketed[next + rank] = make_int2(id[k], (int)chunk_first(wave, lane) + 64 * k);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // all have read it
+            if (rank == n - 1)
+                count[wave][b] = next + n;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");       // the next turn reads what these lanes wrote
+    }
 }
 
 // x += the rows of dY of the tokens token(0) .. token(n - 1), asked for in that

@@ -9,12 +9,13 @@
 // Bound by memory, so one pass over it: a row is held in registers between its sums
 // and its results, by one wave (up to 4096 columns, where there are rows for every
 // wave of the card) or four (up to 16384), by 8, 16 or 32 lanes up to 64, 128 or 256
-// columns (heads: 262144 x 128 BF16 22.5 us, 64.5 with a wave for a row; gradients 36
-// and 105); wider rows are read again, by then from the caches. Measured, BF16: 8192 x 4096 in 24.2 us, 5.5 TB/s, its gradients with a
-// residual's in 57.5, 4.7 TB/s, of which 8 the second launch; one row of 4096 2.4 us
-// on the card, 4.9 with its call. The variance is that of the
-// differences from the mean, not of the squares, so no large mean cancels in
-// it; four waves join their means and sums of squared differences m2 by
+// columns (heads: 262144 x 128 BF16 22.5 us, 64.5 with a wave for each row; gradients
+// 36 and 105); wider rows are read again, by then from the caches. Measured, BF16:
+// 8192 x 4096 in 24.2 us, 5.5 TB/s, its gradients with a residual's in 57.5, 4.7 TB/s,
+// of which 8 the second launch; one row of 4096 2.4 us on the card, 4.9 with its call.
+// The variance is that of the differences from the mean, not of the squares, so no
+// large mean cancels in it; four waves join their means and sums of squared
+// differences m2 by
 //   m2 = m2a + m2b + (mean_a - mean_b)^2 n_a n_b / (n_a + n_b).
 // All statistics and sums are FP32; a result is rounded once, as it is stored.
 #pragma once

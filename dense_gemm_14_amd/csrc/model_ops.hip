@@ -67,8 +67,16 @@ struct EmbedBwdPlan {
     bool few;                   // tokens, in one launch
     int range, groups;          // ids per workgroup (few: of all; else: of the order), workgroups
     int block, blocks, pieces;
-    size_t sorted_at, partial_at, bytes;
+    int shift, buckets, chunks; // many tokens (chunks > 0): ids per bucket 1 << shift
+    size_t sorted_at, partial_at, counts_at, total_at, bucket_start_at, bucketed_at, bytes;
 };
+
+// Tokens from which on they are dealt out to buckets first, and the ids that those
+// hold. Measured, BF16, every workgroup reading all ids and so (us): 32768 of 128000 x
+// 1024 81 and 98, 65536 of 128000 x 1024 120 and 125, 131072 of 256000 x 1024 227 and
+// 191, 262144 of 50000 x 512 205 and 131, 1048576 of 1048576 x 64 2020 and 181.
+constexpr int kBucketTokens = 3 << 15;
+constexpr int64_t kBucketVocab = int64_t(r::MAX_BUCKETS) * r::ORDER_MAX_RANGE;
 
 EmbedBwdPlan plan_embed_bwd(int tokens, int vocab, int cols, int cus)
 {
@@ -92,6 +100,18 @@ EmbedBwdPlan plan_embed_bwd(int tokens, int vocab, int cols, int cus)
     e.sorted_at = align_up((size_t(vocab) + 1) * sizeof(int));
     e.partial_at = e.sorted_at + align_up(size_t(tokens) * 8);
     e.bytes = e.partial_at + size_t(e.blocks) * 2 * cols * sizeof(float);
+    if (tokens >= kBucketTokens && vocab <= kBucketVocab) {
+        e.shift = ceil_log2(ceil_div(vocab, r::MAX_BUCKETS));
+        e.range = 1 << e.shift;
+        e.groups = e.buckets = (int)ceil_div(vocab, e.range);
+        e.chunks = (int)ceil_div(tokens, r::CHUNK);
+        // (read for the last time before the first partial row is written)
+        e.counts_at = e.partial_at;
+        e.total_at = e.counts_at + align_up(size_t(e.chunks) * e.buckets * sizeof(int));
+        e.bucket_start_at = e.total_at + align_up(size_t(e.buckets) * sizeof(int));
+        e.bucketed_at = e.bucket_start_at + align_up((size_t(e.buckets) + 1) * sizeof(int));
+        e.bytes = std::max(e.bytes, e.bucketed_at + size_t(tokens) * 8);
+    }
     return e;
 }
 
@@ -288,6 +308,13 @@ extern "C" int gemm355_embedding_bwd(int tokens, int vocab, int cols, int id_typ
     p.pieces = e.pieces;
     p.scale = scale;
     p.wide = id_type == GEMM355_INT64;
+    p.counts = reinterpret_cast<int *>(ws + e.counts_at);
+    p.total = reinterpret_cast<int *>(ws + e.total_at);
+    p.bucket_start = e.shift > 0 ? reinterpret_cast<int *>(ws + e.bucket_start_at) : p.start;
+    p.bucketed = e.shift > 0 ? reinterpret_cast<int2 *>(ws + e.bucketed_at) : p.sorted;
+    p.shift = e.shift;
+    p.buckets = e.buckets;
+    p.chunks = e.chunks;
     if (e.few)
         return with_type(e_type, [&](auto te) {
             return with_type(y_type, [&](auto ty) {
@@ -310,7 +337,19 @@ extern "C" int gemm355_embedding_bwd(int tokens, int vocab, int cols, int id_typ
     return with_type(e_type, [&](auto te) {
         return with_type(y_type, [&](auto ty) {
             typedef decltype(te) TE;
-            int st = launch_kernel(r::embed_order_kernel<TE>, (unsigned)(e.groups + early_groups), (unsigned)r::ORDER_THREADS, p, s);
+            int st = GEMM355_OK;
+            if (e.chunks > 0) {
+                st = launch_kernel(r::embed_count_kernel<TE>, (unsigned)(e.chunks + early_groups), (unsigned)r::ORDER_THREADS, p, s);
+                if (st == GEMM355_OK)
+                    st = launch_kernel(r::embed_scan_kernel, (unsigned)ceil_div(e.buckets, 64), (unsigned)r::ORDER_THREADS, p, s);
+                if (st == GEMM355_OK)
+                    st = launch_kernel(r::embed_place_kernel, (unsigned)e.chunks, (unsigned)r::ORDER_THREADS, p, s);
+                if (st == GEMM355_OK && e.shift > 0)
+                    st = launch_kernel(r::embed_order_kernel<TE, true>, (unsigned)e.groups, (unsigned)r::ORDER_THREADS, p, s);
+            } else {
+                st = launch_kernel(r::embed_order_kernel<TE, false>, (unsigned)(e.groups + early_groups),
+                                   (unsigned)r::ORDER_THREADS, p, s);
+            }
             if (st != GEMM355_OK)
                 return st;
             st = launch_kernel(r::embed_sums_kernel<TE, decltype(ty)>, (unsigned)(sum_groups + late_groups),

@@ -17,7 +17,8 @@ import dense_gemm_14_amd as g
 HERE = os.path.dirname(os.path.abspath(__file__))
 THREADS = {"embed_kernel": 256, "embed_order_kernel": 1024, "embed_sums_kernel": 256, "embed_few_kernel": 256,
            "embed_join_kernel": 512, "norm_kernel": 256, "norm_wide_kernel": 1024, "norm_bwd_kernel": 1024,
-           "norm_sums_kernel": 1024, "ce_prep_kernel": 256, "ce_join_kernel": 256, "dense_tile_kernel": 512,
+           "norm_sums_kernel": 1024, "embed_count_kernel": 1024, "embed_scan_kernel": 1024, "embed_place_kernel": 1024,
+           "ce_prep_kernel": 256, "ce_join_kernel": 256, "dense_tile_kernel": 512,
            "dense_reduce_kernel": 256, "dense_large_kernel": 256, "dense_large_reduce_kernel": 256}
 
 
@@ -130,7 +131,7 @@ def run(shim, seed, count):
     for _ in range(count):
         rec.lib.gemm355_force_layer_kernel(0)
         rec.entropy(log_size(rng, 1, 3000), log_size(rng, 1, 3000), log_size(rng, 8, 2048, 8), rng)
-        rec.embedding(log_size(rng, 1, 100000), log_size(rng, 1, 300000), log_size(rng, 8, 16384, 8), rng)
+        rec.embedding(log_size(rng, 1, 1000000), log_size(rng, 1, 300000), log_size(rng, 8, 16384, 8), rng)
         rec.norm(log_size(rng, 1, 20000), log_size(rng, 8, 40000, 8), rng)
         rec.lib.gemm355_force_layer_kernel(rng.choice([0, 0, 0, 1, 2, 3, 4, 5]))
         rec.entropy(log_size(rng, 1, 20000), log_size(rng, 1, 300000), log_size(rng, 8, 8192, 8), rng)
