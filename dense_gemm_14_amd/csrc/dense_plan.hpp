@@ -21,6 +21,8 @@ using d::DenseArgs;
 
 // ---- products --------------------------------------------------------------
 
+constexpr int kMaxSplits = 16;
+
 // One product C = op(A) op(B)^T of a batch, as the plans see it.
 struct Shape {
     int M, N, K;      // of one batch entry; N: columns of C
@@ -28,6 +30,7 @@ struct Shape {
     bool symmetric;
     bool gated;
     bool row_k;       // both operands
+    int max_splits = kMaxSplits;   // of 128 x 128 tiles; more than that only with eight steps each
 };
 
 // How a product runs on tiles of one size, in rounds of `grid` workgroups: the
@@ -38,8 +41,6 @@ struct TilePlan {
     size_t workspace_bytes;
     double steps;     // of the busiest workgroup
 };
-constexpr int kMaxSplits = 16;
-
 inline TilePlan plan_tiles(const Shape &s, int side, int cus, int min_steps, bool split)
 {
     TilePlan t = {};
@@ -54,7 +55,8 @@ inline TilePlan plan_tiles(const Shape &s, int side, int cus, int min_steps, boo
     t.splits = 1;
     t.steps_per_split = nk;
     if (split && tail > 0) {
-        int n = std::min({t.grid / tail, kMaxSplits, nk / min_steps});
+        const int most = side == d::TILE ? std::max(kMaxSplits, std::min(s.max_splits, nk / 8)) : kMaxSplits;
+        int n = std::min({t.grid / tail, most, nk / min_steps});
         // no part shorter than min_steps, the last one included
         while (n > 1 && nk - ceil_div(nk, n) * (n - 1) < min_steps)
             --n;
@@ -283,10 +285,14 @@ int product_tile(DenseArgs p, const TilePlan &t, hipStream_t stream)
     // whole rounds, then the last one's runs for each of the eight XCDs
     const int64_t blocks = items / t.grid * t.grid + ceil_div(items % t.grid, 8) * 8;
     int st = launch_kernel(d::dense_tile_kernel<T, LA, LB, EPI, TO>, (unsigned)blocks, (unsigned)d::TILE_THREADS, p, stream);
-    if (st == GEMM355_OK && tail > 0)
-        st = launch_kernel(d::dense_reduce_kernel<EPI, TO>, (unsigned)ceil_div(tail * 8, d::REDUCE_WAVES),
-                           64u * d::REDUCE_WAVES, p, stream);
-    return st;
+    if (st != GEMM355_OK || tail == 0)
+        return st;
+    if constexpr (EPI == d::EPI_ACC) {
+        if (t.splits > kMaxSplits)
+            return launch_kernel(d::dense_reduce_many_kernel<EPI, TO>, (unsigned)(tail * 8), 64u * d::REDUCE_MANY_WAVES, p, stream);
+    }
+    return launch_kernel(d::dense_reduce_kernel<EPI, TO>, (unsigned)ceil_div(tail * 8, d::REDUCE_WAVES),
+                         64u * d::REDUCE_WAVES, p, stream);
 }
 
 template <class T, int LA, int LB, int EPI, class TO>

@@ -334,5 +334,50 @@ __global__ __launch_bounds__(64 * REDUCE_WAVES) void dense_reduce_kernel(DenseAr
     tile_store<EPI, TO>(p, x, tm, tn, pair & 1, pair >> 1, i0, lane);
 }
 
+// The same for more than sixteen splits (a sum over a vocabulary for a few tokens: up to
+// 64 of a tile), which a wave would wait for one after the other: a workgroup per two
+// rows of blocks, its waves each a run of the splits, joined in order through LDS.
+constexpr int REDUCE_MANY_WAVES = 8;
+template <int EPI, class TO>
+__global__ __launch_bounds__(64 * REDUCE_MANY_WAVES) void dense_reduce_many_kernel(DenseArgs p)
+{
+    __shared__ f32x4 part[REDUCE_MANY_WAVES][8][64];
+    take_rows<EPI>(p, TILE);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int unit = (int)blockIdx.x, tail = p.tiles - p.whole, q = unit >> 3;
+    if (q >= tail)
+        return;
+    const int pair = (unit >> 1) & 3, i0 = 2 * (unit & 1);
+    const int per = (p.splits + REDUCE_MANY_WAVES - 1) / REDUCE_MANY_WAVES;
+    const int z0 = wave * per, z1 = min(p.splits, z0 + per);
+    const f32x4 *ws = reinterpret_cast<const f32x4 *>(p.ws) + ((size_t)z0 * (size_t)tail + (size_t)q) * (TILE_FLOATS / 4) +
+                      ((pair * 4 + i0) * 4) * 64 + lane;
+    f32x4 x[2][4] = {};
+#pragma unroll 4
+    for (int z = z0; z < z1; ++z) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[i][j] += ws[(i * 4 + j) * 64];
+        ws += (size_t)tail * (TILE_FLOATS / 4);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        part[wave][k][lane] = x[k >> 2][k & 3];
+    __syncthreads();
+    if (wave != 0)
+        return;
+#pragma unroll
+    for (int w = 1; w < REDUCE_MANY_WAVES; ++w)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k >> 2][k & 3] += part[w][k][lane];
+    int tm, tn;
+    dense_tile<EPI>(p, p.whole + q, tm, tn);
+    tile_store<EPI, TO>(p, x, tm, tn, pair & 1, pair >> 1, i0, lane);
+}
+
 } // namespace dense
 } // namespace gemm355

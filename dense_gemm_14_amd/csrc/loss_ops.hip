@@ -115,6 +115,12 @@ int prep_blocks(int M, int cus) { return (int)std::min<int64_t>(std::max<int64_t
 // Bytes of a piece's gradient of the logits.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 
+// dA of few tokens is a few tiles that each sum over a whole piece of the vocabulary:
+// more workgroups take a share of it than a layer's products are split over (whole
+// gradients with 64 and with 16 at most, us: 5 x 29422 x 72 30.7 and 38.3, 82 x 65635 x
+// 472 99 and 114, 200 x 50000 x 264 78 and 87, 1000 x 20000 x 128 70 and 74).
+constexpr int kSumSplits = 64;
+
 struct BackwardPlan {
     Pieces pieces;
     ProductPlan z[2], a[2], b[2];     // of a piece, of the last one
@@ -160,7 +166,7 @@ BackwardPlan plan_backward(int M, int V, int K, bool wants_a, bool wants_b, int 
     for (int i = 0; i < 2; ++i) {
         const int N = i == 1 ? w.pieces.last : w.pieces.width;
         w.z[i] = plan_product({rows, N, K, 1, false, false}, true, cus);
-        w.a[i] = plan_product({rows, K, N, 1, false, false}, false, cus);
+        w.a[i] = plan_product({rows, K, N, 1, false, false, false, kSumSplits}, false, cus);
         w.b[i] = plan_product({N, K, rows, 1, false, false}, false, cus);
         w.min_steps[i] = w.b[i].kernel <= KERNEL_SPLIT ? d::BIG_MIN_STEPS : 0;
         partials = std::max({partials, w.z[i].workspace_bytes, w.a[i].workspace_bytes, w.b[i].workspace_bytes});

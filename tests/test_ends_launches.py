@@ -19,7 +19,7 @@ THREADS = {"embed_kernel": 256, "embed_order_kernel": 1024, "embed_sums_kernel":
            "embed_join_kernel": 512, "norm_kernel": 256, "norm_wide_kernel": 1024, "norm_bwd_kernel": 1024,
            "norm_sums_kernel": 1024, "embed_count_kernel": 1024, "embed_scan_kernel": 1024, "embed_place_kernel": 1024,
            "ce_prep_kernel": 256, "ce_join_kernel": 256, "dense_tile_kernel": 512,
-           "dense_reduce_kernel": 256, "dense_large_kernel": 256, "dense_large_reduce_kernel": 256}
+           "dense_reduce_kernel": 256, "dense_reduce_many_kernel": 512, "dense_large_kernel": 256, "dense_large_reduce_kernel": 256}
 
 
 def kernel_of(mangled):

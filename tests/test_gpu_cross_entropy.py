@@ -245,6 +245,21 @@ def test_several_pieces(M, V, K):
     close(grads["dB"], dB.cpu(), eB.cpu(), "dB")
 
 
+@pytest.mark.parametrize("kernel", [g.LAYER_AUTO, g.LAYER_TILE])
+@pytest.mark.parametrize("M,V,K,skip", [(2, 40563, 136, 0.0), (82, 65635, 72, 0.1), (129, 20001, 136, 0.5),
+                                        (300, 33000, 72, 0.9)])
+def test_few_tokens_of_many_ids(M, V, K, skip, kernel):
+    need_gpu()
+    print("ce few", M, V, K, kernel, flush=True)
+    A, B, t, w = (x.cuda() for x in inputs(M, V, K, skip=skip))
+    lse = forward_reference(A, B, t)["lse"][0].float()
+    g.force_layer_kernel(kernel)
+    try:
+        check(run_bwd(A, B, t, lse, w), backward_reference(A, B, t, lse, w))
+    finally:
+        g.force_layer_kernel(g.LAYER_AUTO)
+
+
 def test_equal_weights_add_no_rounding():
     # dloss the same everywhere: the gradients are those of ones, times it
     need_gpu()
