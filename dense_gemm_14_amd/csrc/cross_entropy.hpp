@@ -17,7 +17,7 @@
 // together beforehand, and the products take their number from device memory.
 // That also keeps whatever the other rows hold, infinities included, out of dB.
 //
-// Measured: forward of 8192 x 128000, K = 4096 in 6.04 to 6.11 ms, 1420 to 1405
+// Measured: forward of 8192 x 128000, K = 4096 in 6.04 to 6.19 ms, 1420 to 1390
 // TFLOP/s (a library product of these sizes 5.90), bounded by the matrix cores at the
 // power limit; one token 170 us, 6.2 TB/s, bounded by memory. Backward of 4096 x
 // 128000, K = 4096 in 9.13 to 9.35 ms, 1410 to 1378 TFLOP/s: in a piece of 32768
