@@ -154,7 +154,7 @@ def test_a_training_step(T, V, K, N):
         assert rel <= 12 * 2.0 ** -8, (k, rel)
 
 
-@pytest.mark.parametrize("T,V,K,N", SIZES + [(2100, 9000, 264, 264)])
+@pytest.mark.parametrize("T,V,K,N", SIZES + [(2100, 9000, 264, 264), (99000, 3001, 64, 72)])
 def test_captured_and_replayed(T, V, K, N):
     need_gpu()
     print("graph", T, V, K, N, flush=True)
