@@ -121,6 +121,24 @@ constexpr int64_t kPieceBytes = int64_t(256) << 20;
 // 472 99 and 114, 200 x 50000 x 264 78 and 87, 1000 x 20000 x 128 70 and 74).
 constexpr int kSumSplits = 64;
 
+// The small tiles sum a vocabulary up to here; beyond, where their estimates were not
+// fitted and fall short of what they take, 128 x 128 ones, split (whole gradients, small
+// and 128, us: 110 x 4699 x 1120 38 and 45, 2 x 7170 x 2424 56 and 58, 64 x 8000 x 1024
+// 48 and 45, 43 x 9226 x 480 40 and 38, 16 x 16000 x 4096 144 and 123). Both products in
+// one launch, which saves one, somewhat further (so, and apart: 150 x 8000 x 128 28 and
+// 32, 150 x 12696 x 88 47 and 33, 300 x 12000 x 64 40 and 32).
+constexpr int kSmallSums = 7680, kSmallBoth = 10240;
+ProductPlan plan_sum(const Shape &s, int cus)
+{
+    ProductPlan p = plan_product(s, false, cus);
+    if (p.kernel >= KERNEL_SMALL && s.K > kSmallSums && p.us > 0.0) {      // (0: forced)
+        p.kernel = KERNEL_TILE;
+        p.tiles = plan_tile(s, cus);
+        p.workspace_bytes = p.tiles.workspace_bytes;
+    }
+    return p;
+}
+
 struct BackwardPlan {
     Pieces pieces;
     ProductPlan z[2], a[2], b[2];     // of a piece, of the last one
@@ -166,14 +184,14 @@ BackwardPlan plan_backward(int M, int V, int K, bool wants_a, bool wants_b, int 
     for (int i = 0; i < 2; ++i) {
         const int N = i == 1 ? w.pieces.last : w.pieces.width;
         w.z[i] = plan_product({rows, N, K, 1, false, false}, true, cus);
-        w.a[i] = plan_product({rows, K, N, 1, false, false, false, kSumSplits}, false, cus);
+        w.a[i] = plan_sum({rows, K, N, 1, false, false, false, kSumSplits}, cus);
         w.b[i] = plan_product({N, K, rows, 1, false, false}, false, cus);
         w.min_steps[i] = w.b[i].kernel <= KERNEL_SPLIT ? d::BIG_MIN_STEPS : 0;
         partials = std::max({partials, w.z[i].workspace_bytes, w.a[i].workspace_bytes, w.b[i].workspace_bytes});
         depth = std::max(depth, d::ce_depth(rows, splits_of(w.b[i]), w.min_steps[i]));
     }
     // (one launch takes none of the partials and whole steps that are set aside)
-    if (w.pieces.count == 1 && M > 0 && wants_a && wants_b)
+    if (w.pieces.count == 1 && M > 0 && wants_a && wants_b && V <= kSmallBoth)
         w.together = backward_together({M, K, V, 1, false, false}, &w.a[1], {V, K, M, 1, false, false}, &w.b[1], cus);
     size_t at = 0;
     auto take = [&](size_t bytes) {
