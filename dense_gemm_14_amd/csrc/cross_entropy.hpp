@@ -42,7 +42,7 @@ struct CePrepArgs {
     const float *lse, *dloss; // backward (dloss may be NULL: ones)
     int *rows;                // number of kept rows
     int *map, *target;        // of each kept row: where it was, its target
-    float *klse, *weight;     // backward: its lse times log2(e), its weight relative to *scale
+    float *klse, *weight;     // backward: its lse, its weight relative to *scale and loss_excess(lse)
     float *scale;             // backward
     void *ka;                 // the kept rows of A, zeros behind them
     float *loss0, *lse0;      // forward: zeros for rows that are left out
@@ -141,8 +141,9 @@ __global__ __launch_bounds__(CE_THREADS) void ce_prep_kernel(CePrepArgs p)
             p.map[at] = (int)m;
             p.target[at] = target;
             if constexpr (BWD) {
-                p.klse[at] = p.lse[m] * LOG2E;
-                p.weight[at] = p.dloss ? p.dloss[m] / scale : 1.0f;
+                const float lse = p.lse[m], w = p.dloss ? p.dloss[m] / scale : 1.0f;
+                p.klse[at] = lse;
+                p.weight[at] = w / loss_excess(lse);
             }
         } else if (!BWD && m < r1) {
             p.loss0[m] = 0.0f;
@@ -177,7 +178,7 @@ __global__ __launch_bounds__(CE_THREADS) void ce_prep_kernel(CePrepArgs p)
 // Joins the runs of ROWS rows: as many lanes side by side, the others share out
 // the runs.
 struct CeJoinArgs {
-    const f32x2 *stats;      // [run][stride]: {base, sum}
+    const f32x2 *stats;      // [run][stride]: as loss_stat has them
     const float *picked;
     const int *rows, *map;   // or NULL: M rows, in place, whose targets say which are left out
     const void *ids;
@@ -187,13 +188,37 @@ struct CeJoinArgs {
 };
 
 struct CeSum {
-    float base, sum;         // a sum of powers of two under a base that is a whole number, -inf and 0 if there is none
+    float base, sum;         // a sum of powers of two under a base that is a whole number, -inf and 0 if there is none;
+                             // from LOSS_FAR on the largest logit and minus the number of those that are the same
     float rest;              // what was not finite
 };
-__device__ inline CeSum ce_join(const CeSum &a, const CeSum &b)
+__device__ inline CeSum ce_join_near(const CeSum &a, const CeSum &b)
 {
     const float base = fmaxf(a.base, b.base), ref = __builtin_isinf(base) ? 0.0f : base;
     return CeSum{base, a.sum * __builtin_amdgcn_exp2f(a.base - ref) + b.sum * __builtin_amdgcn_exp2f(b.base - ref), a.rest + b.rest};
+}
+// Where one is from LOSS_FAR on: logits that large outweigh all that are smaller, and
+// nothing where there is any that is larger (e^-64 and less). (0 times the sums: NaN stays.)
+__device__ inline CeSum ce_join_far(const CeSum &a, const CeSum &b)
+{
+    const float ka = a.sum < 0.0f || __builtin_isinf(a.base) ? a.base : 0.0f;
+    const float kb = b.sum < 0.0f || __builtin_isinf(b.base) ? b.base : 0.0f;
+    return CeSum{ka >= kb ? a.base : b.base, (ka >= kb ? a.sum : 0.0f) + (kb >= ka ? b.sum : 0.0f),
+                 a.rest + b.rest + 0.0f * (a.sum + b.sum)};
+}
+__device__ inline CeSum ce_join(const CeSum &a, const CeSum &b)
+{
+    return a.sum < 0.0f || b.sum < 0.0f ? ce_join_far(a, b) : ce_join_near(a, b);
+}
+// join(ce_join) where some lane of the wave is `far`, else join(ce_join_near): one
+// branch for several joins.
+template <class F>
+__device__ inline void with_join(bool far, F &&join)
+{
+    if (__ballot(far) != 0)
+        join([](const CeSum &a, const CeSum &b) { return ce_join(a, b); });
+    else
+        join([](const CeSum &a, const CeSum &b) { return ce_join_near(a, b); });
 }
 
 template <int ROWS>
@@ -209,10 +234,19 @@ __global__ __launch_bounds__(CE_THREADS) void ce_join_kernel(CeJoinArgs p)
         for (int i0 = ty; i0 < p.runs; i0 += AHEAD * LANES) {
             f32x2 t[AHEAD];
             float base = -__builtin_inff();
+            bool far = s.sum < 0.0f;
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
                 t[k] = p.stats[(size_t)min(i0 + k * LANES, p.runs - 1) * (size_t)p.stride + (size_t)m];
                 base = fmaxf(base, t[k][0]);
+                far |= t[k][1] < 0.0f;
+            }
+            if (far) {      // one by one
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k)
+                    if (i0 + k * LANES < p.runs)
+                        s = ce_join(s, __builtin_isinf(t[k][0]) ? CeSum{t[k][0], 0.0f, t[k][1]} : CeSum{t[k][0], t[k][1], 0.0f});
+                continue;
             }
             CeSum x = {base, 0.0f, 0.0f};
 #pragma unroll
@@ -222,22 +256,32 @@ __global__ __launch_bounds__(CE_THREADS) void ce_join_kernel(CeJoinArgs p)
                     x.sum += finite ? t[k][1] * __builtin_amdgcn_exp2f(t[k][0] - base) : 0.0f;
                     x.rest += finite ? 0.0f : t[k][1];
                 }
-            s = ce_join(s, x);
+            s = ce_join_near(s, x);
         }
     // the lanes of a row within a wave, then the waves
+    with_join(s.sum < 0.0f, [&](auto join) {
 #pragma unroll
-    for (int d = ROWS; d < 64; d *= 2)
-        s = ce_join(s, CeSum{__shfl_xor(s.base, d), __shfl_xor(s.sum, d), __shfl_xor(s.rest, d)});
+        for (int d = ROWS; d < 64; d *= 2)
+            s = join(s, CeSum{__shfl_xor(s.base, d), __shfl_xor(s.sum, d), __shfl_xor(s.rest, d)});
+    });
     if ((threadIdx.x & 63) < ROWS)
         part[threadIdx.x >> 6][tx] = s;
     __syncthreads();
+    bool far = false;
 #pragma unroll
     for (int w = 0; w < CE_WAVES; ++w)
-        s = w == 0 ? part[0][tx] : ce_join(s, part[w][tx]);
+        far |= part[w][tx].sum < 0.0f;
+    with_join(far, [&](auto join) {
+#pragma unroll
+        for (int w = 0; w < CE_WAVES; ++w)
+            s = w == 0 ? part[0][tx] : join(s, part[w][tx]);
+    });
     if (ty == 0 && m < M) {
-        // base log(2) in 64 bits: rounded to 32 it would be the largest error of all
-        const double base = __builtin_isinf(s.base) ? 0.0 : (double)s.base * 0.69314718055994530942;
-        const float rest = logf(s.sum + s.rest);
+        // in 64 bits: rounded to 32 it would be the largest error of all. Divided by the
+        // log2(e) that the logits were multiplied by, not multiplied by log(2): rounded, that
+        // is 2^-26 off.
+        const double base = __builtin_isinf(s.base) ? 0.0 : s.sum < 0.0f ? (double)s.base : (double)s.base * (1.0 / (double)LOG2E);
+        const float rest = logf(fabsf(s.sum) + s.rest);
         const int row = p.map ? p.map[m] : m;
         const bool out = !p.map && rows::id_at(p.ids, p.wide, (size_t)m, p.V) < 0;
         p.lse[row] = out ? 0.0f : (float)(base + rest);

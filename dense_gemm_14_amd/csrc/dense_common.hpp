@@ -70,7 +70,7 @@ struct DenseArgs {
     const float *lse, *weight;
     int v0;
     int ldc;             // EPI_CE_GRAD: elements from one row of C to the next
-    f32x2 *stats;        // EPI_CE: {base, sum} [run of columns][stats_rows]
+    f32x2 *stats;        // EPI_CE: sums [run of columns][stats_rows], as loss_stat has them
     float *picked;       // the targets' values
     int stats_rows;
     // EPI_ACC

@@ -67,7 +67,7 @@ __device__ inline LossRow loss_row_of(const DenseArgs &p, int m)
         } else {
             r.at = loss_target(p, m);
             if constexpr (EPI == EPI_CE_GRAD) {
-                r.lse = p.lse[m];      // (times log2(e))
+                r.lse = p.lse[m];
                 r.weight = p.weight[m];
             }
         }
@@ -110,13 +110,34 @@ __device__ inline float row_add(float x)
 // infinite: all -inf then give a sum of 0, and +inf one of +inf; NaN is in the sum
 // in any case), so that an argument is one multiply-add with one rounding of its
 // small result, and joining two sums multiplies by a power of two, exactly.
-__device__ inline float loss_base(float top) { return __builtin_isinf(top) ? 0.0f : __builtin_rintf(top * LOG2E); }
-__device__ inline float loss_exp(float z, float base) { return __builtin_amdgcn_exp2f(__builtin_fmaf(z, LOG2E, -base)); }
+// A large base is rounded, by half a step, at most 64 below 1.5 2^30; the arguments
+// are taken from it as it is, so the sum has that difference as a factor.
+// From LOSS_FAR on (a mask's -1e30, say) the difference would be more than a power of
+// two holds, and from 2.4e38 on the product overflows. But FP32 values that are not the
+// same lie 64 and more apart there, and so do those nearer to 0: beside the largest
+// logit no other weighs, to any base. Its run's arguments are z - top: a factor and a
+// base of their own for the row's multiply-adds, and nothing more for each element (330 x
+// 81578, K = 328: 62.8 us with it, 62.0 without; differences taken first instead, in a
+// branch a row, 63.6, in a copy of the code for such rows 85, as it spilt).
+constexpr float LOSS_FAR = 1073741824.0f;      // 2^30
+__device__ inline bool loss_far(float x) { return fabsf(x) >= LOSS_FAR; }
+__device__ inline float loss_factor(float x) { return loss_far(x) ? 1.0f : LOG2E; }
+__device__ inline float loss_base(float top, float factor) { return __builtin_isinf(top) ? 0.0f : __builtin_rintf(top * factor); }
+__device__ inline float loss_exp(float z, float factor, float base) { return __builtin_amdgcn_exp2f(__builtin_fmaf(z, factor, -base)); }
 // {base, sum} as it is stored: base -inf where no value was finite, the sum then 0,
-// +inf or NaN.
+// +inf or NaN; from LOSS_FAR on {top, -sum}.
 __device__ inline f32x2 loss_stat(float top, float base, float sum)
 {
-    return f32x2{__builtin_isinf(top) ? -__builtin_inff() : base, sum};
+    return __builtin_isinf(top) ? f32x2{-__builtin_inff(), sum} : f32x2{base, loss_far(top) ? -sum : sum};
+}
+// What the rounding of a row's base, lse log2(e), multiplies its exponentials by. Below
+// LOSS_EXACT, where all rows are that a network has learnt from, less than 2^-14 of
+// them, the lse's own rounding; from LOSS_FAR on there is none.
+constexpr float LOSS_EXACT = 1024.0f;
+__device__ inline float loss_excess(float lse)
+{
+    const bool none = !(fabsf(lse) >= LOSS_EXACT && fabsf(lse) < LOSS_FAR);
+    return none ? 1.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(lse, LOG2E, -(lse * LOG2E)));
 }
 
 // What a row of blocks reads besides its sums (EPI_ACC: the pieces' before).
@@ -157,7 +178,7 @@ __device__ inline void loss_row(const DenseArgs &p, const __amdgpu_buffer_rsrc_t
             for (int e = 0; e < 4; ++e)
                 top = fmaxf(top, x[j][e]);
         top = row_max(top);
-        const float base = loss_base(top);
+        const float factor = loss_factor(top), base = loss_base(top, factor);
         if (hit) {
             float picked = 0.0f;
             asm volatile("");
@@ -175,7 +196,7 @@ __device__ inline void loss_row(const DenseArgs &p, const __amdgpu_buffer_rsrc_t
             float t[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                t[e] = loss_exp(x[j][e], base);
+                t[e] = loss_exp(x[j][e], factor, base);
             sum += (t[0] + t[1]) + (t[2] + t[3]);
         }
         sum = row_add(sum);
@@ -183,18 +204,20 @@ __device__ inline void loss_row(const DenseArgs &p, const __amdgpu_buffer_rsrc_t
             p.stats[(size_t)(col / (16 * BJ)) * (size_t)p.stats_rows + (size_t)m] = loss_stat(top, base, sum);
     }
     if constexpr (EPI == EPI_CE_GRAD) {
+        const float factor = loss_factor(row.lse), base = row.lse * factor;
 #pragma unroll
         for (int j = 0; j < BJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                x[j][e] = loss_exp(x[j][e], row.lse);
+                x[j][e] = loss_exp(x[j][e], factor, base);
         if (hit) {
             asm volatile("");
+            const float one = loss_excess(row.lse);      // (the weight has it divided out)
 #pragma unroll
             for (int j = 0; j < BJ; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    x[j][e] -= d == 16 * j + e ? 1.0f : 0.0f;
+                    x[j][e] -= d == 16 * j + e ? one : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < BJ; ++j)
@@ -303,11 +326,11 @@ __device__ inline void loss_eight(const DenseArgs &p, float (&x)[8], int m, int 
 #pragma unroll
         for (int d = 1; d < RUNS; d *= 2)
             top = fmaxf(top, __shfl_xor(top, d));
-        const float base = loss_base(top);
+        const float factor = loss_factor(top), base = loss_base(top, factor);
         float sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            sum += loss_exp(x[e], base);
+            sum += loss_exp(x[e], factor, base);
 #pragma unroll
         for (int d = 1; d < RUNS; d *= 2)
             sum += __shfl_xor(sum, d);
@@ -323,9 +346,10 @@ __device__ inline void loss_eight(const DenseArgs &p, float (&x)[8], int m, int 
         if (!in)
             return;
         if constexpr (EPI == EPI_CE_GRAD) {
+            const float factor = loss_factor(r.row.lse), base = r.row.lse * factor, one = loss_excess(r.row.lse);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                x[e] = n + e < p.N ? (loss_exp(x[e], r.row.lse) - (d == e ? 1.0f : 0.0f)) * r.row.weight : 0.0f;
+                x[e] = n + e < p.N ? (loss_exp(x[e], factor, base) - (d == e ? one : 0.0f)) * r.row.weight : 0.0f;
             *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + (size_t)m * (size_t)p.ldc + (size_t)n) =
                 u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
         }

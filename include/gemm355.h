@@ -699,8 +699,8 @@ int gemm355_layer_norm_bwd_workspace_size(int rows, int cols, size_t *bytes);
  *   loss     M FP32 values; their mean or weighted sum is the caller's, who hands
  *            its gradient to the backward call
  *   lse      M FP32 values for gemm_bf16_nt_cross_entropy_bwd
- * Products exact, sums and exponentials FP32; infinities and NaN among the logits
- * go where the formula takes them, within their row. A row that is left out costs
+ * Products exact, sums and exponentials FP32; logits are of any size (a mask's -1e30),
+ * infinities and NaN among them go where the formula takes them, within their row. A row that is left out costs
  * nothing in a product of more than 2^33 multiplications. M == 0 does nothing; with K == 0 every z is 0.
  * A padded to 256 rows and 256 rows of B stay below 2^31 bytes each, else
  * GEMM355_ERR_UNSUPPORTED, as are more than 2^26 tokens or 2^46 logits; B as a whole
