@@ -168,7 +168,8 @@ int with_rows(int cols, bool many, F &&f)
 // and 19.6, 4000 x 8192 FP32 146 and 96, 2000 x 16384 77 and 76.
 bool norm_direct(int rows, int cols, bool fp32) { return rows <= 800 || cols > (fp32 ? 8192 : 16384); }
 
-// Lanes that hold a row where there are many, and the workgroups that walk them. A
+// Lanes that hold a row where there are many, and the workgroups that walk them: none
+// where one launch does it, whose rows may be wider than a workgroup's lanes hold. A
 // lane holds eight columns of FP32 rows and of short ones, sixteen of others.
 int norm_bwd_lanes(int cols, bool fp32)
 {
@@ -177,6 +178,8 @@ int norm_bwd_lanes(int cols, bool fp32)
 }
 int norm_bwd_blocks(int rows, int cols, bool fp32, int cus)
 {
+    if (norm_direct(rows, cols, fp32))
+        return 0;
     return (int)std::min<int64_t>(cus, ceil_div(rows, r::NORM_BWD_THREADS / norm_bwd_lanes(cols, fp32)));
 }
 template <class X, class F>
