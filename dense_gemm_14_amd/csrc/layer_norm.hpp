@@ -37,13 +37,14 @@ struct NormArgs {
     float eps;
 };
 
-// The statistics of part of a row.
+// The statistics of part of a row; of no values where n is 0, which joins as if it had
+// the other's mean: the square of a distance to 0 may be beyond FP32.
 struct Moments {
     float n, mean, m2;
 };
 __device__ inline Moments join(const Moments &a, const Moments &b)
 {
-    const float n = a.n + b.n, d = b.mean - a.mean, part = n > 0.0f ? b.n / n : 0.0f;
+    const float n = a.n + b.n, d = b.n > 0.0f ? b.mean - a.mean : 0.0f, part = n > 0.0f ? b.n / n : 0.0f;
     return Moments{n, a.mean + d * part, a.m2 + b.m2 + d * d * a.n * part};
 }
 
