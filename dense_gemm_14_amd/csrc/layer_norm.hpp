@@ -275,20 +275,23 @@ __device__ inline void norm_bwd_row(const NormBwdArgs &p, int64_t row, bool in, 
     float sg = 0.0f, su = 0.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        // (columns past the last: dy is 0 there)
-        float tg = 0.0f, tu = 0.0f;
+        // (columns past the last have no part in it: dy is 0 there, but the mean's
+        // distance from 0 may be beyond FP32)
+        if (norm_col<LANES>(lane, v) < p.cols) {
+            float tg = 0.0f, tu = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = dy[v].get(e), u = (x[v].get(e) - mean) * rstd, g = d * gamma[v].get(e);
-            if constexpr (COLUMNS) {
-                dg[v][e] += d * u;
-                db[v][e] += d;
+            for (int e = 0; e < 8; ++e) {
+                const float d = dy[v].get(e), u = (x[v].get(e) - mean) * rstd, g = d * gamma[v].get(e);
+                if constexpr (COLUMNS) {
+                    dg[v][e] += d * u;
+                    db[v][e] += d;
+                }
+                tg += g;
+                tu += g * u;
             }
-            tg += g;
-            tu += g * u;
+            sg += tg;
+            su += tu;
         }
-        sg += tg;
-        su += tu;
         // unpacked again below: kept, the values would take the registers of
         // a row more
         x[v].hold();

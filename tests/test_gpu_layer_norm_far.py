@@ -1,13 +1,13 @@
-"""Layer norm of rows so far from zero that their mean's square lies beyond FP32, against
-64 bits, at widths that fill the lanes of a row, leave some of them empty and leave whole
-waves empty."""
+"""Layer norm of rows so far from zero that their mean's square, or the mean in units of
+their spread, lies beyond FP32. Statistics and gradients against 64 bits, at widths that
+fill the lanes of a row, leave some of them empty and leave whole waves empty."""
 import pytest
 import torch
 
 from tests.dense_util import close
 from tests.gpu_util import need_gpu
-from tests.rows_util import V as v32
-from tests.test_gpu_layer_norm import run
+from tests.rows_util import V as v32, norm_bwd, randn
+from tests.test_gpu_layer_norm import check, gen_of, run, run_bwd
 
 pytestmark = pytest.mark.gpu
 BF16, FP32 = torch.bfloat16, torch.float32
@@ -37,3 +37,20 @@ def test_statistics_of_rows_far_from_zero(rows, cols, x_type):
     assert (got["rstd"] >= low * (1 - 8 * v32)).all()
     # |y| = |x - mean| rstd: at most 1, as of any constant row whose mean is off
     assert torch.isfinite(got["Y"]).all() and (got["Y"].abs() <= 1 + 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("rows,cols", WIDTHS)
+@pytest.mark.parametrize("x_type", [BF16, FP32])
+def test_gradients_of_rows_far_from_zero(rows, cols, x_type):
+    # every second row constant at +-2^110, with the rstd of eps = 2^-38: mean times rstd
+    # is 2^129, beyond FP32, and (x - mean) rstd is 0
+    need_gpu()
+    print("norm_bwd far", rows, cols, x_type, flush=True)
+    gen = gen_of(rows + cols)
+    X = torch.randn(rows, cols, generator=gen).to(x_type)
+    mean, rstd = X.double().mean(1).float(), (1 / X.double().std(1, correction=0)).float()
+    X[::2], mean[::2], rstd[::2] = 2.0 ** 110, 2.0 ** 110, 2.0 ** 19
+    X[::4], mean[::4] = -2.0 ** 110, -2.0 ** 110
+    dY, R = randn(gen, rows, cols), randn(gen, rows, cols, dtype=x_type)
+    gamma = randn(gen, cols, dtype=FP32)
+    check(run_bwd(X, gamma, mean, rstd, dY, R, FP32), norm_bwd(X, gamma, mean, rstd, dY, R, FP32))
