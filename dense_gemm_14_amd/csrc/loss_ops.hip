@@ -433,7 +433,7 @@ extern "C" int gemm_bf16_nt_cross_entropy_bwd(int M, int V, int K, const void *A
         const int which = i == w.pieces.count - 1 ? 1 : 0;
         const int N = which ? w.pieces.last : w.pieces.width;
         const size_t from = size_t(i) * w.pieces.width * K * 2;
-        const uint8_t *b = static_cast<const uint8_t *>(B) + from;
+        const uint8_t *b = M > 0 ? static_cast<const uint8_t *>(B) + from : nullptr;
         void *partials = ws + w.partials_at;
         if (M > 0) {
             DenseArgs p = args_of(M, N, K, q.ka, b, q.dz);      // dz
@@ -448,7 +448,7 @@ extern "C" int gemm_bf16_nt_cross_entropy_bwd(int M, int V, int K, const void *A
         // dB = dz^T A, dA += dz B
         const bool one = w.together.kernel != 0;
         DenseArgs pb = args_of(N, K, one ? M : (int)d::ce_depth(std::max(M, 1), q.splits[which], q.min_steps[which]), q.dz,
-                               q.ka, static_cast<uint8_t *>(dB) + from);
+                               q.ka, wants_b ? static_cast<uint8_t *>(dB) + from : nullptr);
         pb.rows = q.rows;
         pb.rows_in_k = 1;
         pb.min_steps = one ? 0 : q.min_steps[which];

@@ -2,7 +2,7 @@
 whatever C++ leaves undefined (a division by zero, a sum beyond its type, arithmetic on
 no pointer, a shift too far), in a process of its own against the stand-in for the HIP
 runtime: the size queries of the embedding, layer norm and cross entropy calls over
-their whole range."""
+their whole range, and every launch of those and of the layer calls."""
 import ctypes
 import os
 import re
@@ -78,12 +78,27 @@ def sizes():
     print("sizes", count)
 
 
+def launches(seed, count):
+    from tests import test_dense_launches, test_ends_launches
+    for t in (test_ends_launches, test_dense_launches):
+        t.run(sys.argv[2], int(seed), int(count))
+    # no tokens, and none of their arrays, over several pieces of the vocabulary
+    rec = test_ends_launches.Recorder(sys.argv[2])
+    rec.call("gemm_bf16_nt_cross_entropy_bwd", (0, 1 << 25, 64),
+             lambda w, n: (0, 1 << 25, 64, None, None, 0, None, None, None, None, rec.DB, w, n, None))
+    print("launches", sum(rec.seen.values()))
+
+
 def test_size_queries(built):
     assert int(child("sizes", *built)[-1]) > 50000
+
+
+def test_launches(built):
+    assert int(child("launches", *built, "5", "300")[-1]) >= 4
 
 
 if __name__ == "__main__":
     import dense_gemm_14_amd
     stand_in = ctypes.CDLL(sys.argv[2], ctypes.RTLD_GLOBAL)
     dense_gemm_14_amd.LIB_PATH = sys.argv[3]
-    {"sizes": sizes}[sys.argv[1]](*sys.argv[4:])
+    {"sizes": sizes, "launches": launches}[sys.argv[1]](*sys.argv[4:])
