@@ -13,14 +13,16 @@
 // epilogue's result, and both products of that piece; dA's sums are kept in FP32
 // between the pieces. A piece's dz, in BF16, is what the workspace has to hold.
 //
-// Rows that are left out (padding, prompts) cost nothing: the kept rows are moved
-// together beforehand, and the products take their number from device memory.
-// That also keeps whatever the other rows hold, infinities included, out of dB.
+// Rows that are left out (padding, prompts) cost nothing in the backward pass and in a
+// forward one of more than 2^33 multiplications: the kept rows are moved together
+// beforehand, and the products take their number from device memory. (Smaller forward
+// products take all rows, which is less than the launch that moves them.) That also
+// keeps whatever the other rows hold, infinities included, out of dB.
 //
-// Measured: forward of 8192 x 128000, K = 4096 in 6.04 to 6.19 ms, 1420 to 1390
-// TFLOP/s (a library product of these sizes 5.90), bounded by the matrix cores at the
-// power limit; one token 170 us, 6.2 TB/s, bounded by memory. Backward of 4096 x
-// 128000, K = 4096 in 9.13 to 9.35 ms, 1410 to 1378 TFLOP/s: in a piece of 32768
+// Measured on several cards: forward of 8192 x 128000, K = 4096 in 5.98 to 6.32 ms, 1437
+// to 1360 TFLOP/s (a library product of these sizes 5.85 to 6.06), bounded by the matrix
+// cores at the power limit; one token 169 us, 6.2 TB/s, bounded by memory. Backward of
+// 4096 x 128000, K = 4096 in 9.06 to 9.48 ms, 1422 to 1359 TFLOP/s: in a piece of 32768
 // columns z and dz, dB and dA in 786, 790 and 742 us under the profiler.
 //
 // dz enters the products in BF16. The rows' weights dloss are taken relative to

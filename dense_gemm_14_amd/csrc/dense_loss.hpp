@@ -2,8 +2,8 @@
 // over a vocabulary (cross_entropy.hpp has the other kernels and the whole):
 //
 //   EPI_CE       z = A B^T of a tile. Nothing of it is stored but, for each row
-//                and run of columns, the sum of 2^(z log2(e) - base) with its base,
-//                and the target's z where the run holds it.
+//                and run of columns, the sum of 2^(z log2(e) - base) with its base
+//                (see loss_base for large z), and the target's z where the run holds it.
 //   EPI_CE_GRAD  z again, C = round((exp(z - lse) - [column = target]) weight),
 //                zeros in the columns between N and the next multiple of 8
 //   EPI_ACC      sums over pieces of the contraction: FP32 sums, added to those

@@ -13,7 +13,9 @@
 //     token against the 8 KiB of its row of dY) and so knows by itself how many
 //     come before its range: no workgroup waits for another, and no pass over
 //     digits is needed. Its sixteen waves each count, then place, a run of tokens.
-//     (From about 100000 tokens on they are dealt out to buckets of ids first.)
+//     (From about 100000 tokens on they are dealt out to buckets of ids first, for up to
+//     2^20 ids. More tokens of larger tables are ordered as here, in a time that grows with
+//     both: 1000000 of 1048577 ids x 64 2140 us.)
 //   * sums: the sorted tokens are cut into blocks of a few. A wave takes a block
 //     and 512 columns and adds the rows of every id whose tokens begin in its
 //     block, to their end; an id with many tokens is instead cut at the blocks'

@@ -10,9 +10,11 @@
 // and its results, by one wave (up to 4096 columns, where there are rows for every
 // wave of the card) or four (up to 16384), by 8, 16 or 32 lanes up to 64, 128 or 256
 // columns (heads: 262144 x 128 BF16 22.5 us, 64.5 with a wave for each row; gradients
-// 36 and 105); wider rows are read again, by then from the caches. Measured, BF16:
-// 8192 x 4096 in 24.2 us, 5.5 TB/s, its gradients with a residual's in 57.5, 4.7 TB/s,
-// of which 8 the second launch; one row of 4096 2.4 us on the card, 4.9 with its call.
+// 36 and 105); wider rows are read again, by then from the caches (1024 x 32768 BF16 in 34
+// to 39 us, gradients 77 to 83). Measured, BF16: 8192 x 4096 in 24.2 us, 5.5 TB/s (29.2
+// with so many arrays in turn that the last-level cache holds none), its gradients with a
+// residual's in 57.5, 4.7 TB/s, of which 8 the second launch; FP32 rows and weights 43
+// and 92; one row of 4096 2.4 us on the card, 4.9 with its call.
 // The variance is that of the differences from the mean, not of the squares, so no
 // large mean cancels in it; four waves join their means and sums of squared
 // differences m2 by

@@ -640,7 +640,10 @@ int gemm355_embedding(int tokens, int vocab, int cols, int id_type, const void *
  * The tokens of one id are added in an order that depends on the ids and sizes
  * alone. The workspace (gemm355_embedding_bwd_workspace_size bytes, NULL where that
  * is 0, as for up to 1024 tokens) is as for the layer calls. vocab == 0 or
- * cols == 0 does nothing; vocab beyond 2^30 is GEMM355_ERR_UNSUPPORTED.
+ * cols == 0 does nothing; vocab beyond 2^30 is GEMM355_ERR_UNSUPPORTED. Hundreds of
+ * thousands of tokens are ordered in a time that is small beside their rows' for
+ * vocab up to 2^20; beyond, in one that grows with tokens * vocab (a million tokens of
+ * as many ids: 0.2 and 2.1 ms).
  */
 int gemm355_embedding_bwd(int tokens, int vocab, int cols, int id_type, const void *ids, int y_type, const void *dY,
                           float scale, int e_type, const void *R, void *dE, void *workspace, size_t workspace_bytes,
