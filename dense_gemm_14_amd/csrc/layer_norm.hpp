@@ -40,14 +40,15 @@ struct NormArgs {
 };
 
 // The statistics of part of a row; of no values where n is 0, which joins as if it had
-// the other's mean: the square of a distance to 0 may be beyond FP32.
+// the other's mean: the square of a distance to 0 may be beyond FP32. (Means that are a
+// distance without end apart are added: infinite, or NaN, as the sum of the row is.)
 struct Moments {
     float n, mean, m2;
 };
 __device__ inline Moments join(const Moments &a, const Moments &b)
 {
     const float n = a.n + b.n, d = b.n > 0.0f ? b.mean - a.mean : 0.0f, part = n > 0.0f ? b.n / n : 0.0f;
-    return Moments{n, a.mean + d * part, a.m2 + b.m2 + d * d * a.n * part};
+    return Moments{n, fabsf(d) < __builtin_inff() ? a.mean + d * part : a.mean + b.mean, a.m2 + b.m2 + d * d * a.n * part};
 }
 
 // A row in the registers of LANES lanes, of which there are 8, 16 or 32 (a wave
